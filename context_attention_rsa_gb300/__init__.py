@@ -29,7 +29,8 @@ __all__ = [
     "host_info", "host_workspace_size", "set_host_copy_mode", "host_copy_path",
     "workspace_size", "ring_schedule", "set_block_kernel",
     "set_wait_limit_ns", "check_device_error", "selftest_wait_timeout", "version",
-    "RSA_F32", "RSA_BF16",
+    "page_plan", "PagePlan", "PLAN_STATUS", "qk_norm_rope", "qk_norm_rope_bwd", "rope_table", "prefix_attn",
+    "prefix_attn_workspace_size", "RSA_F32", "RSA_BF16",
 ]
 
 RSA_F32 = 0
@@ -130,7 +131,8 @@ def load(build: bool = True):
         if _lib is None:
             path = library_path(build)
             lib = ctypes.CDLL(path)
-            for name, args in _SIGS.items():
+            from . import paged
+            for name, args in (*_SIGS.items(), *paged.SIGS.items()):
                 fn = getattr(lib, name)
                 fn.argtypes = args
                 fn.restype = ctypes.c_char_p if name in ("rsa_status_string", "rsa_last_error_string") \
@@ -573,3 +575,7 @@ def check_device_error(stream=None) -> None:
 
 def selftest_wait_timeout(stream=None) -> None:
     _call("rsa_selftest_wait_timeout", _stream(stream))
+
+
+from .paged import (PLAN_STATUS, PagePlan, page_plan, prefix_attn, prefix_attn_workspace_size,  # noqa: E402
+                    qk_norm_rope, qk_norm_rope_bwd, rope_table)

@@ -24,13 +24,6 @@
 
 #include "rsa_internal.h"
 
-#define RSA_TRY(x)                     \
-    do {                               \
-        rsa_status st_ = (x);          \
-        if (st_ != RSA_OK)             \
-            return st_;                \
-    } while (0)
-
 namespace rsa {
 
 static thread_local char g_last_error[512] = "";
@@ -148,7 +141,14 @@ std::atomic<int> g_tc_kernel{0};
 // wrapper reports a launch failure instead of launching, then disarms.
 std::atomic<int> g_inject_countdown{-1};
 
-// True if this launch is to fail (and the failure has been recorded).
+constexpr int kMaxDevices = 64;
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+namespace rsa {
+
 bool injected_failure(const char *what, rsa_status *st)
 {
     int c = g_inject_countdown.load();
@@ -163,8 +163,6 @@ bool injected_failure(const char *what, rsa_status *st)
     return false;
 }
 
-constexpr int kMaxDevices = 64;
-
 rsa_status device_error_word(unsigned int **out)
 {
     void *p = nullptr;
@@ -172,6 +170,8 @@ rsa_status device_error_word(unsigned int **out)
     *out = static_cast<unsigned int *>(p);
     return RSA_OK;
 }
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 // The bf16 kernels are built for sm_103a only.
 rsa_status check_device_for(rsa_dtype dt)
@@ -199,7 +199,18 @@ rsa_status check_device_for(rsa_dtype dt)
     return RSA_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+rsa_status check_ptr(const void *p, const char *name)
+{
+    if (!p)
+        return fail(RSA_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned16(p))
+        return fail(RSA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    return RSA_OK;
+}
+
+}  // namespace rsa
+
+namespace {
 
 rsa_status check_shape(rsa_dtype dt, int B, int H, int64_t T, int d)
 {
@@ -214,15 +225,6 @@ rsa_status check_shape(rsa_dtype dt, int B, int H, int64_t T, int d)
     const int64_t BH = (int64_t)B * H;
     if (BH > 0x7fffffffLL || (dt == RSA_F32 && BH > 65535))
         return fail(RSA_ERR_UNSUPPORTED, "B*H=%lld too large", (long long)BH);
-    return RSA_OK;
-}
-
-rsa_status check_ptr(const void *p, const char *name)
-{
-    if (!p)
-        return fail(RSA_ERR_INVALID_ARG, "%s is NULL", name);
-    if (!aligned16(p))
-        return fail(RSA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
     return RSA_OK;
 }
 
@@ -243,8 +245,6 @@ int round_pairs(int N, int causal, int r, int *qi, int *kj)
 }
 
 int visits(int N, int causal, int i) { return causal ? i + 1 : N; }
-
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct WsLayout {
     size_t acc, oblk, lblk, total;

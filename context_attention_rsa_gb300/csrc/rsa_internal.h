@@ -9,11 +9,18 @@
 
 #include "../../include/rsa.h"
 
+#define RSA_TRY(x)                     \
+    do {                               \
+        rsa_status st_ = (x);          \
+        if (st_ != RSA_OK)             \
+            return st_;                \
+    } while (0)
+
 namespace rsa {
 
 // Device error word values (OR-ed with a site code in the low byte).
 constexpr unsigned int kDevErrTimeout = 0x100u;
-constexpr unsigned int kDevErrBounds = 0x200u;  // a bounds check of an RSA_DEBUG build failed
+constexpr unsigned int kDevErrBounds = 0x200u;  // a bounds check failed (RSA_DEBUG build, or index data)
 
 // The device-side error record.  Kernels get a pointer to `word` and OR codes
 // into it; builds with RSA_DEBUG also keep the first out-of-range index (plus
@@ -24,21 +31,31 @@ struct DeviceError {
     unsigned long long bad_index_plus1;
 };
 
+// Record an index that lies outside its range: the site code and the first
+// such index (plus one).  For index data that only the device sees (lengths,
+// page ids, slots, positions), in every build; the caller skips the access.
+__device__ __forceinline__ void record_bad_index(unsigned int *err, unsigned int site, long long idx)
+{
+    atomicOr(err, kDevErrBounds | site);
+    atomicCAS(&reinterpret_cast<DeviceError *>(err)->bad_index_plus1, 0ull, (unsigned long long)idx + 1ull);
+}
+
 #ifdef RSA_DEBUG
 // Bounds check of an RSA_DEBUG build: false (and recorded, without a trap) if
 // `ok` is false; the caller then skips the access.
 __device__ __forceinline__ bool debug_check(bool ok, unsigned int *err, unsigned int site, long long idx)
 {
-    if (!ok && err) {
-        atomicOr(err, kDevErrBounds | site);
-        atomicCAS(&reinterpret_cast<DeviceError *>(err)->bad_index_plus1, 0ull, (unsigned long long)idx + 1ull);
-    }
+    if (!ok && err)
+        record_bad_index(err, site, idx);
     return ok;
 }
 #define RSA_DCHECK(cond, err, site, idx) ::rsa::debug_check((cond), (err), (site), (long long)(idx))
 #else
 #define RSA_DCHECK(cond, err, site, idx) true
 #endif
+
+// Position axes of a rotation (time, height, width, one more).
+constexpr int kMaxRopeAxes = 4;
 
 // Most pairs one kernel launch takes; longer pair lists are split.
 constexpr int kMaxPairsPerLaunch = 32;
@@ -111,6 +128,84 @@ struct MergeParams {
     MergePair pairs[kMaxPairsPerLaunch];
 };
 
+// One step's plan over a paged cache (rsa_page_plan).
+constexpr int kPagePlanMaxRequests = 16384;  // two ints a request in shared memory
+struct PagePlanParams {
+    const int32_t *cached_len, *new_len;
+    int R, page_shift, max_pages;
+    int64_t n_pages;
+    int32_t *block_table;
+    int64_t table_stride;
+    const int32_t *free_pages;
+    int64_t n_free;
+    const int64_t *free_start;
+    int64_t pos0, max_tokens;
+    int32_t *cu_new, *kv_len;
+    int64_t *slot_map, *positions, *info;
+    unsigned int *err;
+};
+
+// A [T, H, d] operand of the head norm: rows of d contiguous elements, the
+// strides of tokens and heads in elements.
+struct HeadRows {
+    void *data;
+    int64_t token_stride, head_stride;
+};
+
+// Norm and rotation of query and key heads (rsa_qk_norm_rope_fwd and _bwd).
+struct NormRopeParams {
+    int64_t T;
+    int Hq, Hkv, d, f32;
+    HeadRows q, k, v;            // inputs (v only with a cache)
+    HeadRows dq_out, dk_out;     // backward: gradients of the outputs
+    HeadRows q_out, k_out;       // results (backward: gradients of the inputs); k_out.data may be NULL with a cache
+    const void *q_weight, *k_weight;  // [d] of the inputs' type, or NULL for ones
+    float eps;
+    const int64_t *positions;    // [n_axes, T]
+    int n_axes, rot, interleaved;
+    int axis_end[kMaxRopeAxes];  // frequency pairs of axes 0..a end before axis_end[a]
+    const float *cos_sin;        // [max_pos, rot]
+    int64_t max_pos;
+    const int64_t *slot_map;     // [T] or NULL: no cache
+    void *k_cache, *v_cache;     // [n_pages, Hkv, page, d]
+    int64_t n_pages;
+    int page_shift;
+    float *partial;              // backward: [blocks, 2, d]
+    float *dq_weight, *dk_weight;  // backward: [d] each
+    unsigned int *err;
+};
+
+// Attention of packed query rows over a shared prefix and their requests' own
+// paged keys (rsa_prefix_attn_fwd).
+struct PrefixAttnParams {
+    const void *q;               // [T, Hq, d], strides in elements
+    int64_t q_token_stride, q_head_stride;
+    const void *k_cache, *v_cache;  // [n_pages, Hkv, page, d]
+    int64_t T;
+    int Hq, Hkv, G, d, f32;      // G = Hq / Hkv
+    int64_t n_pages;
+    int page_shift;
+    const int32_t *cu_q, *kv_len;  // [R + 1], [R]
+    int R;
+    const int32_t *block_table;  // [R, max_pages], rows table_stride apart
+    int64_t table_stride;
+    int max_pages;
+    const int32_t *prefix_pages;
+    int64_t prefix_len;
+    void *out;                   // [T, Hq, d]
+    float *lse;                  // [T, Hq]
+    // workspace (see paged_sched.cuh)
+    int64_t *plan;               // [R + 3]
+    float *home_o[2], *home_lse[2];  // [T * Hq, d] and [T * Hq]: a row's first piece of the prefix, of its own keys
+    float *slot_o, *slot_lse;    // [workers, 256, d] and [workers, 256]: a worker's first piece, begun by another
+    int workers;
+    uint64_t wait_limit_ns;
+    unsigned int *err;
+};
+constexpr int kPrefixMaxWorkers = 160;   // CTAs of the attention launch: one on each SM
+constexpr int kPrefixUnitRows = 256;     // query rows of one unit at most
+constexpr int kPrefixMaxGroup = 128;     // query heads per key head at most
+
 // Launchers (no validation; the C ABI layer validates).  They return the
 // cudaError_t of the launch.
 cudaError_t launch_block_attn_bf16(const void *q, const void *k, const void *v,
@@ -121,6 +216,14 @@ cudaError_t launch_merge(const MergeParams &p, cudaStream_t s);
 // Fold S partials [S][rows][d] (fp32 o, fp32 lse) into out [rows][d] and lse [rows].
 cudaError_t launch_merge_splits(const float *o_part, const float *lse_part, int S, int64_t rows, int d,
                                 void *out, int out_f32, float *lse, cudaStream_t s);
+cudaError_t launch_page_plan(const PagePlanParams &p, cudaStream_t s);
+cudaError_t launch_qk_norm_rope_fwd(const NormRopeParams &p, cudaStream_t s);
+// Two launches: gradients and partial sums, then the sums of the weights' gradients.
+cudaError_t launch_qk_norm_rope_bwd(const NormRopeParams &p, cudaStream_t s);
+constexpr int kNormRopeBwdBlocks = 608;  // blocks of partial weight gradients: four on each of 152 SMs
+cudaError_t launch_prefix_attn_simt(const PrefixAttnParams &p, cudaStream_t s);
+// Joins the pieces of every row: the second launch of the attention.
+cudaError_t launch_prefix_join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s);
 cudaError_t launch_selftest_wait(uint64_t limit_ns, unsigned int *err, cudaStream_t s);
 // Two-pass ring self-attention (bf16, d = 128, T/N a multiple of 128): per
 // query chunk, score pass into S [BH, Tc, T] fp32 (and per-tile row
@@ -156,6 +259,21 @@ cudaError_t launch_block_attn_bf16_2sm(const void *q, const void *k, const void 
 // unique context id, so a context created later (after cudaDeviceReset, for
 // instance) gets a fresh lookup instead of a stale address.
 rsa_status symbol_address(const void *symbol, void **out);
+
+// Host-side checks and state shared by the C ABI's translation units.
+// True if this launch is to fail by rsa_debug_inject_launch_failure (and the
+// failure has been recorded in *st).
+bool injected_failure(const char *what, rsa_status *st);
+// The device error word of the calling thread's current context.
+rsa_status device_error_word(unsigned int **out);
+// The limit of every device-side wait (rsa_set_wait_limit_ns).
+uint64_t wait_limit_ns();
+// The bf16 kernels are built for sm_103a only.
+rsa_status check_device_for(rsa_dtype dt);
+// A device pointer argument: not NULL and 16-byte aligned.
+rsa_status check_ptr(const void *p, const char *name);
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Set the thread's last-error text and return `st`.
 rsa_status fail(rsa_status st, const char *fmt, ...);

@@ -1,0 +1,358 @@
+"""Serving over a paged KV cache: a step's plan, the norm and rotation of its
+heads with the cache write, and attention behind a shared prefix.
+
+The calls of ``include/rsa.h`` with the same names; as in the rest of the
+binding they only check and marshal arguments.  One decode step:
+
+    plan = page_plan(cached_len, new_len, block_table, free_pages, page_size, n_pages, max_tokens, pos0=prefix_len)
+    for each layer:
+        q, _ = qk_norm_rope(q, k, wq, wk, plan.positions, cos_sin, v=v, slot_map=plan.slot_map,
+                            k_cache=k_cache, v_cache=v_cache)
+        out, lse = prefix_attn(q, k_cache, v_cache, plan.cu_new, block_table, plan.kv_len,
+                               prefix_pages=prefix_pages, prefix_len=prefix_len)
+
+Caches are [n_pages, Hkv, page_size, d]; a step's rows are packed [T, H, d].
+Nothing synchronises, so a step can be captured into a CUDA graph and replayed
+with other lengths: what depends on them is read on the device.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional, Sequence, Tuple
+
+import torch
+
+from . import RSA_BF16, RSA_F32, RsaError, load
+
+PLAN_STATUS = {0: "ok", 1: "negative length", 2: "block table row too short", 3: "too few free pages",
+               4: "more tokens than max_tokens"}
+
+
+class Heads(ctypes.Structure):
+    """rsa_heads: a [T, H, d] operand with its token and head strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class NormRopeArgs(ctypes.Structure):
+    """rsa_qk_norm_rope_args."""
+    _fields_ = [("dt", ctypes.c_int), ("T", ctypes.c_int64), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("q", Heads), ("k", Heads), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int64)]
+
+
+class PagePlan(NamedTuple):
+    """What page_plan leaves for the step (device tensors; info is int64 [4]:
+    status (PLAN_STATUS), tokens, pages taken, first free entry after them)."""
+    cu_new: torch.Tensor
+    kv_len: torch.Tensor
+    slot_map: torch.Tensor
+    positions: torch.Tensor
+    info: torch.Tensor
+
+
+_p, _i32, _i64, _size = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_args = ctypes.POINTER(NormRopeArgs)
+SIGS = {
+    "rsa_page_plan": [_p, _p, _i32, _i32, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _p],
+    "rsa_qk_norm_rope_fwd": [_args, Heads, Heads, Heads, _p, _p, _p, _i32, _i64, _p],
+    "rsa_qk_norm_rope_bwd_workspace_size": [_i32, ctypes.POINTER(_size)],
+    "rsa_qk_norm_rope_bwd": [_args, Heads, Heads, Heads, Heads, _p, _p, _p, _size, _p],
+    "rsa_prefix_attn_workspace_size": [_i32, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_size)],
+    "rsa_prefix_attn_fwd": [_p, _i64, _i64, _p, _p, _i32, _i64, _i32, _i32, _i32, _i32, _i64, _p, _p, _i32, _p, _i64, _i32,
+                            _p, _i64, _p, _p, _p, _size, _p],
+}
+
+_DT = {torch.float32: RSA_F32, torch.bfloat16: RSA_BF16}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
+    return dt
+
+
+def _check(name: str, t, dim: int, dtype: torch.dtype, device: torch.device, contiguous: bool = True) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise TypeError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype or t.dim() != dim:
+        raise ValueError(f"{name} must be a {dim}-d {dtype} tensor (got {t.dim()}-d {t.dtype})")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _heads(name: str, t, dtype: torch.dtype, device: torch.device, shape=None) -> Heads:
+    _check(name, t, 3, dtype, device, contiguous=False)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    T, H, d = t.shape
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # the stride of a dimension of one says nothing: put the dense one in its place
+    if H == 1:
+        hs = d
+    if T == 1:
+        ts = H * hs
+    return Heads(t.data_ptr(), ts, hs)
+
+
+def _call_on(device: torch.device, fn: str, stream, temporaries: Sequence[torch.Tensor], *args) -> None:
+    """The library's call on `device` and `stream` (default: the device's current stream)."""
+    lib = load()
+    current = torch.cuda.current_device()
+    if device.index != current:
+        with torch.cuda.device(device):
+            return _call_on(device, fn, stream, temporaries, *args)
+    if stream is None:
+        handle = torch.cuda.current_stream(current).cuda_stream
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if temporaries and hasattr(stream, "cuda_stream"):
+            # made on the current stream, used on another one: not to be handed out again before it is done
+            for t in temporaries:
+                t.record_stream(stream)
+        elif temporaries and handle != torch.cuda.current_stream(current).cuda_stream:
+            raise ValueError("with a bare stream handle other than the current stream's, pass every output and workspace")
+    st = getattr(lib, fn)(*args, handle)
+    if st != 0:
+        detail = lib.rsa_last_error_string()
+        raise RsaError(fn, st, detail.decode() if detail else "")
+
+
+def page_plan(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+              page_size: int, n_pages: int, max_tokens: int, free_start: Optional[torch.Tensor] = None, pos0: int = 0,
+              out: Optional[PagePlan] = None, stream=None) -> PagePlan:
+    """One step's plan from the requests' lengths (rsa_page_plan): fresh pages
+    from free_pages [n] int32, from entry free_start[0] (int64 [1]) on, are
+    appended to block_table [R, max_pages] int32 in place; each of the new
+    tokens gets its cache slot and position, rows behind them slot -1.
+    cached_len and new_len are int32 [R].  Check info[0] (PLAN_STATUS) where the
+    host can afford to wait: a step that cannot be planned changes nothing."""
+    dev = cached_len.device
+    _check("cached_len", cached_len, 1, torch.int32, dev)
+    R = cached_len.shape[0]
+    _check("new_len", new_len, 1, torch.int32, dev)
+    _check("block_table", block_table, 2, torch.int32, dev, contiguous=False)
+    _check("free_pages", free_pages, 1, torch.int32, dev)
+    if new_len.shape[0] != R or block_table.shape[0] != R:
+        raise ValueError("new_len and block_table must have cached_len's requests")
+    max_pages = block_table.shape[1]
+    if block_table.stride(1) != 1 and max_pages > 1:
+        raise ValueError("rows of block_table must be contiguous")
+    if free_start is not None:
+        _check("free_start", free_start, 1, torch.int64, dev)
+        if free_start.shape[0] < 1:
+            raise ValueError("free_start must hold one entry")
+    made = ()
+    if out is None:
+        i32, i64 = torch.int32, torch.int64
+        out = made = PagePlan(torch.empty(R + 1, dtype=i32, device=dev), torch.empty(R, dtype=i32, device=dev),
+                              torch.empty(max_tokens, dtype=i64, device=dev), torch.empty(max_tokens, dtype=i64, device=dev),
+                              torch.empty(4, dtype=i64, device=dev))
+    else:
+        for name, t, n, dt in (("cu_new", out.cu_new, R + 1, torch.int32), ("kv_len", out.kv_len, R, torch.int32),
+                               ("slot_map", out.slot_map, max_tokens, torch.int64),
+                               ("positions", out.positions, max_tokens, torch.int64), ("info", out.info, 4, torch.int64)):
+            _check("out." + name, t, 1, dt, dev)
+            if t.shape[0] != n:
+                raise ValueError(f"out.{name} must hold {n} entries")
+    _call_on(dev, "rsa_page_plan", stream, made, cached_len.data_ptr(), new_len.data_ptr(), R, page_size, n_pages,
+             block_table.data_ptr(), max_pages if R == 1 else block_table.stride(0), max_pages, free_pages.data_ptr(),
+             free_pages.shape[0], None if free_start is None else free_start.data_ptr(), pos0, max_tokens,
+             out.cu_new.data_ptr(), out.kv_len.data_ptr(), out.slot_map.data_ptr(), out.positions.data_ptr(),
+             out.info.data_ptr())
+    return out
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections) -> NormRopeArgs:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise TypeError("q must be a CUDA tensor [T, Hq, d]")
+    dev, dt = q.device, q.dtype
+    a = NormRopeArgs()
+    a.dt = _dtype(q)
+    T, a.Hq, d = q.shape
+    a.T, a.d = T, d
+    a.q = _heads("q", q, dt, dev)
+    a.k = _heads("k", k, dt, dev)
+    a.Hkv = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q [T, Hq, d] and k [T, Hkv, d] must agree")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check(name, w, 1, dt, dev)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must hold d={d} values")
+            setattr(a, name, w.data_ptr())
+    a.eps, a.interleaved, a.n_axes = eps, int(bool(interleaved)), 1
+    if cos_sin is not None:
+        _check("cos_sin", cos_sin, 2, torch.float32, dev)
+        a.max_pos, a.rot = cos_sin.shape
+        a.cos_sin = cos_sin.data_ptr()
+        axes = 1 if sections is None else len(sections)
+        if not 1 <= axes <= 4:
+            raise ValueError("sections must name one to four axes")
+        a.n_axes = axes
+        if sections is not None:
+            a.sections[:axes] = sections
+        _check("positions", positions, positions.dim() if axes == 1 else 2, torch.int64, dev)
+        if positions.numel() != axes * T or positions.shape[-1] != T:
+            raise ValueError(f"positions must be int64 [{axes}, {T}]" if axes > 1 else f"positions must be int64 [{T}]")
+        a.positions = positions.data_ptr()
+        if axes == 1 and sections is not None and sections[0] != a.rot // 2:
+            raise ValueError("one section must hold all rot/2 frequencies")
+    return a
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6, interleaved: bool = False,
+                 sections: Optional[Sequence[int]] = None, v=None, slot_map=None, k_cache=None, v_cache=None,
+                 q_out=None, k_out=None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """RMS norm of every head of q [T, Hq, d] and k [T, Hkv, d], then the
+    rotation by the tokens' positions (rsa_qk_norm_rope_fwd).  cos_sin
+    [max_pos, rot] fp32 (rope_table makes it; None: no rotation); positions
+    int64 [T], or [axes, T] with `sections` frequencies for each axis.  With
+    slot_map [T] int64, k's results and v's rows go to their slots of k_cache
+    and v_cache [n_pages, Hkv, page_size, d].  Returns (q_out, k_out); k_out is
+    None if it is not given and there is a cache.  q_out may be q and k_out k."""
+    a = _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections)
+    dev, dt = q.device, q.dtype
+    made = []
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        made.append(q_out)
+    if k_out is None and slot_map is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+        made.append(k_out)
+    qo = _heads("q_out", q_out, dt, dev, q.shape)
+    ko = Heads() if k_out is None else _heads("k_out", k_out, dt, dev, k.shape)
+    if slot_map is None:
+        if v is not None or k_cache is not None or v_cache is not None:
+            raise ValueError("v, k_cache and v_cache go with slot_map")
+        _call_on(dev, "rsa_qk_norm_rope_fwd", stream, made, ctypes.byref(a), qo, ko, Heads(), None, None, None, 0, 0)
+        return q_out, k_out
+    _check("slot_map", slot_map, 1, torch.int64, dev)
+    if slot_map.shape[0] != a.T:
+        raise ValueError(f"slot_map must hold T={a.T} slots")
+    vh = _heads("v", v, dt, dev, k.shape)
+    n_pages, page_size = _check_caches(k_cache, v_cache, a.Hkv, a.d, dt, dev)
+    _call_on(dev, "rsa_qk_norm_rope_fwd", stream, made, ctypes.byref(a), qo, ko, vh, slot_map.data_ptr(),
+             k_cache.data_ptr(), v_cache.data_ptr(), page_size, n_pages)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6,
+                     interleaved: bool = False, sections: Optional[Sequence[int]] = None, dq=None, dk=None,
+                     workspace=None, stream=None):
+    """Gradients of qk_norm_rope (rsa_qk_norm_rope_bwd) from those of its
+    results: (dq, dk in q's dtype, dq_weight, dk_weight fp32 [d], None for a
+    weight that is None).  dq may be dq_out and dk may be dk_out."""
+    a = _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections)
+    dev, dt = q.device, q.dtype
+    gq, gk = _heads("dq_out", dq_out, dt, dev, q.shape), _heads("dk_out", dk_out, dt, dev, k.shape)
+    made = []
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=dt, device=dev)
+        made.append(dq)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=dt, device=dev)
+        made.append(dk)
+    dw = torch.empty((2, a.d), dtype=torch.float32, device=dev)
+    made.append(dw)
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        load().rsa_qk_norm_rope_bwd_workspace_size(a.d, ctypes.byref(n))
+        workspace = torch.empty(max(n.value, 1), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    dwq, dwk = dw.unbind(0)
+    dwq, dwk = (None if q_weight is None else dwq), (None if k_weight is None else dwk)
+    _call_on(dev, "rsa_qk_norm_rope_bwd", stream, made, ctypes.byref(a), gq, gk, _heads("dq", dq, dt, dev, q.shape),
+             _heads("dk", dk, dt, dev, k.shape), None if dwq is None else dwq.data_ptr(),
+             None if dwk is None else dwk.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dq, dk, dwq, dwk
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """cos_sin [max_pos, rot] fp32 for qk_norm_rope: frequency i turns by
+    pos * base^(-2i / rot).  The angles are taken in 64 bits (a far position's
+    would lose their fraction in 32)."""
+    half = rot // 2
+    freq = base ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+def _check_caches(k_cache, v_cache, Hkv: int, d: int, dt: torch.dtype, dev: torch.device) -> Tuple[int, int]:
+    _check("k_cache", k_cache, 4, dt, dev)
+    _check("v_cache", v_cache, 4, dt, dev)
+    n_pages, h, page_size, dd = k_cache.shape
+    if v_cache.shape != k_cache.shape or h != Hkv or dd != d:
+        raise ValueError(f"k_cache and v_cache must both be [n_pages, Hkv={Hkv}, page_size, d={d}]")
+    return n_pages, page_size
+
+
+def prefix_attn_workspace_size(dtype: torch.dtype, T: int, Hq: int, Hkv: int, d: int, R: int) -> int:
+    n = ctypes.c_size_t(0)
+    lib = load()
+    st = lib.rsa_prefix_attn_workspace_size(_DT.get(dtype, -1), T, Hq, Hkv, d, R, ctypes.byref(n))
+    if st != 0:
+        raise RsaError("rsa_prefix_attn_workspace_size", st, lib.rsa_last_error_string().decode())
+    return int(n.value)
+
+
+def prefix_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages=None, prefix_len: int = 0, out=None,
+                lse=None, workspace=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of the step's rows q [T, Hq, d] over a prefix that all requests
+    share (tokens [0, prefix_len) in pages prefix_pages) and each request's own
+    kv_len[r] tokens in the pages of its row of block_table
+    (rsa_prefix_attn_fwd).  Request r's rows [cu_q[r], cu_q[r + 1]) are its
+    newest tokens.  Returns (out [T, Hq, d], lse [T, Hq] fp32); rows from
+    cu_q[R] on are left as they were.  Calls that may run at the same time need
+    workspaces of their own (prefix_attn_workspace_size bytes)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise TypeError("q must be a CUDA tensor [T, Hq, d]")
+    dev, dt = q.device, q.dtype
+    code = _dtype(q)
+    T, Hq, d = q.shape
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [n_pages, Hkv, page_size, d]")
+    Hkv = k_cache.shape[1]
+    n_pages, page_size = _check_caches(k_cache, v_cache, Hkv, d, dt, dev)
+    qh = _heads("q", q, dt, dev)
+    _check("cu_q", cu_q, 1, torch.int32, dev)
+    _check("kv_len", kv_len, 1, torch.int32, dev)
+    _check("block_table", block_table, 2, torch.int32, dev, contiguous=False)
+    R, max_pages = block_table.shape
+    if cu_q.shape[0] != R + 1 or kv_len.shape[0] != R:
+        raise ValueError("cu_q [R + 1], kv_len [R] and block_table [R, max_pages] must agree")
+    if block_table.stride(1) != 1 and max_pages > 1:
+        raise ValueError("rows of block_table must be contiguous")
+    if prefix_len:
+        _check("prefix_pages", prefix_pages, 1, torch.int32, dev)
+        if prefix_pages.shape[0] * page_size < prefix_len:
+            raise ValueError(f"prefix_pages hold {prefix_pages.shape[0] * page_size} tokens, prefix_len is {prefix_len}")
+    made = []
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+        made.append(out)
+    else:
+        _check("out", out, 3, dt, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        made.append(lse)
+    else:
+        _check("lse", lse, 2, torch.float32, dev)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [T, Hq]")
+    if workspace is None:
+        workspace = torch.empty(prefix_attn_workspace_size(dt, T, Hq, Hkv, d, R), dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _call_on(dev, "rsa_prefix_attn_fwd", stream, made, qh.data, qh.token_stride, qh.head_stride, k_cache.data_ptr(),
+             v_cache.data_ptr(), code, T, Hq, Hkv, d, page_size, n_pages, cu_q.data_ptr(), kv_len.data_ptr(), R,
+             block_table.data_ptr(), max_pages if R == 1 else block_table.stride(0), max_pages,
+             prefix_pages.data_ptr() if prefix_len else None, prefix_len, out.data_ptr(), lse.data_ptr(),
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out, lse

@@ -415,6 +415,165 @@ rsa_status rsa_decode_attn_fwd(const void *q, const void *k, const void *v, rsa_
                                rsa_stream_t stream);
 
 /*
+ * Serving over a paged KV cache.  The cache of a layer is two arrays of pages,
+ * k_cache and v_cache [n_pages, Hkv, page_size, d]; a page holds page_size
+ * consecutive tokens of one sequence, all key heads.  Slot s of the cache is
+ * row s mod page_size of page s / page_size.  A request's own tokens lie in
+ * the pages of its row of block_table [R, max_pages] (rows table_stride
+ * entries apart); a prefix that all requests share lies in pages of its own.
+ * page_size is 16, 32, 64 or 128.  A step runs rsa_page_plan once, and in
+ * every layer rsa_qk_norm_rope_fwd (which fills the cache) and
+ * rsa_prefix_attn_fwd (which reads it): the decode of "Training and inference
+ * stress this dimension differently" ([P1]) for many sequences that grow.
+ *
+ * Lengths, page ids, slots and positions are data of the device, so that a
+ * captured step can be replayed with other lengths.  They are checked there:
+ * a value outside its range is forced into it or its access skipped, and
+ * rsa_check_device_error reports RSA_ERR_CUDA with the value; the results of
+ * the rows concerned are then unspecified.
+ */
+
+/*
+ * The plan of one step, from the requests' lengths.  With have = ceil(c / P)
+ * and need = ceil((c + n) / P) - have for request r's c = cached_len[r] tokens
+ * in the cache, n = new_len[r] new ones and pages of P = page_size tokens:
+ *   - its fresh pages are the next `need` entries of free_pages, taken from
+ *     entry *free_start on (0 if free_start is NULL) in the requests' order,
+ *     and are written to entries [have, have + need) of its row of block_table;
+ *   - its new tokens are rows [cu_new[r], cu_new[r + 1]) of the step, packed in
+ *     the requests' order (cu_new [R + 1]); token i of them is at
+ *     positions[row] = pos0 + c + i and goes to slot_map[row] = the slot of its
+ *     own token number c + i;
+ *   - kv_len[r] = c + n (the next step's cached_len).
+ * slot_map and positions have max_tokens rows; those behind the last token
+ * (a padded batch) get slot -1 and position 0.  pos0 is the shared prefix'
+ * length, whose tokens are no part of the requests' own.
+ *   info [4]: status, tokens, pages taken, first free entry after them (the
+ * next step's free_start).  A step that cannot be planned changes nothing:
+ * status says why, block_table stays, kv_len = cached_len, cu_new = 0 and all
+ * slots are -1:
+ *   RSA_PLAN_BAD_LENGTH       a negative length
+ *   RSA_PLAN_TABLE_FULL       a request needs more than max_pages pages
+ *   RSA_PLAN_NO_PAGES         free_pages [n_free] does not hold enough
+ *   RSA_PLAN_TOO_MANY_TOKENS  the new tokens exceed max_tokens
+ * (the first that applies).  A page id outside [0, n_pages) leaves its tokens
+ * without slot (-1) and is reported by rsa_check_device_error.  No output may
+ * overlap an input or another output.  At most 16384 requests.  One launch.
+ */
+enum {
+    RSA_PLAN_OK = 0,
+    RSA_PLAN_BAD_LENGTH = 1,
+    RSA_PLAN_TABLE_FULL = 2,
+    RSA_PLAN_NO_PAGES = 3,
+    RSA_PLAN_TOO_MANY_TOKENS = 4
+};
+rsa_status rsa_page_plan(const int32_t *cached_len, const int32_t *new_len, int R, int page_size, int64_t n_pages,
+                         int32_t *block_table, int64_t table_stride, int max_pages, const int32_t *free_pages,
+                         int64_t n_free, const int64_t *free_start, int64_t pos0, int64_t max_tokens, int32_t *cu_new,
+                         int32_t *kv_len, int64_t *slot_map, int64_t *positions, int64_t *info, rsa_stream_t stream);
+
+/*
+ * A [T, H, d] operand whose rows of d elements are contiguous: strides of
+ * tokens and heads in elements, each at least d and a multiple of 16 bytes
+ * (q, k and v cut from one packed projection, for instance).
+ */
+typedef struct {
+    void *data;
+    int64_t token_stride, head_stride;
+} rsa_heads;
+
+/*
+ * RMS norm of every query and key head and the rotation by the tokens'
+ * positions, in one pass:
+ *   xhat = x / sqrt(mean(x^2) + eps) over the d elements of a head,
+ *   y = R(pos) (w o xhat)
+ * with w the weights q_weight or k_weight [d] (dtype dt; NULL: ones) and R the
+ * rotation of the first `rot` elements (a multiple of 16, 0: none), the others
+ * kept.  R turns the pairs (i, i + rot/2), or (2i, 2i + 1) if interleaved, i <
+ * rot/2, by (a, b) -> (a cos - b sin, a sin + b cos).  cos_sin [max_pos, rot]
+ * holds for each position the cosines and then the sines of the rot/2
+ * frequencies (fp32; the caller makes it once, angles best taken in 64 bits).
+ * positions is [n_axes, T]: with several axes (time, height and width of a
+ * video) frequencies [0, sections[0]) go by the first axis' position, the next
+ * sections[1] by the second's, ...; sections add up to rot/2 (not read with
+ * one axis).  Arithmetic is fp32; a result is rounded once.
+ */
+typedef struct {
+    rsa_dtype dt;
+    int64_t T;
+    int Hq, Hkv, d;
+    rsa_heads q, k; /* [T, Hq, d], [T, Hkv, d] */
+    const void *q_weight, *k_weight;
+    float eps;
+    int rot, interleaved, n_axes;
+    int sections[4];
+    const int64_t *positions;
+    const float *cos_sin;
+    int64_t max_pos;
+} rsa_qk_norm_rope_args;
+
+/*
+ * Forward: q_out [T, Hq, d] and k_out [T, Hkv, d], dtype dt; each may be its
+ * input, otherwise the two do not overlap.  With slot_map [T] the results of k
+ * and the rows of v (v [T, Hkv, d], copied) are also written to slots
+ * slot_map[t] of k_cache and v_cache, and k_out.data may then be NULL.  Rows
+ * with a negative slot are not written; other slots are left as they were.
+ * Slots >= 0 have to differ from one another (of two tokens with one slot
+ * either may be left, or parts of both).  One launch.
+ */
+rsa_status rsa_qk_norm_rope_fwd(const rsa_qk_norm_rope_args *args, rsa_heads q_out, rsa_heads k_out, rsa_heads v,
+                                const int64_t *slot_map, void *k_cache, void *v_cache, int page_size, int64_t n_pages,
+                                rsa_stream_t stream);
+
+/*
+ * Backward, from the gradients of the outputs and the forward's inputs:
+ *   g = R(pos)^T dy, c = w o g
+ *   dx = (c - xhat mean(c o xhat)) / sqrt(mean(x^2) + eps)
+ *   dw = sum over tokens and heads of g o xhat          [d], fp32
+ * dq, dk have dtype dt; dq may be dq_out and dk may be dk_out.  dq_weight or
+ * dk_weight may be NULL (not wanted).  The sums run in a fixed order.
+ * workspace: rsa_qk_norm_rope_bwd_workspace_size() bytes.  Two launches.
+ */
+rsa_status rsa_qk_norm_rope_bwd_workspace_size(int d, size_t *bytes);
+rsa_status rsa_qk_norm_rope_bwd(const rsa_qk_norm_rope_args *args, rsa_heads dq_out, rsa_heads dk_out, rsa_heads dq,
+                                rsa_heads dk, float *dq_weight, float *dk_weight, void *workspace, size_t ws_bytes,
+                                rsa_stream_t stream);
+
+/*
+ * Attention of a step's query rows over one prefix that all requests share and
+ * each request's own tokens.  q [T, Hq, d] (strides in elements as rsa_heads),
+ * query head h reading key head h / (Hq / Hkv).  Request r's rows are
+ * [cu_q[r], cu_q[r + 1]); they are the newest n of its kv_len[r] own tokens
+ * (already in the cache), so that row i of them sees
+ *   the whole prefix: tokens [0, prefix_len) in pages prefix_pages[..], and
+ *   its own tokens [0, kv_len[r] - n + i], in the pages of its table row.
+ *   out [T, Hq, d] (dtype dt) = softmax(q K^T / sqrt(d)) V, lse [T, Hq] fp32
+ * over both together.  A row that sees nothing gets out = 0, lse = -inf; rows
+ * behind the last request (from cu_q[R] on) are left as they were.  The keys
+ * and values of the prefix are read once for the whole batch, not once for
+ * each request; prefix_len = 0 is plain attention over a paged cache.  Entries
+ * of block_table past a request's keys are not read, and cache rows past
+ * kv_len or prefix_len may hold anything; rows within them have to be finite
+ * (a token's row that a request's earlier new tokens do not see yet is still
+ * multiplied, by zero).
+ * Hq / Hkv is at most 128.  Meant for steps whose new tokens are few next to
+ * the keys: a request's keys are shared out as if all its new tokens saw all
+ * of them, which costs up to twice the time for a prompt without a past (the
+ * ring is the call for that).  `workspace` holds
+ * rsa_prefix_attn_workspace_size() bytes and is written: calls that may run at
+ * the same time (two streams, two captured graphs) each need their own.  Two
+ * launches; the work is shared out on the device, so a captured call may be
+ * replayed with other lengths.
+ */
+rsa_status rsa_prefix_attn_workspace_size(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int R, size_t *bytes);
+rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
+                               const void *v_cache, rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int page_size,
+                               int64_t n_pages, const int32_t *cu_q, const int32_t *kv_len, int R,
+                               const int32_t *block_table, int64_t table_stride, int max_pages,
+                               const int32_t *prefix_pages, int64_t prefix_len, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, rsa_stream_t stream);
+
+/*
  * Two-pass Ring Self-Attention ([P3] "How It Works", steps 1-2), the form that
  * keeps whole score rows: for each query chunk n in turn, the score pass
  * visits the key chunks in ring order (n - r) mod N and fills the full score
@@ -491,8 +650,9 @@ int rsa_debug_checks(void);
 /*
  * Synchronise `stream`, then read and clear the device error word of the
  * current device: RSA_OK, RSA_ERR_TIMEOUT if a kernel gave up on a wait, or
- * RSA_ERR_CUDA if a bounds check of an RSA_DEBUG build failed (the text gives
- * the site code and the first bad index).
+ * RSA_ERR_CUDA if a bounds check failed, of an RSA_DEBUG build or of index data
+ * that only the device sees (the text gives the site code and the first bad
+ * index).
  */
 rsa_status rsa_check_device_error(rsa_stream_t stream);
 
