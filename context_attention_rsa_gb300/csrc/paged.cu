@@ -449,7 +449,7 @@ rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_
     rsa_status inj;
     if (injected_failure("prefix attention launch", &inj))
         return inj;
-    cudaError_t e = launch_prefix_attn_simt(p, stream);
+    cudaError_t e = dt == RSA_BF16 ? launch_prefix_attn_bf16(p, stream) : launch_prefix_attn_f32(p, stream);
     if (e != cudaSuccess)
         return fail(RSA_ERR_CUDA, "prefix attention launch: %s", cudaGetErrorString(e));
     return RSA_OK;

@@ -175,8 +175,9 @@ struct Walk {
     {
         if (left <= 0)
             return false;
-        while (off >= g.line) {  // (left > 0: a segment with tiles follows)
-            ++seg;
+        while (off >= g.line) {  // (left > 0: a segment with tiles follows, unless the lengths changed meanwhile)
+            if (++seg > p.R)
+                return false;
             off = 0;
             g = segment(p, seg, tokens_per_unit);
         }

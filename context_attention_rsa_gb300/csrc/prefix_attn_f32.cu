@@ -1,5 +1,6 @@
 // Attention of packed query rows over a shared prefix and their requests' own
-// paged keys, on the CUDA cores, and the launch that joins the pieces.
+// paged keys, on the CUDA cores (fp32 inputs, whose results tf32 could not
+// hold), and the launch that joins the pieces of both types.
 //
 //   o = softmax([q Kp^T, q Kr^T] / sqrt(d)) [Vp; Vr]
 // for the prefix' keys p and the request's own keys r, by pieces of the keys
@@ -46,8 +47,6 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void store(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -60,8 +59,8 @@ struct Smem {
     Stretch st;
 };
 
-template <class E, int D>
-__global__ void __launch_bounds__(kThreads) prefix_attn_simt_kernel(const __grid_constant__ PrefixAttnParams p)
+template <int D>
+__global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_constant__ PrefixAttnParams p)
 {
     constexpr int PER = D / 32;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_simt_kernel(const __grid
     const int worker = blockIdx.x;
     const float scale = 1.0f / sqrtf((float)D);
     const int page_mask = (1 << p.page_shift) - 1;
-    const E *kc = static_cast<const E *>(p.k_cache), *vc = static_cast<const E *>(p.v_cache);
+    const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
 
     const Stretch st = find_stretch<kThreads>(p, TU, worker, s.sum, &s.st);
     Walk walk;
@@ -83,8 +82,8 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_simt_kernel(const __grid
         for (int i = threadIdx.x; i < rows * D; i += kThreads) {
             const int row = i / D, c = i - row * D;
             const int64_t token = x.tok + row / G;
-            s.q[row][c] = to_f(static_cast<const E *>(p.q)[token * p.q_token_stride +
-                                                           (x.head * G + row % G) * p.q_head_stride + c]);
+            s.q[row][c] =
+                static_cast<const float *>(p.q)[token * p.q_token_stride + (x.head * G + row % G) * p.q_head_stride + c];
         }
         // Row i * kWarps + warp of the unit, and the keys it sees.
         float m[kWarpRows], l[kWarpRows], o[kWarpRows][PER];
@@ -112,8 +111,8 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_simt_kernel(const __grid
                 float a = 0.f, b = 0.f;
                 if (page >= 0 && page < p.n_pages) {
                     const int64_t at = ((((int64_t)page * p.Hkv + x.head) << p.page_shift) + (j & page_mask)) * D + c;
-                    a = to_f(kc[at]);
-                    b = to_f(vc[at]);
+                    a = kc[at];
+                    b = vc[at];
                 } else if (c == 0) {
                     record_bad_index(p.err, 0x55, page);
                 }
@@ -168,10 +167,10 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_simt_kernel(const __grid
             const bool empty = !(l[i] > 0.f) && l[i] == l[i];
             const float inv = empty ? 0.f : 1.f / l[i], lse = empty ? -INFINITY : m[i] + logf(l[i]);
             if (d.final_) {
-                E *out = static_cast<E *>(p.out) + (token * p.Hq + hq) * D;
+                float *out = static_cast<float *>(p.out) + (token * p.Hq + hq) * D;
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
-                    store(out + lane + 32 * c, o[i][c] * inv);
+                    out[lane + 32 * c] = o[i][c] * inv;
                 if (lane == 0)
                     p.lse[token * p.Hq + hq] = lse;
             } else {
@@ -267,14 +266,14 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_cons
         p.lse[row] = M == -INFINITY ? -INFINITY : M + logf(L);
 }
 
-template <class E, int D>
+template <int D>
 cudaError_t simt(const PrefixAttnParams &p, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(prefix_attn_simt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(Smem<D>));
+    cudaError_t e =
+        cudaFuncSetAttribute(prefix_attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)
         return e;
-    prefix_attn_simt_kernel<E, D><<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
+    prefix_attn_f32_kernel<D><<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_prefix_join(p, kRows / p.G, s);
 }
@@ -291,12 +290,12 @@ cudaError_t join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_prefix_attn_simt(const PrefixAttnParams &p, cudaStream_t s)
+cudaError_t launch_prefix_attn_f32(const PrefixAttnParams &p, cudaStream_t s)
 {
     if (p.d == 128)
-        return p.f32 ? simt<float, 128>(p, s) : simt<__nv_bfloat16, 128>(p, s);
+        return simt<128>(p, s);
     if (p.d == 64)
-        return p.f32 ? simt<float, 64>(p, s) : simt<__nv_bfloat16, 64>(p, s);
+        return simt<64>(p, s);
     return cudaErrorInvalidValue;
 }
 

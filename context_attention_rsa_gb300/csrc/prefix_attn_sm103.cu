@@ -1,0 +1,657 @@
+// Attention of packed query rows over a shared prefix and their requests' own
+// paged keys, on the sm_103a tensor cores (bf16).
+//
+//   o = softmax([q Kp^T, q Kr^T] / sqrt(d)) [Vp; Vr], by pieces of the keys
+// whose (o, lse) the joining launch puts together (prefix_attn_f32.cu).
+//
+// One CTA on each SM takes an equal stretch of all key tiles (paged_sched.cuh)
+// and goes through its pieces.  Warp roles as in the block kernel:
+//   warp 8      producer: the piece's query rows (one 4-D TMA box a 128-row
+//               tile: G heads of floor(128 / G) tokens, so any group size is
+//               loaded without a gather), then K and V tiles through a ring of
+//               shared-memory slots, one TMA box a page and 64 columns, each
+//               lane loading the page whose id it read from the table one tile
+//               ahead.
+//   warp 9      one thread issues the MMAs: S_t = Q K^T from shared memory,
+//               O_t += P_t V with P in TMEM.
+//   warps 0-7   softmax on S_0 and S_1 in turn, two threads a row.
+// A piece runs in one of two forms, by its number of rows:
+//   two tiles   more than 128 rows: S_0 and S_1 are the two row tiles against
+//               the same key tile, as in the block kernel, so that a key tile
+//               serves 256 rows; bound by the softmax chain of each tile.
+//   one tile    up to 128 rows: S_0 and S_1 are the same rows against the even
+//               and the odd key tiles, two independent chains that keep the
+//               loads going; their (m, l, O) lie in the same TMEM lanes and are
+//               put together by the thread that owns the row.  Warps without a
+//               row of the piece only keep the barriers' count, so a decode
+//               step's few rows cost little and HBM is the bound.
+// Values of rows past the keys are not trusted: a tile's K there gives scores
+// that are masked, but 0 * NaN would reach O through V, so the producer clears
+// those rows of V in shared memory before the MMA may read them.
+// The phases of all barriers run on over the CTA's pieces; Q is loaded again as
+// soon as the last S MMA of a piece is done, O is written again once every
+// softmax thread has read it.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "paged_sched.cuh"
+#include "ptx_sm103.cuh"
+#include "tc_common.cuh"
+
+namespace rsa {
+namespace {
+
+using namespace tc;
+using namespace paged;
+
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescale = 8.0f;  // log2 units the maximum may rise before O is rescaled
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kSoftmaxThreads = 256;
+    static constexpr int kProducerWarp = 8;
+    static constexpr int kMmaWarp = 9;
+    static constexpr int kThreads = 320;
+    static constexpr int kBoxes = D / 64;               // 128-byte-wide boxes of a tile
+    static constexpr uint32_t kBoxBytes = 128u * 128u;  // 128 rows x 128 bytes
+    static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
+    static constexpr int kStages = D == 128 ? 4 : 8;    // a power of two: slots and phases are bits of the load's number
+    static constexpr int kStageBits = D == 128 ? 2 : 3;
+    static constexpr uint32_t kKVOff = 2 * kTileBytes;  // after the two Q tiles
+    static constexpr uint32_t kBarOff = kKVOff + kStages * kTileBytes;
+    static constexpr uint32_t kXchOff = kBarOff + 256;  // [2 streams][2 halves][128 rows] maxima, then sums
+    static constexpr uint32_t kSumOff = kXchOff + 2 * 2048;
+    static constexpr uint32_t kSmemBytes = kSumOff + 256 + 1024;
+    static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+    static constexpr int kQF = 0;
+    static constexpr int kKVF = 1;
+    static constexpr int kKVE = kKVF + kStages;
+    static constexpr int kSF = kKVE + kStages;
+    static constexpr int kPF = kSF + 2;
+    static constexpr int kOF = kPF + 2;
+    static constexpr int kTail = kOF + 2;    // a V tile whose last rows the producer clears has landed
+    static constexpr int kQFree = kTail + 1; // every S MMA of the piece is done
+    static constexpr int kOFree = kQFree + 1;// every softmax thread has read the piece's O
+    static constexpr int kDrain = kOFree + 1;
+    static constexpr int kNumBars = kDrain + 1;
+    static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
+    static_assert(sizeof(Stretch) + 8 * (kThreads / 32) <= 256, "scan area");
+};
+
+// How a piece runs; every role works it out for itself.
+struct Form {
+    int tiles;   // key tiles that any of its rows sees
+    bool two;    // two row tiles against each key tile
+    int n[2];    // steps of S_0 and S_1
+};
+
+__device__ __forceinline__ Form form_of(const Piece &x, int tokens_per_tile)
+{
+    const int64_t seen = min(x.keys, x.see0 + (x.ntok - 1));
+    const int64_t end = min(x.t1, seen > 0 ? (seen + kTileKeys - 1) / kTileKeys : 0);
+    Form f;
+    f.tiles = end > x.t0 ? (int)(end - x.t0) : 0;
+    f.two = x.ntok > tokens_per_tile;
+    f.n[0] = f.two ? f.tiles : (f.tiles + 1) >> 1;
+    f.n[1] = f.two ? f.tiles : f.tiles >> 1;
+    return f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefixAttnParams p)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base, sKV = base + C::kKVOff, bars = base + C::kBarOff;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + C::kBarOff + 8 * C::kNumBars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + C::kBarOff + 8 * C::kNumBars + 4);
+    auto BAR = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int worker = blockIdx.x;
+    const int TT = 128 / p.G, TU = 2 * TT;  // tokens of a row tile and of a unit
+    const uint64_t lim_ns = p.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(BAR(C::kQF), 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(BAR(C::kKVF + s), 1);
+            ptx::mbar_init(BAR(C::kKVE + s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(BAR(C::kSF + t), 1);
+            ptx::mbar_init(BAR(C::kPF + t), C::kSoftmaxThreads);
+            ptx::mbar_init(BAR(C::kOF + t), 1);
+        }
+        ptx::mbar_init(BAR(C::kTail), 1);
+        ptx::mbar_init(BAR(C::kQFree), 1);
+        ptx::mbar_init(BAR(C::kOFree), C::kSoftmaxThreads);
+        ptx::mbar_init(BAR(C::kDrain), 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == C::kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    if (warp == C::kProducerWarp && lane == 0) {
+        ptx::tma_prefetch_desc(&tm_q);
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+    }
+    int64_t *s_sum = reinterpret_cast<int64_t *>(gbase + C::kSumOff);
+    const Stretch st = find_stretch<C::kThreads>(p, TU, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + C::kThreads / 32));
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    Walk walk;
+    walk.begin(p, st, TU);
+    Piece x;
+
+    if (warp == C::kProducerWarp) {
+        // ============================= producer =============================
+        const int page = 1 << p.page_shift, per_tile = kTileKeys >> p.page_shift;
+        const int none = (int)(p.n_pages * p.Hkv);  // outside the maps: zeros
+        uint32_t ld = 0, tails = 0, pieces = 0;
+        uint32_t landed[C::kStages];  // the last use of each slot that TMA completes by itself, plus one
+        for (int s = 0; s < C::kStages; ++s)
+            landed[s] = 0;
+        bool ok = true, tail_open = false;
+        while (ok && walk.next(p, TU, x)) {
+            const Form f = form_of(x, TT);
+            if (f.tiles == 0)
+                continue;
+            auto page_row = [&](int64_t tile) -> int {  // this lane's page of a tile, as a row of the maps
+                const int64_t first = tile * kTileKeys + ((int64_t)lane << p.page_shift);
+                if (lane >= per_tile || first >= x.keys)
+                    return none;
+                const int id = x.pages[tile * per_tile + lane];
+                if (id < 0 || id >= p.n_pages) {
+                    record_bad_index(p.err, 0x55, id);
+                    return none;
+                }
+                return id * p.Hkv + x.head;
+            };
+            int row = page_row(x.t0);
+            if (pieces > 0)
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(BAR(C::kQFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x61));
+            if (!ok)
+                break;
+            if (lane == 0) {
+                const int nq = f.two ? 2 : 1;
+                ptx::mbar_arrive_expect_tx(BAR(C::kQF), (uint32_t)(nq * C::kBoxes * 128 * p.G * TT));
+                for (int t = 0; t < nq; ++t)
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        ptx::tma_load_4d(sQ + t * C::kTileBytes + b * C::kBoxBytes, &tm_q, BAR(C::kQF), b * 64, 0, x.head,
+                                         (int)(x.tok + t * TT));
+            }
+            ++pieces;
+            for (int i = 0; ok && i < f.tiles; ++i) {
+                const int64_t tile = x.t0 + i;
+                const int valid = (int)min((int64_t)kTileKeys, x.keys - tile * kTileKeys);
+                const int np = (valid + page - 1) >> p.page_shift;
+                const int next_row = i + 1 < f.tiles ? page_row(tile + 1) : none;
+#pragma unroll 1
+                for (int v = 0; ok && v < 2; ++v, ++ld) {
+                    const int slot = ld & (C::kStages - 1);
+                    const uint32_t use = ld >> C::kStageBits;
+                    if (use > 0)
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(BAR(C::kKVE + slot), (use - 1) & 1, lim_ns, abort_flag,
+                                                                    p.err, 0x62));
+                    if (!ok)
+                        break;
+                    const bool tail = v == 1 && valid < kTileKeys;
+                    const uint32_t bar = tail ? BAR(C::kTail) : BAR(C::kKVF + slot);
+                    const uint32_t dst = sKV + slot * C::kTileBytes;
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(bar, (uint32_t)(np * page * D * 2));
+                    __syncwarp();
+                    if (lane < np)
+#pragma unroll
+                        for (int b = 0; b < C::kBoxes; ++b)
+                            ptx::tma_load_3d(dst + b * C::kBoxBytes + lane * page * 128, v ? &tm_v : &tm_k, bar, b * 64, 0, row);
+                    if (!tail) {
+                        landed[slot] = use + 1;
+                        continue;
+                    }
+                    tail_open = true;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, tails & 1, lim_ns, abort_flag, p.err, 0x63));
+                    if (!ok)
+                        break;
+                    tail_open = false;
+                    ++tails;
+                    // rows [valid, 128), 128 bytes in each box (whole rows: the swizzle stays inside them)
+                    const int n16 = (kTileKeys - valid) * 8;
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        for (int c = lane; c < n16; c += 32)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * C::kBoxBytes +
+                                                                                          valid * 128 + c * 16),
+                                         "r"(0)
+                                         : "memory");
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(BAR(C::kKVF + slot));
+                    landed[slot] = 0;
+                }
+                row = next_row;
+            }
+        }
+        // Every copy this warp started lands before the CTA can exit.
+        volatile int no_abort = 0;
+        if (pieces > 0)
+            ptx::mbar_wait(BAR(C::kQF), (pieces - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
+        if (tail_open)
+            ptx::mbar_wait(BAR(C::kTail), tails & 1, lim_ns, &no_abort, p.err, 0x64);
+        for (int s = 0; s < C::kStages; ++s)
+            if (landed[s])
+                ptx::mbar_wait(BAR(C::kKVF + s), (landed[s] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
+        __syncwarp();
+    } else if (warp == C::kMmaWarp) {
+        // ============================ MMA issuer ============================
+        if (lane == 0) {
+            const uint32_t idesc_qk = ptx::idesc_bf16_f32(128, 128, false);
+            const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
+            const uint64_t dq0 = ptx::smem_desc_sw128(sQ, 16, 1024);
+            const uint64_t dk0 = ptx::smem_desc_sw128(sKV, 16, 1024);
+            const uint64_t dv0 = ptx::smem_desc_sw128(sKV, C::kBoxBytes, 1024);
+            uint32_t ld = 0, pieces = 0, steps[2] = {0, 0};  // loads, pieces and S steps before this piece
+            bool ok = true, any = false;
+            auto full = [&](uint32_t n) {  // the load numbered n has landed
+                return ptx::mbar_wait(BAR(C::kKVF + (n & (C::kStages - 1))), (n >> C::kStageBits) & 1, lim_ns, abort_flag,
+                                      p.err, 0x71);
+            };
+            auto free_slot = [&](uint32_t n) { ptx::mma_commit(BAR(C::kKVE + (n & (C::kStages - 1)))); };
+            auto issue_qk = [&](int t, int q_tile, uint32_t n) {
+                const uint64_t qa = dq0 + ((q_tile * C::kTileBytes) >> 4);
+                const uint64_t kb = dk0 + (((n & (C::kStages - 1)) * C::kTileBytes) >> 4);
+                const uint32_t dst = tmem + (t ? C::kColS1 : C::kColS0);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+                    ptx::mma_ss(dst, qa + off, kb + off, idesc_qk, kk > 0);
+                }
+                ptx::mma_commit(BAR(C::kSF + t));
+            };
+            auto issue_pv = [&](int t, uint32_t n, bool acc) {
+                const uint64_t vb = dv0 + (((n & (C::kStages - 1)) * C::kTileBytes) >> 4);
+                const uint32_t dst = tmem + (t ? C::kColO1 : C::kColO0);
+                const uint32_t pa = tmem + (t ? C::kColS1 : C::kColS0);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    ptx::mma_ts(dst, pa + kk * 8, vb + ((kk * 2048) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
+            };
+            auto p_full = [&](int t, int j) {
+                const bool got = ptx::mbar_wait(BAR(C::kPF + t), (steps[t] + j) & 1, lim_ns, abort_flag, p.err, 0x72);
+                ptx::tc_fence_after();
+                return got;
+            };
+            while (ok && walk.next(p, TU, x)) {
+                const Form f = form_of(x, TT);
+                if (f.tiles == 0)
+                    continue;
+                const int n = f.tiles;
+                any = true;
+                // tile i's K is load ld + 2i, its V load ld + 2i + 1
+                ok = ptx::mbar_wait(BAR(C::kQF), pieces & 1, lim_ns, abort_flag, p.err, 0x70) && full(ld);
+                if (!ok)
+                    break;
+                issue_qk(0, 0, ld);
+                if (f.two) {
+                    issue_qk(1, 1, ld);
+                    free_slot(ld);
+                    if (n == 1)
+                        ptx::mma_commit(BAR(C::kQFree));
+                    if (pieces > 0)
+                        ok = ptx::mbar_wait(BAR(C::kOFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x73);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const uint32_t v = ld + 2 * j + 1, k = v + 1;
+                        const bool more = j + 1 < n;
+                        ok = full(v) && p_full(0, j);
+                        if (!ok)
+                            break;
+                        issue_pv(0, v, j > 0);
+                        if (more) {
+                            ok = full(k);
+                            if (!ok)
+                                break;
+                            issue_qk(0, 0, k);
+                        } else {
+                            ptx::mma_commit(BAR(C::kOF + 0));
+                        }
+                        ok = p_full(1, j);
+                        if (!ok)
+                            break;
+                        issue_pv(1, v, j > 0);
+                        free_slot(v);
+                        if (more) {
+                            issue_qk(1, 1, k);
+                            free_slot(k);
+                            if (j + 2 == n)
+                                ptx::mma_commit(BAR(C::kQFree));  // that was the last S MMA
+                        } else {
+                            ptx::mma_commit(BAR(C::kOF + 1));
+                        }
+                    }
+                } else {
+                    free_slot(ld);
+                    if (n > 1) {
+                        ok = full(ld + 2);
+                        if (!ok)
+                            break;
+                        issue_qk(1, 0, ld + 2);
+                        free_slot(ld + 2);
+                    }
+                    if (n <= 2)
+                        ptx::mma_commit(BAR(C::kQFree));
+                    if (pieces > 0)
+                        ok = ptx::mbar_wait(BAR(C::kOFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x73);
+                    for (int i = 0; ok && i < n; ++i) {  // tile i is step i / 2 of stream i mod 2
+                        const int t = i & 1;
+                        const uint32_t v = ld + 2 * i + 1;
+                        ok = full(v) && p_full(t, i >> 1);
+                        if (!ok)
+                            break;
+                        issue_pv(t, v, i > 1);
+                        free_slot(v);
+                        if (i + 2 < n) {
+                            const uint32_t k = ld + 2 * (i + 2);
+                            ok = full(k);
+                            if (!ok)
+                                break;
+                            issue_qk(t, 0, k);
+                            free_slot(k);
+                            if (i + 3 == n)
+                                ptx::mma_commit(BAR(C::kQFree));
+                        } else {
+                            ptx::mma_commit(BAR(C::kOF + t));
+                        }
+                    }
+                }
+                ld += 2 * n;
+                steps[0] += f.n[0];
+                steps[1] += f.n[1];
+                ++pieces;
+            }
+            if (any) {
+                // Every MMA this thread issued has finished before TMEM is freed.
+                ptx::mma_commit(BAR(C::kDrain));
+                volatile int no_abort = 0;
+                ptx::mbar_wait(BAR(C::kDrain), 0, lim_ns, &no_abort, p.err, 0x74);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ============================== softmax ==============================
+        const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // half of the keys and columns, row of the tile
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tS[2] = {lanes + C::kColS0, lanes + C::kColS1}, tO[2] = {lanes + C::kColO0, lanes + C::kColO1};
+        float *xch = reinterpret_cast<float *>(gbase + C::kXchOff), *xl = xch + 512;
+        const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(d)
+        const int row_tok = row / p.G, row_g = row - row_tok * p.G;
+        uint32_t steps[2] = {0, 0}, drains[2] = {0, 0};
+        bool ok = true;
+        while (ok && walk.next(p, TU, x)) {
+            const Form f = form_of(x, TT);
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // kept maxima in log2 units, this half's sums
+            int64_t allowed[2];  // keys [0, allowed) of the segment are visible to the stream's row
+            bool valid[2], busy[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int ti = row_tok + (f.two ? t * TT : 0);
+                valid[t] = row_tok < TT && ti < x.ntok && (f.two || t == 0);
+                const bool has = row_tok < TT && ti < x.ntok;
+                allowed[t] = has ? min(x.keys, x.see0 + ti) : 0;
+                busy[t] = __any_sync(0xffffffffu, has);
+            }
+            for (int j = 0; ok && j < f.n[0]; ++j) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t == 1 && j >= f.n[1])
+                        continue;  // the same for every softmax thread
+                    const int64_t key0 = (x.t0 + (f.two ? j : 2 * j + t)) * kTileKeys + 64 * h;
+                    uint32_t s[64];
+                    float mx = -INFINITY;
+                    bool got = true;
+                    if (busy[t]) {
+                        got = ptx::mbar_wait(BAR(C::kSF + t), (steps[t] + j) & 1, lim_ns, abort_flag, p.err, 0x80);
+                        got = __all_sync(0xffffffffu, got);
+                        if (got) {
+                            ptx::tc_fence_after();
+                            ptx::tmem_ld64(tS[t] + 64 * h, s);
+                            ptx::tmem_ld_wait64(s);
+                            const int64_t lim = allowed[t] - key0;
+                            if (lim < 64) {
+#pragma unroll
+                                for (int i = 0; i < 64; ++i)
+                                    if ((int64_t)i >= lim)
+                                        s[i] = f2u(-INFINITY);
+                            }
+                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    m4[k] = fmax3(m4[k], u2f(s[i + 2 * k]), u2f(s[i + 2 * k + 1]));
+                            }
+                            mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+                            xch[(t * 2 + h) * 128 + row] = mx;
+                        }
+                    }
+                    // Both halves of every row have read S (and know whether every wait
+                    // succeeded) before P is written over it.
+                    ptx::tc_fence_before();
+                    ok = softmax_bar_and<256>(got);
+                    ptx::tc_fence_after();
+                    if (!ok)
+                        break;
+                    if (busy[t]) {
+                        mx = fmaxf(mx, xch[(t * 2 + (h ^ 1)) * 128 + row]);
+                        const float mnew = mx * sl2;
+                        const bool need = mnew > -INFINITY && (m[t] == -INFINITY || mnew > m[t] + kRescale);
+                        if (__any_sync(0xffffffffu, need)) {
+                            float alpha = 1.f;
+                            if (need) {
+                                alpha = m[t] == -INFINITY ? 0.f : ptx::ex2(m[t] - mnew);
+                                l[t] *= alpha;
+                                m[t] = mnew;
+                            }
+                            if (j > 0) {
+                                // the commit that signalled this S also covered the PV before it: O is stable
+                                const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                                for (int k = 0; k < D / 64; ++k) {
+                                    uint32_t o[32];
+                                    const uint32_t ta = tO[t] + h * (D / 2) + k * 32;
+                                    ptx::tmem_ld32(ta, o);
+                                    ptx::tmem_ld_wait(o);
+#pragma unroll
+                                    for (int i = 0; i < 32; i += 2) {
+                                        const float2 r = __fmul2_rn(make_float2(u2f(o[i]), u2f(o[i + 1])), a2);
+                                        o[i] = f2u(r.x);
+                                        o[i + 1] = f2u(r.y);
+                                    }
+                                    ptx::tmem_st32(ta, o);
+                                }
+                            }
+                        }
+                        // p = 2^(s log2(e) / sqrt(d) - m), rounded to bf16 for the MMA (the sum l keeps
+                        // them in fp32); keys [64h, 64h + 64) go to packed columns [32h, 32h + 32).
+                        const float neg = m[t] == -INFINITY ? 0.f : -m[t];
+                        const float2 c2 = make_float2(sl2, sl2), n2 = make_float2(neg, neg);
+                        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                         make_float2(0.f, 0.f)};
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float2 y = __ffma2_rn(make_float2(u2f(s[2 * i]), u2f(s[2 * i + 1])), c2, n2);
+                            const float p0 = ptx::ex2(y.x), p1 = ptx::ex2(y.y);
+                            acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+                            pk[i] = pack_bf16(p0, p1);
+                        }
+                        ptx::tmem_st32(tS[t] + 32 * h, pk);
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(BAR(C::kPF + t));
+                        const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+                        l[t] += a.x + a.y;
+                    } else {
+                        // (rows of P that nobody wrote only reach the same rows of O)
+                        ptx::mbar_arrive(BAR(C::kPF + t));
+                    }
+                }
+            }
+            if (!ok)
+                break;
+            // ---- the piece's (o, lse) ----
+            bool fin = true;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (f.n[t] > 0) {
+                    fin = fin && ptx::mbar_wait(BAR(C::kOF + t), drains[t] & 1, lim_ns, abort_flag, p.err, 0x81);
+                    fin = __all_sync(0xffffffffu, fin);
+                    ++drains[t];
+                    steps[t] += f.n[t];
+                    xl[(t * 2 + h) * 128 + row] = l[t];
+                }
+            ok = softmax_bar_and<256>(fin);
+            if (!ok)
+                break;
+            ptx::tc_fence_after();
+            float inv[2] = {0.f, 0.f}, lse[2];  // weights of the unnormalised O, and the results' lse
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (f.n[t] > 0)
+                    l[t] += xl[(t * 2 + (h ^ 1)) * 128 + row];
+            if (f.two) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const bool empty = !(l[t] > 0.f) && l[t] == l[t];
+                    inv[t] = empty ? 0.f : 1.f / l[t];
+                    lse[t] = empty ? -INFINITY : (m[t] + ptx::lg2(l[t])) * kLn2;
+                }
+            } else {
+                const float M = fmaxf(m[0], m[1]);
+                const float w0 = m[0] == -INFINITY ? 0.f : ptx::ex2(m[0] - M), w1 = m[1] == -INFINITY ? 0.f : ptx::ex2(m[1] - M);
+                const float L = l[0] * w0 + l[1] * w1;
+                const bool empty = !(L > 0.f) && L == L;
+                inv[0] = empty ? 0.f : w0 / L;
+                inv[1] = empty ? 0.f : w1 / L;
+                lse[0] = empty ? -INFINITY : (M + ptx::lg2(L)) * kLn2;
+                lse[1] = -INFINITY;
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!f.two && t == 1)
+                    continue;
+                const int ti = row_tok + (f.two ? t * TT : 0);
+                const int64_t token = x.tok + ti;
+                const int hq = x.head * p.G + row_g;
+                const Place d = place(p, x, worker, token, hq, ti * p.G + row_g);
+                if (valid[t] && h == 0)
+                    *(d.final_ ? p.lse + token * p.Hq + hq : d.lse) = lse[t];
+                if (!busy[t])
+                    continue;  // the whole warp
+#pragma unroll 1
+                for (int k = 0; k < D / 64; ++k) {
+                    const int col = h * (D / 2) + k * 32;
+                    float v[32];
+                    uint32_t o[32];
+                    if (f.n[t] > 0) {
+                        ptx::tmem_ld32(tO[t] + col, o);
+                        ptx::tmem_ld_wait(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = u2f(o[i]) * inv[t];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = 0.f;
+                    }
+                    if (!f.two && f.n[1] > 0) {
+                        ptx::tmem_ld32(tO[1] + col, o);
+                        ptx::tmem_ld_wait(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = fmaf(u2f(o[i]), inv[1], v[i]);
+                    }
+                    if (valid[t]) {
+                        if (d.final_) {
+                            uint4 *dst =
+                                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + (token * p.Hq + hq) * D + col);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[i] =
+                                    make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                               pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(d.o + col);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (f.tiles > 0) {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(BAR(C::kOFree));
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == C::kMmaWarp) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+cudaError_t launch(const PrefixAttnParams &p, cudaStream_t s)
+{
+    const int TT = 128 / p.G;
+    CUtensorMap mq, mk, mv;
+    const int64_t page = 1ll << p.page_shift;
+    const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.T};
+    const uint64_t qs[3] = {(uint64_t)p.q_head_stride * 2, (uint64_t)p.G * p.q_head_stride * 2, (uint64_t)p.q_token_stride * 2};
+    const uint32_t qb[4] = {64, (uint32_t)p.G, 1, (uint32_t)TT};
+    const uint64_t kd[3] = {(uint64_t)D, (uint64_t)page, (uint64_t)(p.n_pages * p.Hkv)};
+    const uint64_t ks[2] = {(uint64_t)D * 2, (uint64_t)(page * D * 2)};
+    const uint32_t kb[3] = {64, (uint32_t)page, 1};
+    if (!make_bf16_map_sw128(&mq, p.q, 4, qd, qs, qb) || !make_bf16_map_sw128(&mk, p.k_cache, 3, kd, ks, kb) ||
+        !make_bf16_map_sw128(&mv, p.v_cache, 3, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Cfg<D>::kSmemBytes);
+    if (e != cudaSuccess)
+        return e;
+    prefix_attn_kernel<D><<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_prefix_join(p, 2 * TT, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_attn_bf16(const PrefixAttnParams &p, cudaStream_t s)
+{
+    if (p.d == 128)
+        return launch<128>(p, s);
+    if (p.d == 64)
+        return launch<64>(p, s);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace rsa

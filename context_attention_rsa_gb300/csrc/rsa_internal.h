@@ -221,7 +221,8 @@ cudaError_t launch_qk_norm_rope_fwd(const NormRopeParams &p, cudaStream_t s);
 // Two launches: gradients and partial sums, then the sums of the weights' gradients.
 cudaError_t launch_qk_norm_rope_bwd(const NormRopeParams &p, cudaStream_t s);
 constexpr int kNormRopeBwdBlocks = 608;  // blocks of partial weight gradients: four on each of 152 SMs
-cudaError_t launch_prefix_attn_simt(const PrefixAttnParams &p, cudaStream_t s);
+cudaError_t launch_prefix_attn_bf16(const PrefixAttnParams &p, cudaStream_t s);
+cudaError_t launch_prefix_attn_f32(const PrefixAttnParams &p, cudaStream_t s);
 // Joins the pieces of every row: the second launch of the attention.
 cudaError_t launch_prefix_join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s);
 cudaError_t launch_selftest_wait(uint64_t limit_ns, unsigned int *err, cudaStream_t s);
