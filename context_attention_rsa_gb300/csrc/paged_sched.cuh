@@ -8,11 +8,13 @@
 //             G query heads of one key head: the rows that share a key tile
 //   tile      128 keys of a unit
 // All tiles of all units lie on one line: segments in order, in a segment the
-// key heads, in a head the token groups, in a unit its tiles.  The line is cut
-// into `workers` equal stretches, one for each CTA, so that one long request,
-// many short ones and a prefix all fill the GPU alike.  The part of a unit in
-// a stretch is a piece; it leaves a partial (o, lse) for its rows: in the
-// rows' own place (home) if the piece begins the unit, else in the worker's
+// key heads, in a head the token groups, in a unit its tiles.  A unit also
+// takes kUnitCost places before its first tile, for what it costs to begin and
+// to end one, so that many short requests weigh what they take.  The line is
+// cut into `workers` equal stretches, one for each CTA, so that one long
+// request, many short ones and a prefix all fill the GPU alike.  The part of a
+// unit in a stretch is a piece; it leaves a partial (o, lse) for its rows: in
+// the rows' own place (home) if the piece begins the unit, else in the worker's
 // slot, as only a worker's first piece can begin inside a unit.  Workspace:
 // two homes for every row and 256 rows for every worker, whatever the lengths.
 // Every place is written once and joined in a fixed order by the next launch:
@@ -28,33 +30,35 @@ namespace rsa {
 namespace paged {
 
 constexpr int kTileKeys = 128;
+constexpr int kUnitCost = 2;  // in tiles
 
 struct Segment {
-    int64_t tok0, ntok;    // its query tokens
-    int64_t keys;          // its keys
+    int tok0, ntok;        // its query tokens
+    int keys;              // its keys
     const int32_t *pages;  // their pages
-    int64_t groups, tiles; // token groups; key tiles of a unit
-    int64_t line;          // tiles on the line: Hkv * groups * tiles
-    int64_t see0;          // token i of the segment sees keys [0, min(keys, see0 + i)): all of the prefix
+    int groups, tiles;     // token groups; key tiles of a unit
+    int see0;              // token i of the segment sees keys [0, min(keys, see0 + i)): all of the prefix
+    int64_t line;          // places on the line
 };
 
-__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // Segment s, its lengths forced into the buffers (`report`: and recorded).
-__device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int64_t s, int tokens_per_unit, bool report = false)
+__device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, int tokens_per_unit, bool report = false)
 {
     Segment g;
+    const int T = (int)p.T;
     if (s == 0) {
         g.tok0 = 0;
-        g.keys = p.prefix_len;
-        g.ntok = p.prefix_len > 0 ? clamp64(p.cu_q[p.R], 0, p.T) : 0;
+        g.keys = (int)p.prefix_len;
+        g.ntok = p.prefix_len > 0 ? clamp_int(p.cu_q[p.R], 0, T) : 0;
         g.pages = p.prefix_pages;
         g.see0 = g.keys;
     } else {
-        const int64_t r = s - 1, a = p.cu_q[r], b = p.cu_q[r + 1], n = p.kv_len[r];
-        g.tok0 = clamp64(a, 0, p.T);
-        g.ntok = clamp64(b, g.tok0, p.T) - g.tok0;
-        g.keys = clamp64(n, 0, (int64_t)p.max_pages << p.page_shift);
+        const int r = s - 1, a = p.cu_q[r], b = p.cu_q[r + 1], n = p.kv_len[r];
+        g.tok0 = clamp_int(a, 0, T);
+        g.ntok = clamp_int(b, g.tok0, T) - g.tok0;
+        g.keys = clamp_int(n, 0, p.max_pages << p.page_shift);
         g.pages = p.block_table + r * p.table_stride;
         g.see0 = g.keys - g.ntok + 1;
         if (report) {
@@ -64,31 +68,31 @@ __device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int64_t s,
                 record_bad_index(p.err, 0x54, n);
         }
     }
-    g.groups = (g.ntok + tokens_per_unit - 1) / tokens_per_unit;
-    g.tiles = (g.keys + kTileKeys - 1) / kTileKeys;
-    g.line = g.groups * g.tiles * p.Hkv;
+    g.groups = (int)(((int64_t)g.ntok + tokens_per_unit - 1) / tokens_per_unit);
+    g.tiles = (int)(((int64_t)g.keys + kTileKeys - 1) / kTileKeys);
+    g.line = g.tiles > 0 ? (int64_t)g.groups * p.Hkv * (g.tiles + kUnitCost) : 0;
     return g;
 }
 
 // A worker's stretch of the line, and where it begins.
 struct Stretch {
-    int64_t total, share;  // tiles in all, and of a worker
-    int64_t seg, off;      // first segment, and the stretch's first tile on that segment's line
-    int64_t left;          // tiles of this worker
+    int64_t off;   // its first place on that segment's line
+    int64_t left;  // its places
+    int seg;       // its first segment
 };
 
 // Every thread of the block (NT of them) calls this with two words of shared
 // memory a warp.  Worker 0 leaves the plan for the joining launch: plan[s] =
-// the line's tiles before segment s, plan[R + 1] = total, plan[R + 2] = share.
+// the line's places before segment s, plan[R + 1] = total, plan[R + 2] = share.
 template <int NT>
 __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int tokens_per_unit, int worker, int64_t *s_sum,
                                                 Stretch *s_out)
 {
     constexpr int NW = NT / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t nseg = (int64_t)p.R + 1;
+    const int nseg = p.R + 1;
     int64_t total = 0, mine = 0;
-    for (int64_t s = threadIdx.x; s < nseg; s += NT) {
+    for (int s = threadIdx.x; s < nseg; s += NT) {
         mine = segment(p, s, tokens_per_unit, worker == 0).line;
         total += mine;
     }
@@ -105,14 +109,14 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int t
     const int64_t share = (total + p.workers - 1) / p.workers;
     const int64_t at = worker * share;
     if (threadIdx.x == 0)
-        *s_out = Stretch{total, share, nseg, 0, 0};
+        *s_out = Stretch{0, 0, 0};
     if (worker == 0 && threadIdx.x == 0) {
         p.plan[p.R + 1] = total;
         p.plan[p.R + 2] = share;
     }
     int64_t before = 0;
-    for (int64_t s0 = 0; s0 < nseg; s0 += NT) {
-        const int64_t s = s0 + threadIdx.x;
+    for (int s0 = 0; s0 < nseg; s0 += NT) {
+        const int s = s0 + threadIdx.x;
         if (nseg > NT)
             mine = s < nseg ? segment(p, s, tokens_per_unit).line : 0;
         int64_t x = s < nseg ? mine : 0;
@@ -148,55 +152,70 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int t
 
 // One piece: tiles [t0, t1) of a unit.
 struct Piece {
-    int64_t seg;
-    int64_t tok, ntok;     // the unit's tokens
+    int seg;
+    int tok, ntok;         // the unit's tokens
     int head;              // its key head
-    int64_t keys;          // the segment's keys
+    int keys;              // the segment's keys
     const int32_t *pages;
     int64_t see0;          // unit token i sees keys [0, min(keys, see0 + i))
-    int64_t t0, t1;
+    int t0, t1;
     bool first, whole;     // it begins the unit; it is all of it
 };
 
 // Walks a worker's pieces.  Roles of a CTA that walk by themselves see the same pieces.
 struct Walk {
     Segment g;
-    int64_t seg, off, left;
+    int seg, head, group, at;  // at: the next place in the unit
+    int64_t left;
 
     __device__ __forceinline__ void begin(const PrefixAttnParams &p, const Stretch &st, int tokens_per_unit)
     {
-        seg = st.seg;
-        off = st.off;
         left = st.left;
-        if (left > 0)
-            g = segment(p, seg, tokens_per_unit);
+        if (left <= 0)
+            return;
+        seg = st.seg;
+        g = segment(p, seg, tokens_per_unit);
+        const int64_t len = g.tiles + kUnitCost, unit = st.off / len;
+        at = (int)(st.off - unit * len);
+        head = (int)(unit / g.groups);
+        group = (int)(unit - (int64_t)head * g.groups);
     }
     __device__ __forceinline__ bool next(const PrefixAttnParams &p, int tokens_per_unit, Piece &x)
     {
-        if (left <= 0)
-            return false;
-        while (off >= g.line) {  // (left > 0: a segment with tiles follows, unless the lengths changed meanwhile)
-            if (++seg > p.R)
-                return false;
-            off = 0;
-            g = segment(p, seg, tokens_per_unit);
+        while (left > 0) {
+            if (head >= p.Hkv || g.line == 0) {
+                if (++seg > p.R)
+                    return false;  // (only if the lengths changed meanwhile)
+                g = segment(p, seg, tokens_per_unit);
+                head = group = at = 0;
+                continue;
+            }
+            const int take = (int)min((int64_t)(g.tiles + kUnitCost - at), left);
+            const int i0 = group * tokens_per_unit;
+            x.seg = seg;
+            x.tok = g.tok0 + i0;
+            x.ntok = min(tokens_per_unit, g.ntok - i0);
+            x.head = head;
+            x.keys = g.keys;
+            x.pages = g.pages;
+            x.see0 = seg == 0 ? g.keys : (int64_t)g.see0 + i0;
+            x.t0 = max(0, at - kUnitCost);
+            x.t1 = at + take - kUnitCost;
+            x.first = x.t0 == 0;
+            x.whole = x.first && x.t1 == g.tiles;
+            left -= take;
+            at += take;
+            if (at == g.tiles + kUnitCost) {
+                at = 0;
+                if (++group == g.groups) {
+                    group = 0;
+                    ++head;
+                }
+            }
+            if (x.t1 > x.t0)
+                return true;  // (else the stretch ends before the unit's first tile)
         }
-        const int64_t unit = off / g.tiles;
-        x.t0 = off - unit * g.tiles;
-        x.t1 = min(g.tiles, x.t0 + left);
-        x.head = (int)(unit / g.groups);
-        const int64_t i0 = (unit - x.head * g.groups) * tokens_per_unit;
-        x.seg = seg;
-        x.tok = g.tok0 + i0;
-        x.ntok = min((int64_t)tokens_per_unit, g.ntok - i0);
-        x.keys = g.keys;
-        x.pages = g.pages;
-        x.see0 = seg == 0 ? g.keys : g.see0 + i0;
-        x.first = x.t0 == 0;
-        x.whole = x.first && x.t1 == g.tiles;
-        left -= x.t1 - x.t0;
-        off += x.t1 - x.t0;
-        return true;
+        return false;
     }
 };
 
@@ -206,10 +225,10 @@ struct Place {
     bool final_;     // the piece is all there is for the row: straight to out and lse
 };
 
-__device__ __forceinline__ Place place(const PrefixAttnParams &p, const Piece &x, int worker, int64_t token, int hq, int local)
+__device__ __forceinline__ Place place(const PrefixAttnParams &p, const Piece &x, int worker, int token, int hq, int local)
 {
     Place d;
-    const int64_t row = token * p.Hq + hq;
+    const int64_t row = (int64_t)token * p.Hq + hq;
     d.final_ = x.seg > 0 && x.whole && p.prefix_len == 0;
     if (x.first) {
         const int home = x.seg > 0;

@@ -19,6 +19,7 @@
 #include <cmath>
 
 #include "paged_sched.cuh"
+#include "ptx_sm103.cuh"
 
 namespace rsa {
 namespace {
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
 
     const Stretch st = find_stretch<kThreads>(p, TU, worker, s.sum, &s.st);
+    ptx::launch_dependents();
     Walk walk;
     walk.begin(p, st, TU);
     Piece x;
@@ -88,20 +90,19 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
         // Row i * kWarps + warp of the unit, and the keys it sees.
         float m[kWarpRows], l[kWarpRows], o[kWarpRows][PER];
         int64_t see[kWarpRows];
-        int64_t most = 0;  // the keys that any row sees
 #pragma unroll
         for (int i = 0; i < kWarpRows; ++i) {
             const int row = i * kWarps + warp;
             m[i] = -INFINITY;
             l[i] = 0.f;
-            see[i] = row < rows ? min(x.keys, x.see0 + row / G) : 0;
+            see[i] = row < rows ? min((int64_t)x.keys, x.see0 + row / G) : 0;
 #pragma unroll
             for (int c = 0; c < PER; ++c)
                 o[i][c] = 0.f;
         }
-        most = min(x.keys, x.see0 + (x.ntok - 1));
-        const int64_t j1 = min(most, x.t1 * kTileKeys);
-        for (int64_t j0 = x.t0 * kTileKeys; j0 < j1; j0 += kKeys) {
+        const int64_t most = min((int64_t)x.keys, x.see0 + (x.ntok - 1));  // the keys that any row sees
+        const int64_t j1 = min(most, (int64_t)x.t1 * kTileKeys);
+        for (int64_t j0 = (int64_t)x.t0 * kTileKeys; j0 < j1; j0 += kKeys) {
             const int nk = (int)min((int64_t)kKeys, j1 - j0);
             __syncthreads();  // the last block of keys is done with
             for (int i = threadIdx.x; i < nk * D; i += kThreads) {
@@ -161,18 +162,18 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
             const int row = i * kWarps + warp;
             if (row >= rows)
                 continue;
-            const int64_t token = x.tok + row / G;
+            const int token = x.tok + row / G;
             const int hq = x.head * G + row % G;
             const Place d = place(p, x, worker, token, hq, row);
             const bool empty = !(l[i] > 0.f) && l[i] == l[i];
             const float inv = empty ? 0.f : 1.f / l[i], lse = empty ? -INFINITY : m[i] + logf(l[i]);
             if (d.final_) {
-                float *out = static_cast<float *>(p.out) + (token * p.Hq + hq) * D;
+                float *out = static_cast<float *>(p.out) + ((int64_t)token * p.Hq + hq) * D;
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
                     out[lane + 32 * c] = o[i][c] * inv;
                 if (lane == 0)
-                    p.lse[token * p.Hq + hq] = lse;
+                    p.lse[(int64_t)token * p.Hq + hq] = lse;
             } else {
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
 
 // The request of a token: the last r with cu_q[r] <= token (requests without
 // tokens share their successor's row), by 32-way search; -1 behind the last one.
-__device__ __forceinline__ int64_t request_of(const PrefixAttnParams &p, int64_t token)
+__device__ __forceinline__ int request_of(const PrefixAttnParams &p, int token)
 {
     const int lane = threadIdx.x & 31;
     if (token >= p.cu_q[p.R])
@@ -196,8 +197,7 @@ __device__ __forceinline__ int64_t request_of(const PrefixAttnParams &p, int64_t
     int64_t lo = 0, n = p.R;  // the answer is in [lo, lo + n)
     while (n > 1) {
         const int64_t step = (n + 31) / 32;
-        const int64_t at = lo + lane * step;
-        const bool below = lane * step < n && p.cu_q[at] <= token;
+        const bool below = lane * step < n && p.cu_q[lo + lane * step] <= token;
         const unsigned vote = __ballot_sync(0xffffffffu, below);
         if (!vote)
             return -1;  // (rows before cu_q[0])
@@ -205,10 +205,20 @@ __device__ __forceinline__ int64_t request_of(const PrefixAttnParams &p, int64_t
         n = min(step, n - k * step);
         lo += k * step;
     }
-    return lo;
+    return (int)lo;
 }
 
-// One warp a row (token, query head): lane c owns columns [c * PER, ...).
+// A row's pieces in one segment: its home, then one slot for each worker after the first.
+struct Pieces {
+    const float *o, *lse;  // home
+    int64_t slot;          // row of the first slot; the next are kPrefixUnitRows apart
+    int n;
+};
+
+// One warp a row (token, query head).  Lane i brings the lse of piece i, so that
+// all of them are in flight together and their weights known before the first o
+// is needed; the loads of the o rows then depend on nothing.  Lane c owns
+// columns [c * PER, (c + 1) * PER).
 template <class E, int D>
 __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_constant__ PrefixAttnParams p, int tokens_per_unit)
 {
@@ -217,44 +227,79 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_cons
     const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= p.T * p.Hq)
         return;
-    const int64_t token = row / p.Hq;
-    const int hq = (int)(row - token * p.Hq), head = hq / p.G;
-    const int64_t r = request_of(p, token);
+    const int token = (int)(row / p.Hq);
+    const int hq = (int)(row - (int64_t)token * p.Hq), head = hq / p.G;
+    const int r = request_of(p, token);
     if (r < 0)
         return;  // rows behind the last request stay as they are
-    const int64_t share = p.plan[p.R + 2];
+    Segment g[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        g[s] = segment(p, s == 0 ? 0 : 1 + r, tokens_per_unit);
+    ptx::wait_for_launch_before();  // so far only the call's inputs were read
+    const int64_t share = p.plan[p.R + 2], before[2] = {0, p.plan[1 + r]};
+    Pieces pc[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int i = token - g[s].tok0;
+        pc[s].n = 0;
+        if (g[s].line == 0 || i < 0 || i >= g[s].ntok)
+            continue;  // (outside: only where cu_q does not ascend)
+        const int64_t unit = (int64_t)head * g[s].groups + i / tokens_per_unit;
+        const int64_t at = before[s] + unit * (g[s].tiles + kUnitCost) + kUnitCost;  // the unit's first tile
+        const int64_t w0 = at / share, w1 = (at + g[s].tiles - 1) / share;
+        if (s == 1 && w0 == w1 && p.prefix_len == 0)
+            return;  // one piece: it went straight to out
+        pc[s].o = p.home_o[s] + row * D;
+        pc[s].lse = p.home_lse[s] + row;
+        pc[s].slot = (w0 + 1) * kPrefixUnitRows + (i % tokens_per_unit) * p.G + (hq - head * p.G);
+        pc[s].n = (int)(w1 - w0) + 1;
+    }
+    const int n = pc[0].n + pc[1].n;
+    auto locate = [&](int i, const float *&o, const float *&lse) {  // piece i of the row
+        const int s = i >= pc[0].n;
+        const int k = i - (s ? pc[0].n : 0);
+        const int64_t slot = (s ? pc[1].slot : pc[0].slot) + (int64_t)(k - 1) * kPrefixUnitRows;
+        o = k == 0 ? (s ? pc[1].o : pc[0].o) : p.slot_o + slot * D;
+        lse = k == 0 ? (s ? pc[1].lse : pc[0].lse) : p.slot_lse + slot;
+    };
     float M = -INFINITY, L = 0.f, acc[PER];
 #pragma unroll
     for (int c = 0; c < PER; ++c)
         acc[c] = 0.f;
-    auto add = [&](const float *o, float lse) {
-        if (lse == -INFINITY)
-            return;  // an empty piece: its o is not read
-        const float mn = fmaxf(M, lse);
-        const float a = expf(M - mn), b = expf(lse - mn);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int m = min(32, n - i0);
+        const float *o = nullptr, *at = nullptr;
+        float lse = -INFINITY;
+        if (lane < m) {
+            locate(i0 + lane, o, at);
+            lse = *at;
+        }
+        const float mn = fmaxf(M, warp_max(lse));
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float w = expf(lse - base), a = expf(M - base);
+        L = L * a + warp_sum(w);
         M = mn;
-        L = L * a + b;
 #pragma unroll
         for (int c = 0; c < PER; ++c)
-            acc[c] = fmaf(o[lane * PER + c], b, acc[c] * a);
-    };
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int64_t seg = s == 0 ? 0 : 1 + r;
-        const Segment g = segment(p, seg, tokens_per_unit);
-        const int64_t i = token - g.tok0;
-        if (g.line == 0 || i < 0 || i >= g.ntok)
-            continue;  // (outside: only where cu_q does not ascend)
-        const int64_t unit = head * g.groups + i / tokens_per_unit;
-        const int64_t at = p.plan[seg] + unit * g.tiles;
-        const int64_t w0 = at / share, w1 = (at + g.tiles - 1) / share;
-        if (s == 1 && w0 == w1 && p.prefix_len == 0)
-            return;  // one piece: it went straight to out
-        add(p.home_o[s] + row * D, p.home_lse[s][row]);
-        const int local = (int)(i % tokens_per_unit) * p.G + (hq - head * p.G);
-        for (int64_t w = w0 + 1; w <= w1; ++w) {
-            const int64_t slot = w * kPrefixUnitRows + local;
-            add(p.slot_o + slot * D, p.slot_lse[slot]);
+            acc[c] *= a;
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float *oi = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), i));
+            if (wi == 0.f)
+                continue;  // an empty piece: its o is not read
+            if constexpr (PER == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(oi + lane * 4);
+                acc[0] = fmaf(wi, x.x, acc[0]);
+                acc[1] = fmaf(wi, x.y, acc[1]);
+                acc[2] = fmaf(wi, x.z, acc[2]);
+                acc[3] = fmaf(wi, x.w, acc[3]);
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(oi + lane * 2);
+                acc[0] = fmaf(wi, x.x, acc[0]);
+                acc[1] = fmaf(wi, x.y, acc[1]);
+            }
         }
     }
     const float inv = M == -INFINITY ? 0.f : 1.f / L;
@@ -284,8 +329,16 @@ cudaError_t join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s)
     const int64_t blocks = (p.T * p.Hq + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    prefix_join_kernel<E, D><<<(unsigned)blocks, kThreads, 0, s>>>(p, tokens_per_unit);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<E, D>, p, tokens_per_unit);
 }
 
 }  // namespace

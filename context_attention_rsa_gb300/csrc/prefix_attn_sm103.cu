@@ -25,12 +25,16 @@
 //               put together by the thread that owns the row.  Warps without a
 //               row of the piece only keep the barriers' count, so a decode
 //               step's few rows cost little and HBM is the bound.
-// Values of rows past the keys are not trusted: a tile's K there gives scores
-// that are masked, but 0 * NaN would reach O through V, so the producer clears
-// those rows of V in shared memory before the MMA may read them.
-// The phases of all barriers run on over the CTA's pieces; Q is loaded again as
-// soon as the last S MMA of a piece is done, O is written again once every
-// softmax thread has read it.
+// Rows past the keys are not trusted: a score of such a key is masked, but its
+// 0 * NaN would reach O through V.  So they are never loaded: a tile's boxes of
+// pages it does not have lie outside the tensor map, which fills them with
+// zeros, and the box of a page that is v < page keys long starts v - page rows
+// before the page, so that its first page - v rows are zeros and its keys end
+// where the box ends.  The softmax masks those columns; the keys' order within
+// a tile does not matter to it.
+// The phases of all barriers run on over the CTA's pieces; one-tile pieces take
+// the two Q tiles in turn, so that the next piece's loads are under way while
+// one computes; O is written again once every softmax thread has read it.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -66,15 +70,14 @@ struct Cfg {
     static constexpr uint32_t kSumOff = kXchOff + 2 * 2048;
     static constexpr uint32_t kSmemBytes = kSumOff + 256 + 1024;
     static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
-    static constexpr int kQF = 0;
-    static constexpr int kKVF = 1;
+    static constexpr int kQF = 0;            // one for each Q tile
+    static constexpr int kKVF = kQF + 2;
     static constexpr int kKVE = kKVF + kStages;
     static constexpr int kSF = kKVE + kStages;
     static constexpr int kPF = kSF + 2;
     static constexpr int kOF = kPF + 2;
-    static constexpr int kTail = kOF + 2;    // a V tile whose last rows the producer clears has landed
-    static constexpr int kQFree = kTail + 1; // every S MMA of the piece is done
-    static constexpr int kOFree = kQFree + 1;// every softmax thread has read the piece's O
+    static constexpr int kQFree = kOF + 2;    // one for each Q tile: every S MMA of its piece is done
+    static constexpr int kOFree = kQFree + 2; // every softmax thread has read the piece's O
     static constexpr int kDrain = kOFree + 1;
     static constexpr int kNumBars = kDrain + 1;
     static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
@@ -90,10 +93,10 @@ struct Form {
 
 __device__ __forceinline__ Form form_of(const Piece &x, int tokens_per_tile)
 {
-    const int64_t seen = min(x.keys, x.see0 + (x.ntok - 1));
-    const int64_t end = min(x.t1, seen > 0 ? (seen + kTileKeys - 1) / kTileKeys : 0);
+    const int64_t seen = min((int64_t)x.keys, x.see0 + (x.ntok - 1));
+    const int end = min(x.t1, seen > 0 ? (int)((seen + kTileKeys - 1) / kTileKeys) : 0);
     Form f;
-    f.tiles = end > x.t0 ? (int)(end - x.t0) : 0;
+    f.tiles = max(0, end - x.t0);
     f.two = x.ntok > tokens_per_tile;
     f.n[0] = f.two ? f.tiles : (f.tiles + 1) >> 1;
     f.n[1] = f.two ? f.tiles : f.tiles >> 1;
@@ -121,7 +124,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint64_t lim_ns = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
-        ptx::mbar_init(BAR(C::kQF), 1);
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(BAR(C::kKVF + s), 1);
             ptx::mbar_init(BAR(C::kKVE + s), 1);
@@ -130,9 +132,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ptx::mbar_init(BAR(C::kSF + t), 1);
             ptx::mbar_init(BAR(C::kPF + t), C::kSoftmaxThreads);
             ptx::mbar_init(BAR(C::kOF + t), 1);
+            ptx::mbar_init(BAR(C::kQF + t), 1);
+            ptx::mbar_init(BAR(C::kQFree + t), 1);
         }
-        ptx::mbar_init(BAR(C::kTail), 1);
-        ptx::mbar_init(BAR(C::kQFree), 1);
         ptx::mbar_init(BAR(C::kOFree), C::kSoftmaxThreads);
         ptx::mbar_init(BAR(C::kDrain), 1);
         *abort_flag = 0;
@@ -149,6 +151,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     int64_t *s_sum = reinterpret_cast<int64_t *>(gbase + C::kSumOff);
     const Stretch st = find_stretch<C::kThreads>(p, TU, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + C::kThreads / 32));
+    ptx::launch_dependents();  // the joining launch finds its rows' pieces while this one computes
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -162,19 +165,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         // ============================= producer =============================
         const int page = 1 << p.page_shift, per_tile = kTileKeys >> p.page_shift;
         const int none = (int)(p.n_pages * p.Hkv);  // outside the maps: zeros
-        uint32_t ld = 0, tails = 0, pieces = 0;
-        uint32_t landed[C::kStages];  // the last use of each slot that TMA completes by itself, plus one
+        uint32_t ld = 0, q_use[2] = {0, 0};
+        int q_slot = 0;
+        uint32_t landed[C::kStages];  // uses of each slot
         for (int s = 0; s < C::kStages; ++s)
             landed[s] = 0;
-        bool ok = true, tail_open = false;
+        bool ok = true;
         while (ok && walk.next(p, TU, x)) {
             const Form f = form_of(x, TT);
             if (f.tiles == 0)
                 continue;
-            auto page_row = [&](int64_t tile) -> int {  // this lane's page of a tile, as a row of the maps
-                const int64_t first = tile * kTileKeys + ((int64_t)lane << p.page_shift);
-                if (lane >= per_tile || first >= x.keys)
+            // This lane's page of a tile: its row of the maps and the row of the page
+            // the box starts at.
+            auto page_row = [&](int tile, int &first) -> int {
+                const int left = x.keys - tile * kTileKeys - (lane << p.page_shift);  // keys from this page on
+                first = left < page ? left - page : 0;
+                if (lane >= per_tile || left <= 0) {
+                    first = 0;
                     return none;
+                }
                 const int id = x.pages[tile * per_tile + lane];
                 if (id < 0 || id >= p.n_pages) {
                     record_bad_index(p.err, 0x55, id);
@@ -182,27 +191,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 }
                 return id * p.Hkv + x.head;
             };
-            int row = page_row(x.t0);
-            if (pieces > 0)
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(BAR(C::kQFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x61));
-            if (!ok)
-                break;
-            if (lane == 0) {
-                const int nq = f.two ? 2 : 1;
-                ptx::mbar_arrive_expect_tx(BAR(C::kQF), (uint32_t)(nq * C::kBoxes * 128 * p.G * TT));
-                for (int t = 0; t < nq; ++t)
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        ptx::tma_load_4d(sQ + t * C::kTileBytes + b * C::kBoxBytes, &tm_q, BAR(C::kQF), b * 64, 0, x.head,
-                                         (int)(x.tok + t * TT));
-            }
-            ++pieces;
-            for (int i = 0; ok && i < f.tiles; ++i) {
-                const int64_t tile = x.t0 + i;
-                const int valid = (int)min((int64_t)kTileKeys, x.keys - tile * kTileKeys);
-                const int np = (valid + page - 1) >> p.page_shift;
-                const int next_row = i + 1 < f.tiles ? page_row(tile + 1) : none;
+            int first, row = page_row(x.t0, first);
+            const int q0 = f.two ? 0 : q_slot, q1 = f.two ? 2 : q_slot + 1;
 #pragma unroll 1
-                for (int v = 0; ok && v < 2; ++v, ++ld) {
+            for (int t = q0; ok && t < q1; ++t) {
+                if (q_use[t] > 0)
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(BAR(C::kQFree + t), (q_use[t] - 1) & 1, lim_ns, abort_flag,
+                                                                p.err, 0x61));
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(BAR(C::kQF + t), (uint32_t)(C::kBoxes * 128 * p.G * TT));
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        ptx::tma_load_4d(sQ + t * C::kTileBytes + b * C::kBoxBytes, &tm_q, BAR(C::kQF + t), b * 64, 0, x.head,
+                                         x.tok + (t - q0) * TT);
+                }
+                ++q_use[t];
+            }
+            if (!f.two)
+                q_slot ^= 1;
+            for (int i = 0; ok && i < f.tiles; ++i) {
+                int next_first = 0;
+                const int next_row = i + 1 < f.tiles ? page_row(x.t0 + i + 1, next_first) : none;
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v, ++ld) {
                     const int slot = ld & (C::kStages - 1);
                     const uint32_t use = ld >> C::kStageBits;
                     if (use > 0)
@@ -210,49 +222,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                                                                     p.err, 0x62));
                     if (!ok)
                         break;
-                    const bool tail = v == 1 && valid < kTileKeys;
-                    const uint32_t bar = tail ? BAR(C::kTail) : BAR(C::kKVF + slot);
-                    const uint32_t dst = sKV + slot * C::kTileBytes;
                     if (lane == 0)
-                        ptx::mbar_arrive_expect_tx(bar, (uint32_t)(np * page * D * 2));
+                        ptx::mbar_arrive_expect_tx(BAR(C::kKVF + slot), C::kTileBytes);
                     __syncwarp();
-                    if (lane < np)
+                    if (lane < per_tile)
 #pragma unroll
                         for (int b = 0; b < C::kBoxes; ++b)
-                            ptx::tma_load_3d(dst + b * C::kBoxBytes + lane * page * 128, v ? &tm_v : &tm_k, bar, b * 64, 0, row);
-                    if (!tail) {
-                        landed[slot] = use + 1;
-                        continue;
-                    }
-                    tail_open = true;
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, tails & 1, lim_ns, abort_flag, p.err, 0x63));
-                    if (!ok)
-                        break;
-                    tail_open = false;
-                    ++tails;
-                    // rows [valid, 128), 128 bytes in each box (whole rows: the swizzle stays inside them)
-                    const int n16 = (kTileKeys - valid) * 8;
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        for (int c = lane; c < n16; c += 32)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + b * C::kBoxBytes +
-                                                                                          valid * 128 + c * 16),
-                                         "r"(0)
-                                         : "memory");
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        ptx::mbar_arrive(BAR(C::kKVF + slot));
-                    landed[slot] = 0;
+                            ptx::tma_load_3d(sKV + slot * C::kTileBytes + b * C::kBoxBytes + lane * page * 128,
+                                             v ? &tm_v : &tm_k, BAR(C::kKVF + slot), b * 64, first, row);
+                    landed[slot] = use + 1;
                 }
                 row = next_row;
+                first = next_first;
             }
         }
         // Every copy this warp started lands before the CTA can exit.
         volatile int no_abort = 0;
-        if (pieces > 0)
-            ptx::mbar_wait(BAR(C::kQF), (pieces - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
-        if (tail_open)
-            ptx::mbar_wait(BAR(C::kTail), tails & 1, lim_ns, &no_abort, p.err, 0x64);
+        for (int t = 0; t < 2; ++t)
+            if (q_use[t] > 0)
+                ptx::mbar_wait(BAR(C::kQF + t), (q_use[t] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
         for (int s = 0; s < C::kStages; ++s)
             if (landed[s])
                 ptx::mbar_wait(BAR(C::kKVF + s), (landed[s] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
@@ -266,6 +254,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const uint64_t dk0 = ptx::smem_desc_sw128(sKV, 16, 1024);
             const uint64_t dv0 = ptx::smem_desc_sw128(sKV, C::kBoxBytes, 1024);
             uint32_t ld = 0, pieces = 0, steps[2] = {0, 0};  // loads, pieces and S steps before this piece
+            uint32_t q_use[2] = {0, 0};
+            int q_slot = 0;
             bool ok = true, any = false;
             auto full = [&](uint32_t n) {  // the load numbered n has landed
                 return ptx::mbar_wait(BAR(C::kKVF + (n & (C::kStages - 1))), (n >> C::kStageBits) & 1, lim_ns, abort_flag,
@@ -303,15 +293,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const int n = f.tiles;
                 any = true;
                 // tile i's K is load ld + 2i, its V load ld + 2i + 1
-                ok = ptx::mbar_wait(BAR(C::kQF), pieces & 1, lim_ns, abort_flag, p.err, 0x70) && full(ld);
-                if (!ok)
-                    break;
-                issue_qk(0, 0, ld);
+                auto q_full = [&](int t) {
+                    return ptx::mbar_wait(BAR(C::kQF + t), q_use[t]++ & 1, lim_ns, abort_flag, p.err, 0x70);
+                };
                 if (f.two) {
+                    ok = q_full(0) && q_full(1) && full(ld);
+                    if (!ok)
+                        break;
+                    issue_qk(0, 0, ld);
                     issue_qk(1, 1, ld);
                     free_slot(ld);
+                    auto q_free = [&] {
+                        ptx::mma_commit(BAR(C::kQFree + 0));
+                        ptx::mma_commit(BAR(C::kQFree + 1));
+                    };
                     if (n == 1)
-                        ptx::mma_commit(BAR(C::kQFree));
+                        q_free();
                     if (pieces > 0)
                         ok = ptx::mbar_wait(BAR(C::kOFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x73);
                     for (int j = 0; ok && j < n; ++j) {
@@ -338,22 +335,28 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                             issue_qk(1, 1, k);
                             free_slot(k);
                             if (j + 2 == n)
-                                ptx::mma_commit(BAR(C::kQFree));  // that was the last S MMA
+                                q_free();  // that was the last S MMA
                         } else {
                             ptx::mma_commit(BAR(C::kOF + 1));
                         }
                     }
                 } else {
+                    const int q = q_slot;
+                    q_slot ^= 1;
+                    ok = q_full(q) && full(ld);
+                    if (!ok)
+                        break;
+                    issue_qk(0, q, ld);
                     free_slot(ld);
                     if (n > 1) {
                         ok = full(ld + 2);
                         if (!ok)
                             break;
-                        issue_qk(1, 0, ld + 2);
+                        issue_qk(1, q, ld + 2);
                         free_slot(ld + 2);
                     }
                     if (n <= 2)
-                        ptx::mma_commit(BAR(C::kQFree));
+                        ptx::mma_commit(BAR(C::kQFree + q));
                     if (pieces > 0)
                         ok = ptx::mbar_wait(BAR(C::kOFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x73);
                     for (int i = 0; ok && i < n; ++i) {  // tile i is step i / 2 of stream i mod 2
@@ -369,10 +372,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                             ok = full(k);
                             if (!ok)
                                 break;
-                            issue_qk(t, 0, k);
+                            issue_qk(t, q, k);
                             free_slot(k);
                             if (i + 3 == n)
-                                ptx::mma_commit(BAR(C::kQFree));
+                                ptx::mma_commit(BAR(C::kQFree + q));
                         } else {
                             ptx::mma_commit(BAR(C::kOF + t));
                         }
@@ -404,14 +407,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         while (ok && walk.next(p, TU, x)) {
             const Form f = form_of(x, TT);
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // kept maxima in log2 units, this half's sums
-            int64_t allowed[2];  // keys [0, allowed) of the segment are visible to the stream's row
+            int allowed[2];  // keys [0, allowed) of the segment are visible to the stream's row
             bool valid[2], busy[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int ti = row_tok + (f.two ? t * TT : 0);
                 valid[t] = row_tok < TT && ti < x.ntok && (f.two || t == 0);
                 const bool has = row_tok < TT && ti < x.ntok;
-                allowed[t] = has ? min(x.keys, x.see0 + ti) : 0;
+                allowed[t] = has ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + ti)) : 0;
                 busy[t] = __any_sync(0xffffffffu, has);
             }
             for (int j = 0; ok && j < f.n[0]; ++j) {
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 for (int t = 0; t < 2; ++t) {
                     if (t == 1 && j >= f.n[1])
                         continue;  // the same for every softmax thread
-                    const int64_t key0 = (x.t0 + (f.two ? j : 2 * j + t)) * kTileKeys + 64 * h;
+                    const int key0 = (x.t0 + (f.two ? j : 2 * j + t)) * kTileKeys;
                     uint32_t s[64];
                     float mx = -INFINITY;
                     bool got = true;
@@ -430,11 +433,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                             ptx::tc_fence_after();
                             ptx::tmem_ld64(tS[t] + 64 * h, s);
                             ptx::tmem_ld_wait64(s);
-                            const int64_t lim = allowed[t] - key0;
-                            if (lim < 64) {
+                            const int lim = allowed[t] - key0;  // keys of the tile that the row sees
+                            if (lim < kTileKeys) {
+                                // Column c is key c, except in the segment's last page: its keys end
+                                // where the page's box ends (see the producer).
+                                const int page = 1 << p.page_shift, held = min(kTileKeys, x.keys - key0);
+                                const int last = (held - 1) & ~(page - 1), gap = last + page - held;
+                                const int e0 = min(lim, last) - 64 * h, b1 = last + gap - 64 * h,
+                                          e1 = min(lim + gap, last + page) - 64 * h;
 #pragma unroll
                                 for (int i = 0; i < 64; ++i)
-                                    if ((int64_t)i >= lim)
+                                    if (i >= e0 && (i < b1 || i >= e1))
                                         s[i] = f2u(-INFINITY);
                             }
                             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -555,11 +564,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 if (!f.two && t == 1)
                     continue;
                 const int ti = row_tok + (f.two ? t * TT : 0);
-                const int64_t token = x.tok + ti;
+                const int token = x.tok + ti;
                 const int hq = x.head * p.G + row_g;
                 const Place d = place(p, x, worker, token, hq, ti * p.G + row_g);
                 if (valid[t] && h == 0)
-                    *(d.final_ ? p.lse + token * p.Hq + hq : d.lse) = lse[t];
+                    *(d.final_ ? p.lse + ((int64_t)token * p.Hq + hq) : d.lse) = lse[t];
                 if (!busy[t])
                     continue;  // the whole warp
 #pragma unroll 1
@@ -587,8 +596,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     }
                     if (valid[t]) {
                         if (d.final_) {
-                            uint4 *dst =
-                                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + (token * p.Hq + hq) * D + col);
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                                   ((int64_t)token * p.Hq + hq) * D + col);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 dst[i] =

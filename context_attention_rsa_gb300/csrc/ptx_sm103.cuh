@@ -440,6 +440,22 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask)
         : "memory");
 }
 
+// ---- programmatic dependent launch ---------------------------------------------
+
+// The next launch on the stream, if it was made for it, may begin before this
+// grid has ended ...
+__device__ __forceinline__ void launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ... and waits here until the grids before it have ended and their writes are
+// visible.
+__device__ __forceinline__ void wait_for_launch_before()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---- special functions ---------------------------------------------------------
 
 __device__ __forceinline__ float ex2(float x)
