@@ -76,12 +76,13 @@ __device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, int
 
 // A worker's stretch of the line, and where it begins.
 struct Stretch {
+    Segment g;     // its first segment
     int64_t off;   // its first place on that segment's line
     int64_t left;  // its places
-    int seg;       // its first segment
+    int seg;
 };
 
-// Every thread of the block (NT of them) calls this with two words of shared
+// Every thread of the block (NT of them) calls this with a word of shared
 // memory a warp.  Worker 0 leaves the plan for the joining launch: plan[s] =
 // the line's places before segment s, plan[R + 1] = total, plan[R + 2] = share.
 template <int NT>
@@ -91,60 +92,62 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int t
     constexpr int NW = NT / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nseg = p.R + 1;
-    int64_t total = 0, mine = 0;
-    for (int s = threadIdx.x; s < nseg; s += NT) {
-        mine = segment(p, s, tokens_per_unit, worker == 0).line;
-        total += mine;
+    // The line's length: with up to NT segments it falls out of the scan below.
+    int64_t total = 0;
+    if (nseg > NT) {
+        for (int s = threadIdx.x; s < nseg; s += NT)
+            total += segment(p, s, tokens_per_unit).line;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0)
+            s_sum[warp] = total;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            total += s_sum[w];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0)
-        s_sum[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w)
-        total += s_sum[w];
-    const int64_t share = (total + p.workers - 1) / p.workers;
-    const int64_t at = worker * share;
     if (threadIdx.x == 0)
-        *s_out = Stretch{0, 0, 0};
-    if (worker == 0 && threadIdx.x == 0) {
-        p.plan[p.R + 1] = total;
-        p.plan[p.R + 2] = share;
-    }
+        s_out->left = 0;
     int64_t before = 0;
     for (int s0 = 0; s0 < nseg; s0 += NT) {
         const int s = s0 + threadIdx.x;
-        if (nseg > NT)
-            mine = s < nseg ? segment(p, s, tokens_per_unit).line : 0;
-        int64_t x = s < nseg ? mine : 0;
-        const int64_t line = x;
+        Segment g;
+        g.line = 0;
+        if (s < nseg)
+            g = segment(p, s, tokens_per_unit, worker == 0);
+        int64_t x = g.line;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o)
                 x += y;
         }
-        __syncthreads();  // s_sum is free again
+        __syncthreads();  // s_sum is free
         if (lane == 31)
             s_sum[warp] = x;
         __syncthreads();
-        int64_t first = before + x - line;
+        int64_t first = before + x - g.line;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             if (w < warp)
                 first += s_sum[w];
             before += s_sum[w];
         }
-        if (worker == 0 && s < nseg)
-            p.plan[s] = first;
-        if (line > 0 && at >= first && at < first + line) {
-            s_out->seg = s;
-            s_out->off = at - first;
-            s_out->left = min(share, total - at);
+        if (nseg <= NT)
+            total = before;
+        const int64_t share = (total + p.workers - 1) / p.workers, at = worker * share;
+        if (worker == 0) {
+            if (s < nseg)
+                p.plan[s] = first;
+            if (s == p.R) {
+                p.plan[p.R + 1] = total;
+                p.plan[p.R + 2] = share;
+            }
         }
+        if (g.line > 0 && at >= first && at < first + g.line)
+            *s_out = Stretch{g, at - first, min(share, total - at), s};
     }
     __syncthreads();
     return *s_out;
@@ -168,13 +171,13 @@ struct Walk {
     int seg, head, group, at;  // at: the next place in the unit
     int64_t left;
 
-    __device__ __forceinline__ void begin(const PrefixAttnParams &p, const Stretch &st, int tokens_per_unit)
+    __device__ __forceinline__ void begin(const Stretch &st)
     {
         left = st.left;
         if (left <= 0)
             return;
         seg = st.seg;
-        g = segment(p, seg, tokens_per_unit);
+        g = st.g;
         const int64_t len = g.tiles + kUnitCost, unit = st.off / len;
         at = (int)(st.off - unit * len);
         head = (int)(unit / g.groups);

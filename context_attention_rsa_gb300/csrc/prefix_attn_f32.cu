@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     const Stretch st = find_stretch<kThreads>(p, TU, worker, s.sum, &s.st);
     ptx::launch_dependents();
     Walk walk;
-    walk.begin(p, st, TU);
+    walk.begin(st);
     Piece x;
     while (walk.next(p, TU, x)) {
         const int rows = (int)x.ntok * G;

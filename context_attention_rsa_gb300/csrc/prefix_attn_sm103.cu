@@ -37,6 +37,7 @@
 // one computes; O is written again once every softmax thread has read it.
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <cmath>
 
 #include "paged_sched.cuh"
@@ -103,6 +104,12 @@ __device__ __forceinline__ Form form_of(const Piece &x, int tokens_per_tile)
     return f;
 }
 
+// Bits [0, n) of 64, n clamped.
+__device__ __forceinline__ uint64_t columns(int n)
+{
+    return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -158,7 +165,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
 
     Walk walk;
-    walk.begin(p, st, TU);
+    walk.begin(st);
     Piece x;
 
     if (warp == C::kProducerWarp) {
@@ -407,14 +414,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         while (ok && walk.next(p, TU, x)) {
             const Form f = form_of(x, TT);
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // kept maxima in log2 units, this half's sums
-            int allowed[2];  // keys [0, allowed) of the segment are visible to the stream's row
+            // Keys [0, allowed) of the segment are visible to the stream's row.  A lane
+            // without a row need not mask anything: what it computes reaches only the
+            // same lane's O, which nobody reads.
+            int allowed[2];
             bool valid[2], busy[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int ti = row_tok + (f.two ? t * TT : 0);
                 valid[t] = row_tok < TT && ti < x.ntok && (f.two || t == 0);
                 const bool has = row_tok < TT && ti < x.ntok;
-                allowed[t] = has ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + ti)) : 0;
+                allowed[t] = has ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + ti)) : INT_MAX;
                 busy[t] = __any_sync(0xffffffffu, has);
             }
             for (int j = 0; ok && j < f.n[0]; ++j) {
@@ -439,12 +449,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                                 // where the page's box ends (see the producer).
                                 const int page = 1 << p.page_shift, held = min(kTileKeys, x.keys - key0);
                                 const int last = (held - 1) & ~(page - 1), gap = last + page - held;
-                                const int e0 = min(lim, last) - 64 * h, b1 = last + gap - 64 * h,
-                                          e1 = min(lim + gap, last + page) - 64 * h;
+                                const uint64_t seen = (columns(min(lim, last) - 64 * h) |
+                                                       (columns(min(lim + gap, last + page) - 64 * h) &
+                                                        ~columns(last + gap - 64 * h)));
+                                const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (i >= e0 && (i < b1 || i >= e1))
+                                for (int i = 0; i < 32; ++i) {
+                                    if (!(lo & (1u << i)))
                                         s[i] = f2u(-INFINITY);
+                                    if (!(hi & (1u << i)))
+                                        s[i + 32] = f2u(-INFINITY);
+                                }
                             }
                             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
