@@ -4,14 +4,15 @@
 //   segment   one set of keys and the query tokens that see it: segment 0 is
 //             the shared prefix with every token of the batch, segment 1 + r
 //             request r's own keys with its own tokens
-//   unit      up to `tokens_per_unit` consecutive tokens of a segment with all
+//   unit      up to `unit_tokens` consecutive tokens of a segment with all
 //             G query heads of one key head: the rows that share a key tile
 //   tile      128 keys of a unit
 // All tiles of all units lie on one line: segments in order, in a segment the
-// key heads, in a head the token groups, in a unit its tiles.  A unit also
-// takes kUnitCost places before its first tile, for what it costs to begin and
-// to end one, so that many short requests weigh what they take.  The line is
-// cut into `workers` equal stretches, one for each CTA, so that one long
+// key heads, in a head the token groups, in a unit its tiles.  A tile takes one
+// place, or heavy_tile of them where its unit has many rows, and a unit
+// kUnitCost places before its first tile, for what it costs to begin and to end
+// one, so that a place takes about the same time everywhere.  The line is cut
+// into `workers` equal stretches, one for each CTA, so that one long
 // request, many short ones and a prefix all fill the GPU alike.  The part of a
 // unit in a stretch is a piece; it leaves a partial (o, lse) for its rows: in
 // the rows' own place (home) if the piece begins the unit, else in the worker's
@@ -30,7 +31,7 @@ namespace rsa {
 namespace paged {
 
 constexpr int kTileKeys = 128;
-constexpr int kUnitCost = 2;  // in tiles
+constexpr int kUnitCost = 3;
 
 struct Segment {
     int tok0, ntok;        // its query tokens
@@ -38,13 +39,16 @@ struct Segment {
     const int32_t *pages;  // their pages
     int groups, tiles;     // token groups; key tiles of a unit
     int see0;              // token i of the segment sees keys [0, min(keys, see0 + i)): all of the prefix
+    int cost;              // places of a tile
     int64_t line;          // places on the line
+
+    __device__ __forceinline__ int64_t unit_line() const { return (int64_t)tiles * cost + kUnitCost; }
 };
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // Segment s, its lengths forced into the buffers (`report`: and recorded).
-__device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, int tokens_per_unit, bool report = false)
+__device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, bool report = false)
 {
     Segment g;
     const int T = (int)p.T;
@@ -68,9 +72,10 @@ __device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, int
                 record_bad_index(p.err, 0x54, n);
         }
     }
-    g.groups = (int)(((int64_t)g.ntok + tokens_per_unit - 1) / tokens_per_unit);
+    g.groups = (int)(((int64_t)g.ntok + p.unit_tokens - 1) / p.unit_tokens);
     g.tiles = (int)(((int64_t)g.keys + kTileKeys - 1) / kTileKeys);
-    g.line = g.tiles > 0 ? (int64_t)g.groups * p.Hkv * (g.tiles + kUnitCost) : 0;
+    g.cost = g.ntok > p.light_tokens ? p.heavy_tile : 1;
+    g.line = g.tiles > 0 ? (int64_t)g.groups * p.Hkv * g.unit_line() : 0;
     return g;
 }
 
@@ -86,7 +91,7 @@ struct Stretch {
 // memory a warp.  Worker 0 leaves the plan for the joining launch: plan[s] =
 // the line's places before segment s, plan[R + 1] = total, plan[R + 2] = share.
 template <int NT>
-__device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int tokens_per_unit, int worker, int64_t *s_sum,
+__device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int worker, int64_t *s_sum,
                                                 Stretch *s_out)
 {
     constexpr int NW = NT / 32;
@@ -96,7 +101,7 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int t
     int64_t total = 0;
     if (nseg > NT) {
         for (int s = threadIdx.x; s < nseg; s += NT)
-            total += segment(p, s, tokens_per_unit).line;
+            total += segment(p, s).line;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -116,7 +121,7 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int t
         Segment g;
         g.line = 0;
         if (s < nseg)
-            g = segment(p, s, tokens_per_unit, worker == 0);
+            g = segment(p, s, worker == 0);
         int64_t x = g.line;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -137,7 +142,9 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int t
         }
         if (nseg <= NT)
             total = before;
-        const int64_t share = (total + p.workers - 1) / p.workers, at = worker * share;
+        // (a stretch is never shorter than a tile, so that every one inside a unit has a piece of it)
+        const int64_t share = max((total + p.workers - 1) / p.workers, (int64_t)(p.T > p.light_tokens ? p.heavy_tile : 1));
+        const int64_t at = worker * share;
         if (worker == 0) {
             if (s < nseg)
                 p.plan[s] = first;
@@ -168,8 +175,8 @@ struct Piece {
 // Walks a worker's pieces.  Roles of a CTA that walk by themselves see the same pieces.
 struct Walk {
     Segment g;
-    int seg, head, group, at;  // at: the next place in the unit
-    int64_t left;
+    int seg, head, group;
+    int64_t at, left;  // the next place in the unit; places left
 
     __device__ __forceinline__ void begin(const Stretch &st)
     {
@@ -178,37 +185,42 @@ struct Walk {
             return;
         seg = st.seg;
         g = st.g;
-        const int64_t len = g.tiles + kUnitCost, unit = st.off / len;
-        at = (int)(st.off - unit * len);
+        const int64_t len = g.unit_line(), unit = st.off / len;
+        at = st.off - unit * len;
         head = (int)(unit / g.groups);
         group = (int)(unit - (int64_t)head * g.groups);
     }
-    __device__ __forceinline__ bool next(const PrefixAttnParams &p, int tokens_per_unit, Piece &x)
+    // The first tile that begins at place `u` of the unit or later.
+    __device__ __forceinline__ int first_tile(int64_t u) const
+    {
+        return u <= kUnitCost ? 0 : (int)((u - kUnitCost + g.cost - 1) / g.cost);
+    }
+    __device__ __forceinline__ bool next(const PrefixAttnParams &p, Piece &x)
     {
         while (left > 0) {
             if (head >= p.Hkv || g.line == 0) {
                 if (++seg > p.R)
                     return false;  // (only if the lengths changed meanwhile)
-                g = segment(p, seg, tokens_per_unit);
+                g = segment(p, seg);
                 head = group = at = 0;
                 continue;
             }
-            const int take = (int)min((int64_t)(g.tiles + kUnitCost - at), left);
-            const int i0 = group * tokens_per_unit;
+            const int64_t len = g.unit_line(), end = min(len, at + left);
+            const int i0 = group * p.unit_tokens;
             x.seg = seg;
             x.tok = g.tok0 + i0;
-            x.ntok = min(tokens_per_unit, g.ntok - i0);
+            x.ntok = min(p.unit_tokens, g.ntok - i0);
             x.head = head;
             x.keys = g.keys;
             x.pages = g.pages;
             x.see0 = seg == 0 ? g.keys : (int64_t)g.see0 + i0;
-            x.t0 = max(0, at - kUnitCost);
-            x.t1 = at + take - kUnitCost;
+            x.t0 = first_tile(at);
+            x.t1 = first_tile(end);
             x.first = x.t0 == 0;
             x.whole = x.first && x.t1 == g.tiles;
-            left -= take;
-            at += take;
-            if (at == g.tiles + kUnitCost) {
+            left -= end - at;
+            at = end;
+            if (at == len) {
                 at = 0;
                 if (++group == g.groups) {
                     group = 0;
@@ -216,33 +228,16 @@ struct Walk {
                 }
             }
             if (x.t1 > x.t0)
-                return true;  // (else the stretch ends before the unit's first tile)
+                return true;  // (else no tile begins in this part)
         }
         return false;
     }
 };
 
-// Where row (token, head hq) of a piece goes; `local` is its row in the unit.
-struct Place {
-    float *o, *lse;  // fp32 partial
-    bool final_;     // the piece is all there is for the row: straight to out and lse
-};
-
-__device__ __forceinline__ Place place(const PrefixAttnParams &p, const Piece &x, int worker, int token, int hq, int local)
+// The piece is all there is for its rows: its (o, lse) is the result.
+__device__ __forceinline__ bool is_result(const PrefixAttnParams &p, const Piece &x)
 {
-    Place d;
-    const int64_t row = (int64_t)token * p.Hq + hq;
-    d.final_ = x.seg > 0 && x.whole && p.prefix_len == 0;
-    if (x.first) {
-        const int home = x.seg > 0;
-        d.o = p.home_o[home] + row * p.d;
-        d.lse = p.home_lse[home] + row;
-    } else {
-        const int64_t slot = (int64_t)worker * kPrefixUnitRows + local;
-        d.o = p.slot_o + slot * p.d;
-        d.lse = p.slot_lse + slot;
-    }
-    return d;
+    return x.seg > 0 && x.whole && p.prefix_len == 0;
 }
 
 }  // namespace paged

@@ -67,18 +67,18 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     extern __shared__ __align__(16) unsigned char raw[];
     Smem<D> &s = *reinterpret_cast<Smem<D> *>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.G, TU = kRows / G;
+    const int G = p.G;
     const int worker = blockIdx.x;
     const float scale = 1.0f / sqrtf((float)D);
     const int page_mask = (1 << p.page_shift) - 1;
     const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
 
-    const Stretch st = find_stretch<kThreads>(p, TU, worker, s.sum, &s.st);
+    const Stretch st = find_stretch<kThreads>(p, worker, s.sum, &s.st);
     ptx::launch_dependents();
     Walk walk;
     walk.begin(st);
     Piece x;
-    while (walk.next(p, TU, x)) {
+    while (walk.next(p, x)) {
         const int rows = (int)x.ntok * G;
         __syncthreads();  // the last piece's rows are done with q
         for (int i = threadIdx.x; i < rows * D; i += kThreads) {
@@ -164,23 +164,25 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                 continue;
             const int token = x.tok + row / G;
             const int hq = x.head * G + row % G;
-            const Place d = place(p, x, worker, token, hq, row);
             const bool empty = !(l[i] > 0.f) && l[i] == l[i];
-            const float inv = empty ? 0.f : 1.f / l[i], lse = empty ? -INFINITY : m[i] + logf(l[i]);
-            if (d.final_) {
-                float *out = static_cast<float *>(p.out) + ((int64_t)token * p.Hq + hq) * D;
-#pragma unroll
-                for (int c = 0; c < PER; ++c)
-                    out[lane + 32 * c] = o[i][c] * inv;
-                if (lane == 0)
-                    p.lse[(int64_t)token * p.Hq + hq] = lse;
+            const float inv = empty ? 0.f : 1.f / l[i];
+            const int64_t at = (int64_t)token * p.Hq + hq, slot = (int64_t)worker * kPrefixUnitRows + row;
+            float *dst, *lse;
+            if (is_result(p, x)) {
+                dst = static_cast<float *>(p.out) + at * D;
+                lse = p.lse + at;
+            } else if (x.first) {
+                dst = p.home_o[x.seg > 0] + at * D;
+                lse = p.home_lse[x.seg > 0] + at;
             } else {
-#pragma unroll
-                for (int c = 0; c < PER; ++c)
-                    d.o[lane + 32 * c] = o[i][c] * inv;
-                if (lane == 0)
-                    *d.lse = lse;
+                dst = p.slot_o + slot * D;
+                lse = p.slot_lse + slot;
             }
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                dst[lane + 32 * c] = o[i][c] * inv;
+            if (lane == 0)
+                *lse = empty ? -INFINITY : m[i] + logf(l[i]);
         }
     }
 }
@@ -220,7 +222,7 @@ struct Pieces {
 // is needed; the loads of the o rows then depend on nothing.  Lane c owns
 // columns [c * PER, (c + 1) * PER).
 template <class E, int D>
-__global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_constant__ PrefixAttnParams p, int tokens_per_unit)
+__global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_constant__ PrefixAttnParams p)
 {
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_cons
     Segment g[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-        g[s] = segment(p, s == 0 ? 0 : 1 + r, tokens_per_unit);
+        g[s] = segment(p, s == 0 ? 0 : 1 + r);
     ptx::wait_for_launch_before();  // so far only the call's inputs were read
     const int64_t share = p.plan[p.R + 2], before[2] = {0, p.plan[1 + r]};
     Pieces pc[2];
@@ -245,14 +247,14 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_cons
         pc[s].n = 0;
         if (g[s].line == 0 || i < 0 || i >= g[s].ntok)
             continue;  // (outside: only where cu_q does not ascend)
-        const int64_t unit = (int64_t)head * g[s].groups + i / tokens_per_unit;
-        const int64_t at = before[s] + unit * (g[s].tiles + kUnitCost) + kUnitCost;  // the unit's first tile
-        const int64_t w0 = at / share, w1 = (at + g[s].tiles - 1) / share;
+        const int64_t unit = (int64_t)head * g[s].groups + i / p.unit_tokens;
+        const int64_t at = before[s] + unit * g[s].unit_line() + kUnitCost;  // the unit's first tile
+        const int64_t w0 = at / share, w1 = (at + (int64_t)(g[s].tiles - 1) * g[s].cost) / share;
         if (s == 1 && w0 == w1 && p.prefix_len == 0)
             return;  // one piece: it went straight to out
         pc[s].o = p.home_o[s] + row * D;
         pc[s].lse = p.home_lse[s] + row;
-        pc[s].slot = (w0 + 1) * kPrefixUnitRows + (i % tokens_per_unit) * p.G + (hq - head * p.G);
+        pc[s].slot = (w0 + 1) * kPrefixUnitRows + (i % p.unit_tokens) * p.G + (hq - head * p.G);
         pc[s].n = (int)(w1 - w0) + 1;
     }
     const int n = pc[0].n + pc[1].n;
@@ -312,19 +314,22 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_cons
 }
 
 template <int D>
-cudaError_t simt(const PrefixAttnParams &p, cudaStream_t s)
+cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
 {
+    PrefixAttnParams p = p_in;
+    p.unit_tokens = p.light_tokens = kRows / p.G;
+    p.heavy_tile = 1;
     cudaError_t e =
         cudaFuncSetAttribute(prefix_attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)
         return e;
     prefix_attn_f32_kernel<D><<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_prefix_join(p, kRows / p.G, s);
+    return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }
 
 template <class E, int D>
-cudaError_t join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s)
+cudaError_t join(const PrefixAttnParams &p, cudaStream_t s)
 {
     const int64_t blocks = (p.T * p.Hq + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL)
@@ -338,7 +343,7 @@ cudaError_t join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<E, D>, p, tokens_per_unit);
+    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<E, D>, p);
 }
 
 }  // namespace
@@ -352,12 +357,12 @@ cudaError_t launch_prefix_attn_f32(const PrefixAttnParams &p, cudaStream_t s)
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefix_join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s)
+cudaError_t launch_prefix_join(const PrefixAttnParams &p, cudaStream_t s)
 {
     if (p.d == 128)
-        return p.f32 ? join<float, 128>(p, tokens_per_unit, s) : join<__nv_bfloat16, 128>(p, tokens_per_unit, s);
+        return p.f32 ? join<float, 128>(p, s) : join<__nv_bfloat16, 128>(p, s);
     if (p.d == 64)
-        return p.f32 ? join<float, 64>(p, tokens_per_unit, s) : join<__nv_bfloat16, 64>(p, tokens_per_unit, s);
+        return p.f32 ? join<float, 64>(p, s) : join<__nv_bfloat16, 64>(p, s);
     return cudaErrorInvalidValue;
 }
 

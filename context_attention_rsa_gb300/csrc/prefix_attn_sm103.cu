@@ -14,17 +14,18 @@
 //               ahead.
 //   warp 9      one thread issues the MMAs: S_t = Q K^T from shared memory,
 //               O_t += P_t V with P in TMEM.
-//   warps 0-7   softmax on S_0 and S_1 in turn, two threads a row.
+//   warps 0-7   softmax, two threads a row (warps w and w + 4), in turn on the
+//               two S tiles in TMEM.
 // A piece runs in one of two forms, by its number of rows:
 //   two tiles   more than 128 rows: S_0 and S_1 are the two row tiles against
 //               the same key tile, as in the block kernel, so that a key tile
 //               serves 256 rows; bound by the softmax chain of each tile.
-//   one tile    up to 128 rows: S_0 and S_1 are the same rows against the even
-//               and the odd key tiles, two independent chains that keep the
-//               loads going; their (m, l, O) lie in the same TMEM lanes and are
-//               put together by the thread that owns the row.  Warps without a
-//               row of the piece only keep the barriers' count, so a decode
-//               step's few rows cost little and HBM is the bound.
+//   one tile    up to 128 rows: S_0 and S_1 take the key tiles in turn, the S
+//               MMAs two tiles ahead of PV and on into the next pieces; O_0 and
+//               O_1 take the pieces in turn, so that a piece's result is written
+//               while the next one is under way.  Warps without a row of the
+//               piece only pass the barriers on, so a decode step's few rows
+//               cost little and HBM is the bound.
 // Rows past the keys are not trusted: a score of such a key is masked, but its
 // 0 * NaN would reach O through V.  So they are never loaded: a tile's boxes of
 // pages it does not have lie outside the tensor map, which fills them with
@@ -39,6 +40,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "paged_sched.cuh"
 #include "ptx_sm103.cuh"
@@ -52,7 +54,36 @@ using namespace paged;
 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;  // log2 units the maximum may rise before O is rescaled
+constexpr int kHeavyTile = 2;     // a key tile against two row tiles takes about three times one against one (see below)
 constexpr float kLn2 = 0.69314718055994531f;
+
+// A piece as the producer hands it to the other roles.
+struct Work {
+    int tiles;            // key tiles that any of its rows sees; -1: no piece follows
+    int two;              // two row tiles against each key tile
+    int t0, keys;         // its first tile; the segment's keys
+    int64_t see0;         // unit token i sees keys [0, min(keys, see0 + i))
+    int tok, ntok, head;  // the unit's tokens and key head
+    int to;               // where its rows go: kHome + (0 prefix, 1 own), kSlot or kResult
+};
+constexpr int kHome = 0, kSlot = 2, kResult = 3;
+
+__device__ __forceinline__ Work work_of(const Piece &x, const PrefixAttnParams &p)
+{
+    const int64_t seen = min((int64_t)x.keys, x.see0 + (x.ntok - 1));
+    const int end = min(x.t1, seen > 0 ? (int)((seen + kTileKeys - 1) / kTileKeys) : 0);
+    Work w;
+    w.tiles = max(0, end - x.t0);
+    w.two = x.ntok > p.light_tokens;
+    w.t0 = x.t0;
+    w.keys = x.keys;
+    w.see0 = x.see0;
+    w.tok = x.tok;
+    w.ntok = x.ntok;
+    w.head = x.head;
+    w.to = !x.first ? kSlot : (is_result(p, x) ? kResult : kHome + (x.seg > 0));
+    return w;
+}
 
 template <int D>
 struct Cfg {
@@ -65,11 +96,14 @@ struct Cfg {
     static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
     static constexpr int kStages = D == 128 ? 4 : 8;    // a power of two: slots and phases are bits of the load's number
     static constexpr int kStageBits = D == 128 ? 2 : 3;
+    static constexpr int kPairs = kStages / 2, kPairBits = kStageBits - 1;  // a tile's K and V lie in one pair of slots
     static constexpr uint32_t kKVOff = 2 * kTileBytes;  // after the two Q tiles
     static constexpr uint32_t kBarOff = kKVOff + kStages * kTileBytes;
-    static constexpr uint32_t kXchOff = kBarOff + 256;  // [2 streams][2 halves][128 rows] maxima, then sums
+    static constexpr uint32_t kXchOff = kBarOff + 512;  // [2 S tiles][2 halves][128 rows] maxima, then sums
     static constexpr uint32_t kSumOff = kXchOff + 2 * 2048;
-    static constexpr uint32_t kSmemBytes = kSumOff + 256 + 1024;
+    static constexpr int kWork = 8;                       // pieces handed out and not yet taken by every role
+    static constexpr uint32_t kWorkOff = kSumOff + 256;   // their descriptions
+    static constexpr uint32_t kSmemBytes = kWorkOff + kWork * sizeof(Work) + 1024;
     static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
     static constexpr int kQF = 0;            // one for each Q tile
     static constexpr int kKVF = kQF + 2;
@@ -78,30 +112,31 @@ struct Cfg {
     static constexpr int kPF = kSF + 2;
     static constexpr int kOF = kPF + 2;
     static constexpr int kQFree = kOF + 2;    // one for each Q tile: every S MMA of its piece is done
-    static constexpr int kOFree = kQFree + 2; // every softmax thread has read the piece's O
-    static constexpr int kDrain = kOFree + 1;
+    static constexpr int kOFree = kQFree + 2; // one for each O: every softmax thread has read the piece's
+    static constexpr int kWF = kOFree + 2;    // a piece's description is there
+    static constexpr int kWE = kWF + kWork;   // ... has been read by the MMA thread and the softmax warps
+    static constexpr int kDrain = kWE + kWork;
     static constexpr int kNumBars = kDrain + 1;
-    static_assert(kNumBars * 8 + 8 <= 256, "barrier area");
+    static_assert(kNumBars * 8 + 8 <= 512, "barrier area");
     static_assert(sizeof(Stretch) + 8 * (kThreads / 32) <= 256, "scan area");
 };
 
-// How a piece runs; every role works it out for itself.
-struct Form {
-    int tiles;   // key tiles that any of its rows sees
-    bool two;    // two row tiles against each key tile
-    int n[2];    // steps of S_0 and S_1
-};
-
-__device__ __forceinline__ Form form_of(const Piece &x, int tokens_per_tile)
+// The two warps that share rows (w and w + 4, pair w mod 4): named barriers 2 to
+// 5, 64 threads each, returning whether `v` holds in all of them.  A pair votes
+// after every wait, so that both its warps give up together; no barrier but the
+// kernel's last one joins two pairs, which may give up at different places.
+__device__ __forceinline__ bool pair_bar_and(int pair, bool v)
 {
-    const int64_t seen = min((int64_t)x.keys, x.see0 + (x.ntok - 1));
-    const int end = min(x.t1, seen > 0 ? (int)((seen + kTileKeys - 1) / kTileKeys) : 0);
-    Form f;
-    f.tiles = max(0, end - x.t0);
-    f.two = x.ntok > tokens_per_tile;
-    f.n[0] = f.two ? f.tiles : (f.tiles + 1) >> 1;
-    f.n[1] = f.two ? f.tiles : f.tiles >> 1;
-    return f;
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\t"
+        "setp.ne.u32 pi, %1, 0;\n\t"
+        "barrier.cta.red.and.pred po, %2, 64, pi;\n\t"
+        "selp.u32 %0, 1, 0, po;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(2 + pair)
+        : "memory");
+    return r != 0;
 }
 
 // Bits [0, n) of 64, n clamped.
@@ -127,7 +162,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = blockIdx.x;
-    const int TT = 128 / p.G, TU = 2 * TT;  // tokens of a row tile and of a unit
+    const int TT = p.light_tokens;  // tokens of a row tile
     const uint64_t lim_ns = p.wait_limit_ns;
 
     if (threadIdx.x == 0) {
@@ -141,8 +176,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ptx::mbar_init(BAR(C::kOF + t), 1);
             ptx::mbar_init(BAR(C::kQF + t), 1);
             ptx::mbar_init(BAR(C::kQFree + t), 1);
+            ptx::mbar_init(BAR(C::kOFree + t), C::kSoftmaxThreads);
         }
-        ptx::mbar_init(BAR(C::kOFree), C::kSoftmaxThreads);
+        for (int i = 0; i < C::kWork; ++i) {
+            ptx::mbar_init(BAR(C::kWF + i), 1);
+            ptx::mbar_init(BAR(C::kWE + i), 1 + C::kSoftmaxThreads / 32);
+        }
         ptx::mbar_init(BAR(C::kDrain), 1);
         *abort_flag = 0;
         ptx::fence_barrier_init();
@@ -157,16 +196,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
     }
     int64_t *s_sum = reinterpret_cast<int64_t *>(gbase + C::kSumOff);
-    const Stretch st = find_stretch<C::kThreads>(p, TU, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + C::kThreads / 32));
+    const Stretch st = find_stretch<C::kThreads>(p, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + C::kThreads / 32));
     ptx::launch_dependents();  // the joining launch finds its rows' pieces while this one computes
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    Walk walk;
-    walk.begin(st);
-    Piece x;
+    Work *work = reinterpret_cast<Work *>(gbase + C::kWorkOff);
 
     if (warp == C::kProducerWarp) {
         // ============================= producer =============================
@@ -177,10 +214,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         uint32_t landed[C::kStages];  // uses of each slot
         for (int s = 0; s < C::kStages; ++s)
             landed[s] = 0;
+        uint32_t pieces = 0;
         bool ok = true;
-        while (ok && walk.next(p, TU, x)) {
-            const Form f = form_of(x, TT);
-            if (f.tiles == 0)
+        auto wait = [&](int bar, uint32_t phase, int site) {
+            return __all_sync(0xffffffffu, ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
+        };
+        Walk walk;
+        walk.begin(st);
+        Piece x;
+        for (bool more = true; ok && more; ++pieces) {
+            more = walk.next(p, x);
+            const Work f = work_of(x, p);
+            const int at = pieces % C::kWork;
+            if (pieces >= C::kWork)
+                ok = wait(C::kWE + at, pieces / C::kWork - 1, 0x65);
+            if (!ok)
+                break;
+            if (lane == 0) {
+                if (more)
+                    work[at] = f;
+                else
+                    work[at].tiles = -1;
+                ptx::mbar_arrive(BAR(C::kWF + at));
+            }
+            if (!more || f.tiles == 0)
                 continue;
             // This lane's page of a tile: its row of the maps and the row of the page
             // the box starts at.
@@ -203,8 +260,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll 1
             for (int t = q0; ok && t < q1; ++t) {
                 if (q_use[t] > 0)
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(BAR(C::kQFree + t), (q_use[t] - 1) & 1, lim_ns, abort_flag,
-                                                                p.err, 0x61));
+                    ok = wait(C::kQFree + t, q_use[t] - 1, 0x61);
                 if (!ok)
                     break;
                 if (lane == 0) {
@@ -225,8 +281,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     const int slot = ld & (C::kStages - 1);
                     const uint32_t use = ld >> C::kStageBits;
                     if (use > 0)
-                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(BAR(C::kKVE + slot), (use - 1) & 1, lim_ns, abort_flag,
-                                                                    p.err, 0x62));
+                        ok = wait(C::kKVE + slot, use - 1, 0x62);
                     if (!ok)
                         break;
                     if (lane == 0)
@@ -260,18 +315,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const uint64_t dq0 = ptx::smem_desc_sw128(sQ, 16, 1024);
             const uint64_t dk0 = ptx::smem_desc_sw128(sKV, 16, 1024);
             const uint64_t dv0 = ptx::smem_desc_sw128(sKV, C::kBoxBytes, 1024);
-            uint32_t ld = 0, pieces = 0, steps[2] = {0, 0};  // loads, pieces and S steps before this piece
-            uint32_t q_use[2] = {0, 0};
-            int q_slot = 0;
-            bool ok = true, any = false;
-            auto full = [&](uint32_t n) {  // the load numbered n has landed
-                return ptx::mbar_wait(BAR(C::kKVF + (n & (C::kStages - 1))), (n >> C::kStageBits) & 1, lim_ns, abort_flag,
-                                      p.err, 0x71);
+            uint32_t done = 0;                                          // tiles whose PV has been issued
+            uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, o_use[2] = {0, 0};  // uses of the Q tiles, of S and P, of O
+            int q_slot = 0, o_slot = 0;
+            bool ok = true;
+            auto wait = [&](int bar, uint32_t phase, int site) {
+                return ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site);
+            };
+            auto full = [&](uint32_t n) {  // the load numbered n has landed (tile i's K is load 2i, its V load 2i + 1)
+                return wait(C::kKVF + (n & (C::kStages - 1)), n >> C::kStageBits, 0x71);
             };
             auto free_slot = [&](uint32_t n) { ptx::mma_commit(BAR(C::kKVE + (n & (C::kStages - 1)))); };
-            auto issue_qk = [&](int t, int q_tile, uint32_t n) {
+            auto issue_qk = [&](int t, int q_tile, int slot) {
                 const uint64_t qa = dq0 + ((q_tile * C::kTileBytes) >> 4);
-                const uint64_t kb = dk0 + (((n & (C::kStages - 1)) * C::kTileBytes) >> 4);
+                const uint64_t kb = dk0 + ((slot * C::kTileBytes) >> 4);
                 const uint32_t dst = tmem + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
@@ -280,120 +337,159 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 }
                 ptx::mma_commit(BAR(C::kSF + t));
             };
-            auto issue_pv = [&](int t, uint32_t n, bool acc) {
-                const uint64_t vb = dv0 + (((n & (C::kStages - 1)) * C::kTileBytes) >> 4);
-                const uint32_t dst = tmem + (t ? C::kColO1 : C::kColO0);
+            auto issue_pv = [&](int o, int t, int slot, bool acc) {
+                const uint64_t vb = dv0 + ((slot * C::kTileBytes) >> 4);
+                const uint32_t dst = tmem + (o ? C::kColO1 : C::kColO0);
                 const uint32_t pa = tmem + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     ptx::mma_ts(dst, pa + kk * 8, vb + ((kk * 2048) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
             };
-            auto p_full = [&](int t, int j) {
-                const bool got = ptx::mbar_wait(BAR(C::kPF + t), (steps[t] + j) & 1, lim_ns, abort_flag, p.err, 0x72);
+            auto p_full = [&](int t) {
+                const bool got = wait(C::kPF + t, p_use[t]++, 0x72);
                 ptx::tc_fence_after();
                 return got;
             };
-            while (ok && walk.next(p, TU, x)) {
-                const Form f = form_of(x, TT);
-                if (f.tiles == 0)
-                    continue;
-                const int n = f.tiles;
-                any = true;
-                // tile i's K is load ld + 2i, its V load ld + 2i + 1
-                auto q_full = [&](int t) {
-                    return ptx::mbar_wait(BAR(C::kQF + t), q_use[t]++ & 1, lim_ns, abort_flag, p.err, 0x70);
-                };
-                if (f.two) {
-                    ok = q_full(0) && q_full(1) && full(ld);
+            // The piece that last used O has been read.
+            auto o_free = [&](int o) {
+                const uint32_t n = o_use[o]++;
+                return n == 0 || wait(C::kOFree + o, n - 1, 0x73);
+            };
+            // The piece whose S MMAs are issued, and the one whose PVs are: the first is up
+            // to two tiles ahead of the second, so at most three pieces lie after the second.
+            uint32_t taken = 0;         // descriptions read
+            int n = 0, two = 0, i = 0;  // the first's tiles (-1: none), form and tile
+            int back_n = 0, back_i = 0, ahead_n[3] = {0, 0, 0}, waiting = 0;
+            auto next_piece = [&] {
+                i = 0;
+                do {
+                    const int at = taken % C::kWork;
+                    ok = wait(C::kWF + at, taken / C::kWork, 0x75);
+                    if (!ok)
+                        return;
+                    n = work[at].tiles;
+                    two = work[at].two;
+                    ptx::mbar_arrive(BAR(C::kWE + at));
+                    ++taken;
+                } while (n == 0);
+                ahead_n[0] = waiting == 0 ? n : ahead_n[0];
+                ahead_n[1] = waiting == 1 ? n : ahead_n[1];
+                ahead_n[2] = waiting == 2 ? n : ahead_n[2];
+                ++waiting;
+            };
+            auto next_back = [&] {
+                back_i = 0;
+                back_n = ahead_n[0];
+                ahead_n[0] = ahead_n[1];
+                ahead_n[1] = ahead_n[2];
+                --waiting;
+            };
+            next_piece();
+            while (ok && n > 0) {
+                next_back();
+                if (two) {
+                    ok = wait(C::kQF + 0, q_use[0]++, 0x70) && wait(C::kQF + 1, q_use[1]++, 0x70) && full(2 * done);
                     if (!ok)
                         break;
-                    issue_qk(0, 0, ld);
-                    issue_qk(1, 1, ld);
-                    free_slot(ld);
+                    const int first = (2 * done) & (C::kStages - 1);
+                    issue_qk(0, 0, first);
+                    issue_qk(1, 1, first);
+                    free_slot(2 * done);
                     auto q_free = [&] {
                         ptx::mma_commit(BAR(C::kQFree + 0));
                         ptx::mma_commit(BAR(C::kQFree + 1));
                     };
                     if (n == 1)
                         q_free();
-                    if (pieces > 0)
-                        ok = ptx::mbar_wait(BAR(C::kOFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x73);
-                    for (int j = 0; ok && j < n; ++j) {
-                        const uint32_t v = ld + 2 * j + 1, k = v + 1;
+                    ok = o_free(0) && o_free(1);
+                    // One step with its slots known at compile time: K(j) and V(j) are in
+                    // pair `kPair` of the ring, K(j + 1) in the next one, so that the MMAs'
+                    // descriptors are constants of the kernel (3% faster than computed ones).
+                    auto step = [&](auto pair, int j) -> bool {
+                        constexpr int kPair = decltype(pair)::value, kV = 2 * kPair + 1, kK = 2 * ((kPair + 1) % C::kPairs);
+                        const uint32_t tile = done + j;
                         const bool more = j + 1 < n;
-                        ok = full(v) && p_full(0, j);
-                        if (!ok)
-                            break;
-                        issue_pv(0, v, j > 0);
+                        if (!wait(C::kKVF + kV, tile >> C::kPairBits, 0x71) || !p_full(0))
+                            return false;
+                        issue_pv(0, 0, kV, j > 0);
                         if (more) {
-                            ok = full(k);
-                            if (!ok)
-                                break;
-                            issue_qk(0, 0, k);
+                            if (!wait(C::kKVF + kK, (tile + 1) >> C::kPairBits, 0x71))
+                                return false;
+                            issue_qk(0, 0, kK);
                         } else {
                             ptx::mma_commit(BAR(C::kOF + 0));
                         }
-                        ok = p_full(1, j);
-                        if (!ok)
-                            break;
-                        issue_pv(1, v, j > 0);
-                        free_slot(v);
+                        if (!p_full(1))
+                            return false;
+                        issue_pv(1, 1, kV, j > 0);
+                        ptx::mma_commit(BAR(C::kKVE + kV));
                         if (more) {
-                            issue_qk(1, 1, k);
-                            free_slot(k);
+                            issue_qk(1, 1, kK);
+                            ptx::mma_commit(BAR(C::kKVE + kK));
                             if (j + 2 == n)
                                 q_free();  // that was the last S MMA
                         } else {
                             ptx::mma_commit(BAR(C::kOF + 1));
                         }
+                        return true;
+                    };
+                    for (int j = 0; ok && j < n; ++j) {
+                        const int pair = (done + j) & (C::kPairs - 1);
+                        if (pair == 0)
+                            ok = step(std::integral_constant<int, 0>(), j);
+                        else if (pair == 1)
+                            ok = step(std::integral_constant<int, 1>(), j);
+                        else if (pair == 2)
+                            ok = step(std::integral_constant<int, 2 % C::kPairs>(), j);
+                        else
+                            ok = step(std::integral_constant<int, 3 % C::kPairs>(), j);
                     }
-                } else {
-                    const int q = q_slot;
-                    q_slot ^= 1;
-                    ok = q_full(q) && full(ld);
-                    if (!ok)
-                        break;
-                    issue_qk(0, q, ld);
-                    free_slot(ld);
-                    if (n > 1) {
-                        ok = full(ld + 2);
+                    done += n;
+                    if (ok)
+                        next_piece();
+                    continue;
+                }
+                // A run of one-tile pieces: S MMAs run two tiles ahead of PV, over the
+                // pieces' borders.
+                uint32_t ahead = done;  // tiles whose S has been issued
+                while (ok) {
+                    while (ok && ahead - done < 2 && n > 0 && !two) {
+                        if (i == 0)
+                            ok = wait(C::kQF + q_slot, q_use[q_slot]++, 0x70);
+                        ok = ok && full(2 * ahead);
                         if (!ok)
                             break;
-                        issue_qk(1, q, ld + 2);
-                        free_slot(ld + 2);
-                    }
-                    if (n <= 2)
-                        ptx::mma_commit(BAR(C::kQFree + q));
-                    if (pieces > 0)
-                        ok = ptx::mbar_wait(BAR(C::kOFree), (pieces - 1) & 1, lim_ns, abort_flag, p.err, 0x73);
-                    for (int i = 0; ok && i < n; ++i) {  // tile i is step i / 2 of stream i mod 2
-                        const int t = i & 1;
-                        const uint32_t v = ld + 2 * i + 1;
-                        ok = full(v) && p_full(t, i >> 1);
-                        if (!ok)
-                            break;
-                        issue_pv(t, v, i > 1);
-                        free_slot(v);
-                        if (i + 2 < n) {
-                            const uint32_t k = ld + 2 * (i + 2);
-                            ok = full(k);
-                            if (!ok)
-                                break;
-                            issue_qk(t, q, k);
-                            free_slot(k);
-                            if (i + 3 == n)
-                                ptx::mma_commit(BAR(C::kQFree + q));
-                        } else {
-                            ptx::mma_commit(BAR(C::kOF + t));
+                        issue_qk(ahead & 1, q_slot, (2 * ahead) & (C::kStages - 1));
+                        free_slot(2 * ahead);
+                        ++ahead;
+                        if (++i == n) {
+                            ptx::mma_commit(BAR(C::kQFree + q_slot));
+                            q_slot ^= 1;
+                            next_piece();
                         }
                     }
+                    if (!ok)
+                        break;
+                    const int t = done & 1;
+                    const uint32_t v = 2 * done + 1;
+                    if (back_i == 0)
+                        ok = o_free(o_slot);
+                    ok = ok && full(v) && p_full(t);
+                    if (!ok)
+                        break;
+                    issue_pv(o_slot, t, v & (C::kStages - 1), back_i > 0);
+                    free_slot(v);
+                    ++done;
+                    if (++back_i == back_n) {
+                        ptx::mma_commit(BAR(C::kOF + o_slot));
+                        o_slot ^= 1;
+                        if (ahead == done && !(n > 0 && !two))
+                            break;  // the run is over; the next piece begins above
+                        next_back();
+                    }
                 }
-                ld += 2 * n;
-                steps[0] += f.n[0];
-                steps[1] += f.n[1];
-                ++pieces;
             }
-            if (any) {
+            if (q_use[0] + q_use[1] > 0) {
                 // Every MMA this thread issued has finished before TMEM is freed.
                 ptx::mma_commit(BAR(C::kDrain));
                 volatile int no_abort = 0;
@@ -405,233 +501,280 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         // ============================== softmax ==============================
         const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // half of the keys and columns, row of the tile
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS[2] = {lanes + C::kColS0, lanes + C::kColS1}, tO[2] = {lanes + C::kColO0, lanes + C::kColO1};
         float *xch = reinterpret_cast<float *>(gbase + C::kXchOff), *xl = xch + 512;
         const float sl2 = 1.4426950408889634f / sqrtf((float)D);  // log2(e) / sqrt(d)
         const int row_tok = row / p.G, row_g = row - row_tok * p.G;
-        uint32_t steps[2] = {0, 0}, drains[2] = {0, 0};
+        uint32_t done = 0;                                // tiles before this piece
+        uint32_t s_use0 = 0, s_use1 = 0, o_use0 = 0, o_use1 = 0;  // uses of S and of O before now
+        int o_slot = 0;
         bool ok = true;
-        while (ok && walk.next(p, TU, x)) {
-            const Form f = form_of(x, TT);
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // kept maxima in log2 units, this half's sums
-            // Keys [0, allowed) of the segment are visible to the stream's row.  A lane
-            // without a row need not mask anything: what it computes reaches only the
-            // same lane's O, which nobody reads.
-            int allowed[2];
-            bool valid[2], busy[2];
+        auto wait = [&](int bar, uint32_t phase, int site) {
+            return __all_sync(0xffffffffu, ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
+        };
+
+        // What a thread keeps of a row's tiles so far.
+        struct Row {
+            float m, l;   // kept maximum in log2 units, this half's sum
+            int allowed;  // keys [0, allowed) of the segment are visible
+        };
+        // Scores of this thread's 64 keys of a tile, masked; their maximum goes to the other half.
+        auto scores = [&](int t, int key0, const Row &r, int keys, uint32_t *s) -> float {
+            ptx::tc_fence_after();
+            ptx::tmem_ld64(lanes + (t ? C::kColS1 : C::kColS0) + 64 * h, s);
+            ptx::tmem_ld_wait64(s);
+            const int lim = r.allowed - key0;  // keys of the tile that the row sees
+            if (lim < kTileKeys) {
+                // Column c is key c, except in the segment's last page: its keys end
+                // where the page's box ends (see the producer).
+                const int page = 1 << p.page_shift, held = min(kTileKeys, keys - key0);
+                const int last = (held - 1) & ~(page - 1), gap = last + page - held;
+                const uint64_t seen =
+                    columns(min(lim, last) - 64 * h) |
+                    (columns(min(lim + gap, last + page) - 64 * h) & ~columns(last + gap - 64 * h));
+                const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int ti = row_tok + (f.two ? t * TT : 0);
-                valid[t] = row_tok < TT && ti < x.ntok && (f.two || t == 0);
-                const bool has = row_tok < TT && ti < x.ntok;
-                allowed[t] = has ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + ti)) : INT_MAX;
-                busy[t] = __any_sync(0xffffffffu, has);
+                for (int i = 0; i < 32; ++i) {
+                    if (!(lo & (1u << i)))
+                        s[i] = f2u(-INFINITY);
+                    if (!(hi & (1u << i)))
+                        s[i + 32] = f2u(-INFINITY);
+                }
             }
-            for (int j = 0; ok && j < f.n[0]; ++j) {
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t == 1 && j >= f.n[1])
-                        continue;  // the same for every softmax thread
-                    const int key0 = (x.t0 + (f.two ? j : 2 * j + t)) * kTileKeys;
+            for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    m4[k] = fmax3(m4[k], u2f(s[i + 2 * k]), u2f(s[i + 2 * k + 1]));
+            }
+            const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+            xch[(t * 2 + h) * 128 + row] = mx;
+            return mx;
+        };
+        // The maximum moves only when it grows by more than kRescale: O and l are then
+        // multiplied by what 2^-m became (O only if a PV has written it: `old_o`).
+        auto raise = [&](Row &r, float mx, uint32_t tO, bool old_o) {
+            const float mnew = mx * sl2;
+            const bool need = mnew > -INFINITY && (r.m == -INFINITY || mnew > r.m + kRescale);
+            if (!__any_sync(0xffffffffu, need))
+                return;
+            float alpha = 1.f;
+            if (need) {
+                alpha = r.m == -INFINITY ? 0.f : ptx::ex2(r.m - mnew);
+                r.l *= alpha;
+                r.m = mnew;
+            }
+            if (old_o) {
+                const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                for (int k = 0; k < D / 64; ++k) {
+                    uint32_t o[32];
+                    const uint32_t ta = tO + h * (D / 2) + k * 32;
+                    ptx::tmem_ld32(ta, o);
+                    ptx::tmem_ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = __fmul2_rn(make_float2(u2f(o[i]), u2f(o[i + 1])), a2);
+                        o[i] = f2u(y.x);
+                        o[i + 1] = f2u(y.y);
+                    }
+                    ptx::tmem_st32(ta, o);
+                }
+            }
+        };
+        // p = 2^(s log2(e) / sqrt(d) - m), rounded to bf16 for the MMA (the sum l takes
+        // them in fp32); keys [64h, 64h + 64) go to packed columns [32h, 32h + 32) over S.
+        auto probabilities = [&](int t, Row &r, const uint32_t *s) {
+            const float neg = r.m == -INFINITY ? 0.f : -r.m;
+            const float2 c2 = make_float2(sl2, sl2), n2 = make_float2(neg, neg);
+            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float2 y = __ffma2_rn(make_float2(u2f(s[2 * i]), u2f(s[2 * i + 1])), c2, n2);
+                const float p0 = ptx::ex2(y.x), p1 = ptx::ex2(y.y);
+                acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+                pk[i] = pack_bf16(p0, p1);
+            }
+            ptx::tmem_st32(lanes + (t ? C::kColS1 : C::kColS0) + 32 * h, pk);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(BAR(C::kPF + t));
+            const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+            r.l += a.x + a.y;
+        };
+        // Where a row's result goes.
+        struct Out {
+            void *o;
+            float *lse;
+            float m, l;
+            bool valid;
+        };
+        auto out_of = [&](const Work &x, int ti, const Row &r) {
+            const int token = x.tok + ti, hq = x.head * p.G + row_g;
+            const int64_t at = (int64_t)token * p.Hq + hq, slot = (int64_t)worker * kPrefixUnitRows + (ti * p.G + row_g);
+            Out d;
+            if (x.to == kResult) {
+                d.o = static_cast<__nv_bfloat16 *>(p.out) + at * D;
+                d.lse = p.lse + at;
+            } else if (x.to == kSlot) {
+                d.o = p.slot_o + slot * D;
+                d.lse = p.slot_lse + slot;
+            } else {
+                d.o = p.home_o[x.to] + at * D;
+                d.lse = p.home_lse[x.to] + at;
+            }
+            d.m = r.m;
+            d.l = r.l;
+            d.valid = row_tok < TT && ti < x.ntok;
+            return d;
+        };
+
+        // The last piece's rows, whose O is still being computed while the next piece's
+        // first scores are: written after those.  One copy of this and of the step
+        // below serves both forms (code that is cold costs more than it computes).
+        struct {
+            Out out, second;  // second: the second row tile's
+            int slot, n;      // first O; row tiles
+            bool on, has_o, bf16;
+        } late;
+        late.on = false;
+        auto write_late = [&]() -> bool {
+            late.on = false;
+#pragma unroll 1
+            for (int e = 0; e < late.n; ++e, late.out = late.second, late.slot ^= 1) {
+                const Out &out = late.out;
+                const bool any = __any_sync(0xffffffffu, out.valid);
+                float l = out.l;
+                if (late.has_o) {
+                    const bool got = wait(C::kOF + late.slot, late.slot ? o_use1++ : o_use0++, 0x81);
+                    xl[(e * 2 + h) * 128 + row] = l;
+                    if (!pair_bar_and(warp & 3, got))
+                        return false;
+                    ptx::tc_fence_after();
+                    l += xl[(e * 2 + (h ^ 1)) * 128 + row];
+                }
+                const bool empty = !(l > 0.f) && l == l;
+                const float inv = empty ? 0.f : 1.f / l;
+                if (out.valid && h == 0)
+                    *out.lse = empty ? -INFINITY : (out.m + ptx::lg2(l)) * kLn2;
+                if (any) {
+#pragma unroll 1
+                    for (int k = 0; k < D / 64; ++k) {
+                        const int col = h * (D / 2) + k * 32;
+                        uint32_t o[32];
+                        if (late.has_o) {
+                            ptx::tmem_ld32(lanes + (late.slot ? C::kColO1 : C::kColO0) + col, o);
+                            ptx::tmem_ld_wait(o);
+                        }
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = late.has_o ? u2f(o[i]) * inv : 0.f;
+                        if (out.valid) {
+                            if (late.bf16) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out.o) + col);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    dst[i] =
+                                        make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                                   pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                            } else {
+                                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out.o) + col);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (late.has_o) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(BAR(C::kOFree + late.slot));
+                }
+            }
+            return true;
+        };
+
+        for (uint32_t pieces = 0; ok; ++pieces) {
+            const int at = pieces % C::kWork;
+            ok = pair_bar_and(warp & 3, wait(C::kWF + at, pieces / C::kWork, 0x83));
+            if (!ok)
+                break;
+            const Work f = work[at];
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(BAR(C::kWE + at));
+            const int tiles = max(f.tiles, 0), steps = f.two ? 2 * tiles : tiles;
+            // The row of this step's tile and, in the form with two tiles, of the other
+            // one: they change places after every step.
+            Row cur, other;
+            auto row_of = [&](int ti) {
+                // A lane without a row need not mask anything: what it computes reaches
+                // only the same lane's O, which nobody reads.
+                const bool has = row_tok < TT && ti < f.ntok;
+                return Row{-INFINITY, 0.f, has ? (int)max((int64_t)0, min((int64_t)f.keys, f.see0 + ti)) : INT_MAX};
+            };
+            cur = row_of(row_tok);
+            other = f.two ? row_of(row_tok + TT) : cur;
+#pragma unroll 1
+            for (int k = 0; ok && k < max(steps, 1); ++k) {
+                if (steps > 0) {
+                    const int j = f.two ? k >> 1 : k;  // tile of the piece
+                    const int t = f.two ? k & 1 : (done + k) & 1;
+                    const bool busy = __any_sync(0xffffffffu, cur.allowed != INT_MAX);
                     uint32_t s[64];
                     float mx = -INFINITY;
-                    bool got = true;
-                    if (busy[t]) {
-                        got = ptx::mbar_wait(BAR(C::kSF + t), (steps[t] + j) & 1, lim_ns, abort_flag, p.err, 0x80);
-                        got = __all_sync(0xffffffffu, got);
-                        if (got) {
-                            ptx::tc_fence_after();
-                            ptx::tmem_ld64(tS[t] + 64 * h, s);
-                            ptx::tmem_ld_wait64(s);
-                            const int lim = allowed[t] - key0;  // keys of the tile that the row sees
-                            if (lim < kTileKeys) {
-                                // Column c is key c, except in the segment's last page: its keys end
-                                // where the page's box ends (see the producer).
-                                const int page = 1 << p.page_shift, held = min(kTileKeys, x.keys - key0);
-                                const int last = (held - 1) & ~(page - 1), gap = last + page - held;
-                                const uint64_t seen = (columns(min(lim, last) - 64 * h) |
-                                                       (columns(min(lim + gap, last + page) - 64 * h) &
-                                                        ~columns(last + gap - 64 * h)));
-                                const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    if (!(lo & (1u << i)))
-                                        s[i] = f2u(-INFINITY);
-                                    if (!(hi & (1u << i)))
-                                        s[i + 32] = f2u(-INFINITY);
-                                }
-                            }
-                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int i = 0; i < 64; i += 8) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    m4[k] = fmax3(m4[k], u2f(s[i + 2 * k]), u2f(s[i + 2 * k + 1]));
-                            }
-                            mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-                            xch[(t * 2 + h) * 128 + row] = mx;
-                        }
-                    }
-                    // Both halves of every row have read S (and know whether every wait
-                    // succeeded) before P is written over it.
+                    const bool got = wait(C::kSF + t, t ? s_use1++ : s_use0++, 0x80);
+                    if (got && busy)
+                        mx = scores(t, (f.t0 + j) * kTileKeys, cur, f.keys, s);
+                    // Both halves of the rows have read S before P is written over it.
                     ptx::tc_fence_before();
-                    ok = softmax_bar_and<256>(got);
+                    ok = pair_bar_and(warp & 3, got);
                     ptx::tc_fence_after();
                     if (!ok)
                         break;
-                    if (busy[t]) {
+                    if (busy) {
                         mx = fmaxf(mx, xch[(t * 2 + (h ^ 1)) * 128 + row]);
-                        const float mnew = mx * sl2;
-                        const bool need = mnew > -INFINITY && (m[t] == -INFINITY || mnew > m[t] + kRescale);
-                        if (__any_sync(0xffffffffu, need)) {
-                            float alpha = 1.f;
-                            if (need) {
-                                alpha = m[t] == -INFINITY ? 0.f : ptx::ex2(m[t] - mnew);
-                                l[t] *= alpha;
-                                m[t] = mnew;
-                            }
-                            if (j > 0) {
-                                // the commit that signalled this S also covered the PV before it: O is stable
-                                const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll 1
-                                for (int k = 0; k < D / 64; ++k) {
-                                    uint32_t o[32];
-                                    const uint32_t ta = tO[t] + h * (D / 2) + k * 32;
-                                    ptx::tmem_ld32(ta, o);
-                                    ptx::tmem_ld_wait(o);
-#pragma unroll
-                                    for (int i = 0; i < 32; i += 2) {
-                                        const float2 r = __fmul2_rn(make_float2(u2f(o[i]), u2f(o[i + 1])), a2);
-                                        o[i] = f2u(r.x);
-                                        o[i + 1] = f2u(r.y);
-                                    }
-                                    ptx::tmem_st32(ta, o);
-                                }
-                            }
+                        if (j > 0 && !f.two && __any_sync(0xffffffffu, mx * sl2 > cur.m + kRescale)) {
+                            // O may still be under the PV of the tile before: that one frees its V
+                            // slot.  (With two tiles the commit that signalled this S covers it.)
+                            const uint32_t v = 2 * (done + j) - 1;
+                            ok = pair_bar_and(warp & 3, wait(C::kKVE + (v & (C::kStages - 1)), v >> C::kStageBits, 0x82));
+                            if (!ok)
+                                break;
+                            ptx::tc_fence_after();
                         }
-                        // p = 2^(s log2(e) / sqrt(d) - m), rounded to bf16 for the MMA (the sum l keeps
-                        // them in fp32); keys [64h, 64h + 64) go to packed columns [32h, 32h + 32).
-                        const float neg = m[t] == -INFINITY ? 0.f : -m[t];
-                        const float2 c2 = make_float2(sl2, sl2), n2 = make_float2(neg, neg);
-                        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                         make_float2(0.f, 0.f)};
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float2 y = __ffma2_rn(make_float2(u2f(s[2 * i]), u2f(s[2 * i + 1])), c2, n2);
-                            const float p0 = ptx::ex2(y.x), p1 = ptx::ex2(y.y);
-                            acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
-                            pk[i] = pack_bf16(p0, p1);
-                        }
-                        ptx::tmem_st32(tS[t] + 32 * h, pk);
-                        ptx::tmem_st_wait();
-                        ptx::tc_fence_before();
-                        ptx::mbar_arrive(BAR(C::kPF + t));
-                        const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-                        l[t] += a.x + a.y;
+                        const int o = f.two ? t : o_slot;
+                        raise(cur, mx, lanes + (o ? C::kColO1 : C::kColO0), j > 0);
+                        probabilities(t, cur, s);
                     } else {
                         // (rows of P that nobody wrote only reach the same rows of O)
                         ptx::mbar_arrive(BAR(C::kPF + t));
                     }
+                    if (f.two) {
+                        const Row r = cur;
+                        cur = other;
+                        other = r;
+                    }
                 }
+                if (k == 0 && late.on)
+                    ok = write_late();
             }
-            if (!ok)
+            if (!ok || f.tiles < 0)
                 break;
-            // ---- the piece's (o, lse) ----
-            bool fin = true;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (f.n[t] > 0) {
-                    fin = fin && ptx::mbar_wait(BAR(C::kOF + t), drains[t] & 1, lim_ns, abort_flag, p.err, 0x81);
-                    fin = __all_sync(0xffffffffu, fin);
-                    ++drains[t];
-                    steps[t] += f.n[t];
-                    xl[(t * 2 + h) * 128 + row] = l[t];
-                }
-            ok = softmax_bar_and<256>(fin);
-            if (!ok)
-                break;
-            ptx::tc_fence_after();
-            float inv[2] = {0.f, 0.f}, lse[2];  // weights of the unnormalised O, and the results' lse
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (f.n[t] > 0)
-                    l[t] += xl[(t * 2 + (h ^ 1)) * 128 + row];
-            if (f.two) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const bool empty = !(l[t] > 0.f) && l[t] == l[t];
-                    inv[t] = empty ? 0.f : 1.f / l[t];
-                    lse[t] = empty ? -INFINITY : (m[t] + ptx::lg2(l[t])) * kLn2;
-                }
-            } else {
-                const float M = fmaxf(m[0], m[1]);
-                const float w0 = m[0] == -INFINITY ? 0.f : ptx::ex2(m[0] - M), w1 = m[1] == -INFINITY ? 0.f : ptx::ex2(m[1] - M);
-                const float L = l[0] * w0 + l[1] * w1;
-                const bool empty = !(L > 0.f) && L == L;
-                inv[0] = empty ? 0.f : w0 / L;
-                inv[1] = empty ? 0.f : w1 / L;
-                lse[0] = empty ? -INFINITY : (M + ptx::lg2(L)) * kLn2;
-                lse[1] = -INFINITY;
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (!f.two && t == 1)
-                    continue;
-                const int ti = row_tok + (f.two ? t * TT : 0);
-                const int token = x.tok + ti;
-                const int hq = x.head * p.G + row_g;
-                const Place d = place(p, x, worker, token, hq, ti * p.G + row_g);
-                if (valid[t] && h == 0)
-                    *(d.final_ ? p.lse + ((int64_t)token * p.Hq + hq) : d.lse) = lse[t];
-                if (!busy[t])
-                    continue;  // the whole warp
-#pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
-                    const int col = h * (D / 2) + k * 32;
-                    float v[32];
-                    uint32_t o[32];
-                    if (f.n[t] > 0) {
-                        ptx::tmem_ld32(tO[t] + col, o);
-                        ptx::tmem_ld_wait(o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = u2f(o[i]) * inv[t];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = 0.f;
-                    }
-                    if (!f.two && f.n[1] > 0) {
-                        ptx::tmem_ld32(tO[1] + col, o);
-                        ptx::tmem_ld_wait(o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = fmaf(u2f(o[i]), inv[1], v[i]);
-                    }
-                    if (valid[t]) {
-                        if (d.final_) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                                   ((int64_t)token * p.Hq + hq) * D + col);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                dst[i] =
-                                    make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                               pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(d.o + col);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        }
-                    }
-                    __syncwarp();
-                }
-            }
-            if (f.tiles > 0) {
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(BAR(C::kOFree));
-            }
+            done += tiles;
+            late.out = out_of(f, row_tok, cur);
+            if (f.two)
+                late.second = out_of(f, row_tok + TT, other);
+            late.n = f.two ? 2 : 1;
+            late.slot = f.two ? 0 : o_slot;
+            late.has_o = tiles > 0;
+            late.bf16 = f.to == kResult;
+            late.on = true;
+            if (tiles > 0 && !f.two)
+                o_slot ^= 1;
         }
     }
 
@@ -644,9 +787,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch(const PrefixAttnParams &p, cudaStream_t s)
+cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
 {
+    PrefixAttnParams p = p_in;
     const int TT = 128 / p.G;
+    p.unit_tokens = 2 * TT;
+    p.light_tokens = TT;
+    p.heavy_tile = kHeavyTile;
     CUtensorMap mq, mk, mv;
     const int64_t page = 1ll << p.page_shift;
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.T};
@@ -664,7 +811,7 @@ cudaError_t launch(const PrefixAttnParams &p, cudaStream_t s)
         return e;
     prefix_attn_kernel<D><<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_prefix_join(p, 2 * TT, s);
+    return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }
 
 }  // namespace

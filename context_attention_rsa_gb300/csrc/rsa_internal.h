@@ -198,7 +198,11 @@ struct PrefixAttnParams {
     int64_t *plan;               // [R + 3]
     float *home_o[2], *home_lse[2];  // [T * Hq, d] and [T * Hq]: a row's first piece of the prefix, of its own keys
     float *slot_o, *slot_lse;    // [workers, 256, d] and [workers, 256]: a worker's first piece, begun by another
+    // how the launcher's kernel cuts the work
     int workers;
+    int unit_tokens;             // query tokens of a unit at most
+    int light_tokens;            // a unit of more tokens than this costs heavy_tile a key tile, not 1
+    int heavy_tile;
     uint64_t wait_limit_ns;
     unsigned int *err;
 };
@@ -224,7 +228,7 @@ constexpr int kNormRopeBwdBlocks = 608;  // blocks of partial weight gradients: 
 cudaError_t launch_prefix_attn_bf16(const PrefixAttnParams &p, cudaStream_t s);
 cudaError_t launch_prefix_attn_f32(const PrefixAttnParams &p, cudaStream_t s);
 // Joins the pieces of every row: the second launch of the attention.
-cudaError_t launch_prefix_join(const PrefixAttnParams &p, int tokens_per_unit, cudaStream_t s);
+cudaError_t launch_prefix_join(const PrefixAttnParams &p, cudaStream_t s);
 cudaError_t launch_selftest_wait(uint64_t limit_ns, unsigned int *err, cudaStream_t s);
 // Two-pass ring self-attention (bf16, d = 128, T/N a multiple of 128): per
 // query chunk, score pass into S [BH, Tc, T] fp32 (and per-tile row
