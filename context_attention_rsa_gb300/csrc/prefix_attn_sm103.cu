@@ -9,9 +9,9 @@
 //   warp 8      producer: the piece's query rows (one 4-D TMA box a 128-row
 //               tile: G heads of floor(128 / G) tokens, so any group size is
 //               loaded without a gather), then K and V tiles through a ring of
-//               shared-memory slots, one TMA box a page and 64 columns, each
-//               lane loading the page whose id it read from the table one tile
-//               ahead.
+//               shared-memory slots, one TMA box a page, each lane loading the
+//               page whose id it read from the table one tile ahead.  It also
+//               walks the work for the others and hands them each piece.
 //   warp 9      one thread issues the MMAs: S_t = Q K^T from shared memory,
 //               O_t += P_t V with P in TMEM.
 //   warps 0-7   softmax, two threads a row (warps w and w + 4), in turn on the
@@ -27,12 +27,12 @@
 //               piece only pass the barriers on, so a decode step's few rows
 //               cost little and HBM is the bound.
 // Rows past the keys are not trusted: a score of such a key is masked, but its
-// 0 * NaN would reach O through V.  So they are never loaded: a tile's boxes of
-// pages it does not have lie outside the tensor map, which fills them with
-// zeros, and the box of a page that is v < page keys long starts v - page rows
-// before the page, so that its first page - v rows are zeros and its keys end
-// where the box ends.  The softmax masks those columns; the keys' order within
-// a tile does not matter to it.
+// 0 * NaN would reach O through V.  So they are never loaded: the segment's last,
+// shorter tile is brought in groups of 8 rows; groups without keys lie outside the
+// tensor map, which fills them with zeros, and the box of a group of v < 8 keys
+// starts 8 - v rows early, on keys that are there already or before the page, on
+// zeros.  The softmax masks those columns; the keys' order within a tile does not
+// matter to it.
 // The phases of all barriers run on over the CTA's pieces; one-tile pieces take
 // the two Q tiles in turn, so that the next piece's loads are under way while
 // one computes; O is written again once every softmax thread has read it.
@@ -91,9 +91,14 @@ struct Cfg {
     static constexpr int kProducerWarp = 8;
     static constexpr int kMmaWarp = 9;
     static constexpr int kThreads = 320;
-    static constexpr int kBoxes = D / 64;               // 128-byte-wide boxes of a tile
-    static constexpr uint32_t kBoxBytes = 128u * 128u;  // 128 rows x 128 bytes
-    static constexpr uint32_t kTileBytes = kBoxes * kBoxBytes;
+    static constexpr int kHalves = D / 64;              // 128-byte halves of a row
+    static constexpr uint32_t kTileBytes = kHalves * 128u * 128u;
+    // A Q tile is two (d = 64: one) boxes of 128 rows x 128 bytes.  A K or V tile is
+    // made of groups of 8 rows, the group's first halves and then its second ones (8
+    // rows x 128 bytes each, a swizzle atom): so one box brings a whole page, in the
+    // order it lies in memory, and the MMA still finds each half's atoms evenly spaced.
+    static constexpr uint32_t kQBoxBytes = 128u * 128u;
+    static constexpr uint32_t kGroupBytes = kHalves * 1024u;
     static constexpr int kStages = D == 128 ? 4 : 8;    // a power of two: slots and phases are bits of the load's number
     static constexpr int kStageBits = D == 128 ? 2 : 3;
     static constexpr int kPairs = kStages / 2, kPairBits = kStageBits - 1;  // a tile's K and V lie in one pair of slots
@@ -148,7 +153,8 @@ __device__ __forceinline__ uint64_t columns(int n)
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefixAttnParams p)
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k8,
+                       const __grid_constant__ CUtensorMap tm_v8, const __grid_constant__ PrefixAttnParams p)
 {
     using C = Cfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -239,23 +245,27 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             }
             if (!more || f.tiles == 0)
                 continue;
-            // This lane's page of a tile: its row of the maps and the row of the page
-            // the box starts at.
-            auto page_row = [&](int tile, int &first) -> int {
-                const int left = x.keys - tile * kTileKeys - (lane << p.page_shift);  // keys from this page on
-                first = left < page ? left - page : 0;
-                if (lane >= per_tile || left <= 0) {
-                    first = 0;
-                    return none;
-                }
-                const int id = x.pages[tile * per_tile + lane];
+            // What this lane loads of a tile: a page of a full tile, a group of 8 rows of
+            // the segment's last, shorter one.
+            auto find = [&](int tile, int &row, int &first) {
+                const int held = min(kTileKeys, x.keys - tile * kTileKeys);
+                const int step = held < kTileKeys ? 8 : page, key = lane * step;
+                row = none;
+                first = 0;
+                if (key >= held)
+                    return;  // (a group without keys: zeros)
+                const int id = x.pages[tile * per_tile + (key >> p.page_shift)];
                 if (id < 0 || id >= p.n_pages) {
                     record_bad_index(p.err, 0x55, id);
-                    return none;
+                    return;
                 }
-                return id * p.Hkv + x.head;
+                row = id * p.Hkv + x.head;
+                // a group of v < 8 keys ends with them: its box starts 8 - v rows early, on
+                // rows of the same page or, before its first, on zeros
+                first = (key & (page - 1)) - max(0, key + 8 - held);
             };
-            int first, row = page_row(x.t0, first);
+            int first, row;
+            find(x.t0, row, first);
             const int q0 = f.two ? 0 : q_slot, q1 = f.two ? 2 : q_slot + 1;
 #pragma unroll 1
             for (int t = q0; ok && t < q1; ++t) {
@@ -264,9 +274,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 if (!ok)
                     break;
                 if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(BAR(C::kQF + t), (uint32_t)(C::kBoxes * 128 * p.G * TT));
-                    for (int b = 0; b < C::kBoxes; ++b)
-                        ptx::tma_load_4d(sQ + t * C::kTileBytes + b * C::kBoxBytes, &tm_q, BAR(C::kQF + t), b * 64, 0, x.head,
+                    ptx::mbar_arrive_expect_tx(BAR(C::kQF + t), (uint32_t)(C::kHalves * 128 * p.G * TT));
+                    for (int b = 0; b < C::kHalves; ++b)
+                        ptx::tma_load_4d(sQ + t * C::kTileBytes + b * C::kQBoxBytes, &tm_q, BAR(C::kQF + t), b * 64, 0, x.head,
                                          x.tok + (t - q0) * TT);
                 }
                 ++q_use[t];
@@ -274,8 +284,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (!f.two)
                 q_slot ^= 1;
             for (int i = 0; ok && i < f.tiles; ++i) {
-                int next_first = 0;
-                const int next_row = i + 1 < f.tiles ? page_row(x.t0 + i + 1, next_first) : none;
+                const bool full = x.keys - (x.t0 + i) * kTileKeys >= kTileKeys;
+                int next_first = 0, next_row = none;
+                if (i + 1 < f.tiles)
+                    find(x.t0 + i + 1, next_row, next_first);
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v, ++ld) {
                     const int slot = ld & (C::kStages - 1);
@@ -287,11 +299,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     if (lane == 0)
                         ptx::mbar_arrive_expect_tx(BAR(C::kKVF + slot), C::kTileBytes);
                     __syncwarp();
-                    if (lane < per_tile)
-#pragma unroll
-                        for (int b = 0; b < C::kBoxes; ++b)
-                            ptx::tma_load_3d(sKV + slot * C::kTileBytes + b * C::kBoxBytes + lane * page * 128,
-                                             v ? &tm_v : &tm_k, BAR(C::kKVF + slot), b * 64, first, row);
+                    const uint32_t dst = sKV + slot * C::kTileBytes;
+                    if (full) {
+                        if (lane < per_tile)
+                            ptx::tma_load_5d(dst + lane * (page >> 3) * C::kGroupBytes, v ? &tm_v : &tm_k,
+                                             BAR(C::kKVF + slot), 0, 0, 0, 0, row);
+                    } else if (lane < kTileKeys / 8) {
+                        ptx::tma_load_4d(dst + lane * C::kGroupBytes, v ? &tm_v8 : &tm_k8, BAR(C::kKVF + slot), 0, first, 0,
+                                         row);
+                    }
                     landed[slot] = use + 1;
                 }
                 row = next_row;
@@ -313,8 +329,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             const uint32_t idesc_qk = ptx::idesc_bf16_f32(128, 128, false);
             const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
             const uint64_t dq0 = ptx::smem_desc_sw128(sQ, 16, 1024);
-            const uint64_t dk0 = ptx::smem_desc_sw128(sKV, 16, 1024);
-            const uint64_t dv0 = ptx::smem_desc_sw128(sKV, C::kBoxBytes, 1024);
+            const uint64_t dk0 = ptx::smem_desc_sw128(sKV, 16, C::kGroupBytes);
+            const uint64_t dv0 = ptx::smem_desc_sw128(sKV, 1024, C::kGroupBytes);
             uint32_t done = 0;                                          // tiles whose PV has been issued
             uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, o_use[2] = {0, 0};  // uses of the Q tiles, of S and P, of O
             int q_slot = 0, o_slot = 0;
@@ -332,8 +348,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const uint32_t dst = tmem + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-                    ptx::mma_ss(dst, qa + off, kb + off, idesc_qk, kk > 0);
+                    const uint32_t q_off = ((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4;
+                    const uint32_t k_off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                    ptx::mma_ss(dst, qa + q_off, kb + k_off, idesc_qk, kk > 0);
                 }
                 ptx::mma_commit(BAR(C::kSF + t));
             };
@@ -343,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const uint32_t pa = tmem + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    ptx::mma_ts(dst, pa + kk * 8, vb + ((kk * 2048) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
+                    ptx::mma_ts(dst, pa + kk * 8, vb + ((kk * 2 * C::kGroupBytes) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
             };
             auto p_full = [&](int t) {
                 const bool got = wait(C::kPF + t, p_use[t]++, 0x72);
@@ -524,13 +541,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ptx::tmem_ld_wait64(s);
             const int lim = r.allowed - key0;  // keys of the tile that the row sees
             if (lim < kTileKeys) {
-                // Column c is key c, except in the segment's last page: its keys end
-                // where the page's box ends (see the producer).
-                const int page = 1 << p.page_shift, held = min(kTileKeys, keys - key0);
-                const int last = (held - 1) & ~(page - 1), gap = last + page - held;
-                const uint64_t seen =
-                    columns(min(lim, last) - 64 * h) |
-                    (columns(min(lim + gap, last + page) - 64 * h) & ~columns(last + gap - 64 * h));
+                // Column c is key c, except in the last group of 8 of a shorter tile: its
+                // keys end where the group ends (see the producer).
+                const int held = min(kTileKeys, keys - key0), last = (held - 1) & ~7, gap = last + 8 - held;
+                const uint64_t seen = columns(min(lim, last) - 64 * h) |
+                                      (columns(min(lim + gap, last + 8) - 64 * h) & ~columns(last + gap - 64 * h));
                 const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -794,22 +809,27 @@ cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
     p.unit_tokens = 2 * TT;
     p.light_tokens = TT;
     p.heavy_tile = kHeavyTile;
-    CUtensorMap mq, mk, mv;
-    const int64_t page = 1ll << p.page_shift;
+    CUtensorMap mq, mk, mv, mk8, mv8;
+    const uint64_t page = 1ull << p.page_shift, heads = (uint64_t)(p.n_pages * p.Hkv), halves = D / 64;
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.T};
     const uint64_t qs[3] = {(uint64_t)p.q_head_stride * 2, (uint64_t)p.G * p.q_head_stride * 2, (uint64_t)p.q_token_stride * 2};
     const uint32_t qb[4] = {64, (uint32_t)p.G, 1, (uint32_t)TT};
-    const uint64_t kd[3] = {(uint64_t)D, (uint64_t)page, (uint64_t)(p.n_pages * p.Hkv)};
-    const uint64_t ks[2] = {(uint64_t)D * 2, (uint64_t)(page * D * 2)};
-    const uint32_t kb[3] = {64, (uint32_t)page, 1};
-    if (!make_bf16_map_sw128(&mq, p.q, 4, qd, qs, qb) || !make_bf16_map_sw128(&mk, p.k_cache, 3, kd, ks, kb) ||
-        !make_bf16_map_sw128(&mv, p.v_cache, 3, kd, ks, kb))
+    // A page of a key head as [group of 8 rows][half][row][64]; 8 rows of it as [half][row][64].
+    const uint64_t kd[5] = {64, 8, halves, page / 8, heads};
+    const uint64_t ks[4] = {D * 2, 128, D * 16, page * D * 2};
+    const uint32_t kb[5] = {64, 8, (uint32_t)halves, (uint32_t)page / 8, 1};
+    const uint64_t gd[4] = {64, page, halves, heads};
+    const uint64_t gs[3] = {D * 2, 128, page * D * 2};
+    const uint32_t gb[4] = {64, 8, (uint32_t)halves, 1};
+    if (!make_bf16_map_sw128(&mq, p.q, 4, qd, qs, qb) || !make_bf16_map_sw128(&mk, p.k_cache, 5, kd, ks, kb) ||
+        !make_bf16_map_sw128(&mv, p.v_cache, 5, kd, ks, kb) || !make_bf16_map_sw128(&mk8, p.k_cache, 4, gd, gs, gb) ||
+        !make_bf16_map_sw128(&mv8, p.v_cache, 4, gd, gs, gb))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Cfg<D>::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    prefix_attn_kernel<D><<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, p);
+    prefix_attn_kernel<D><<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, mk8, mv8, p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }
