@@ -150,6 +150,103 @@ __device__ __forceinline__ uint64_t columns(int n)
     return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
 }
 
+// What a softmax thread keeps of a row's tiles so far.
+struct Row {
+    float m, l;   // kept maximum in log2 units, this half's sum
+    int allowed;  // keys [0, allowed) of the segment are visible
+};
+
+// The scores of this thread's 64 keys of a tile (half h of it), masked; their
+// maximum is returned.  lim: keys of the tile that the row sees; held: keys of the
+// tile.
+__device__ __forceinline__ float read_scores(uint32_t tS, int h, int lim, int held, uint32_t (&s)[64])
+{
+    ptx::tc_fence_after();
+    ptx::tmem_ld64(tS + 64 * h, s);
+    ptx::tmem_ld_wait64(s);
+    if (lim < kTileKeys) {
+        // Column c is key c, except in the last group of 8 of a shorter tile: its
+        // keys end where the group ends (see the producer).
+        const int last = (held - 1) & ~7, gap = last + 8 - held;
+        const uint64_t seen = columns(min(lim, last) - 64 * h) |
+                              (columns(min(lim + gap, last + 8) - 64 * h) & ~columns(last + gap - 64 * h));
+        const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (!(lo & (1u << i)))
+                s[i] = f2u(-INFINITY);
+            if (!(hi & (1u << i)))
+                s[i + 32] = f2u(-INFINITY);
+        }
+    }
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 64; i += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            m4[k] = fmax3(m4[k], u2f(s[i + 2 * k]), u2f(s[i + 2 * k + 1]));
+    }
+    return fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+}
+
+// The maximum moves only when it grows by more than kRescale: l and, if a PV has
+// written it (`old_o`), this half's columns of O are then multiplied by what 2^-m
+// became.
+template <int D>
+__device__ __forceinline__ void raise_max(Row &r, float mnew, uint32_t tO, int h, bool old_o)
+{
+    const bool need = mnew > -INFINITY && (r.m == -INFINITY || mnew > r.m + kRescale);
+    if (!__any_sync(0xffffffffu, need))
+        return;
+    float alpha = 1.f;
+    if (need) {
+        alpha = r.m == -INFINITY ? 0.f : ptx::ex2(r.m - mnew);
+        r.l *= alpha;
+        r.m = mnew;
+    }
+    if (old_o) {
+        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+        for (int k = 0; k < D / 64; ++k) {
+            uint32_t o[32];
+            const uint32_t ta = tO + h * (D / 2) + k * 32;
+            ptx::tmem_ld32(ta, o);
+            ptx::tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 y = __fmul2_rn(make_float2(u2f(o[i]), u2f(o[i + 1])), a2);
+                o[i] = f2u(y.x);
+                o[i + 1] = f2u(y.y);
+            }
+            ptx::tmem_st32(ta, o);
+        }
+    }
+}
+
+// p = 2^(s log2(e) / sqrt(d) - m), rounded to bf16 for the MMA (the sum l takes
+// them in fp32); keys [64h, 64h + 64) go to packed columns [32h, 32h + 32) over S,
+// and `bar` learns that they are there.
+__device__ __forceinline__ void write_probabilities(uint32_t tS, int h, float sl2, Row &r, const uint32_t (&s)[64], uint32_t bar)
+{
+    const float neg = r.m == -INFINITY ? 0.f : -r.m;
+    const float2 c2 = make_float2(sl2, sl2), n2 = make_float2(neg, neg);
+    float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    uint32_t pk[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float2 y = __ffma2_rn(make_float2(u2f(s[2 * i]), u2f(s[2 * i + 1])), c2, n2);
+        const float p0 = ptx::ex2(y.x), p1 = ptx::ex2(y.y);
+        acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
+        pk[i] = pack_bf16(p0, p1);
+    }
+    ptx::tmem_st32(tS + 32 * h, pk);
+    ptx::tmem_st_wait();
+    ptx::tc_fence_before();
+    ptx::mbar_arrive(bar);
+    const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+    r.l += a.x + a.y;
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -529,139 +626,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             return __all_sync(0xffffffffu, ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
         };
 
-        // What a thread keeps of a row's tiles so far.
-        struct Row {
-            float m, l;   // kept maximum in log2 units, this half's sum
-            int allowed;  // keys [0, allowed) of the segment are visible
-        };
-        // Scores of this thread's 64 keys of a tile, masked; their maximum goes to the other half.
-        auto scores = [&](int t, int key0, const Row &r, int keys, uint32_t *s) -> float {
-            ptx::tc_fence_after();
-            ptx::tmem_ld64(lanes + (t ? C::kColS1 : C::kColS0) + 64 * h, s);
-            ptx::tmem_ld_wait64(s);
-            const int lim = r.allowed - key0;  // keys of the tile that the row sees
-            if (lim < kTileKeys) {
-                // Column c is key c, except in the last group of 8 of a shorter tile: its
-                // keys end where the group ends (see the producer).
-                const int held = min(kTileKeys, keys - key0), last = (held - 1) & ~7, gap = last + 8 - held;
-                const uint64_t seen = columns(min(lim, last) - 64 * h) |
-                                      (columns(min(lim + gap, last + 8) - 64 * h) & ~columns(last + gap - 64 * h));
-                const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (!(lo & (1u << i)))
-                        s[i] = f2u(-INFINITY);
-                    if (!(hi & (1u << i)))
-                        s[i + 32] = f2u(-INFINITY);
-                }
-            }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 64; i += 8) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    m4[k] = fmax3(m4[k], u2f(s[i + 2 * k]), u2f(s[i + 2 * k + 1]));
-            }
-            const float mx = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-            xch[(t * 2 + h) * 128 + row] = mx;
-            return mx;
-        };
-        // The maximum moves only when it grows by more than kRescale: O and l are then
-        // multiplied by what 2^-m became (O only if a PV has written it: `old_o`).
-        auto raise = [&](Row &r, float mx, uint32_t tO, bool old_o) {
-            const float mnew = mx * sl2;
-            const bool need = mnew > -INFINITY && (r.m == -INFINITY || mnew > r.m + kRescale);
-            if (!__any_sync(0xffffffffu, need))
-                return;
-            float alpha = 1.f;
-            if (need) {
-                alpha = r.m == -INFINITY ? 0.f : ptx::ex2(r.m - mnew);
-                r.l *= alpha;
-                r.m = mnew;
-            }
-            if (old_o) {
-                const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
-                    uint32_t o[32];
-                    const uint32_t ta = tO + h * (D / 2) + k * 32;
-                    ptx::tmem_ld32(ta, o);
-                    ptx::tmem_ld_wait(o);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 y = __fmul2_rn(make_float2(u2f(o[i]), u2f(o[i + 1])), a2);
-                        o[i] = f2u(y.x);
-                        o[i + 1] = f2u(y.y);
-                    }
-                    ptx::tmem_st32(ta, o);
-                }
-            }
-        };
-        // p = 2^(s log2(e) / sqrt(d) - m), rounded to bf16 for the MMA (the sum l takes
-        // them in fp32); keys [64h, 64h + 64) go to packed columns [32h, 32h + 32) over S.
-        auto probabilities = [&](int t, Row &r, const uint32_t *s) {
-            const float neg = r.m == -INFINITY ? 0.f : -r.m;
-            const float2 c2 = make_float2(sl2, sl2), n2 = make_float2(neg, neg);
-            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float2 y = __ffma2_rn(make_float2(u2f(s[2 * i]), u2f(s[2 * i + 1])), c2, n2);
-                const float p0 = ptx::ex2(y.x), p1 = ptx::ex2(y.y);
-                acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(p0, p1));
-                pk[i] = pack_bf16(p0, p1);
-            }
-            ptx::tmem_st32(lanes + (t ? C::kColS1 : C::kColS0) + 32 * h, pk);
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(BAR(C::kPF + t));
-            const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-            r.l += a.x + a.y;
-        };
-        // Where a row's result goes.
-        struct Out {
-            void *o;
-            float *lse;
-            float m, l;
-            bool valid;
-        };
-        auto out_of = [&](const Work &x, int ti, const Row &r) {
-            const int token = x.tok + ti, hq = x.head * p.G + row_g;
-            const int64_t at = (int64_t)token * p.Hq + hq, slot = (int64_t)worker * kPrefixUnitRows + (ti * p.G + row_g);
-            Out d;
-            if (x.to == kResult) {
-                d.o = static_cast<__nv_bfloat16 *>(p.out) + at * D;
-                d.lse = p.lse + at;
-            } else if (x.to == kSlot) {
-                d.o = p.slot_o + slot * D;
-                d.lse = p.slot_lse + slot;
-            } else {
-                d.o = p.home_o[x.to] + at * D;
-                d.lse = p.home_lse[x.to] + at;
-            }
-            d.m = r.m;
-            d.l = r.l;
-            d.valid = row_tok < TT && ti < x.ntok;
-            return d;
-        };
-
         // The last piece's rows, whose O is still being computed while the next piece's
-        // first scores are: written after those.  One copy of this and of the step
-        // below serves both forms (code that is cold costs more than it computes).
+        // first scores are: written after those.
         struct {
-            Out out, second;  // second: the second row tile's
-            int slot, n;      // first O; row tiles
-            bool on, has_o, bf16;
+            float m[2], l[2];  // of the row in each row tile
+            int at, slot;      // its description; its first O
+            bool on;
         } late;
         late.on = false;
         auto write_late = [&]() -> bool {
             late.on = false;
+            const Work &w = work[late.at];
+            const bool has_o = w.tiles > 0;
 #pragma unroll 1
-            for (int e = 0; e < late.n; ++e, late.out = late.second, late.slot ^= 1) {
-                const Out &out = late.out;
-                const bool any = __any_sync(0xffffffffu, out.valid);
-                float l = out.l;
-                if (late.has_o) {
+            for (int e = 0; e <= w.two; ++e) {
+                const int ti = row_tok + e * TT, token = w.tok + ti, hq = w.head * p.G + row_g;
+                const bool valid = row_tok < TT && ti < w.ntok, any = __any_sync(0xffffffffu, valid);
+                const float m = e ? late.m[1] : late.m[0];
+                float l = e ? late.l[1] : late.l[0];
+                if (has_o) {
                     const bool got = wait(C::kOF + late.slot, late.slot ? o_use1++ : o_use0++, 0x81);
                     xl[(e * 2 + h) * 128 + row] = l;
                     if (!pair_bar_and(warp & 3, got))
@@ -671,31 +654,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 }
                 const bool empty = !(l > 0.f) && l == l;
                 const float inv = empty ? 0.f : 1.f / l;
-                if (out.valid && h == 0)
-                    *out.lse = empty ? -INFINITY : (out.m + ptx::lg2(l)) * kLn2;
+                // where the row goes: the result, the worker's slot or the row's home
+                const int64_t at = (int64_t)token * p.Hq + hq, own = (int64_t)worker * kPrefixUnitRows + (ti * p.G + row_g);
+                const bool bf16 = w.to == kResult;
+                float *po, *pl;
+                if (w.to == kResult) {
+                    po = reinterpret_cast<float *>(static_cast<__nv_bfloat16 *>(p.out) + at * D);
+                    pl = p.lse + at;
+                } else if (w.to == kSlot) {
+                    po = p.slot_o + own * D;
+                    pl = p.slot_lse + own;
+                } else {
+                    po = p.home_o[w.to] + at * D;
+                    pl = p.home_lse[w.to] + at;
+                }
+                if (valid && h == 0)
+                    *pl = empty ? -INFINITY : (m + ptx::lg2(l)) * kLn2;
                 if (any) {
 #pragma unroll 1
                     for (int k = 0; k < D / 64; ++k) {
                         const int col = h * (D / 2) + k * 32;
                         uint32_t o[32];
-                        if (late.has_o) {
+                        if (has_o) {
                             ptx::tmem_ld32(lanes + (late.slot ? C::kColO1 : C::kColO0) + col, o);
                             ptx::tmem_ld_wait(o);
                         }
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            v[i] = late.has_o ? u2f(o[i]) * inv : 0.f;
-                        if (out.valid) {
-                            if (late.bf16) {
-                                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out.o) + col);
+                            v[i] = has_o ? u2f(o[i]) * inv : 0.f;
+                        if (valid) {
+                            if (bf16) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(po) + col);
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
                                     dst[i] =
                                         make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                                    pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
                             } else {
-                                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out.o) + col);
+                                float4 *dst = reinterpret_cast<float4 *>(po + col);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
                                     dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -704,11 +701,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         __syncwarp();
                     }
                 }
-                if (late.has_o) {
+                if (has_o) {
                     ptx::tc_fence_before();
                     ptx::mbar_arrive(BAR(C::kOFree + late.slot));
                 }
+                late.slot ^= 1;
             }
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(BAR(C::kWE + late.at));
             return true;
         };
 
@@ -717,78 +718,102 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ok = pair_bar_and(warp & 3, wait(C::kWF + at, pieces / C::kWork, 0x83));
             if (!ok)
                 break;
-            const Work f = work[at];
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive(BAR(C::kWE + at));
-            const int tiles = max(f.tiles, 0), steps = f.two ? 2 * tiles : tiles;
-            // The row of this step's tile and, in the form with two tiles, of the other
-            // one: they change places after every step.
-            Row cur, other;
-            auto row_of = [&](int ti) {
+            const Work &f = work[at];  // given back when its rows have been written
+            const int tiles = max(f.tiles, 0), t0 = f.t0, keys = f.keys;
+            const bool two = f.two != 0, last = f.tiles < 0;
+            Row r[2];  // of the two row tiles; with one, of it
+            uint32_t s[64];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 // A lane without a row need not mask anything: what it computes reaches
                 // only the same lane's O, which nobody reads.
+                const int ti = row_tok + (two ? t * TT : 0);
                 const bool has = row_tok < TT && ti < f.ntok;
-                return Row{-INFINITY, 0.f, has ? (int)max((int64_t)0, min((int64_t)f.keys, f.see0 + ti)) : INT_MAX};
-            };
-            cur = row_of(row_tok);
-            other = f.two ? row_of(row_tok + TT) : cur;
-#pragma unroll 1
-            for (int k = 0; ok && k < max(steps, 1); ++k) {
-                if (steps > 0) {
-                    const int j = f.two ? k >> 1 : k;  // tile of the piece
-                    const int t = f.two ? k & 1 : (done + k) & 1;
-                    const bool busy = __any_sync(0xffffffffu, cur.allowed != INT_MAX);
-                    uint32_t s[64];
-                    float mx = -INFINITY;
-                    const bool got = wait(C::kSF + t, t ? s_use1++ : s_use0++, 0x80);
-                    if (got && busy)
-                        mx = scores(t, (f.t0 + j) * kTileKeys, cur, f.keys, s);
-                    // Both halves of the rows have read S before P is written over it.
-                    ptx::tc_fence_before();
-                    ok = pair_bar_and(warp & 3, got);
-                    ptx::tc_fence_after();
-                    if (!ok)
-                        break;
-                    if (busy) {
-                        mx = fmaxf(mx, xch[(t * 2 + (h ^ 1)) * 128 + row]);
-                        if (j > 0 && !f.two && __any_sync(0xffffffffu, mx * sl2 > cur.m + kRescale)) {
-                            // O may still be under the PV of the tile before: that one frees its V
-                            // slot.  (With two tiles the commit that signalled this S covers it.)
-                            const uint32_t v = 2 * (done + j) - 1;
-                            ok = pair_bar_and(warp & 3, wait(C::kKVE + (v & (C::kStages - 1)), v >> C::kStageBits, 0x82));
-                            if (!ok)
-                                break;
-                            ptx::tc_fence_after();
+                r[t] = Row{-INFINITY, 0.f, has ? (int)max((int64_t)0, min((int64_t)keys, f.see0 + ti)) : INT_MAX};
+            }
+            if (two && tiles > 0) {
+                if (late.on)
+                    ok = write_late();
+                for (int j = 0; ok && j < tiles; ++j) {
+                    const int key0 = (t0 + j) * kTileKeys;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const bool busy = __any_sync(0xffffffffu, r[t].allowed != INT_MAX);
+                        float mx = -INFINITY;
+                        const bool got = wait(C::kSF + t, (t ? s_use1 : s_use0) + j, 0x80);
+                        if (got && busy) {
+                            mx = read_scores(lanes + (t ? C::kColS1 : C::kColS0), h, r[t].allowed - key0,
+                                             min(kTileKeys, keys - key0), s);
+                            xch[(t * 2 + h) * 128 + row] = mx;
                         }
-                        const int o = f.two ? t : o_slot;
-                        raise(cur, mx, lanes + (o ? C::kColO1 : C::kColO0), j > 0);
-                        probabilities(t, cur, s);
-                    } else {
-                        // (rows of P that nobody wrote only reach the same rows of O)
-                        ptx::mbar_arrive(BAR(C::kPF + t));
-                    }
-                    if (f.two) {
-                        const Row r = cur;
-                        cur = other;
-                        other = r;
+                        // Both halves of the rows have read S before P is written over it.
+                        ptx::tc_fence_before();
+                        ok = pair_bar_and(warp & 3, got);
+                        ptx::tc_fence_after();
+                        if (!ok)
+                            break;
+                        if (busy) {
+                            mx = fmaxf(mx, xch[(t * 2 + (h ^ 1)) * 128 + row]) * sl2;
+                            // (the commit that signalled this S also covered the PV before it: O is stable)
+                            raise_max<D>(r[t], mx, lanes + (t ? C::kColO1 : C::kColO0), h, j > 0);
+                            write_probabilities(lanes + (t ? C::kColS1 : C::kColS0), h, sl2, r[t], s, BAR(C::kPF + t));
+                        } else {
+                            // (rows of P that nobody wrote only reach the same rows of O)
+                            ptx::mbar_arrive(BAR(C::kPF + t));
+                        }
                     }
                 }
-                if (k == 0 && late.on)
-                    ok = write_late();
+                s_use0 += tiles;
+                s_use1 += tiles;
+            } else {
+                const bool busy = __any_sync(0xffffffffu, r[0].allowed != INT_MAX);
+#pragma unroll 1
+                for (int j = 0; ok && (j < tiles || late.on); ++j) {
+                    if (j < tiles) {
+                        const int key0 = (t0 + j) * kTileKeys, t = (done + j) & 1;
+                        const uint32_t tS = lanes + (t ? C::kColS1 : C::kColS0);
+                        float mx = -INFINITY;
+                        const bool got = wait(C::kSF + t, t ? s_use1++ : s_use0++, 0x80);
+                        if (got && busy) {
+                            mx = read_scores(tS, h, r[0].allowed - key0, min(kTileKeys, keys - key0), s);
+                            xch[(t * 2 + h) * 128 + row] = mx;
+                        }
+                        ptx::tc_fence_before();
+                        ok = pair_bar_and(warp & 3, got);
+                        ptx::tc_fence_after();
+                        if (!ok)
+                            break;
+                        if (busy) {
+                            mx = fmaxf(mx, xch[(t * 2 + (h ^ 1)) * 128 + row]) * sl2;
+                            if (j > 0 && __any_sync(0xffffffffu, mx > r[0].m + kRescale)) {
+                                // O may still be under the PV of the tile before: that one frees its V slot.
+                                const uint32_t v = 2 * (done + j) - 1;
+                                ok = pair_bar_and(warp & 3, wait(C::kKVE + (v & (C::kStages - 1)), v >> C::kStageBits, 0x82));
+                                if (!ok)
+                                    break;
+                                ptx::tc_fence_after();
+                            }
+                            raise_max<D>(r[0], mx, lanes + (o_slot ? C::kColO1 : C::kColO0), h, j > 0);
+                            write_probabilities(tS, h, sl2, r[0], s, BAR(C::kPF + t));
+                        } else {
+                            ptx::mbar_arrive(BAR(C::kPF + t));
+                        }
+                    }
+                    if (late.on)
+                        ok = write_late();
+                }
             }
-            if (!ok || f.tiles < 0)
+            if (!ok || last)
                 break;
             done += tiles;
-            late.out = out_of(f, row_tok, cur);
-            if (f.two)
-                late.second = out_of(f, row_tok + TT, other);
-            late.n = f.two ? 2 : 1;
-            late.slot = f.two ? 0 : o_slot;
-            late.has_o = tiles > 0;
-            late.bf16 = f.to == kResult;
+            late.at = at;
+            late.m[0] = r[0].m;
+            late.l[0] = r[0].l;
+            late.m[1] = r[1].m;
+            late.l[1] = r[1].l;
+            late.slot = two ? 0 : o_slot;
             late.on = true;
-            if (tiles > 0 && !f.two)
+            if (tiles > 0 && !two)
                 o_slot ^= 1;
         }
     }
