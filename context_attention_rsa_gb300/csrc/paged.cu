@@ -179,7 +179,7 @@ PrefixLayout prefix_layout(int64_t T, int Hq, int d, int R)
 {
     PrefixLayout w;
     const size_t rows_ = (size_t)T * Hq, slots = (size_t)kPrefixMaxWorkers * kPrefixUnitRows;
-    w.plan = align256(((size_t)R + 3) * 8);
+    w.plan = align256(((size_t)R + 2) * 8);
     w.home_o = align256(rows_ * d * 4);
     w.home_lse = align256(rows_ * 4);
     w.slot_o = align256(slots * d * 4);

@@ -8,13 +8,13 @@
 //             G query heads of one key head: the rows that share a key tile
 //   tile      128 keys of a unit
 // All tiles of all units lie on one line: segments in order, in a segment the
-// key heads, in a head the token groups, in a unit its tiles.  A tile takes one
-// place, or heavy_tile of them where its unit has many rows, and a unit
+// key heads, in a head the token groups, in a unit its tiles.  A tile takes
+// light_tile places, or heavy_tile where its unit has many rows, and a unit
 // kUnitCost places before its first tile, for what it costs to begin and to end
 // one, so that a place takes about the same time everywhere.  The line is cut
-// into `workers` equal stretches, one for each CTA, so that one long
-// request, many short ones and a prefix all fill the GPU alike.  The part of a
-// unit in a stretch is a piece; it leaves a partial (o, lse) for its rows: in
+// into `workers` equal stretches, one for each CTA, so that one long request,
+// many short ones and a prefix all fill the GPU alike.  The tiles of a unit that
+// begin in a stretch are a piece; it leaves a partial (o, lse) for its rows: in
 // the rows' own place (home) if the piece begins the unit, else in the worker's
 // slot, as only a worker's first piece can begin inside a unit.  Workspace:
 // two homes for every row and 256 rows for every worker, whatever the lengths.
@@ -31,7 +31,7 @@ namespace rsa {
 namespace paged {
 
 constexpr int kTileKeys = 128;
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 2;
 
 struct Segment {
     int tok0, ntok;        // its query tokens
@@ -74,9 +74,16 @@ __device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, boo
     }
     g.groups = (int)(((int64_t)g.ntok + p.unit_tokens - 1) / p.unit_tokens);
     g.tiles = (int)(((int64_t)g.keys + kTileKeys - 1) / kTileKeys);
-    g.cost = g.ntok > p.light_tokens ? p.heavy_tile : 1;
+    g.cost = g.ntok > p.light_tokens ? p.heavy_tile : p.light_tile;
     g.line = g.tiles > 0 ? (int64_t)g.groups * p.Hkv * g.unit_line() : 0;
     return g;
+}
+
+// Places of a worker on a line of `total`: never less than a tile takes, so that
+// every stretch inside a unit has a piece of it.
+__device__ __forceinline__ int64_t share_of(const PrefixAttnParams &p, int64_t total)
+{
+    return max((total + p.workers - 1) / p.workers, (int64_t)(p.T > p.light_tokens ? p.heavy_tile : p.light_tile));
 }
 
 // A worker's stretch of the line, and where it begins.
@@ -88,8 +95,8 @@ struct Stretch {
 };
 
 // Every thread of the block (NT of them) calls this with a word of shared
-// memory a warp.  Worker 0 leaves the plan for the joining launch: plan[s] =
-// the line's places before segment s, plan[R + 1] = total, plan[R + 2] = share.
+// memory a warp.  Worker 0 leaves the sums for the joining launch: plan[s] = the
+// line's places before segment s, plan[R + 1] = all of them.
 template <int NT>
 __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int worker, int64_t *s_sum,
                                                 Stretch *s_out)
@@ -142,16 +149,13 @@ __device__ __forceinline__ Stretch find_stretch(const PrefixAttnParams &p, int w
         }
         if (nseg <= NT)
             total = before;
-        // (a stretch is never shorter than a tile, so that every one inside a unit has a piece of it)
-        const int64_t share = max((total + p.workers - 1) / p.workers, (int64_t)(p.T > p.light_tokens ? p.heavy_tile : 1));
+        const int64_t share = share_of(p, total);
         const int64_t at = worker * share;
         if (worker == 0) {
             if (s < nseg)
                 p.plan[s] = first;
-            if (s == p.R) {
+            if (s == p.R)
                 p.plan[p.R + 1] = total;
-                p.plan[p.R + 2] = share;
-            }
         }
         if (g.line > 0 && at >= first && at < first + g.line)
             *s_out = Stretch{g, at - first, min(share, total - at), s};

@@ -226,37 +226,55 @@ __global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_cons
 {
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= p.T * p.Hq)
-        return;
+    const int64_t row = min((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), p.T * p.Hq - 1);  // (spare warps repeat a row)
     const int token = (int)(row / p.Hq);
     const int hq = (int)(row - (int64_t)token * p.Hq), head = hq / p.G;
     const int r = request_of(p, token);
-    if (r < 0)
-        return;  // rows behind the last request stay as they are
-    Segment g[2];
+    const Segment g[2] = {segment(p, 0), r < 0 ? Segment() : segment(p, 1 + r)};
+    // Where the row's pieces are follows from the lengths alone.  With up to 31
+    // requests, one segment a lane, the warp works it out itself, all of it while the
+    // attention launch still computes (2 us less for a short call); with more that
+    // would cost every row a scan, and it takes the sums that worker 0 has left.
+    int64_t total, before = 0;
+    const bool few = p.R < 32;
+    if (few) {
+        const int64_t line = lane <= p.R ? segment(p, lane).line : 0;
+        total = line;
+        before = lane <= r ? line : 0;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-        g[s] = segment(p, s == 0 ? 0 : 1 + r);
-    ptx::wait_for_launch_before();  // so far only the call's inputs were read
-    const int64_t share = p.plan[p.R + 2], before[2] = {0, p.plan[1 + r]};
+        for (int o = 16; o > 0; o >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+    } else {
+        ptx::wait_for_launch_before();
+        total = p.plan[p.R + 1];
+        before = p.plan[1 + max(r, 0)];
+    }
+    const int64_t share = share_of(p, total);
+    bool whole = false;
     Pieces pc[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const int i = token - g[s].tok0;
         pc[s].n = 0;
-        if (g[s].line == 0 || i < 0 || i >= g[s].ntok)
+        const int i = token - g[s].tok0;
+        if (r < 0 || g[s].line == 0 || i < 0 || i >= g[s].ntok)
             continue;  // (outside: only where cu_q does not ascend)
         const int64_t unit = (int64_t)head * g[s].groups + i / p.unit_tokens;
-        const int64_t at = before[s] + unit * g[s].unit_line() + kUnitCost;  // the unit's first tile
+        const int64_t at = (s == 0 ? 0 : before) + unit * g[s].unit_line() + kUnitCost;  // the unit's first tile
         const int64_t w0 = at / share, w1 = (at + (int64_t)(g[s].tiles - 1) * g[s].cost) / share;
-        if (s == 1 && w0 == w1 && p.prefix_len == 0)
-            return;  // one piece: it went straight to out
+        whole = s == 1 && w0 == w1 && p.prefix_len == 0;
         pc[s].o = p.home_o[s] + row * D;
         pc[s].lse = p.home_lse[s] + row;
         pc[s].slot = (w0 + 1) * kPrefixUnitRows + (i % p.unit_tokens) * p.G + (hq - head * p.G);
         pc[s].n = (int)(w1 - w0) + 1;
     }
+    // Every thread waits, also where it has nothing to join: the launch after this one
+    // waits only for this one.
+    if (few)
+        ptx::wait_for_launch_before();
+    if (r < 0 || whole)
+        return;  // a row behind the last request stays as it is; a single piece went straight to out
     const int n = pc[0].n + pc[1].n;
     auto locate = [&](int i, const float *&o, const float *&lse) {  // piece i of the row
         const int s = i >= pc[0].n;
@@ -318,7 +336,7 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
 {
     PrefixAttnParams p = p_in;
     p.unit_tokens = p.light_tokens = kRows / p.G;
-    p.heavy_tile = 1;
+    p.light_tile = p.heavy_tile = 2;
     cudaError_t e =
         cudaFuncSetAttribute(prefix_attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)

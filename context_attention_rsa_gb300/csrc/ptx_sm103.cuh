@@ -451,20 +451,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask)
         : "memory");
 }
 
-// ---- register split: every warp of a warpgroup -----------------------------------
-
-template <int N>
-__device__ __forceinline__ void give_registers()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <int N>
-__device__ __forceinline__ void take_registers()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // ---- programmatic dependent launch ---------------------------------------------
 
 // The next launch on the stream, if it was made for it, may begin before this

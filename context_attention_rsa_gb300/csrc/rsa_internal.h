@@ -195,14 +195,14 @@ struct PrefixAttnParams {
     void *out;                   // [T, Hq, d]
     float *lse;                  // [T, Hq]
     // workspace (see paged_sched.cuh)
-    int64_t *plan;               // [R + 3]
+    int64_t *plan;               // [R + 2]
     float *home_o[2], *home_lse[2];  // [T * Hq, d] and [T * Hq]: a row's first piece of the prefix, of its own keys
     float *slot_o, *slot_lse;    // [workers, 256, d] and [workers, 256]: a worker's first piece, begun by another
     // how the launcher's kernel cuts the work
     int workers;
     int unit_tokens;             // query tokens of a unit at most
-    int light_tokens;            // a unit of more tokens than this costs heavy_tile a key tile, not 1
-    int heavy_tile;
+    int light_tokens;            // a unit of more tokens than this costs heavy_tile places a key tile, else light_tile
+    int light_tile, heavy_tile;
     uint64_t wait_limit_ns;
     unsigned int *err;
 };
