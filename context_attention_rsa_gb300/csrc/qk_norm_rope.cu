@@ -12,13 +12,18 @@
 // over all tokens and heads.
 //
 // Bound by HBM: every element is read once and written once, about 10 (20
-// backward) operations apart.  So each thread moves 16-byte pieces, a row of d
-// elements lies across L = d * size / 16 lanes, its two sums (one per row and
-// direction) are shuffles among those lanes, and a group of L lanes takes
-// kHeads heads of one token with all their loads in flight at once: the
-// token's cosines and sines are read once per group.  The partner of a
-// half-turned element is in another lane: one shuffle.  All arithmetic is in
-// 32 bits; the result is rounded once, at the store.
+// backward) operations apart.  A row of d elements lies across L = d * size / 16
+// lanes, its sums are shuffles among those, and a group of L lanes takes kHeads
+// heads of one token with all their loads in flight at once: the token's cosines
+// and sines are read once per group.  Which elements a lane holds depends on the
+// rotation (Layout):
+//   whole   halves of the whole row turn (rot = d): 8 bytes of each half, so that a
+//           lane has both elements of its pairs and turns them two at a time with
+//           packed fp32 arithmetic;
+//   pairs   interleaved: 16 bytes in a row, which are whole pairs;
+//   part    halves of the first rot < d elements: 16 bytes in a row; the pairs'
+//           other elements are in another lane, one shuffle each.
+// All arithmetic is in 32 bits; the result is rounded once, at the store.
 #include <cuda_bf16.h>
 
 #include "rsa_internal.h"
@@ -28,79 +33,99 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 16 bytes of a row as floats.
+enum Layout { kWhole, kPairs, kPart };
+
+// What a lane holds of a row: N elements, 16 bytes, as floats two by two.
 template <class E>
 struct Piece;
 template <>
 struct Piece<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(const uint4 &u, float *x)
+    static __device__ __forceinline__ void unpack(const uint4 &u, float2 *x)
     {
-        x[0] = __uint_as_float(u.x);
-        x[1] = __uint_as_float(u.y);
-        x[2] = __uint_as_float(u.z);
-        x[3] = __uint_as_float(u.w);
+        x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
-    static __device__ __forceinline__ uint4 pack(const float *x)
+    static __device__ __forceinline__ uint4 pack(const float2 *x)
     {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x), __float_as_uint(x[1].y));
     }
 };
 template <>
 struct Piece<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void two(uint32_t w, float *x)
+    static __device__ __forceinline__ float2 two(uint32_t w)
     {
-        x[0] = __uint_as_float(w << 16);
-        x[1] = __uint_as_float(w & 0xffff0000u);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    static __device__ __forceinline__ uint32_t one(float a, float b)
+    static __device__ __forceinline__ uint32_t one(const float2 &x)
     {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);  // nearest even: the one rounding of the result
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);  // nearest even: the one rounding of the result
         return *reinterpret_cast<const uint32_t *>(&h);
     }
-    static __device__ __forceinline__ void unpack(const uint4 &u, float *x)
+    static __device__ __forceinline__ void unpack(const uint4 &u, float2 *x)
     {
-        two(u.x, x);
-        two(u.y, x + 2);
-        two(u.z, x + 4);
-        two(u.w, x + 6);
+        x[0] = two(u.x);
+        x[1] = two(u.y);
+        x[2] = two(u.z);
+        x[3] = two(u.w);
     }
-    static __device__ __forceinline__ uint4 pack(const float *x)
+    static __device__ __forceinline__ uint4 pack(const float2 *x)
     {
-        return make_uint4(one(x[0], x[1]), one(x[2], x[3]), one(x[4], x[5]), one(x[6], x[7]));
+        return make_uint4(one(x[0]), one(x[1]), one(x[2]), one(x[3]));
     }
 };
 
-template <class E, int D>
+template <class E, int D, Layout kLayout>
 struct Shape {
-    static constexpr int N = Piece<E>::N;      // elements of a thread
+    static constexpr int N = Piece<E>::N;      // elements of a lane
     static constexpr int L = D / N;            // lanes of a row
     static constexpr int kGroups = kThreads / L;
+    // A lane's first element (kWhole: of its first run of N / 2; the second one is D / 2 on).
+    static __device__ __forceinline__ int first(int lane) { return kLayout == kWhole ? lane * (N / 2) : lane * N; }
+    static __device__ __forceinline__ uint4 load(const E *row, int e0)
+    {
+        if constexpr (kLayout == kWhole) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(row + e0), b = *reinterpret_cast<const uint2 *>(row + e0 + D / 2);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            return *reinterpret_cast<const uint4 *>(row + e0);
+        }
+    }
+    static __device__ __forceinline__ void store(E *row, int e0, const uint4 &u)
+    {
+        if constexpr (kLayout == kWhole) {
+            *reinterpret_cast<uint2 *>(row + e0) = make_uint2(u.x, u.y);
+            *reinterpret_cast<uint2 *>(row + e0 + D / 2) = make_uint2(u.z, u.w);
+        } else {
+            *reinterpret_cast<uint4 *>(row + e0) = u;
+        }
+    }
 };
 
-// This lane's part of a row's rotation: the factors of its elements (half) or
-// pairs (interleaved).  A lane's elements turn all or not at all, and its
-// partner's elements are its own pairs' others, as rot/2 is a multiple of 8.
-template <int N, bool INTER>
+// This lane's part of a row's rotation: cosines and sines of its pairs (kPart: of
+// its elements, the sines negated in the pairs' first ones).  A lane's elements
+// turn all or not at all, and its partner's elements are its own pairs' others, as
+// rot/2 is a multiple of 8.
+template <int N, Layout kLayout>
 struct Turn {
-    static constexpr int M = INTER ? N / 2 : N;
-    float c[M], s[M];  // half: s is negated in the pairs' first elements
+    static constexpr int M = kLayout == kPart ? N / 2 : N / 4;
+    float2 c[M], s[M];
     bool on;
-    int partner;  // lane of the row
+    int partner;  // kPart: lane of the row
 };
 
-template <int N, bool INTER>
-__device__ __forceinline__ Turn<N, INTER> load_turn(const NormRopeParams &p, int64_t t, int e0)
+template <int N, Layout kLayout>
+__device__ __forceinline__ Turn<N, kLayout> load_turn(const NormRopeParams &p, int64_t t, int e0)
 {
-    constexpr int M = Turn<N, INTER>::M;
-    Turn<N, INTER> w = {};
+    constexpr int M = Turn<N, kLayout>::M;
+    Turn<N, kLayout> w = {};
     const int half = p.rot >> 1;
-    w.on = e0 < p.rot;
+    w.on = kLayout == kWhole || e0 < p.rot;
     if (!w.on)
         return w;
-    const bool second = !INTER && e0 >= half;
-    const int f0 = INTER ? e0 >> 1 : (second ? e0 - half : e0);
+    const bool second = kLayout == kPart && e0 >= half;
+    const int f0 = kLayout == kPairs ? e0 >> 1 : (second ? e0 - half : e0);
     w.partner = (second ? e0 - half : e0 + half) / N;
     auto row = [&](int axis) {
         int64_t pos = p.positions[axis * p.T + t];
@@ -112,35 +137,37 @@ __device__ __forceinline__ Turn<N, INTER> load_turn(const NormRopeParams &p, int
     };
     if (p.n_axes == 1) {
         const float *r = row(0) + f0;
-        if constexpr (M % 4 == 0) {
+        if constexpr (M % 2 == 0) {
 #pragma unroll
-            for (int i = 0; i < M; i += 4) {
-                const float4 c = *reinterpret_cast<const float4 *>(r + i);
-                const float4 n = *reinterpret_cast<const float4 *>(r + half + i);
-                w.c[i] = c.x, w.c[i + 1] = c.y, w.c[i + 2] = c.z, w.c[i + 3] = c.w;
-                w.s[i] = n.x, w.s[i + 1] = n.y, w.s[i + 2] = n.z, w.s[i + 3] = n.w;
+            for (int i = 0; i < M; i += 2) {
+                const float4 c = *reinterpret_cast<const float4 *>(r + 2 * i);
+                const float4 n = *reinterpret_cast<const float4 *>(r + half + 2 * i);
+                w.c[i] = make_float2(c.x, c.y), w.c[i + 1] = make_float2(c.z, c.w);
+                w.s[i] = make_float2(n.x, n.y), w.s[i + 1] = make_float2(n.z, n.w);
             }
         } else {
-            const float2 c = *reinterpret_cast<const float2 *>(r);
-            const float2 n = *reinterpret_cast<const float2 *>(r + half);
-            w.c[0] = c.x, w.c[1] = c.y;
-            w.s[0] = n.x, w.s[1] = n.y;
+            w.c[0] = *reinterpret_cast<const float2 *>(r);
+            w.s[0] = *reinterpret_cast<const float2 *>(r + half);
         }
     } else {
         int axis = 0;
-#pragma unroll
-        for (int i = 0; i < M; ++i) {
-            while (f0 + i >= p.axis_end[axis])
+        auto next = [&](int f, float &c, float &n) {
+            while (f >= p.axis_end[axis])
                 ++axis;
             const float *r = row(axis);
-            w.c[i] = r[f0 + i];
-            w.s[i] = r[half + f0 + i];
+            c = r[f];
+            n = r[half + f];
+        };
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            next(f0 + 2 * i, w.c[i].x, w.s[i].x);
+            next(f0 + 2 * i + 1, w.c[i].y, w.s[i].y);
         }
     }
-    if (!INTER && !second) {
+    if (kLayout == kPart && !second) {
 #pragma unroll
         for (int i = 0; i < M; ++i)
-            w.s[i] = -w.s[i];
+            w.s[i] = make_float2(-w.s[i].x, -w.s[i].y);
     }
     return w;
 }
@@ -153,25 +180,37 @@ __device__ __forceinline__ unsigned row_mask()
     return L == 32 ? 0xffffffffu : ((1u << (L & 31)) - 1u) << (threadIdx.x & 31 & ~(L - 1));
 }
 
-// y turned by the angles (direction 1) or back (-1), in place.
-template <int N, int L, bool INTER>
-__device__ __forceinline__ void turn(const NormRopeParams &p, const Turn<N, INTER> &w, float *y, float direction)
+__device__ __forceinline__ float2 neg(const float2 &x) { return make_float2(-x.x, -x.y); }
+
+// y turned by the angles (or back), in place.
+template <bool kBack, int N, int L, Layout kLayout>
+__device__ __forceinline__ void turn(const NormRopeParams &p, const Turn<N, kLayout> &w, float2 *y)
 {
-    if constexpr (INTER) {
+    if constexpr (kLayout == kWhole) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float2 a = y[i], b = y[i + N / 4], s = kBack ? neg(w.s[i]) : w.s[i];
+            y[i] = __ffma2_rn(a, w.c[i], neg(__fmul2_rn(b, s)));
+            y[i + N / 4] = __ffma2_rn(a, s, __fmul2_rn(b, w.c[i]));
+        }
+    } else if constexpr (kLayout == kPairs) {
         if (w.on) {
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
-                const float a = y[2 * i], b = y[2 * i + 1], s = w.s[i] * direction;
-                y[2 * i] = a * w.c[i] - b * s;
-                y[2 * i + 1] = a * s + b * w.c[i];
+                const float a = y[i].x, b = y[i].y, c = i & 1 ? w.c[i / 2].y : w.c[i / 2].x;
+                const float s0 = i & 1 ? w.s[i / 2].y : w.s[i / 2].x, s = kBack ? -s0 : s0;
+                y[i].x = a * c - b * s;
+                y[i].y = a * s + b * c;
             }
         }
     } else if (p.rot > 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float o = __shfl_sync(row_mask<L>(), y[i], w.partner, L);
+        for (int i = 0; i < N / 2; ++i) {
+            float2 o;
+            o.x = __shfl_sync(row_mask<L>(), y[i].x, w.partner, L);
+            o.y = __shfl_sync(row_mask<L>(), y[i].y, w.partner, L);
             if (w.on)
-                y[i] = y[i] * w.c[i] + o * (w.s[i] * direction);
+                y[i] = __ffma2_rn(y[i], w.c[i], __fmul2_rn(o, kBack ? neg(w.s[i]) : w.s[i]));
         }
     }
 }
@@ -185,40 +224,38 @@ __device__ __forceinline__ float row_sum(float x)
     return x;
 }
 
-template <class E, int N>
-__device__ __forceinline__ void load_weight(const void *w, int e0, float *x)
+template <class E, int D, Layout kLayout>
+__device__ __forceinline__ void load_weight(const void *w, int e0, float2 *x)
 {
+    using S = Shape<E, D, kLayout>;
     if (w) {
-        Piece<E>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const E *>(w) + e0), x);
+        Piece<E>::unpack(S::load(static_cast<const E *>(w), e0), x);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            x[i] = 1.f;
+        for (int i = 0; i < S::N / 2; ++i)
+            x[i] = make_float2(1.f, 1.f);
     }
 }
 
 template <class E>
-__device__ __forceinline__ const uint4 *row_in(const HeadRows &h, int64_t t, int head, int e0)
+__device__ __forceinline__ E *row_of(const HeadRows &h, int64_t t, int head)
 {
-    return reinterpret_cast<const uint4 *>(static_cast<const E *>(h.data) + t * h.token_stride + head * h.head_stride + e0);
+    return static_cast<E *>(h.data) + t * h.token_stride + head * h.head_stride;
 }
 
-template <class E>
-__device__ __forceinline__ uint4 *row_out(const HeadRows &h, int64_t t, int head, int e0)
-{
-    return reinterpret_cast<uint4 *>(static_cast<E *>(h.data) + t * h.token_stride + head * h.head_stride + e0);
-}
+__device__ __forceinline__ float both(const float2 &x) { return x.x + x.y; }
 
 // Forward: a group of L lanes takes up to kHeads heads of one token: of q, of
 // k, or (copied to the cache) of v.
-template <class E, int D, bool INTER, int kHeads>
+template <class E, int D, Layout kLayout, int kHeads>
 __global__ void __launch_bounds__(kThreads)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p, int q_chunks, int kv_chunks)
 {
-    constexpr int N = Shape<E, D>::N, L = Shape<E, D>::L;
-    const int lane = threadIdx.x % L, e0 = lane * N;
+    using S = Shape<E, D, kLayout>;
+    constexpr int N = S::N, L = S::L;
+    const int lane = threadIdx.x % L, e0 = S::first(lane);
     const int chunks = q_chunks + kv_chunks * (p.slot_map ? 2 : 1);
-    const int64_t item = (int64_t)blockIdx.x * Shape<E, D>::kGroups + threadIdx.x / L;
+    const int64_t item = (int64_t)blockIdx.x * S::kGroups + threadIdx.x / L;
     if (item >= p.T * chunks)
         return;  // the whole row of lanes leaves together
     const int64_t t = item / chunks;
@@ -234,7 +271,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
         if (i < n)
-            raw[i] = *row_in<E>(in, t, h0 + i, e0);
+            raw[i] = S::load(row_of<E>(in, t, h0 + i), e0);
         else
             raw[i] = make_uint4(0u, 0u, 0u, 0u);
 
@@ -247,28 +284,28 @@ __global__ void __launch_bounds__(kThreads)
         if (slot >= 0 && page < p.n_pages) {
             head_step = (int64_t)D << p.page_shift;
             cache = static_cast<E *>(what == 1 ? p.k_cache : p.v_cache) + (page * p.Hkv + h0) * head_step +
-                    (slot & ((1 << p.page_shift) - 1)) * D + e0;
+                    (slot & ((1 << p.page_shift) - 1)) * D;
         } else if (slot >= 0) {
             record_bad_index(p.err, 0x52, slot);
         }
     }
     if (what != 2) {
-        float w[N];
-        load_weight<E, N>(what == 0 ? p.q_weight : p.k_weight, e0, w);
-        const Turn<N, INTER> tw = load_turn<N, INTER>(p, t, e0);
+        float2 w[N / 2];
+        load_weight<E, D, kLayout>(what == 0 ? p.q_weight : p.k_weight, e0, w);
+        const Turn<N, kLayout> tw = load_turn<N, kLayout>(p, t, e0);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-            float x[N];
+            float2 x[N / 2], ss = make_float2(0.f, 0.f);
             Piece<E>::unpack(raw[i], x);
-            float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                ss = fmaf(x[e], x[e], ss);
-            const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + p.eps);
+            for (int e = 0; e < N / 2; ++e)
+                ss = __ffma2_rn(x[e], x[e], ss);
+            const float r = rsqrtf(row_sum<L>(both(ss)) * (1.f / D) + p.eps);
+            const float2 r2 = make_float2(r, r);
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                x[e] = x[e] * r * w[e];
-            turn<N, L>(p, tw, x, 1.f);
+            for (int e = 0; e < N / 2; ++e)
+                x[e] = __fmul2_rn(__fmul2_rn(x[e], r2), w[e]);
+            turn<false, N, L>(p, tw, x);
             raw[i] = Piece<E>::pack(x);
         }
     }
@@ -278,9 +315,9 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kHeads; ++i)
         if (i < n) {
             if (keep)
-                *row_out<E>(out, t, h0 + i, e0) = raw[i];
+                S::store(row_of<E>(out, t, h0 + i), e0, raw[i]);
             if (cache)
-                *reinterpret_cast<uint4 *>(cache + i * head_step) = raw[i];
+                S::store(cache + i * head_step, e0, raw[i]);
         }
 }
 
@@ -288,16 +325,17 @@ __global__ void __launch_bounds__(kThreads)
 // keeps its part of the weights' gradients in registers; the block's groups
 // are summed in shared memory and leave one row of partial sums, so that the
 // result does not depend on any order of atomics.
-template <class E, int D, bool INTER, int kHeads>
+template <class E, int D, Layout kLayout, int kHeads>
 __global__ void __launch_bounds__(kThreads)
     qk_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, int q_chunks, int kv_chunks)
 {
-    constexpr int N = Shape<E, D>::N, L = Shape<E, D>::L, G = Shape<E, D>::kGroups;
+    using S = Shape<E, D, kLayout>;
+    constexpr int N = S::N, L = S::L, G = S::kGroups;
     __shared__ float part[G][D];
-    const int lane = threadIdx.x % L, e0 = lane * N, group = threadIdx.x / L;
+    const int lane = threadIdx.x % L, e0 = S::first(lane), group = threadIdx.x / L;
     const int chunks = q_chunks + kv_chunks;
     const int64_t items = p.T * chunks;
-    float aq[N] = {}, ak[N] = {};
+    float2 aq[N / 2] = {}, ak[N / 2] = {};
     for (int64_t item = (int64_t)blockIdx.x * G + group; item < items; item += (int64_t)gridDim.x * G) {
         const int64_t t = item / chunks;
         const int c = (int)(item - t * chunks);
@@ -309,42 +347,46 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < kHeads; ++i)
             if (i < n) {
-                xr[i] = *row_in<E>(in, t, h0 + i, e0);
-                yr[i] = *row_in<E>(dy, t, h0 + i, e0);
+                xr[i] = S::load(row_of<E>(in, t, h0 + i), e0);
+                yr[i] = S::load(row_of<E>(dy, t, h0 + i), e0);
             }
-        float w[N];
-        load_weight<E, N>(is_q ? p.q_weight : p.k_weight, e0, w);
-        const Turn<N, INTER> tw = load_turn<N, INTER>(p, t, e0);
+        float2 w[N / 2];
+        load_weight<E, D, kLayout>(is_q ? p.q_weight : p.k_weight, e0, w);
+        const Turn<N, kLayout> tw = load_turn<N, kLayout>(p, t, e0);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i)
             if (i < n) {  // the same for every lane of the row
-                float x[N], g[N];
+                float2 x[N / 2], g[N / 2], ss = make_float2(0.f, 0.f), sd = ss;
                 Piece<E>::unpack(xr[i], x);
                 Piece<E>::unpack(yr[i], g);
-                turn<N, L>(p, tw, g, -1.f);
-                float ss = 0.f, sd = 0.f;
+                turn<true, N, L>(p, tw, g);
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    ss = fmaf(x[e], x[e], ss);
-                    sd = fmaf(g[e] * w[e], x[e], sd);
+                for (int e = 0; e < N / 2; ++e) {
+                    ss = __ffma2_rn(x[e], x[e], ss);
+                    sd = __ffma2_rn(__fmul2_rn(g[e], w[e]), x[e], sd);
                 }
-                const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + p.eps);
-                const float m = row_sum<L>(sd) * (1.f / D) * r;  // mean(c o xhat)
+                const float r = rsqrtf(row_sum<L>(both(ss)) * (1.f / D) + p.eps);
+                const float m = -row_sum<L>(both(sd)) * (1.f / D) * r;  // -mean(c o xhat)
+                const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float xh = x[e] * r, dw = g[e] * xh;
-                    aq[e] += is_q ? dw : 0.f;
-                    ak[e] += is_q ? 0.f : dw;
-                    g[e] = r * (g[e] * w[e] - xh * m);
+                for (int e = 0; e < N / 2; ++e) {
+                    const float2 xh = __fmul2_rn(x[e], r2);
+                    if (is_q)
+                        aq[e] = __ffma2_rn(g[e], xh, aq[e]);
+                    else
+                        ak[e] = __ffma2_rn(g[e], xh, ak[e]);
+                    g[e] = __fmul2_rn(r2, __ffma2_rn(g[e], w[e], __fmul2_rn(xh, m2)));
                 }
-                *row_out<E>(dx, t, h0 + i, e0) = Piece<E>::pack(g);
+                S::store(row_of<E>(dx, t, h0 + i), e0, Piece<E>::pack(g));
             }
     }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            part[group][e0 + e] = which ? ak[e] : aq[e];
+        for (int e = 0; e < N / 2; ++e) {
+            const int at = e0 + (kLayout == kWhole && e >= N / 4 ? D / 2 - N / 2 : 0) + 2 * e;
+            *reinterpret_cast<float2 *>(&part[group][at]) = which ? ak[e] : aq[e];
+        }
         __syncthreads();
         if (threadIdx.x < D) {
             float a = 0.f;
@@ -378,28 +420,28 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *partial,
     }
 }
 
-template <class E, int D, bool INTER>
+template <class E, int D, Layout kLayout>
 cudaError_t launch_fwd(const NormRopeParams &p, cudaStream_t s)
 {
     constexpr int kHeads = 4;
     const int qc = (p.Hq + kHeads - 1) / kHeads, kc = (p.Hkv + kHeads - 1) / kHeads;
     const int64_t items = p.T * (qc + kc * (p.slot_map ? 2 : 1));
-    const int64_t blocks = (items + Shape<E, D>::kGroups - 1) / Shape<E, D>::kGroups;
+    const int64_t blocks = (items + Shape<E, D, kLayout>::kGroups - 1) / Shape<E, D, kLayout>::kGroups;
     if (blocks > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    qk_norm_rope_kernel<E, D, INTER, kHeads><<<(unsigned)blocks, kThreads, 0, s>>>(p, qc, kc);
+    qk_norm_rope_kernel<E, D, kLayout, kHeads><<<(unsigned)blocks, kThreads, 0, s>>>(p, qc, kc);
     return cudaGetLastError();
 }
 
-template <class E, int D, bool INTER>
+template <class E, int D, Layout kLayout>
 cudaError_t launch_bwd(const NormRopeParams &p, cudaStream_t s)
 {
     constexpr int kHeads = 2;
     const int qc = (p.Hq + kHeads - 1) / kHeads, kc = (p.Hkv + kHeads - 1) / kHeads;
     const int64_t items = p.T * (qc + kc);
-    const int64_t want = (items + Shape<E, D>::kGroups - 1) / Shape<E, D>::kGroups;
+    const int64_t want = (items + Shape<E, D, kLayout>::kGroups - 1) / Shape<E, D, kLayout>::kGroups;
     const int blocks = (int)(want < kNormRopeBwdBlocks ? want : kNormRopeBwdBlocks);
-    qk_norm_rope_bwd_kernel<E, D, INTER, kHeads><<<blocks, kThreads, 0, s>>>(p, qc, kc);
+    qk_norm_rope_bwd_kernel<E, D, kLayout, kHeads><<<blocks, kThreads, 0, s>>>(p, qc, kc);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -411,8 +453,10 @@ template <class E, int D>
 cudaError_t launch(const NormRopeParams &p, bool backward, cudaStream_t s)
 {
     if (p.interleaved)
-        return backward ? launch_bwd<E, D, true>(p, s) : launch_fwd<E, D, true>(p, s);
-    return backward ? launch_bwd<E, D, false>(p, s) : launch_fwd<E, D, false>(p, s);
+        return backward ? launch_bwd<E, D, kPairs>(p, s) : launch_fwd<E, D, kPairs>(p, s);
+    if (p.rot == D)
+        return backward ? launch_bwd<E, D, kWhole>(p, s) : launch_fwd<E, D, kWhole>(p, s);
+    return backward ? launch_bwd<E, D, kPart>(p, s) : launch_fwd<E, D, kPart>(p, s);
 }
 
 cudaError_t launch_any(const NormRopeParams &p, bool backward, cudaStream_t s)
