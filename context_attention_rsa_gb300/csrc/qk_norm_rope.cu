@@ -13,10 +13,13 @@
 //
 // Bound by HBM: every element is read once and written once, about 10 (20
 // backward) operations apart.  A row of d elements lies across L = d * size / 16
-// lanes, its sums are shuffles among those, and a group of L lanes takes kHeads
-// heads of one token with all their loads in flight at once: the token's cosines
-// and sines are read once per group.  Which elements a lane holds depends on the
-// rotation (Layout):
+// lanes, its sums are shuffles among those.  A group of L lanes goes through a run
+// of items (kHeads heads of one token each): their rows come by 16-byte
+// asynchronous copies into a ring of kStages items in shared memory, so that the
+// bytes in flight do not sit in registers and do not wait for the arithmetic
+// (loaded into registers an item at a time, a 32768-token prompt took 305 us); the
+// token's cosines and sines are read when the token changes.  Which elements a lane
+// holds depends on the rotation (Layout):
 //   whole   halves of the whole row turn (rot = d): 8 bytes of each half, so that a
 //           lane has both elements of its pairs and turns them two at a time with
 //           packed fp32 arithmetic;
@@ -32,6 +35,8 @@ namespace rsa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kStages = 4;       // items of a group's ring
+constexpr int kBlocksPerSm = 3;  // 64 KB of ring each
 
 enum Layout { kWhole, kPairs, kPart };
 
@@ -83,6 +88,7 @@ struct Shape {
     static constexpr int kGroups = kThreads / L;
     // A lane's first element (kWhole: of its first run of N / 2; the second one is D / 2 on).
     static __device__ __forceinline__ int first(int lane) { return kLayout == kWhole ? lane * (N / 2) : lane * N; }
+    // (also of a row in shared memory)
     static __device__ __forceinline__ uint4 load(const E *row, int e0)
     {
         if constexpr (kLayout == kWhole) {
@@ -245,141 +251,234 @@ __device__ __forceinline__ E *row_of(const HeadRows &h, int64_t t, int head)
 
 __device__ __forceinline__ float both(const float2 &x) { return x.x + x.y; }
 
-// Forward: a group of L lanes takes up to kHeads heads of one token: of q, of
-// k, or (copied to the cache) of v.
+__device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int kPending>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// A group's place in the items: chunk c (of kHeads heads) of token t.
+struct Item {
+    int64_t t;
+    int c;
+    __device__ __forceinline__ void step(int chunks)
+    {
+        if (++c == chunks) {
+            c = 0;
+            ++t;
+        }
+    }
+};
+
+// The group's run of items: equal runs, the same number for every group but the last ones.
+struct Run {
+    Item first;
+    int n;
+};
+__device__ __forceinline__ Run run_of(int64_t items, int chunks, int groups_per_block)
+{
+    const int64_t groups = (int64_t)gridDim.x * groups_per_block, each = (items + groups - 1) / groups;
+    const int64_t g = (int64_t)blockIdx.x * groups_per_block + threadIdx.x / (kThreads / groups_per_block);
+    const int64_t i0 = min(items, g * each);
+    return Run{{i0 / chunks, (int)(i0 % chunks)}, (int)(min(items, i0 + each) - i0)};
+}
+
+// Forward: an item is up to kHeads heads of q, of k, or (copied to the cache) of v.
 template <class E, int D, Layout kLayout, int kHeads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     qk_norm_rope_kernel(const __grid_constant__ NormRopeParams p, int q_chunks, int kv_chunks)
 {
     using S = Shape<E, D, kLayout>;
     constexpr int N = S::N, L = S::L;
-    const int lane = threadIdx.x % L, e0 = S::first(lane);
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x % L, e0 = S::first(lane), group = threadIdx.x / L;
+    E *ring = reinterpret_cast<E *>(smem) + group * (kStages * kHeads * D);  // [kStages][kHeads][D]
     const int chunks = q_chunks + kv_chunks * (p.slot_map ? 2 : 1);
-    const int64_t item = (int64_t)blockIdx.x * S::kGroups + threadIdx.x / L;
-    if (item >= p.T * chunks)
-        return;  // the whole row of lanes leaves together
-    const int64_t t = item / chunks;
-    int c = (int)(item - t * chunks);
-    const int what = c < q_chunks ? 0 : (c < q_chunks + kv_chunks ? 1 : 2);
-    c -= what == 0 ? 0 : (what == 1 ? q_chunks : q_chunks + kv_chunks);
-    const HeadRows &in = what == 0 ? p.q : (what == 1 ? p.k : p.v);
-    const int heads = what == 0 ? p.Hq : p.Hkv;
-    const int h0 = c * kHeads;
-    const int n = min(kHeads, heads - h0);
-
-    uint4 raw[kHeads];
+    const Run run = run_of(p.T * chunks, chunks, S::kGroups);
+    // what an item is of: 0 q, 1 k, 2 v; its first head and their number
+    struct Part {
+        int what, h0, n;
+    };
+    auto part = [&](int c) {
+        Part x;
+        x.what = c < q_chunks ? 0 : (c < q_chunks + kv_chunks ? 1 : 2);
+        x.h0 = (c - (x.what == 0 ? 0 : (x.what == 1 ? q_chunks : q_chunks + kv_chunks))) * kHeads;
+        x.n = min(kHeads, (x.what == 0 ? p.Hq : p.Hkv) - x.h0);
+        return x;
+    };
+    Item ahead = run.first;
+    auto fetch = [&](int k) {
+        if (k < run.n) {
+            const Part x = part(ahead.c);
+            const HeadRows &in = x.what == 0 ? p.q : (x.what == 1 ? p.k : p.v);
+            const E *src = row_of<E>(in, ahead.t, x.h0) + lane * N;
+            E *dst = ring + (k % kStages) * (kHeads * D) + lane * N;
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-        if (i < n)
-            raw[i] = S::load(row_of<E>(in, t, h0 + i), e0);
-        else
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-
-    // The token's rows of the cache, if it has a slot.
-    E *cache = nullptr;
-    int64_t head_step = 0;
-    if (what != 0 && p.slot_map) {
-        const int64_t slot = p.slot_map[t];
-        const int64_t page = slot >> p.page_shift;
-        if (slot >= 0 && page < p.n_pages) {
-            head_step = (int64_t)D << p.page_shift;
-            cache = static_cast<E *>(what == 1 ? p.k_cache : p.v_cache) + (page * p.Hkv + h0) * head_step +
-                    (slot & ((1 << p.page_shift) - 1)) * D;
-        } else if (slot >= 0) {
-            record_bad_index(p.err, 0x52, slot);
+            for (int i = 0; i < kHeads; ++i)
+                if (i < x.n)
+                    copy_async(dst + i * D, src + i * in.head_stride);
+            ahead.step(chunks);
         }
-    }
-    if (what != 2) {
-        float2 w[N / 2];
-        load_weight<E, D, kLayout>(what == 0 ? p.q_weight : p.k_weight, e0, w);
-        const Turn<N, kLayout> tw = load_turn<N, kLayout>(p, t, e0);
+        copies_commit();
+    };
+    for (int k = 0; k < kStages - 1; ++k)
+        fetch(k);
+    Item at = run.first;
+    int64_t token = -1, slot = -1;
+    int weight = -1;
+    float2 w[N / 2];
+    Turn<N, kLayout> tw;
+    for (int k = 0; k < run.n; ++k, at.step(chunks)) {
+        fetch(k + kStages - 1);
+        if (at.t != token) {
+            token = at.t;
+            tw = load_turn<N, kLayout>(p, token, e0);
+            slot = p.slot_map ? p.slot_map[token] : -1;
+        }
+        const Part x = part(at.c);
+        if (x.what != 2 && x.what != weight) {
+            weight = x.what;
+            load_weight<E, D, kLayout>(weight == 0 ? p.q_weight : p.k_weight, e0, w);
+        }
+        // The token's rows of the cache, if it has a slot.
+        E *cache = nullptr;
+        const int64_t head_step = (int64_t)D << p.page_shift;
+        if (x.what != 0 && slot >= 0) {
+            const int64_t page = slot >> p.page_shift;
+            if (page < p.n_pages)
+                cache = static_cast<E *>(x.what == 1 ? p.k_cache : p.v_cache) + (page * p.Hkv + x.h0) * head_step +
+                        (slot & ((1 << p.page_shift) - 1)) * D;
+            else
+                record_bad_index(p.err, 0x52, slot);
+        }
+        const HeadRows &out = x.what == 0 ? p.q_out : p.k_out;
+        const bool keep = x.what != 2 && out.data;
+        copies_wait<kStages - 1>();
+        __syncwarp(row_mask<L>());  // the other lanes' copies too
+        const E *src = ring + (k % kStages) * (kHeads * D);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-            float2 x[N / 2], ss = make_float2(0.f, 0.f);
-            Piece<E>::unpack(raw[i], x);
+            if (i >= x.n)
+                break;  // the same for every lane of the row
+            uint4 raw = S::load(src + i * D, e0);
+            if (x.what != 2) {
+                float2 y[N / 2], ss = make_float2(0.f, 0.f);
+                Piece<E>::unpack(raw, y);
 #pragma unroll
-            for (int e = 0; e < N / 2; ++e)
-                ss = __ffma2_rn(x[e], x[e], ss);
-            const float r = rsqrtf(row_sum<L>(both(ss)) * (1.f / D) + p.eps);
-            const float2 r2 = make_float2(r, r);
+                for (int e = 0; e < N / 2; ++e)
+                    ss = __ffma2_rn(y[e], y[e], ss);
+                const float r = rsqrtf(row_sum<L>(both(ss)) * (1.f / D) + p.eps);
+                const float2 r2 = make_float2(r, r);
 #pragma unroll
-            for (int e = 0; e < N / 2; ++e)
-                x[e] = __fmul2_rn(__fmul2_rn(x[e], r2), w[e]);
-            turn<false, N, L>(p, tw, x);
-            raw[i] = Piece<E>::pack(x);
-        }
-    }
-    const HeadRows &out = what == 0 ? p.q_out : p.k_out;
-    const bool keep = what != 2 && out.data;
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-        if (i < n) {
+                for (int e = 0; e < N / 2; ++e)
+                    y[e] = __fmul2_rn(__fmul2_rn(y[e], r2), w[e]);
+                turn<false, N, L>(p, tw, y);
+                raw = Piece<E>::pack(y);
+            }
             if (keep)
-                S::store(row_of<E>(out, t, h0 + i), e0, raw[i]);
+                S::store(row_of<E>(out, token, x.h0 + i), e0, raw);
             if (cache)
-                S::store(cache + i * head_step, e0, raw[i]);
+                S::store(cache + i * head_step, e0, raw);
         }
+        __syncwarp(row_mask<L>());  // every lane has read the item: its place may be filled again
+    }
 }
 
-// Backward: as above, but a group goes through many (token, heads) items and
-// keeps its part of the weights' gradients in registers; the block's groups
-// are summed in shared memory and leave one row of partial sums, so that the
-// result does not depend on any order of atomics.
+// Backward: as above with two rows a head, of x and of dy; a group keeps its part
+// of the weights' gradients in registers; the block's groups are summed in shared
+// memory and leave one row of partial sums, so that the result does not depend on
+// any order of atomics.
 template <class E, int D, Layout kLayout, int kHeads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     qk_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams p, int q_chunks, int kv_chunks)
 {
     using S = Shape<E, D, kLayout>;
     constexpr int N = S::N, L = S::L, G = S::kGroups;
-    __shared__ float part[G][D];
+    extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x % L, e0 = S::first(lane), group = threadIdx.x / L;
+    E *ring = reinterpret_cast<E *>(smem) + group * (kStages * 2 * kHeads * D);  // [kStages][x, dy][kHeads][D]
     const int chunks = q_chunks + kv_chunks;
-    const int64_t items = p.T * chunks;
+    const Run run = run_of(p.T * chunks, chunks, G);
     float2 aq[N / 2] = {}, ak[N / 2] = {};
-    for (int64_t item = (int64_t)blockIdx.x * G + group; item < items; item += (int64_t)gridDim.x * G) {
-        const int64_t t = item / chunks;
-        const int c = (int)(item - t * chunks);
-        const bool is_q = c < q_chunks;
-        const int h0 = (is_q ? c : c - q_chunks) * kHeads;
-        const int n = min(kHeads, (is_q ? p.Hq : p.Hkv) - h0);
-        const HeadRows &in = is_q ? p.q : p.k, &dy = is_q ? p.dq_out : p.dk_out, &dx = is_q ? p.q_out : p.k_out;
-        uint4 xr[kHeads], yr[kHeads];
+    Item ahead = run.first;
+    auto fetch = [&](int k) {
+        if (k < run.n) {
+            const bool is_q = ahead.c < q_chunks;
+            const int h0 = (is_q ? ahead.c : ahead.c - q_chunks) * kHeads, n = min(kHeads, (is_q ? p.Hq : p.Hkv) - h0);
+            const HeadRows &in = is_q ? p.q : p.k, &dy = is_q ? p.dq_out : p.dk_out;
+            const E *xs = row_of<E>(in, ahead.t, h0) + lane * N, *ys = row_of<E>(dy, ahead.t, h0) + lane * N;
+            E *dst = ring + (k % kStages) * (2 * kHeads * D) + lane * N;
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-            if (i < n) {
-                xr[i] = S::load(row_of<E>(in, t, h0 + i), e0);
-                yr[i] = S::load(row_of<E>(dy, t, h0 + i), e0);
-            }
-        float2 w[N / 2];
-        load_weight<E, D, kLayout>(is_q ? p.q_weight : p.k_weight, e0, w);
-        const Turn<N, kLayout> tw = load_turn<N, kLayout>(p, t, e0);
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-            if (i < n) {  // the same for every lane of the row
-                float2 x[N / 2], g[N / 2], ss = make_float2(0.f, 0.f), sd = ss;
-                Piece<E>::unpack(xr[i], x);
-                Piece<E>::unpack(yr[i], g);
-                turn<true, N, L>(p, tw, g);
-#pragma unroll
-                for (int e = 0; e < N / 2; ++e) {
-                    ss = __ffma2_rn(x[e], x[e], ss);
-                    sd = __ffma2_rn(__fmul2_rn(g[e], w[e]), x[e], sd);
+            for (int i = 0; i < kHeads; ++i)
+                if (i < n) {
+                    copy_async(dst + i * D, xs + i * in.head_stride);
+                    copy_async(dst + (kHeads + i) * D, ys + i * dy.head_stride);
                 }
-                const float r = rsqrtf(row_sum<L>(both(ss)) * (1.f / D) + p.eps);
-                const float m = -row_sum<L>(both(sd)) * (1.f / D) * r;  // -mean(c o xhat)
-                const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+            ahead.step(chunks);
+        }
+        copies_commit();
+    };
+    for (int k = 0; k < kStages - 1; ++k)
+        fetch(k);
+    Item at = run.first;
+    int64_t token = -1;
+    int weight = -1;
+    float2 w[N / 2];
+    Turn<N, kLayout> tw;
+    for (int k = 0; k < run.n; ++k, at.step(chunks)) {
+        fetch(k + kStages - 1);
+        if (at.t != token) {
+            token = at.t;
+            tw = load_turn<N, kLayout>(p, token, e0);
+        }
+        const bool is_q = at.c < q_chunks;
+        const int h0 = (is_q ? at.c : at.c - q_chunks) * kHeads, n = min(kHeads, (is_q ? p.Hq : p.Hkv) - h0);
+        const HeadRows &dx = is_q ? p.q_out : p.k_out;
+        if (weight != is_q) {
+            weight = is_q;
+            load_weight<E, D, kLayout>(is_q ? p.q_weight : p.k_weight, e0, w);
+        }
+        copies_wait<kStages - 1>();
+        __syncwarp(row_mask<L>());
+        const E *src = ring + (k % kStages) * (2 * kHeads * D);
 #pragma unroll
-                for (int e = 0; e < N / 2; ++e) {
-                    const float2 xh = __fmul2_rn(x[e], r2);
-                    if (is_q)
-                        aq[e] = __ffma2_rn(g[e], xh, aq[e]);
-                    else
-                        ak[e] = __ffma2_rn(g[e], xh, ak[e]);
-                    g[e] = __fmul2_rn(r2, __ffma2_rn(g[e], w[e], __fmul2_rn(xh, m2)));
-                }
-                S::store(row_of<E>(dx, t, h0 + i), e0, Piece<E>::pack(g));
+        for (int i = 0; i < kHeads; ++i) {
+            if (i >= n)
+                break;  // the same for every lane of the row
+            float2 x[N / 2], g[N / 2], ss = make_float2(0.f, 0.f), sd = ss;
+            Piece<E>::unpack(S::load(src + i * D, e0), x);
+            Piece<E>::unpack(S::load(src + (kHeads + i) * D, e0), g);
+            turn<true, N, L>(p, tw, g);
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) {
+                ss = __ffma2_rn(x[e], x[e], ss);
+                sd = __ffma2_rn(__fmul2_rn(g[e], w[e]), x[e], sd);
             }
+            const float r = rsqrtf(row_sum<L>(both(ss)) * (1.f / D) + p.eps);
+            const float m = -row_sum<L>(both(sd)) * (1.f / D) * r;  // -mean(c o xhat)
+            const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) {
+                const float2 xh = __fmul2_rn(x[e], r2);
+                if (is_q)
+                    aq[e] = __ffma2_rn(g[e], xh, aq[e]);
+                else
+                    ak[e] = __ffma2_rn(g[e], xh, ak[e]);
+                g[e] = __fmul2_rn(r2, __ffma2_rn(g[e], w[e], __fmul2_rn(xh, m2)));
+            }
+            S::store(row_of<E>(dx, token, h0 + i), e0, Piece<E>::pack(g));
+        }
+        __syncwarp(row_mask<L>());
     }
+    __syncthreads();  // the ring becomes the sums' table
+    float(*part)[D] = reinterpret_cast<float(*)[D]>(smem);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
@@ -420,29 +519,46 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *partial,
     }
 }
 
+// Blocks for `items`, at most `most`; ring bytes of a block: kHeads rows (of `rows` tensors) a stage and group.
+template <class E, int D, Layout kLayout>
+int blocks_for(int64_t items, int most)
+{
+    const int64_t want = (items + Shape<E, D, kLayout>::kGroups - 1) / Shape<E, D, kLayout>::kGroups;
+    return (int)(want < most ? want : most);
+}
+
+template <class E, int D, Layout kLayout>
+constexpr int ring_bytes(int kHeads, int rows)
+{
+    return Shape<E, D, kLayout>::kGroups * kStages * rows * kHeads * D * (int)sizeof(E);
+}
+
 template <class E, int D, Layout kLayout>
 cudaError_t launch_fwd(const NormRopeParams &p, cudaStream_t s)
 {
-    constexpr int kHeads = 4;
+    constexpr int kHeads = 4, kSmem = ring_bytes<E, D, kLayout>(kHeads, 1);
+    auto kernel = qk_norm_rope_kernel<E, D, kLayout, kHeads>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
     const int qc = (p.Hq + kHeads - 1) / kHeads, kc = (p.Hkv + kHeads - 1) / kHeads;
-    const int64_t items = p.T * (qc + kc * (p.slot_map ? 2 : 1));
-    const int64_t blocks = (items + Shape<E, D, kLayout>::kGroups - 1) / Shape<E, D, kLayout>::kGroups;
-    if (blocks > 0x7fffffffLL)
-        return cudaErrorInvalidConfiguration;
-    qk_norm_rope_kernel<E, D, kLayout, kHeads><<<(unsigned)blocks, kThreads, 0, s>>>(p, qc, kc);
+    const int blocks = blocks_for<E, D, kLayout>(p.T * (qc + kc * (p.slot_map ? 2 : 1)), kBlocksPerSm * 152);
+    kernel<<<blocks, kThreads, kSmem, s>>>(p, qc, kc);
     return cudaGetLastError();
 }
 
 template <class E, int D, Layout kLayout>
 cudaError_t launch_bwd(const NormRopeParams &p, cudaStream_t s)
 {
-    constexpr int kHeads = 2;
+    constexpr int kHeads = 2, kSmem = ring_bytes<E, D, kLayout>(kHeads, 2);
+    auto kernel = qk_norm_rope_bwd_kernel<E, D, kLayout, kHeads>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
     const int qc = (p.Hq + kHeads - 1) / kHeads, kc = (p.Hkv + kHeads - 1) / kHeads;
-    const int64_t items = p.T * (qc + kc);
-    const int64_t want = (items + Shape<E, D, kLayout>::kGroups - 1) / Shape<E, D, kLayout>::kGroups;
-    const int blocks = (int)(want < kNormRopeBwdBlocks ? want : kNormRopeBwdBlocks);
-    qk_norm_rope_bwd_kernel<E, D, kLayout, kHeads><<<blocks, kThreads, 0, s>>>(p, qc, kc);
-    cudaError_t e = cudaGetLastError();
+    const int blocks = blocks_for<E, D, kLayout>(p.T * (qc + kc), kNormRopeBwdBlocks);
+    kernel<<<blocks, kThreads, kSmem, s>>>(p, qc, kc);
+    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     weight_grad_kernel<<<dim3(D / 32, 2), 1024, 0, s>>>(p.partial, blocks, D, p.dq_weight, p.dk_weight);

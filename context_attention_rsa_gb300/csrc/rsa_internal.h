@@ -224,7 +224,7 @@ cudaError_t launch_page_plan(const PagePlanParams &p, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_fwd(const NormRopeParams &p, cudaStream_t s);
 // Two launches: gradients and partial sums, then the sums of the weights' gradients.
 cudaError_t launch_qk_norm_rope_bwd(const NormRopeParams &p, cudaStream_t s);
-constexpr int kNormRopeBwdBlocks = 608;  // blocks of partial weight gradients: four on each of 152 SMs
+constexpr int kNormRopeBwdBlocks = 304;  // blocks of partial weight gradients: two on each of 152 SMs
 cudaError_t launch_prefix_attn_bf16(const PrefixAttnParams &p, cudaStream_t s);
 cudaError_t launch_prefix_attn_f32(const PrefixAttnParams &p, cudaStream_t s);
 // Joins the pieces of every row: the second launch of the attention.
