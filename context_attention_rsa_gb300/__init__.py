@@ -127,6 +127,8 @@ def load(build: bool = True):
     """Load librsa.so (building it in-tree first if it is stale); the
     RSA_DEBUG variant when the environment sets RSA_DEBUG=1."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path(build)

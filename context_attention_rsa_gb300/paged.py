@@ -18,6 +18,7 @@ with other lengths: what depends on them is read on the device.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -53,12 +54,16 @@ class PagePlan(NamedTuple):
 
 
 _p, _i32, _i64, _size = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-_args = ctypes.POINTER(NormRopeArgs)
+# NormRopeArgs as one packed record (native alignment): filling the ctypes fields one by
+# one cost more than the launch.
+_NORM_ROPE = struct.Struct("@iqiiiPqqPqqPPfiiiiiiiPPq")
+assert _NORM_ROPE.size == ctypes.sizeof(NormRopeArgs)
+
 SIGS = {
     "rsa_page_plan": [_p, _p, _i32, _i32, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _p],
-    "rsa_qk_norm_rope_fwd": [_args, Heads, Heads, Heads, _p, _p, _p, _i32, _i64, _p],
+    "rsa_qk_norm_rope_fwd": [_p, Heads, Heads, Heads, _p, _p, _p, _i32, _i64, _p],
     "rsa_qk_norm_rope_bwd_workspace_size": [_i32, ctypes.POINTER(_size)],
-    "rsa_qk_norm_rope_bwd": [_args, Heads, Heads, Heads, Heads, _p, _p, _p, _size, _p],
+    "rsa_qk_norm_rope_bwd": [_p, Heads, Heads, Heads, Heads, _p, _p, _p, _size, _p],
     "rsa_prefix_attn_workspace_size": [_i32, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_size)],
     "rsa_prefix_attn_fwd": [_p, _i64, _i64, _p, _p, _i32, _i64, _i32, _i32, _i32, _i32, _i64, _p, _p, _i32, _p, _i64, _i32,
                             _p, _i64, _p, _p, _p, _size, _p],
@@ -75,19 +80,24 @@ def _dtype(t: torch.Tensor) -> int:
 
 
 def _check(name: str, t, dim: int, dtype: torch.dtype, device: torch.device, contiguous: bool = True) -> None:
+    try:
+        if t.dtype is dtype and t.dim() == dim and t.device == device and (not contiguous or t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
         raise TypeError(f"{name} must be a CUDA tensor on {device}")
     if t.dtype != dtype or t.dim() != dim:
         raise ValueError(f"{name} must be a {dim}-d {dtype} tensor (got {t.dim()}-d {t.dtype})")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _heads(name: str, t, dtype: torch.dtype, device: torch.device, shape=None) -> Heads:
+def _row_layout(name: str, t, dtype: torch.dtype, device: torch.device, shape=None) -> Tuple[int, int, int]:
+    """Address, token and head stride of a [T, H, d] operand."""
     _check(name, t, 3, dtype, device, contiguous=False)
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
     T, H, d = t.shape
+    if shape is not None and (T, H, d) != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (got {(T, H, d)})")
     ts, hs, es = t.stride()
     if es != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
@@ -96,26 +106,36 @@ def _heads(name: str, t, dtype: torch.dtype, device: torch.device, shape=None) -
         hs = d
     if T == 1:
         ts = H * hs
-    return Heads(t.data_ptr(), ts, hs)
+    return t.data_ptr(), ts, hs
+
+
+def _heads(name: str, t, dtype: torch.dtype, device: torch.device, shape=None) -> Heads:
+    return Heads(*_row_layout(name, t, dtype, device, shape))
+
+
+# The device's current stream as a bare handle (a Stream object takes longer to make than a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call_on(device: torch.device, fn: str, stream, temporaries: Sequence[torch.Tensor], *args) -> None:
     """The library's call on `device` and `stream` (default: the device's current stream)."""
-    lib = load()
-    current = torch.cuda.current_device()
-    if device.index != current:
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call_on(device, fn, stream, temporaries, *args)
-    if stream is None:
-        handle = torch.cuda.current_stream(current).cuda_stream
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if temporaries and hasattr(stream, "cuda_stream"):
+    handle = _raw_stream(index)
+    if stream is not None:
+        if hasattr(stream, "cuda_stream"):
+            handle = stream.cuda_stream
             # made on the current stream, used on another one: not to be handed out again before it is done
             for t in temporaries:
                 t.record_stream(stream)
-        elif temporaries and handle != torch.cuda.current_stream(current).cuda_stream:
+        elif temporaries and handle != int(stream):
             raise ValueError("with a bare stream handle other than the current stream's, pass every output and workspace")
+        else:
+            handle = int(stream)
+    lib = load()
     st = getattr(lib, fn)(*args, handle)
     if st != 0:
         detail = lib.rsa_last_error_string()
@@ -167,43 +187,44 @@ def page_plan(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torc
     return out
 
 
-def _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections) -> NormRopeArgs:
+def _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections) -> bytes:
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
         raise TypeError("q must be a CUDA tensor [T, Hq, d]")
     dev, dt = q.device, q.dtype
-    a = NormRopeArgs()
-    a.dt = _dtype(q)
-    T, a.Hq, d = q.shape
-    a.T, a.d = T, d
-    a.q = _heads("q", q, dt, dev)
-    a.k = _heads("k", k, dt, dev)
-    a.Hkv = k.shape[1]
+    code = _dtype(q)
+    T, Hq, d = q.shape
+    q_at, k_at = _row_layout("q", q, dt, dev), _row_layout("k", k, dt, dev)
     if k.shape[0] != T or k.shape[2] != d:
         raise ValueError("q [T, Hq, d] and k [T, Hkv, d] must agree")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check(name, w, 1, dt, dev)
-            if w.shape[0] != d:
-                raise ValueError(f"{name} must hold d={d} values")
-            setattr(a, name, w.data_ptr())
-    a.eps, a.interleaved, a.n_axes = eps, int(bool(interleaved)), 1
+    wq = wk = rot = max_pos = table = pos = 0
+    if q_weight is not None:
+        _check("q_weight", q_weight, 1, dt, dev)
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        _check("k_weight", k_weight, 1, dt, dev)
+        wk = k_weight.data_ptr()
+    if (wq and q_weight.shape[0] != d) or (wk and k_weight.shape[0] != d):
+        raise ValueError(f"q_weight and k_weight must hold d={d} values")
+    axes, parts = 1, (0, 0, 0, 0)
     if cos_sin is not None:
         _check("cos_sin", cos_sin, 2, torch.float32, dev)
-        a.max_pos, a.rot = cos_sin.shape
-        a.cos_sin = cos_sin.data_ptr()
-        axes = 1 if sections is None else len(sections)
-        if not 1 <= axes <= 4:
-            raise ValueError("sections must name one to four axes")
-        a.n_axes = axes
+        max_pos, rot = cos_sin.shape
+        table = cos_sin.data_ptr()
         if sections is not None:
-            a.sections[:axes] = sections
+            axes = len(sections)
+            if not 1 <= axes <= 4:
+                raise ValueError("sections must name one to four axes")
+            if axes == 1 and sections[0] != rot // 2:
+                raise ValueError("one section must hold all rot/2 frequencies")
+            parts = (*sections, 0, 0, 0)[:4]
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a CUDA tensor")
         _check("positions", positions, positions.dim() if axes == 1 else 2, torch.int64, dev)
-        if positions.numel() != axes * T or positions.shape[-1] != T:
+        if positions.shape[-1] != T or positions.numel() != axes * T:
             raise ValueError(f"positions must be int64 [{axes}, {T}]" if axes > 1 else f"positions must be int64 [{T}]")
-        a.positions = positions.data_ptr()
-        if axes == 1 and sections is not None and sections[0] != a.rot // 2:
-            raise ValueError("one section must hold all rot/2 frequencies")
-    return a
+        pos = positions.data_ptr()
+    return _NORM_ROPE.pack(code, T, Hq, k.shape[1], d, *q_at, *k_at, wq, wk, eps, rot, 1 if interleaved else 0, axes, *parts,
+                           pos, table, max_pos)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6, interleaved: bool = False,
@@ -217,28 +238,28 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6
     and v_cache [n_pages, Hkv, page_size, d].  Returns (q_out, k_out); k_out is
     None if it is not given and there is a cache.  q_out may be q and k_out k."""
     a = _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections)
-    dev, dt = q.device, q.dtype
+    dev, dt, q_shape, k_shape = q.device, q.dtype, tuple(q.shape), tuple(k.shape)
     made = []
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        q_out = torch.empty(q_shape, dtype=dt, device=dev)
         made.append(q_out)
     if k_out is None and slot_map is None:
-        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+        k_out = torch.empty(k_shape, dtype=dt, device=dev)
         made.append(k_out)
-    qo = _heads("q_out", q_out, dt, dev, q.shape)
-    ko = Heads() if k_out is None else _heads("k_out", k_out, dt, dev, k.shape)
+    qo = _heads("q_out", q_out, dt, dev, q_shape)
+    ko = Heads() if k_out is None else _heads("k_out", k_out, dt, dev, k_shape)
     if slot_map is None:
         if v is not None or k_cache is not None or v_cache is not None:
             raise ValueError("v, k_cache and v_cache go with slot_map")
-        _call_on(dev, "rsa_qk_norm_rope_fwd", stream, made, ctypes.byref(a), qo, ko, Heads(), None, None, None, 0, 0)
+        _call_on(dev, "rsa_qk_norm_rope_fwd", stream, made, a, qo, ko, Heads(), None, None, None, 0, 0)
         return q_out, k_out
     _check("slot_map", slot_map, 1, torch.int64, dev)
-    if slot_map.shape[0] != a.T:
-        raise ValueError(f"slot_map must hold T={a.T} slots")
-    vh = _heads("v", v, dt, dev, k.shape)
-    n_pages, page_size = _check_caches(k_cache, v_cache, a.Hkv, a.d, dt, dev)
-    _call_on(dev, "rsa_qk_norm_rope_fwd", stream, made, ctypes.byref(a), qo, ko, vh, slot_map.data_ptr(),
-             k_cache.data_ptr(), v_cache.data_ptr(), page_size, n_pages)
+    if slot_map.shape[0] != q_shape[0]:
+        raise ValueError(f"slot_map must hold T={q_shape[0]} slots")
+    vh = _heads("v", v, dt, dev, k_shape)
+    n_pages, page_size = _check_caches(k_cache, v_cache, k_shape[1], k_shape[2], dt, dev)
+    _call_on(dev, "rsa_qk_norm_rope_fwd", stream, made, a, qo, ko, vh, slot_map.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), page_size, n_pages)
     return q_out, k_out
 
 
@@ -249,26 +270,24 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_si
     results: (dq, dk in q's dtype, dq_weight, dk_weight fp32 [d], None for a
     weight that is None).  dq may be dq_out and dk may be dk_out."""
     a = _norm_rope_args(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections)
-    dev, dt = q.device, q.dtype
-    gq, gk = _heads("dq_out", dq_out, dt, dev, q.shape), _heads("dk_out", dk_out, dt, dev, k.shape)
+    dev, dt, q_shape, k_shape = q.device, q.dtype, tuple(q.shape), tuple(k.shape)
+    gq, gk = _heads("dq_out", dq_out, dt, dev, q_shape), _heads("dk_out", dk_out, dt, dev, k_shape)
     made = []
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=dt, device=dev)
-        made.append(dq)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=dt, device=dev)
-        made.append(dk)
-    dw = torch.empty((2, a.d), dtype=torch.float32, device=dev)
-    made.append(dw)
+
+    def make(shape, dtype):
+        made.append(torch.empty(shape, dtype=dtype, device=dev))
+        return made[-1]
+    dq = make(q_shape, dt) if dq is None else dq
+    dk = make(k_shape, dt) if dk is None else dk
+    d = q_shape[2]
+    dwq = None if q_weight is None else make((d,), torch.float32)
+    dwk = None if k_weight is None else make((d,), torch.float32)
     if workspace is None:
         n = ctypes.c_size_t(0)
-        load().rsa_qk_norm_rope_bwd_workspace_size(a.d, ctypes.byref(n))
-        workspace = torch.empty(max(n.value, 1), dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    dwq, dwk = dw.unbind(0)
-    dwq, dwk = (None if q_weight is None else dwq), (None if k_weight is None else dwk)
-    _call_on(dev, "rsa_qk_norm_rope_bwd", stream, made, ctypes.byref(a), gq, gk, _heads("dq", dq, dt, dev, q.shape),
-             _heads("dk", dk, dt, dev, k.shape), None if dwq is None else dwq.data_ptr(),
+        load().rsa_qk_norm_rope_bwd_workspace_size(d, ctypes.byref(n))
+        workspace = make((max(n.value, 1),), torch.uint8)
+    _call_on(dev, "rsa_qk_norm_rope_bwd", stream, made, a, gq, gk, _heads("dq", dq, dt, dev, q_shape),
+             _heads("dk", dk, dt, dev, k_shape), None if dwq is None else dwq.data_ptr(),
              None if dwk is None else dwk.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dwq, dwk
 
@@ -319,7 +338,7 @@ def prefix_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages=Non
         raise ValueError("k_cache must be [n_pages, Hkv, page_size, d]")
     Hkv = k_cache.shape[1]
     n_pages, page_size = _check_caches(k_cache, v_cache, Hkv, d, dt, dev)
-    qh = _heads("q", q, dt, dev)
+    q_at = _row_layout("q", q, dt, dev)
     _check("cu_q", cu_q, 1, torch.int32, dev)
     _check("kv_len", kv_len, 1, torch.int32, dev)
     _check("block_table", block_table, 2, torch.int32, dev, contiguous=False)
@@ -350,7 +369,7 @@ def prefix_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages=Non
     if workspace is None:
         workspace = torch.empty(prefix_attn_workspace_size(dt, T, Hq, Hkv, d, R), dtype=torch.uint8, device=dev)
         made.append(workspace)
-    _call_on(dev, "rsa_prefix_attn_fwd", stream, made, qh.data, qh.token_stride, qh.head_stride, k_cache.data_ptr(),
+    _call_on(dev, "rsa_prefix_attn_fwd", stream, made, *q_at, k_cache.data_ptr(),
              v_cache.data_ptr(), code, T, Hq, Hkv, d, page_size, n_pages, cu_q.data_ptr(), kv_len.data_ptr(), R,
              block_table.data_ptr(), max_pages if R == 1 else block_table.stride(0), max_pages,
              prefix_pages.data_ptr() if prefix_len else None, prefix_len, out.data_ptr(), lse.data_ptr(),
