@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kLoads = 8;            // lengths a thread has in flight (one at a time, 4000 requests took 5 us to read)
 constexpr int kTokensPerThread = 4;  // one search of the request serves four consecutive rows
 
 // Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
@@ -41,26 +42,42 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
 {
     extern __shared__ int smem[];
     int *s_cu = smem;               // [R + 1] first row of each request
-    int *s_pg = smem + (p.R + 1);   // [R + 1] fresh pages before each request
+    int *s_pg = s_cu + (p.R + 1);   // [R + 1] fresh pages before each request
+    int *s_c = s_pg + (p.R + 1);    // [R] cached lengths
     __shared__ long long s_wt[kWarps], s_wp[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int R = p.R, P = 1 << p.page_shift;
 
     // ---- lengths, and what makes the whole step impossible --------------------
+    const long long start = p.free_start ? *p.free_start : 0;
     int bad_len = 0, bad_row = 0;
-    for (int r = tid; r < R; r += kThreads) {
-        const long long c = p.cached_len[r], n = p.new_len[r];
-        long long need = 0;
-        if (c < 0 || n < 0) {
-            bad_len = 1;
-        } else {
-            const long long all = (c + n + P - 1) >> p.page_shift;
-            need = all - ((c + P - 1) >> p.page_shift);
-            if (all > p.max_pages)
-                bad_row = 1;
+    for (int rb = tid; rb < R; rb += kThreads * kLoads) {
+        int cs[kLoads], ns[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = rb + i * kThreads;
+            cs[i] = r < R ? p.cached_len[r] : 0;
+            ns[i] = r < R ? p.new_len[r] : 0;
         }
-        s_cu[r] = (int)max(n, 0ll);
-        s_pg[r] = (int)need;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = rb + i * kThreads;
+            const long long c = cs[i], n = ns[i];
+            long long need = 0;
+            if (c < 0 || n < 0) {
+                bad_len = 1;
+            } else {
+                const long long all = (c + n + P - 1) >> p.page_shift;
+                need = all - ((c + P - 1) >> p.page_shift);
+                if (all > p.max_pages)
+                    bad_row = 1;
+            }
+            if (r < R) {
+                s_cu[r] = (int)max(n, 0ll);
+                s_pg[r] = (int)need;
+                s_c[r] = cs[i];
+            }
+        }
     }
     bad_len = __syncthreads_or(bad_len);
     bad_row = __syncthreads_or(bad_row);
@@ -110,7 +127,6 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
         s_cu[R] = (int)tokens;
         s_pg[R] = (int)pages;
     }
-    const long long start = p.free_start ? *p.free_start : 0;
     __syncthreads();
     int code = 0;
     if (bad_len)
@@ -134,42 +150,50 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
     for (long long r = g0; r <= R; r += gn) {
         p.cu_new[r] = ok ? s_cu[r] : 0;
         if (r < R)
-            p.kv_len[r] = p.cached_len[r] + (ok ? p.new_len[r] : 0);
+            p.kv_len[r] = s_c[r] + (ok ? s_cu[r + 1] - s_cu[r] : 0);
     }
     // ---- fresh pages --------------------------------------------------------------
     if (ok)
         for (long long i = g0; i < pages; i += gn) {
             const int r = last_not_above(s_pg, R, (int)i);
-            const long long have = ((long long)p.cached_len[r] + P - 1) >> p.page_shift;
+            const long long have = ((long long)s_c[r] + P - 1) >> p.page_shift;
             p.block_table[r * p.table_stride + have + (i - s_pg[r])] = p.free_pages[start + i];
         }
     // ---- tokens -------------------------------------------------------------------
     for (long long i0 = g0 * kTokensPerThread; i0 < p.max_tokens; i0 += gn * kTokensPerThread) {
-        int r = -1;
-        long long c = 0, have = 0, slot[kTokensPerThread], pos[kTokensPerThread];
-        int end = 0;
+        // First where each row's page id is, then all the ids at once.
+        int r = 0;
+        long long at[kTokensPerThread], slot[kTokensPerThread], pos[kTokensPerThread];
+        const int32_t *from[kTokensPerThread];
 #pragma unroll
         for (int k = 0; k < kTokensPerThread; ++k) {
             const long long i = i0 + k;
-            slot[k] = -1;
-            pos[k] = 0;
+            from[k] = nullptr;
+            at[k] = 0;
             if (!ok || i >= tokens)
                 continue;
-            if (r < 0 || i >= end) {
-                // (requests without a new token share their successor's first row: the
-                // last of them is the one that owns it)
+            // (requests without a new token share their successor's first row: the last
+            // of them is the one that owns it)
+            if (k == 0)
                 r = last_not_above(s_cu, R, (int)i);
-                c = p.cached_len[r];
-                have = (c + P - 1) >> p.page_shift;
-                end = s_cu[r + 1];
-            }
-            const long long at = c + (i - s_cu[r]), j = at >> p.page_shift;
-            const int page = j < have ? p.block_table[r * p.table_stride + j] : p.free_pages[start + s_pg[r] + (j - have)];
-            pos[k] = p.pos0 + at;
-            if (page >= 0 && page < p.n_pages)
-                slot[k] = ((long long)page << p.page_shift) + (at & (P - 1));
-            else
-                record_bad_index(p.err, 0x50, page);
+            else if (i >= s_cu[r + 1])
+                r = i < s_cu[min(r + 2, R)] ? r + 1 : last_not_above(s_cu, R, (int)i);
+            at[k] = s_c[r] + (i - s_cu[r]);
+            const long long j = at[k] >> p.page_shift, have = ((long long)s_c[r] + P - 1) >> p.page_shift;
+            from[k] = j < have ? p.block_table + r * p.table_stride + j : p.free_pages + start + s_pg[r] + (j - have);
+        }
+        int page[kTokensPerThread];
+#pragma unroll
+        for (int k = 0; k < kTokensPerThread; ++k)
+            page[k] = from[k] ? *from[k] : 0;
+#pragma unroll
+        for (int k = 0; k < kTokensPerThread; ++k) {
+            slot[k] = -1;
+            pos[k] = from[k] ? p.pos0 + at[k] : 0;
+            if (from[k] && page[k] >= 0 && page[k] < p.n_pages)
+                slot[k] = ((long long)page[k] << p.page_shift) + (at[k] & (P - 1));
+            else if (from[k])
+                record_bad_index(p.err, 0x50, page[k]);
         }
         if (i0 + kTokensPerThread <= p.max_tokens) {
 #pragma unroll
@@ -192,17 +216,17 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
 
 cudaError_t launch_page_plan(const PagePlanParams &p, cudaStream_t s)
 {
-    const size_t smem = (size_t)(p.R + 1) * 8;
+    const size_t smem = (size_t)(p.R + 1) * 12;
     if (smem > 48 * 1024 - 1024) {
         cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)((kPagePlanMaxRequests + 1) * 8));
+                                             (int)((kPagePlanMaxRequests + 1) * 12));
         if (e != cudaSuccess)
             return e;
     }
-    // Enough blocks for one pass over the tokens, at most one wave: every block pays the scan.
+    // Enough blocks for one pass over the tokens, at most two on each SM: every block pays the scan.
     const int64_t work = (p.max_tokens + kTokensPerThread - 1) / kTokensPerThread;
     int64_t blocks = ((work > p.R ? work : p.R) + kThreads - 1) / kThreads;
-    blocks = blocks < 1 ? 1 : (blocks > 152 ? 152 : blocks);
+    blocks = blocks < 1 ? 1 : (blocks > 304 ? 304 : blocks);
     page_plan_kernel<<<(unsigned)blocks, kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }

@@ -8,7 +8,8 @@
 //   M = max_i lse_i, L = M + ln sum e^{lse_i - M}, o = sum e^{lse_i - L} o_i.
 //
 // A CTA takes its stretch of the work (paged_sched.cuh).  It brings 32 keys and
-// values at a time into shared memory; a warp owns up to 16 rows of the unit.
+// values at a time into shared memory, by asynchronous copies one block ahead of
+// the arithmetic; a warp owns up to 16 rows of the unit.
 // Lane k scores key k (a dot product along d, its own row of K from shared
 // memory, the query broadcast), maximum and sum are shuffles, and for the
 // output lane c owns columns c, c + 32, ... with the probabilities broadcast.
@@ -51,11 +52,19 @@ __device__ __forceinline__ float warp_sum(float x)
 __device__ __forceinline__ void store(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
+// 16 bytes to shared memory; zeros if not `there`.
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
 template <int D>
 struct Smem {
     float q[kRows][D];
-    float k[kKeys][D + 4];  // (+ 4: the lanes' rows fall into different banks)
-    float v[kKeys][D];
+    float k[2][kKeys][D + 4];  // (+ 4: the lanes' rows fall into different banks)
+    float v[2][kKeys][D];
     int64_t sum[kWarps];
     Stretch st;
 };
@@ -102,25 +111,49 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
         }
         const int64_t most = min((int64_t)x.keys, x.see0 + (x.ntok - 1));  // the keys that any row sees
         const int64_t j1 = min(most, (int64_t)x.t1 * kTileKeys);
-        for (int64_t j0 = (int64_t)x.t0 * kTileKeys; j0 < j1; j0 += kKeys) {
-            const int nk = (int)min((int64_t)kKeys, j1 - j0);
-            __syncthreads();  // the last block of keys is done with
-            for (int i = threadIdx.x; i < nk * D; i += kThreads) {
-                const int key = i / D, c = i - key * D;
-                const int64_t j = j0 + key;
-                const int page = x.pages[j >> p.page_shift];
-                float a = 0.f, b = 0.f;
-                if (page >= 0 && page < p.n_pages) {
-                    const int64_t at = ((((int64_t)page * p.Hkv + x.head) << p.page_shift) + (j & page_mask)) * D + c;
-                    a = kc[at];
-                    b = vc[at];
-                } else if (c == 0) {
-                    record_bad_index(p.err, 0x55, page);
-                }
-                s.k[key][c] = a;
-                s.v[key][c] = b;
+        const int64_t j00 = (int64_t)x.t0 * kTileKeys;
+        // Block b of 32 keys: this thread copies 16 bytes of kCopies keys, whose pages'
+        // ids it read a block before.  Keys past the last one are not copied.
+        constexpr int kPieces = D / 4, kCopies = kKeys * kPieces / kThreads;
+        const int piece = threadIdx.x % kPieces, key0 = threadIdx.x / kPieces;
+        int ids[kCopies];
+        auto look_up = [&](int64_t j0) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int64_t j = j0 + key0 + i * (kThreads / kPieces);
+                ids[i] = j < j1 ? x.pages[j >> p.page_shift] : 0;
             }
-            __syncthreads();
+        };
+        auto fetch = [&](int64_t j0, int buffer) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int key = key0 + i * (kThreads / kPieces);
+                const int64_t j = j0 + key;
+                if (j < j1) {
+                    int id = ids[i];
+                    const bool bad = id < 0 || id >= p.n_pages;  // (its keys count as zeros)
+                    if (bad) {
+                        record_bad_index(p.err, 0x55, id);
+                        id = 0;
+                    }
+                    const int64_t at =
+                        ((((int64_t)id * p.Hkv + x.head) << p.page_shift) + (j & page_mask)) * D + piece * 4;
+                    copy_async(&s.k[buffer][key][piece * 4], kc + at, !bad);
+                    copy_async(&s.v[buffer][key][piece * 4], vc + at, !bad);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look_up(j00);
+        fetch(j00, 0);
+        look_up(j00 + kKeys);
+        int buffer = 0;
+        for (int64_t j0 = j00; j0 < j1; j0 += kKeys, buffer ^= 1) {
+            const int nk = (int)min((int64_t)kKeys, j1 - j0);
+            fetch(j0 + kKeys, buffer ^ 1);
+            look_up(j0 + 2 * kKeys);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();  // every thread's copies of this block
 #pragma unroll
             for (int i = 0; i < kWarpRows; ++i) {
                 const int row = i * kWarps + warp;
@@ -130,7 +163,8 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                 float sc = -INFINITY;
                 if (lane < n) {
                     float dot = 0.f;
-                    const float4 *a = reinterpret_cast<const float4 *>(s.q[row]), *b = reinterpret_cast<const float4 *>(s.k[lane]);
+                    const float4 *a = reinterpret_cast<const float4 *>(s.q[row]),
+                                 *b = reinterpret_cast<const float4 *>(s.k[buffer][lane]);
 #pragma unroll 8
                     for (int c = 0; c < D / 4; ++c) {
                         const float4 u = a[c], w = b[c];
@@ -153,9 +187,10 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                     const float pk = __shfl_sync(0xffffffffu, pj, k);
 #pragma unroll
                     for (int c = 0; c < PER; ++c)
-                        o[i][c] = fmaf(pk, s.v[k][lane + 32 * c], o[i][c]);
+                        o[i][c] = fmaf(pk, s.v[buffer][k][lane + 32 * c], o[i][c]);
                 }
             }
+            __syncthreads();  // the block is done with: its buffer is filled next
         }
 #pragma unroll
         for (int i = 0; i < kWarpRows; ++i) {

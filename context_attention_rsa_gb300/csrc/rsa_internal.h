@@ -129,7 +129,7 @@ struct MergeParams {
 };
 
 // One step's plan over a paged cache (rsa_page_plan).
-constexpr int kPagePlanMaxRequests = 16384;  // two ints a request in shared memory
+constexpr int kPagePlanMaxRequests = 16384;  // three ints a request in shared memory
 struct PagePlanParams {
     const int32_t *cached_len, *new_len;
     int R, page_shift, max_pages;
