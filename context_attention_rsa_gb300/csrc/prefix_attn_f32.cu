@@ -9,12 +9,12 @@
 //
 // A CTA takes its stretch of the work (paged_sched.cuh).  It brings 32 keys and
 // values at a time into shared memory, by asynchronous copies one block ahead of
-// the arithmetic; a warp owns up to 16 rows of the unit.
+// the arithmetic; a warp owns up to 8 rows of the unit.
 // Lane k scores key k (a dot product along d, its own row of K from shared
-// memory, the query broadcast), maximum and sum are shuffles, and for the
-// output lane c owns columns c, c + 32, ... with the probabilities broadcast.
-// Bound by shared-memory loads and fp32 arithmetic.  Values of masked keys are
-// never touched: they may hold anything.
+// memory, the queries broadcast), maximum and sum are shuffles, and for the output
+// lane c owns columns c, c + 32, ... with the probabilities broadcast.  All of a
+// warp's rows go through a block together, so that K and V are read from shared
+// memory once for them; shared memory is the bound.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -27,8 +27,10 @@ namespace {
 
 using namespace paged;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kRows = 128;            // rows of a unit
 constexpr int kWarpRows = kRows / kWarps;
 constexpr int kKeys = 32;             // keys of a block
@@ -65,9 +67,40 @@ struct Smem {
     float q[kRows][D];
     float k[2][kKeys][D + 4];  // (+ 4: the lanes' rows fall into different banks)
     float v[2][kKeys][D];
+    float p[kRows][kKeys];  // the block's probabilities
     int64_t sum[kWarps];
     Stretch st;
 };
+
+// The ids of the pages of this thread's keys (j, j + step, ...; below j1) ...
+template <int kCopies>
+__device__ __forceinline__ void look_up(const PrefixAttnParams &p, const Piece &x, int64_t j, int step, int64_t j1, int (&ids)[kCopies])
+{
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i, j += step)
+        ids[i] = j < j1 ? x.pages[j >> p.page_shift] : 0;
+}
+
+// ... and the copies of them: 16 bytes of each key and value, from column 4 * piece.
+template <int D, int kCopies>
+__device__ __forceinline__ void fetch(const PrefixAttnParams &p, const Piece &x, Smem<D> &s, int buffer, int key, int piece, int step,
+                                      int64_t j0, int64_t j1, const int (&ids)[kCopies])
+{
+    const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i, key += step) {
+        const int64_t j = j0 + key;
+        if (j < j1) {
+            const bool there = ids[i] >= 0 && ids[i] < p.n_pages;  // (the keys of another id count as zeros)
+            if (!there)
+                record_bad_index(p.err, 0x55, ids[i]);
+            const int64_t row = (((int64_t)(there ? ids[i] : 0) * p.Hkv + x.head) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
+            copy_async(&s.k[buffer][key][piece * 4], kc + row * D + piece * 4, there);
+            copy_async(&s.v[buffer][key][piece * 4], vc + row * D + piece * 4, there);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_constant__ PrefixAttnParams p)
@@ -79,8 +112,6 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     const int G = p.G;
     const int worker = blockIdx.x;
     const float scale = 1.0f / sqrtf((float)D);
-    const int page_mask = (1 << p.page_shift) - 1;
-    const float *kc = static_cast<const float *>(p.k_cache), *vc = static_cast<const float *>(p.v_cache);
 
     const Stretch st = find_stretch<kThreads>(p, worker, s.sum, &s.st);
     ptx::launch_dependents();
@@ -90,13 +121,14 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     while (walk.next(p, x)) {
         const int rows = (int)x.ntok * G;
         __syncthreads();  // the last piece's rows are done with q
-        for (int i = threadIdx.x; i < rows * D; i += kThreads) {
-            const int row = i / D, c = i - row * D;
-            const int64_t token = x.tok + row / G;
-            s.q[row][c] =
-                static_cast<const float *>(p.q)[token * p.q_token_stride + (x.head * G + row % G) * p.q_head_stride + c];
+#pragma unroll 4
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+            const int row = i / (D / 4), c = i % (D / 4) * 4;
+            const int64_t at = (int64_t)(x.tok + row / G) * p.q_token_stride + (x.head * G + row % G) * p.q_head_stride + c;
+            *reinterpret_cast<float4 *>(&s.q[row][c]) = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
         }
-        // Row i * kWarps + warp of the unit, and the keys it sees.
+        // Rows i * kWarps + warp of the unit, i < mine, and the keys they see.
+        const int mine = max(0, (rows - warp + kWarps - 1) / kWarps);
         float m[kWarpRows], l[kWarpRows], o[kWarpRows][PER];
         int64_t see[kWarpRows];
 #pragma unroll
@@ -117,77 +149,84 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
         constexpr int kPieces = D / 4, kCopies = kKeys * kPieces / kThreads;
         const int piece = threadIdx.x % kPieces, key0 = threadIdx.x / kPieces;
         int ids[kCopies];
-        auto look_up = [&](int64_t j0) {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int64_t j = j0 + key0 + i * (kThreads / kPieces);
-                ids[i] = j < j1 ? x.pages[j >> p.page_shift] : 0;
-            }
-        };
-        auto fetch = [&](int64_t j0, int buffer) {
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int key = key0 + i * (kThreads / kPieces);
-                const int64_t j = j0 + key;
-                if (j < j1) {
-                    int id = ids[i];
-                    const bool bad = id < 0 || id >= p.n_pages;  // (its keys count as zeros)
-                    if (bad) {
-                        record_bad_index(p.err, 0x55, id);
-                        id = 0;
-                    }
-                    const int64_t at =
-                        ((((int64_t)id * p.Hkv + x.head) << p.page_shift) + (j & page_mask)) * D + piece * 4;
-                    copy_async(&s.k[buffer][key][piece * 4], kc + at, !bad);
-                    copy_async(&s.v[buffer][key][piece * 4], vc + at, !bad);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        look_up(j00);
-        fetch(j00, 0);
-        look_up(j00 + kKeys);
+        look_up<kCopies>(p, x, j00 + key0, kThreads / kPieces, j1, ids);
+        fetch<D, kCopies>(p, x, s, 0, key0, piece, kThreads / kPieces, j00, j1, ids);
+        look_up<kCopies>(p, x, j00 + kKeys + key0, kThreads / kPieces, j1, ids);
         int buffer = 0;
         for (int64_t j0 = j00; j0 < j1; j0 += kKeys, buffer ^= 1) {
             const int nk = (int)min((int64_t)kKeys, j1 - j0);
-            fetch(j0 + kKeys, buffer ^ 1);
-            look_up(j0 + 2 * kKeys);
+            fetch<D, kCopies>(p, x, s, buffer ^ 1, key0, piece, kThreads / kPieces, j0 + kKeys, j1, ids);
+            look_up<kCopies>(p, x, j0 + 2 * kKeys + key0, kThreads / kPieces, j1, ids);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();  // every thread's copies of this block
+            // (four chains of sums a row: a warp has few rows to hide their latency behind)
+            float4 dot[kWarpRows];
+#pragma unroll
+            for (int i = 0; i < kWarpRows; ++i)
+                dot[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < nk) {
+#pragma unroll 4
+                for (int c = 0; c < D / 4; ++c) {
+                    const float4 w = *reinterpret_cast<const float4 *>(&s.k[buffer][lane][4 * c]);
+#pragma unroll
+                    for (int i = 0; i < kWarpRows; ++i) {
+                        if (i >= mine)
+                            break;  // the same for the whole warp
+                        const float4 u = *reinterpret_cast<const float4 *>(&s.q[i * kWarps + warp][4 * c]);
+                        dot[i].x = fmaf(u.x, w.x, dot[i].x);
+                        dot[i].y = fmaf(u.y, w.y, dot[i].y);
+                        dot[i].z = fmaf(u.z, w.z, dot[i].z);
+                        dot[i].w = fmaf(u.w, w.w, dot[i].w);
+                    }
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kWarpRows; ++i) {
-                const int row = i * kWarps + warp;
-                const int n = (int)min((int64_t)nk, see[i] - j0);  // keys of the block that the row sees
-                if (n <= 0)
-                    continue;  // the same for the whole warp
-                float sc = -INFINITY;
-                if (lane < n) {
-                    float dot = 0.f;
-                    const float4 *a = reinterpret_cast<const float4 *>(s.q[row]),
-                                 *b = reinterpret_cast<const float4 *>(s.k[buffer][lane]);
-#pragma unroll 8
-                    for (int c = 0; c < D / 4; ++c) {
-                        const float4 u = a[c], w = b[c];
-                        dot = fmaf(u.x, w.x, dot);
-                        dot = fmaf(u.y, w.y, dot);
-                        dot = fmaf(u.z, w.z, dot);
-                        dot = fmaf(u.w, w.w, dot);
-                    }
-                    sc = dot * scale;
-                }
+                if (i >= mine)
+                    break;
+                const float sc = lane < min((int64_t)nk, see[i] - j0) ? ((dot[i].x + dot[i].y) + (dot[i].z + dot[i].w)) * scale : -INFINITY;
                 const float mn = fmaxf(m[i], warp_max(sc));
                 const float base = mn == -INFINITY ? 0.f : mn;
-                const float alpha = expf(m[i] - base), pj = lane < n ? expf(sc - base) : 0.f;
+                const float alpha = expf(m[i] - base), pj = expf(sc - base);
                 l[i] = l[i] * alpha + warp_sum(pj);
                 m[i] = mn;
+                s.p[i * kWarps + warp][lane] = pj;
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
                     o[i][c] *= alpha;
-                for (int k = 0; k < n; ++k) {
-                    const float pk = __shfl_sync(0xffffffffu, pj, k);
+            }
+            __syncwarp();
+            int k = 0;
+            for (; k + 4 <= nk; k += 4) {
+                float v[4][PER];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int c = 0; c < PER; ++c)
-                        o[i][c] = fmaf(pk, s.v[buffer][k][lane + 32 * c], o[i][c]);
+                        v[e][c] = s.v[buffer][k + e][lane + 32 * c];
+#pragma unroll
+                for (int i = 0; i < kWarpRows; ++i) {
+                    if (i >= mine)
+                        break;
+                    const float4 pk = *reinterpret_cast<const float4 *>(&s.p[i * kWarps + warp][k]);
+#pragma unroll
+                    for (int c = 0; c < PER; ++c)
+                        o[i][c] = fmaf(pk.w, v[3][c], fmaf(pk.z, v[2][c], fmaf(pk.y, v[1][c], fmaf(pk.x, v[0][c], o[i][c]))));
+                }
+            }
+            for (; k < nk; ++k) {
+                float v[PER];
+#pragma unroll
+                for (int c = 0; c < PER; ++c)
+                    v[c] = s.v[buffer][k][lane + 32 * c];
+#pragma unroll
+                for (int i = 0; i < kWarpRows; ++i) {
+                    if (i >= mine)
+                        break;
+                    const float pk = s.p[i * kWarps + warp][k];
+#pragma unroll
+                    for (int c = 0; c < PER; ++c)
+                        o[i][c] = fmaf(pk, v[c], o[i][c]);
                 }
             }
             __syncthreads();  // the block is done with: its buffer is filled next
@@ -257,11 +296,11 @@ struct Pieces {
 // is needed; the loads of the o rows then depend on nothing.  Lane c owns
 // columns [c * PER, (c + 1) * PER).
 template <class E, int D>
-__global__ void __launch_bounds__(kThreads) prefix_join_kernel(const __grid_constant__ PrefixAttnParams p)
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixAttnParams p)
 {
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t row = min((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), p.T * p.Hq - 1);  // (spare warps repeat a row)
+    const int64_t row = min((int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5), p.T * p.Hq - 1);  // (spare warps repeat a row)
     const int token = (int)(row / p.Hq);
     const int hq = (int)(row - (int64_t)token * p.Hq), head = hq / p.G;
     const int r = request_of(p, token);
@@ -384,7 +423,7 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
 template <class E, int D>
 cudaError_t join(const PrefixAttnParams &p, cudaStream_t s)
 {
-    const int64_t blocks = (p.T * p.Hq + kWarps - 1) / kWarps;
+    const int64_t blocks = (p.T * p.Hq + kJoinWarps - 1) / kJoinWarps;
     if (blocks > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute early;
@@ -392,7 +431,7 @@ cudaError_t join(const PrefixAttnParams &p, cudaStream_t s)
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
