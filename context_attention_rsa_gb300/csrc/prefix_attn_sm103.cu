@@ -40,7 +40,6 @@
 
 #include <climits>
 #include <cmath>
-#include <type_traits>
 
 #include "paged_sched.cuh"
 #include "ptx_sm103.cuh"
@@ -151,6 +150,102 @@ __device__ __forceinline__ uint64_t columns(int n)
 {
     return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
 }
+
+// The thread that issues the MMAs.  (Everything it does in a step is inlined: a
+// lambda called from two places is not, and what it refers to then lives in memory.)
+template <int D>
+struct Issuer {
+    using C = Cfg<D>;
+    uint32_t tmem, bars;
+    uint64_t dq0, dk0, dv0;  // descriptors of the first Q tile, K and V slot
+    uint64_t lim_ns;
+    volatile int *abort_flag;
+    unsigned int *err;
+    uint32_t q_use0 = 0, q_use1 = 0, p_use0 = 0, p_use1 = 0, o_use0 = 0, o_use1 = 0;  // uses of the Q tiles, of S and P, of O
+
+    __device__ __forceinline__ bool wait(int bar, uint32_t phase, int site)
+    {
+        return ptx::mbar_wait(bars + 8u * (uint32_t)bar, phase & 1, lim_ns, abort_flag, err, site);
+    }
+    __device__ __forceinline__ bool ready(int bar, uint32_t phase) { return ptx::mbar_test_wait(bars + 8u * (uint32_t)bar, phase & 1); }
+    __device__ __forceinline__ void commit(int bar) { ptx::mma_commit(bars + 8u * (uint32_t)bar); }
+    // The load numbered n has landed (tile i's K is load 2i, its V load 2i + 1); may be overwritten.
+    __device__ __forceinline__ bool full(uint32_t n) { return wait(C::kKVF + (n & (C::kStages - 1)), n >> C::kStageBits, 0x71); }
+    __device__ __forceinline__ void free_slot(uint32_t n) { commit(C::kKVE + (n & (C::kStages - 1))); }
+    __device__ __forceinline__ bool q_full(int t) { return wait(C::kQF + t, t ? q_use1++ : q_use0++, 0x70); }
+    __device__ __forceinline__ void q_free()
+    {
+        commit(C::kQFree + 0);
+        commit(C::kQFree + 1);
+    }
+    __device__ __forceinline__ bool p_full(int t)
+    {
+        const bool got = wait(C::kPF + t, t ? p_use1++ : p_use0++, 0x72);
+        ptx::tc_fence_after();
+        return got;
+    }
+    // The piece that last used O has been read.
+    __device__ __forceinline__ bool o_free(int o)
+    {
+        const uint32_t n = o ? o_use1++ : o_use0++;
+        return n == 0 || wait(C::kOFree + o, n - 1, 0x73);
+    }
+    __device__ __forceinline__ void issue_qk(int t, int q_tile, int slot)
+    {
+        const uint64_t qa = dq0 + ((q_tile * C::kTileBytes) >> 4), kb = dk0 + ((slot * C::kTileBytes) >> 4);
+        const uint32_t dst = tmem + (t ? C::kColS1 : C::kColS0);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t q_off = ((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4;
+            const uint32_t k_off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+            ptx::mma_ss(dst, qa + q_off, kb + k_off, ptx::idesc_bf16_f32(128, 128, false), kk > 0);
+        }
+        commit(C::kSF + t);
+    }
+    __device__ __forceinline__ void issue_pv(int o, int t, int slot, bool acc)
+    {
+        const uint64_t vb = dv0 + ((slot * C::kTileBytes) >> 4);
+        const uint32_t dst = tmem + (o ? C::kColO1 : C::kColO0), pa = tmem + (t ? C::kColS1 : C::kColS0);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_ts(dst, pa + kk * 8, vb + ((kk * 2 * C::kGroupBytes) >> 4), ptx::idesc_bf16_f32(128, D, true),
+                        (acc || kk > 0) ? 1u : 0u);
+    }
+    // Key tile j of n against two row tiles, the piece's first tile being `done`: PV of
+    // both, each followed by its S of the next tile.  The slots are known at compile
+    // time, K(j) and V(j) in pair kPair of the ring and K(j + 1) in the next one, so
+    // that the descriptors are constants of the kernel.
+    template <int kPair>
+    __device__ __forceinline__ bool step(uint32_t done, int j, int n)
+    {
+        constexpr int kV = 2 * kPair + 1, kK = 2 * ((kPair + 1) % C::kPairs);
+        const uint32_t tile = done + j;
+        const bool more = j + 1 < n;
+        if (!wait(C::kKVF + kV, tile >> C::kPairBits, 0x71) || !p_full(0))
+            return false;
+        issue_pv(0, 0, kV, j > 0);
+        if (more) {
+            if (!wait(C::kKVF + kK, (tile + 1) >> C::kPairBits, 0x71))
+                return false;
+            issue_qk(0, 0, kK);
+        } else {
+            commit(C::kOF + 0);
+        }
+        if (!p_full(1))
+            return false;
+        issue_pv(1, 1, kV, j > 0);
+        commit(C::kKVE + kV);
+        if (more) {
+            issue_qk(1, 1, kK);
+            commit(C::kKVE + kK);
+            if (j + 2 == n)
+                q_free();  // that was the last S MMA
+        } else {
+            commit(C::kOF + 1);
+        }
+        return true;
+    }
+};
 
 // What a softmax thread keeps of a row's tiles so far.
 struct Row {
@@ -425,189 +520,116 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     } else if (warp == C::kMmaWarp) {
         // ============================ MMA issuer ============================
         if (lane == 0) {
-            const uint32_t idesc_qk = ptx::idesc_bf16_f32(128, 128, false);
-            const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
-            const uint64_t dq0 = ptx::smem_desc_sw128(sQ, 16, 1024);
-            const uint64_t dk0 = ptx::smem_desc_sw128(sKV, 16, C::kGroupBytes);
-            const uint64_t dv0 = ptx::smem_desc_sw128(sKV, 1024, C::kGroupBytes);
-            uint32_t done = 0;                                          // tiles whose PV has been issued
-            uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, o_use[2] = {0, 0};  // uses of the Q tiles, of S and P, of O
-            int q_slot = 0, o_slot = 0;
-            bool ok = true;
-            auto wait = [&](int bar, uint32_t phase, int site) {
-                return ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site);
-            };
-            auto full = [&](uint32_t n) {  // the load numbered n has landed (tile i's K is load 2i, its V load 2i + 1)
-                return wait(C::kKVF + (n & (C::kStages - 1)), n >> C::kStageBits, 0x71);
-            };
-            auto free_slot = [&](uint32_t n) { ptx::mma_commit(BAR(C::kKVE + (n & (C::kStages - 1)))); };
-            auto issue_qk = [&](int t, int q_tile, int slot) {
-                const uint64_t qa = dq0 + ((q_tile * C::kTileBytes) >> 4);
-                const uint64_t kb = dk0 + ((slot * C::kTileBytes) >> 4);
-                const uint32_t dst = tmem + (t ? C::kColS1 : C::kColS0);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t q_off = ((kk >> 2) * C::kQBoxBytes + (kk & 3) * 32) >> 4;
-                    const uint32_t k_off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-                    ptx::mma_ss(dst, qa + q_off, kb + k_off, idesc_qk, kk > 0);
-                }
-                ptx::mma_commit(BAR(C::kSF + t));
-            };
-            auto issue_pv = [&](int o, int t, int slot, bool acc) {
-                const uint64_t vb = dv0 + ((slot * C::kTileBytes) >> 4);
-                const uint32_t dst = tmem + (o ? C::kColO1 : C::kColO0);
-                const uint32_t pa = tmem + (t ? C::kColS1 : C::kColS0);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    ptx::mma_ts(dst, pa + kk * 8, vb + ((kk * 2 * C::kGroupBytes) >> 4), idesc_pv, (acc || kk > 0) ? 1u : 0u);
-            };
-            auto p_full = [&](int t) {
-                const bool got = wait(C::kPF + t, p_use[t]++, 0x72);
-                ptx::tc_fence_after();
-                return got;
-            };
-            // The piece that last used O has been read.
-            auto o_free = [&](int o) {
-                const uint32_t n = o_use[o]++;
-                return n == 0 || wait(C::kOFree + o, n - 1, 0x73);
-            };
+            Issuer<D> mma;
+            mma.tmem = tmem;
+            mma.bars = bars;
+            mma.dq0 = ptx::smem_desc_sw128(sQ, 16, 1024);
+            mma.dk0 = ptx::smem_desc_sw128(sKV, 16, C::kGroupBytes);
+            mma.dv0 = ptx::smem_desc_sw128(sKV, 1024, C::kGroupBytes);
+            mma.lim_ns = lim_ns;
+            mma.abort_flag = abort_flag;
+            mma.err = p.err;
             // The piece whose S MMAs are issued, and the one whose PVs are: the first is up
             // to two tiles ahead of the second, so at most three pieces lie after the second.
-            uint32_t taken = 0;         // descriptions read
-            int n = 0, two = 0, i = 0;  // the first's tiles (-1: none), form and tile
-            int back_n = 0, back_i = 0, ahead_n[3] = {0, 0, 0}, waiting = 0;
-            auto next_piece = [&] {
-                i = 0;
-                do {
-                    const int at = taken % C::kWork;
-                    ok = wait(C::kWF + at, taken / C::kWork, 0x75);
+            uint32_t done = 0, ahead = 0;  // tiles whose PV, whose S has been issued
+            uint32_t taken = 0;            // descriptions read
+            int n = 0, two = 0, i = 0;     // the first's tiles (0: to be read, -1: none), form and tile
+            int back_n = 0, back_i = 0, ahead0 = 0, ahead1 = 0, ahead2 = 0, waiting = 0;
+            int q_slot = 0, o_slot = 0;
+            bool ok = true;
+            for (;;) {
+                // ---- S, as far ahead as may be ----
+                while (ok && n >= 0 && (n == 0 || (!two && ahead - done < 2))) {
+                    if (n == 0) {
+                        // (While a PV is to be issued only if the next piece is there: the
+                        // producer may be waiting for the rows that this PV completes.)
+                        const int at = taken % C::kWork;
+                        if (ahead > done && !mma.ready(C::kWF + at, taken / C::kWork))
+                            break;
+                        ok = mma.wait(C::kWF + at, taken / C::kWork, 0x75);
+                        if (!ok)
+                            break;
+                        n = work[at].tiles;
+                        two = work[at].two;
+                        ptx::mbar_arrive(BAR(C::kWE + at));
+                        ++taken;
+                        i = 0;
+                        if (n != 0) {
+                            ahead0 = waiting == 0 ? n : ahead0;
+                            ahead1 = waiting == 1 ? n : ahead1;
+                            ahead2 = waiting == 2 ? n : ahead2;
+                            ++waiting;
+                        }
+                        continue;
+                    }
+                    ok = (i > 0 || mma.q_full(q_slot)) && mma.full(2 * ahead);
                     if (!ok)
-                        return;
-                    n = work[at].tiles;
-                    two = work[at].two;
-                    ptx::mbar_arrive(BAR(C::kWE + at));
-                    ++taken;
-                } while (n == 0);
-                ahead_n[0] = waiting == 0 ? n : ahead_n[0];
-                ahead_n[1] = waiting == 1 ? n : ahead_n[1];
-                ahead_n[2] = waiting == 2 ? n : ahead_n[2];
-                ++waiting;
-            };
-            auto next_back = [&] {
-                back_i = 0;
-                back_n = ahead_n[0];
-                ahead_n[0] = ahead_n[1];
-                ahead_n[1] = ahead_n[2];
-                --waiting;
-            };
-            next_piece();
-            while (ok && n > 0) {
-                next_back();
-                if (two) {
-                    ok = wait(C::kQF + 0, q_use[0]++, 0x70) && wait(C::kQF + 1, q_use[1]++, 0x70) && full(2 * done);
+                        break;
+                    mma.issue_qk(ahead & 1, q_slot, (2 * ahead) & (C::kStages - 1));
+                    mma.free_slot(2 * ahead);
+                    ++ahead;
+                    if (++i == n) {
+                        mma.commit(C::kQFree + q_slot);
+                        q_slot ^= 1;
+                        n = 0;
+                    }
+                }
+                if (!ok || (n < 0 && ahead == done))
+                    break;
+                if (back_i == back_n) {
+                    back_i = 0;
+                    back_n = ahead0;
+                    ahead0 = ahead1;
+                    ahead1 = ahead2;
+                    --waiting;
+                }
+                if (n > 0 && two && ahead == done) {
+                    // ---- a piece with two row tiles, by itself ----
+                    ok = mma.q_full(0) && mma.q_full(1) && mma.full(2 * done);
                     if (!ok)
                         break;
                     const int first = (2 * done) & (C::kStages - 1);
-                    issue_qk(0, 0, first);
-                    issue_qk(1, 1, first);
-                    free_slot(2 * done);
-                    auto q_free = [&] {
-                        ptx::mma_commit(BAR(C::kQFree + 0));
-                        ptx::mma_commit(BAR(C::kQFree + 1));
-                    };
+                    mma.issue_qk(0, 0, first);
+                    mma.issue_qk(1, 1, first);
+                    mma.free_slot(2 * done);
                     if (n == 1)
-                        q_free();
-                    ok = o_free(0) && o_free(1);
-                    // One step with its slots known at compile time: K(j) and V(j) are in
-                    // pair `kPair` of the ring, K(j + 1) in the next one, so that the MMAs'
-                    // descriptors are constants of the kernel (3% faster than computed ones).
-                    auto step = [&](auto pair, int j) -> bool {
-                        constexpr int kPair = decltype(pair)::value, kV = 2 * kPair + 1, kK = 2 * ((kPair + 1) % C::kPairs);
-                        const uint32_t tile = done + j;
-                        const bool more = j + 1 < n;
-                        if (!wait(C::kKVF + kV, tile >> C::kPairBits, 0x71) || !p_full(0))
-                            return false;
-                        issue_pv(0, 0, kV, j > 0);
-                        if (more) {
-                            if (!wait(C::kKVF + kK, (tile + 1) >> C::kPairBits, 0x71))
-                                return false;
-                            issue_qk(0, 0, kK);
-                        } else {
-                            ptx::mma_commit(BAR(C::kOF + 0));
-                        }
-                        if (!p_full(1))
-                            return false;
-                        issue_pv(1, 1, kV, j > 0);
-                        ptx::mma_commit(BAR(C::kKVE + kV));
-                        if (more) {
-                            issue_qk(1, 1, kK);
-                            ptx::mma_commit(BAR(C::kKVE + kK));
-                            if (j + 2 == n)
-                                q_free();  // that was the last S MMA
-                        } else {
-                            ptx::mma_commit(BAR(C::kOF + 1));
-                        }
-                        return true;
-                    };
+                        mma.q_free();
+                    ok = mma.o_free(0) && mma.o_free(1);
                     for (int j = 0; ok && j < n; ++j) {
                         const int pair = (done + j) & (C::kPairs - 1);
                         if (pair == 0)
-                            ok = step(std::integral_constant<int, 0>(), j);
+                            ok = mma.template step<0>(done, j, n);
                         else if (pair == 1)
-                            ok = step(std::integral_constant<int, 1>(), j);
-                        else if (pair == 2)
-                            ok = step(std::integral_constant<int, 2 % C::kPairs>(), j);
-                        else
-                            ok = step(std::integral_constant<int, 3 % C::kPairs>(), j);
-                    }
-                    done += n;
-                    if (ok)
-                        next_piece();
-                    continue;
-                }
-                // A run of one-tile pieces: S MMAs run two tiles ahead of PV, over the
-                // pieces' borders.
-                uint32_t ahead = done;  // tiles whose S has been issued
-                while (ok) {
-                    while (ok && ahead - done < 2 && n > 0 && !two) {
-                        if (i == 0)
-                            ok = wait(C::kQF + q_slot, q_use[q_slot]++, 0x70);
-                        ok = ok && full(2 * ahead);
-                        if (!ok)
-                            break;
-                        issue_qk(ahead & 1, q_slot, (2 * ahead) & (C::kStages - 1));
-                        free_slot(2 * ahead);
-                        ++ahead;
-                        if (++i == n) {
-                            ptx::mma_commit(BAR(C::kQFree + q_slot));
-                            q_slot ^= 1;
-                            next_piece();
+                            ok = mma.template step<1>(done, j, n);
+                        if constexpr (C::kPairs == 4) {
+                            if (pair == 2)
+                                ok = mma.template step<2>(done, j, n);
+                            else if (pair == 3)
+                                ok = mma.template step<3>(done, j, n);
                         }
                     }
-                    if (!ok)
-                        break;
-                    const int t = done & 1;
-                    const uint32_t v = 2 * done + 1;
-                    if (back_i == 0)
-                        ok = o_free(o_slot);
-                    ok = ok && full(v) && p_full(t);
-                    if (!ok)
-                        break;
-                    issue_pv(o_slot, t, v & (C::kStages - 1), back_i > 0);
-                    free_slot(v);
-                    ++done;
-                    if (++back_i == back_n) {
-                        ptx::mma_commit(BAR(C::kOF + o_slot));
-                        o_slot ^= 1;
-                        if (ahead == done && !(n > 0 && !two))
-                            break;  // the run is over; the next piece begins above
-                        next_back();
-                    }
+                    done += n;
+                    ahead = done;
+                    back_i = back_n;
+                    n = 0;
+                    continue;
+                }
+                // ---- PV of a piece with one row tile ----
+                const uint32_t v = 2 * done + 1;
+                ok = (back_i > 0 || mma.o_free(o_slot)) && mma.full(v) && mma.p_full(done & 1);
+                if (!ok)
+                    break;
+                mma.issue_pv(o_slot, done & 1, v & (C::kStages - 1), back_i > 0);
+                mma.free_slot(v);
+                ++done;
+                if (++back_i == back_n) {
+                    mma.commit(C::kOF + o_slot);
+                    o_slot ^= 1;
                 }
             }
-            if (q_use[0] + q_use[1] > 0) {
+            if (taken > 0) {
                 // Every MMA this thread issued has finished before TMEM is freed.
-                ptx::mma_commit(BAR(C::kDrain));
+                mma.commit(C::kDrain);
                 volatile int no_abort = 0;
                 ptx::mbar_wait(BAR(C::kDrain), 0, lim_ns, &no_abort, p.err, 0x74);
             }

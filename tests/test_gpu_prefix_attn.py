@@ -123,6 +123,25 @@ def test_rows_that_see_nothing_and_rows_behind_the_batch(dtype):
             assert torch.isneginf(lse[1:3]).all() and torch.isneginf(lse[6:8]).all() and (out[6:8] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
+def test_long_runs_of_rows_that_see_nothing(dtype):
+    # far more new rows than cached tokens: most of the request's row groups have no key to see, dozens of them one
+    # after the other in one worker's share, between groups and requests that do
+    need_cuda()
+    for prefix, G in ((0, 8), (100, 3), (0, 1)):
+        new, lens = [1, 3000, 1, 700, 2], [40, 130, 300, 0, 9]
+        b = Batch(new, lens, prefix, 2 * G, 2, 64, 32, dtype)
+        out, lse = b.run()
+        rsa.check_device_error()
+        if prefix == 0:
+            hidden = 3000 - 130
+            assert torch.isneginf(lse[1:1 + hidden]).all() and (out[1:1 + hidden] == 0).all()
+        # rows at both ends of every run against the definition
+        keep = torch.tensor([0, 1, 1 + 3000 - 131, 1 + 3000 - 130, 3000, 3001, 3002, 3701, 3702, 3703])
+        r = b.reference()
+        ref.assert_prefix_attn(out[keep.cuda()], lse[keep.cuda()], tuple(x[keep.numpy()] for x in r), dtype)
+
+
 def test_large_scores_and_infinite_values_in_masked_rows():
     need_cuda()
     # (rows past kv_len and prefix_len are NaN in every batch); scores of thousands do not overflow
