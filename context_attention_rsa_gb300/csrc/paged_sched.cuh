@@ -31,7 +31,7 @@ namespace rsa {
 namespace paged {
 
 constexpr int kTileKeys = 128;
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 3;
 
 struct Segment {
     int tok0, ntok;        // its query tokens

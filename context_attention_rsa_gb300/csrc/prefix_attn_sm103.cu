@@ -54,7 +54,7 @@ using namespace paged;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;  // log2 units the maximum may rise before O is rescaled
 // Places of a key tile (kUnitCost for a unit): measured next to one another, a tile
-// against two row tiles took 1.85 us, one against one 1.28 us, a unit 1.2 us more.
+// against two row tiles took 1.7 us, one against one 1.2 us, a unit 1.7 us more.
 constexpr int kLightTile = 2, kHeavyTile = 3;
 constexpr float kLn2 = 0.69314718055994531f;
 
