@@ -29,6 +29,7 @@
 // All arithmetic is in 32 bits; the result is rounded once, at the store.
 #include <cuda_bf16.h>
 
+#include "ptx_sm103.cuh"
 #include "rsa_internal.h"
 
 namespace rsa {
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     E *ring = reinterpret_cast<E *>(smem) + group * (kStages * 2 * kHeads * D);  // [kStages][x, dy][kHeads][D]
     const int chunks = q_chunks + kv_chunks;
     const Run run = run_of(p.T * chunks, chunks, G);
+    ptx::launch_dependents();  // the sums' launch is made ready meanwhile
     float2 aq[N / 2] = {}, ak[N / 2] = {};
     Item ahead = run.first;
     auto fetch = [&](int k) {
@@ -502,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const float *partial, int blocks, int d, float *dwq, float *dwk)
 {
     __shared__ float s[32][33];
+    ptx::wait_for_launch_before();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
     float a = 0.f;
     for (int b = y; b < blocks; b += 32)
@@ -561,8 +564,16 @@ cudaError_t launch_bwd(const NormRopeParams &p, cudaStream_t s)
     e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    weight_grad_kernel<<<dim3(D / 32, 2), 1024, 0, s>>>(p.partial, blocks, D, p.dq_weight, p.dk_weight);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / 32, 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weight_grad_kernel, (const float *)p.partial, blocks, D, p.dq_weight, p.dk_weight);
 }
 
 template <class E, int D>
