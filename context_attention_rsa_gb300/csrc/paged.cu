@@ -198,7 +198,7 @@ rsa_status check_prefix_shape(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, i
     RSA_TRY(check_head_dim(d));
     if (Hq / Hkv > kPrefixMaxGroup)
         return fail(RSA_ERR_UNSUPPORTED, "Hq / Hkv = %d exceeds %d query heads per key head", Hq / Hkv, kPrefixMaxGroup);
-    if (T > 0x7fffffffLL || T * (int64_t)Hq > (1ll << 33))
+    if (T > (1ll << 30) || T * (int64_t)Hq > (1ll << 33))
         return fail(RSA_ERR_UNSUPPORTED, "T=%lld tokens of Hq=%d heads: too many rows", (long long)T, Hq);
     return RSA_OK;
 }

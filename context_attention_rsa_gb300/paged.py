@@ -127,10 +127,13 @@ def _call_on(device: torch.device, fn: str, stream, temporaries: Sequence[torch.
     handle = _raw_stream(index)
     if stream is not None:
         if hasattr(stream, "cuda_stream"):
+            if temporaries and stream.cuda_stream != handle:
+                # made on the current stream, used on another one: their memory may still be in use
+                # there, and is not to be handed out again before the call is done
+                stream.wait_stream(torch.cuda.current_stream(index))
+                for t in temporaries:
+                    t.record_stream(stream)
             handle = stream.cuda_stream
-            # made on the current stream, used on another one: not to be handed out again before it is done
-            for t in temporaries:
-                t.record_stream(stream)
         elif temporaries and handle != int(stream):
             raise ValueError("with a bare stream handle other than the current stream's, pass every output and workspace")
         else:
@@ -151,6 +154,8 @@ def page_plan(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torc
     tokens gets its cache slot and position, rows behind them slot -1.
     cached_len and new_len are int32 [R].  Check info[0] (PLAN_STATUS) where the
     host can afford to wait: a step that cannot be planned changes nothing."""
+    if not isinstance(cached_len, torch.Tensor) or not cached_len.is_cuda:
+        raise TypeError("cached_len must be a CUDA tensor")
     dev = cached_len.device
     _check("cached_len", cached_len, 1, torch.int32, dev)
     R = cached_len.shape[0]

@@ -127,3 +127,36 @@ def test_prompt_then_captured_decode(dtype, d, page, prefix, pad):
                     seen[r].append((ref.to64(ko[j]), ref.to64(cut(x)[2][j])))
         assert [len(s) for s in seen] == lens
     rsa.check_device_error()
+
+
+def test_outputs_made_for_another_stream_wait_for_their_memory():
+    # The memory of a tensor that the current stream still reads may be handed out for a call's outputs: a call on
+    # another stream must not write it before that reading is done.
+    need_cuda()
+    T, H, d = 4096, 8, 128
+    k = torch.randn(T, H, d, device="cuda")
+    x = torch.full((T, H, d), 7.0, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)   # some ten milliseconds on the current stream
+    y = x.clone()
+    at = x.data_ptr()
+    del x
+    q, _ = rsa.qk_norm_rope(k, k, None, None, None, None, stream=side)
+    assert q.data_ptr() == at       # (the block came back at once: else this shows nothing)
+    torch.cuda.synchronize()
+    assert (y == 7).all()
+
+
+def test_host_tensors_are_refused_with_a_gpu_at_hand():
+    need_cuda()
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(TypeError):
+        rsa.page_plan(i32(2), i32(2), i32(2, 2), i32(4), 16, 4, 8)
+    with pytest.raises(TypeError):
+        rsa.page_plan(i32(2).cuda(), i32(2), i32(2, 2).cuda(), i32(4).cuda(), 16, 4, 8)
+    x = torch.zeros(2, 2, 64, device="cuda")
+    with pytest.raises(TypeError):
+        rsa.qk_norm_rope(x, x.cpu(), None, None, None, None)
+    with pytest.raises(TypeError):
+        rsa.prefix_attn(x, x.view(1, 2, 1, 128).cpu(), x, i32(3), i32(2, 1), i32(2))
