@@ -2,7 +2,6 @@
 // its heads with the cache write, and attention behind a shared prefix.
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "rsa_internal.h"
 
@@ -193,6 +192,8 @@ rsa_status check_prefix_shape(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, i
     RSA_TRY(check_dtype(dt));
     if (T < 1 || Hq < 1 || Hkv < 1 || R < 1)
         return fail(RSA_ERR_INVALID_ARG, "T, Hq, Hkv, R must be >= 1 (got %lld, %d, %d, %d)", (long long)T, Hq, Hkv, R);
+    if (R > (1 << 30))
+        return fail(RSA_ERR_UNSUPPORTED, "R=%d: more than 2^30 requests", R);
     if (Hq % Hkv)
         return fail(RSA_ERR_INVALID_ARG, "Hkv=%d does not divide Hq=%d", Hkv, Hq);
     RSA_TRY(check_head_dim(d));
@@ -396,14 +397,27 @@ rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_
         return fail(RSA_ERR_INVALID_ARG,
                     "max_pages=%d (rows %lld apart): at least 1, at most the row and 2^31-1 keys are wanted", max_pages,
                     (long long)table_stride);
-    if (prefix_len < 0 || prefix_len > 0x7fffffffLL)
-        return fail(RSA_ERR_INVALID_ARG, "prefix_len=%lld must be in [0, 2^31-1]", (long long)prefix_len);
+    if (prefix_len < 0 || prefix_len > (1ll << 31) - 128)  // (a tile's last key is still an int)
+        return fail(RSA_ERR_INVALID_ARG, "prefix_len=%lld must be in [0, 2^31-128]", (long long)prefix_len);
     if (prefix_len > 0)
         RSA_TRY(check_i32_ptr(prefix_pages, "prefix_pages"));
     const PrefixLayout lay = prefix_layout(T, Hq, d, R);
     RSA_TRY(check_ptr(workspace, "workspace"));
     if (ws_bytes < lay.total)
         return fail(RSA_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", ws_bytes, lay.total);
+    // Rows are read again after others have been written.
+    const int64_t size = dt == RSA_F32 ? 4 : 2, cache = n_pages * Hkv * page_size * d * size;
+    const struct {
+        const void *p;
+        int64_t n;
+        const char *name;
+    } bufs[] = {{q, ((T - 1) * q_token_stride + (Hq - 1) * q_head_stride + d) * size, "q"}, {k_cache, cache, "k_cache"},
+                {v_cache, cache, "v_cache"}, {out, T * Hq * d * size, "out"}, {lse, T * Hq * 4, "lse"},
+                {workspace, (int64_t)lay.total, "workspace"}};
+    for (int i = 3; i < 6; ++i)  // what is written
+        for (int j = 0; j < i; ++j)
+            if (overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n))
+                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", bufs[i].name, bufs[j].name);
     RSA_TRY(check_device_for(dt));
     PrefixAttnParams p;
     memset(&p, 0, sizeof p);

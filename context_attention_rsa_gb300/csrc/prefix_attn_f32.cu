@@ -396,13 +396,14 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
             }
         }
     }
-    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    const bool empty = !(L > 0.f) && L == L;  // (a NaN stays one)
+    const float inv = empty ? 0.f : 1.f / L;
     E *out = static_cast<E *>(p.out) + row * D + lane * PER;
 #pragma unroll
     for (int c = 0; c < PER; ++c)
         store(out + c, acc[c] * inv);
     if (lane == 0)
-        p.lse[row] = M == -INFINITY ? -INFINITY : M + logf(L);
+        p.lse[row] = empty ? -INFINITY : M + logf(L);
 }
 
 template <int D>

@@ -20,6 +20,8 @@
  *   - Tensors are dense row-major.  q, k, v and out are [B, H, T, d]
  *     (d = d_k, the head dimension); lse is [B, H, T].  "Row" means one
  *     (b, h, t) query row.
+ *     (The calls for serving over a paged KV cache take packed tokens
+ *     [T, H, d] and pages instead; their section says which.)
  *   - Pointers named q, k, v, out, lse, o_*, lse_* and workspace are DEVICE
  *     pointers on the current CUDA device, 16-byte aligned (the *_host
  *     arguments of rsa_ring_attn_fwd_host are host pointers).  The caller
@@ -549,21 +551,22 @@ rsa_status rsa_qk_norm_rope_bwd(const rsa_qk_norm_rope_args *args, rsa_heads dq_
  *   its own tokens [0, kv_len[r] - n + i], in the pages of its table row.
  *   out [T, Hq, d] (dtype dt) = softmax(q K^T / sqrt(d)) V, lse [T, Hq] fp32
  * over both together.  A row that sees nothing gets out = 0, lse = -inf; rows
- * behind the last request (from cu_q[R] on) are left as they were.  The keys
+ * of no request (before cu_q[0], from cu_q[R] on) are left as they were.  The keys
  * and values of the prefix are read once for the whole batch, not once for
  * each request; prefix_len = 0 is plain attention over a paged cache.  Entries
  * of block_table past a request's keys are not read, and cache rows past
  * kv_len or prefix_len may hold anything; rows within them have to be finite
  * (a token's row that a request's earlier new tokens do not see yet is still
  * multiplied, by zero).
- * Hq / Hkv is at most 128.  Meant for steps whose new tokens are few next to
+ * Hq / Hkv is at most 128.  What is written (out, lse, workspace) overlaps
+ * nothing else.  prefix_len is the call's own: a captured call keeps it, while
+ * its lengths, tables and page ids may change.  Meant for steps whose new tokens are few next to
  * the keys: a request's keys are shared out as if all its new tokens saw all
  * of them, which costs up to twice the time for a prompt without a past (the
  * ring is the call for that).  `workspace` holds
- * rsa_prefix_attn_workspace_size() bytes and is written: calls that may run at
- * the same time (two streams, two captured graphs) each need their own.  Two
- * launches; the work is shared out on the device, so a captured call may be
- * replayed with other lengths.
+ * rsa_prefix_attn_workspace_size() bytes: calls that may run at the same time
+ * (two streams, two captured graphs) each need their own.  Two launches; the
+ * work is shared out on the device, from the lengths that it finds there.
  */
 rsa_status rsa_prefix_attn_workspace_size(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int R, size_t *bytes);
 rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,

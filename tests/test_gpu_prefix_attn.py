@@ -155,6 +155,51 @@ def test_large_scores_and_infinite_values_in_masked_rows():
         rsa.check_device_error()
 
 
+@pytest.mark.parametrize("prefix", [0, 200])
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
+def test_a_request_of_nan_stays_by_itself(dtype, prefix):
+    # the others' rows keep their bits; its own are NaN, their lse too unless only the values are
+    need_cuda()
+    for what in ("q", "k", "v"):
+        b = Batch([1, 3, 1, 2], [70, 300, 5, 129], prefix, 8, 2, 128, 32, dtype)
+        want, wl = b.run()
+        if what == "q":
+            b.q[1:4] = float("nan")
+        else:
+            (b.kc if what == "k" else b.vc)[int(b.table[1, 2]), :, 7] = float("nan")
+        out, lse = b.run()
+        keep = [0, 4, 5, 6]
+        assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], wl[keep])
+        assert out[1:4].isnan().all()
+        assert torch.equal(lse[1:4], wl[1:4]) if what == "v" else lse[1:4].isnan().all()
+    rsa.check_device_error()
+
+
+@pytest.mark.parametrize("prefix", [0, 100])
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
+def test_more_requests_than_threads(dtype, prefix):
+    # a block looks at the lengths in several turns; requests without tokens and without keys among them
+    need_cuda()
+    rng = np.random.default_rng(7)
+    new = rng.integers(0, 3, 1100)
+    lens = np.where(rng.integers(0, 9, 1100) == 0, 0, new + rng.integers(0, 60, 1100))
+    Batch(new.tolist(), lens.tolist(), prefix, 4, 2, 64, 16, dtype).check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
+def test_rows_before_the_first_request(dtype):
+    need_cuda()
+    for prefix in (0, 150):
+        b = Batch([1, 2], [100, 40], prefix, 6, 2, 64, 32, dtype, extra=5)
+        b.cu += 3
+        out, lse = torch.full((8, 6, 64), 7.0, dtype=dtype, device="cuda"), torch.full((8, 6), 8.0, device="cuda")
+        b.run(out=out, lse=lse)
+        rsa.check_device_error()
+        ref.assert_prefix_attn(out[3:6], lse[3:6], tuple(x[3:6] for x in b.reference()), dtype)
+        for rows in (slice(0, 3), slice(6, 8)):
+            assert (out[rows] == 7).all() and (lse[rows] == 8).all()
+
+
 def test_one_request_equals_the_dense_decode():
     # the same keys as a dense cache of the library's own decode
     need_cuda()

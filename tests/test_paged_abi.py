@@ -134,6 +134,23 @@ def test_prefix_attn_refuses(kw, code):
     assert attn_call(**kw) == code, rsa.load().rsa_last_error_string()
 
 
+# addresses far enough apart for the shape above: 1024 bytes a token of q, 16 KB of cache a page and key head
+APART = dict(q=0x1000000, kc=0x2000000, vc=0x3000000, out=0x4000000, lse=0x5000000, ws=0x10000000, nb=0x10000000)
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(out=0x1000000), b"out overlaps q"), (dict(out=0x1000000 + 15 * 2048), b"out overlaps q"),
+    (dict(out=0x2000000 + 100 * 2 * 64 * 128 * 2 - 16), b"out overlaps k_cache"), (dict(lse=0x3000010), b"lse overlaps v_cache"),
+    (dict(lse=0x4000010), b"lse overlaps out"), (dict(ws=0x4000000 - 0x1000000), b"workspace overlaps"),
+    (dict(ws=0x800000), b"workspace overlaps q"),
+    (dict(plen=(1 << 31) - 127), b"prefix_len"), (dict(plen=(1 << 31) - 1), b"prefix_len"),
+    (dict(R=(1 << 30) + 1, nb=1 << 40, ws=1 << 41), b"requests"),
+])
+def test_prefix_attn_refuses_overlaps_and_lengths_that_do_not_fit(kw, what):
+    code = attn_call(**{**APART, **kw})
+    assert code in (INVALID, UNSUPPORTED) and what in rsa.load().rsa_last_error_string(), rsa.load().rsa_last_error_string()
+
+
 def test_prefix_attn_workspace_size():
     # a plan, two homes for every row, 256 rows for each of 160 workers; no term in the lengths
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
