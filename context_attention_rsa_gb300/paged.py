@@ -18,6 +18,7 @@ with other lengths: what depends on them is read on the device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import NamedTuple, Optional, Sequence, Tuple
 
@@ -113,6 +114,13 @@ def _heads(name: str, t, dtype: torch.dtype, device: torch.device, shape=None) -
     return Heads(*_row_layout(name, t, dtype, device, shape))
 
 
+def _new_rows(shape, dtype: torch.dtype, device: torch.device, made: list) -> Tuple[torch.Tensor, Heads]:
+    """A dense [T, H, d] result."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    made.append(t)
+    return t, Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+
+
 # The device's current stream as a bare handle (a Stream object takes longer to make than a launch).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -143,6 +151,16 @@ def _call_on(device: torch.device, fn: str, stream, temporaries: Sequence[torch.
     if st != 0:
         detail = lib.rsa_last_error_string()
         raise RsaError(fn, st, detail.decode() if detail else "")
+
+
+def _workspace(n: int, device: torch.device, stream, made: list) -> Tuple[int, int]:
+    """Address and bytes of device memory for one call, kept by `made` until it is enqueued."""
+    if stream is None:
+        # (after a launch a tensor costs 2 to 4 us more to make than its memory)
+        made.append(torch.UntypedStorage(n, device=device))
+    else:
+        made.append(torch.empty(n, dtype=torch.uint8, device=device))  # (can be recorded on another stream)
+    return made[-1].data_ptr(), n
 
 
 def page_plan(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -246,13 +264,15 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6
     dev, dt, q_shape, k_shape = q.device, q.dtype, tuple(q.shape), tuple(k.shape)
     made = []
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=dt, device=dev)
-        made.append(q_out)
-    if k_out is None and slot_map is None:
-        k_out = torch.empty(k_shape, dtype=dt, device=dev)
-        made.append(k_out)
-    qo = _heads("q_out", q_out, dt, dev, q_shape)
-    ko = Heads() if k_out is None else _heads("k_out", k_out, dt, dev, k_shape)
+        q_out, qo = _new_rows(q_shape, dt, dev, made)
+    else:
+        qo = _heads("q_out", q_out, dt, dev, q_shape)
+    if k_out is not None:
+        ko = _heads("k_out", k_out, dt, dev, k_shape)
+    elif slot_map is None:
+        k_out, ko = _new_rows(k_shape, dt, dev, made)
+    else:
+        ko = Heads()
     if slot_map is None:
         if v is not None or k_cache is not None or v_cache is not None:
             raise ValueError("v, k_cache and v_cache go with slot_map")
@@ -268,6 +288,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=None)
+def _norm_rope_bwd_workspace_size(d: int) -> int:
+    n = ctypes.c_size_t(0)
+    load().rsa_qk_norm_rope_bwd_workspace_size(d, ctypes.byref(n))
+    return n.value or 1  # (the call itself refuses another d)
+
+
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6,
                      interleaved: bool = False, sections: Optional[Sequence[int]] = None, dq=None, dk=None,
                      workspace=None, stream=None):
@@ -278,22 +305,28 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_si
     dev, dt, q_shape, k_shape = q.device, q.dtype, tuple(q.shape), tuple(k.shape)
     gq, gk = _heads("dq_out", dq_out, dt, dev, q_shape), _heads("dk_out", dk_out, dt, dev, k_shape)
     made = []
-
-    def make(shape, dtype):
-        made.append(torch.empty(shape, dtype=dtype, device=dev))
-        return made[-1]
-    dq = make(q_shape, dt) if dq is None else dq
-    dk = make(k_shape, dt) if dk is None else dk
+    if dq is None:
+        dq, dqh = _new_rows(q_shape, dt, dev, made)
+    else:
+        dqh = _heads("dq", dq, dt, dev, q_shape)
+    if dk is None:
+        dk, dkh = _new_rows(k_shape, dt, dev, made)
+    else:
+        dkh = _heads("dk", dk, dt, dev, k_shape)
     d = q_shape[2]
-    dwq = None if q_weight is None else make((d,), torch.float32)
-    dwk = None if k_weight is None else make((d,), torch.float32)
+    dwq = dwk = None
+    if q_weight is not None:
+        dwq = torch.empty(d, dtype=torch.float32, device=dev)
+        made.append(dwq)
+    if k_weight is not None:
+        dwk = torch.empty(d, dtype=torch.float32, device=dev)
+        made.append(dwk)
     if workspace is None:
-        n = ctypes.c_size_t(0)
-        load().rsa_qk_norm_rope_bwd_workspace_size(d, ctypes.byref(n))
-        workspace = make((max(n.value, 1),), torch.uint8)
-    _call_on(dev, "rsa_qk_norm_rope_bwd", stream, made, a, gq, gk, _heads("dq", dq, dt, dev, q_shape),
-             _heads("dk", dk, dt, dev, k_shape), None if dwq is None else dwq.data_ptr(),
-             None if dwk is None else dwk.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        ws = _workspace(_norm_rope_bwd_workspace_size(d), dev, stream, made)
+    else:
+        ws = workspace.data_ptr(), workspace.nbytes
+    _call_on(dev, "rsa_qk_norm_rope_bwd", stream, made, a, gq, gk, dqh, dkh, None if dwq is None else dwq.data_ptr(),
+             None if dwk is None else dwk.data_ptr(), *ws)
     return dq, dk, dwq, dwk
 
 
@@ -316,6 +349,7 @@ def _check_caches(k_cache, v_cache, Hkv: int, d: int, dt: torch.dtype, dev: torc
     return n_pages, page_size
 
 
+@functools.lru_cache(maxsize=1024)
 def prefix_attn_workspace_size(dtype: torch.dtype, T: int, Hq: int, Hkv: int, d: int, R: int) -> int:
     n = ctypes.c_size_t(0)
     lib = load()
@@ -372,11 +406,12 @@ def prefix_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages=Non
         if lse.shape != q.shape[:2]:
             raise ValueError("lse must be [T, Hq]")
     if workspace is None:
-        workspace = torch.empty(prefix_attn_workspace_size(dt, T, Hq, Hkv, d, R), dtype=torch.uint8, device=dev)
-        made.append(workspace)
+        ws = _workspace(prefix_attn_workspace_size(dt, T, Hq, Hkv, d, R), dev, stream, made)
+    else:
+        ws = workspace.data_ptr(), workspace.nbytes
     _call_on(dev, "rsa_prefix_attn_fwd", stream, made, *q_at, k_cache.data_ptr(),
              v_cache.data_ptr(), code, T, Hq, Hkv, d, page_size, n_pages, cu_q.data_ptr(), kv_len.data_ptr(), R,
              block_table.data_ptr(), max_pages if R == 1 else block_table.stride(0), max_pages,
              prefix_pages.data_ptr() if prefix_len else None, prefix_len, out.data_ptr(), lse.data_ptr(),
-             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+             *ws)
     return out, lse
