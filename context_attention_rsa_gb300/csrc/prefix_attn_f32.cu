@@ -7,14 +7,15 @@
 // whose (o, lse) are joined with
 //   M = max_i lse_i, L = M + ln sum e^{lse_i - M}, o = sum e^{lse_i - L} o_i.
 //
-// A CTA takes its stretch of the work (paged_sched.cuh).  It brings 32 keys and
-// values at a time into shared memory, by asynchronous copies one block ahead of
-// the arithmetic; a warp owns up to 8 rows of the unit.
-// Lane k scores key k (a dot product along d, its own row of K from shared
-// memory, the queries broadcast), maximum and sum are shuffles, and for the output
-// lane c owns columns c, c + 32, ... with the probabilities broadcast.  All of a
-// warp's rows go through a block together, so that K and V are read from shared
-// memory once for them; shared memory is the bound.
+// A CTA takes its stretch of the work (paged_sched.cuh).  It brings 128 (d = 64) or
+// 64 keys and values at a time into shared memory, by asynchronous copies one such
+// turn ahead of the arithmetic, in blocks of 32 keys.  A warp takes up to 8 rows of
+// the unit through a block: lane (x, y) of 8 x 4 scores keys x, x + 8, .. for rows y
+// and y + 4, and owns columns 4x.. of each 32 of the same rows of the output, so that
+// every value read from shared memory, which is the bound, serves several products
+// and a row's maximum and factors stay in its lanes.  A unit of few rows leaves warps
+// over: they are then cut into 2 or 4 key groups, which take the turn's blocks in
+// parallel and join their rows at the end of the piece.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -32,7 +33,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
 constexpr int kRows = 128;            // rows of a unit
-constexpr int kWarpRows = kRows / kWarps;
+constexpr int kWarpRows = 8;
 constexpr int kKeys = 32;             // keys of a block
 
 __device__ __forceinline__ float warp_max(float x)
@@ -64,10 +65,12 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src, bool ther
 
 template <int D>
 struct Smem {
-    float q[kRows][D];
-    float k[2][kKeys][D + 4];  // (+ 4: the lanes' rows fall into different banks)
-    float v[2][kKeys][D];
-    float p[kRows][kKeys];  // the block's probabilities
+    static constexpr int kBlocks = D == 64 ? 4 : 2, kTurn = kBlocks * kKeys;  // of a turn
+    // (rows are padded so that 8 rows of K and 4 of the others fall into different banks)
+    float q[kRows][D + 4];
+    float k[2][kTurn][D + 4];
+    float v[2][kTurn][D];
+    float p[kWarps][kWarpRows][kKeys + 8];  // a warp's probabilities of its block
     int64_t sum[kWarps];
     Stretch st;
 };
@@ -102,13 +105,123 @@ __device__ __forceinline__ void fetch(const PrefixAttnParams &p, const Piece &x,
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
+// A lane's rows of a piece: y and y + 4 of its warp's.
+template <int D>
+struct Rows {
+    static constexpr int H = D / 32;
+    float m[2], l[2];  // (l: of this lane's keys)
+    float4 o[2][H];
+    int see[2];  // they see keys [0, see) of the segment
+};
+
+__device__ __forceinline__ void add_product(float4 &o, float p, const float4 &v)
+{
+    const float2 pp = make_float2(p, p);
+    const float2 a = __ffma2_rn(pp, make_float2(v.x, v.y), make_float2(o.x, o.y));
+    const float2 b = __ffma2_rn(pp, make_float2(v.z, v.w), make_float2(o.z, o.w));
+    o = make_float4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ void scale_by(float4 &o, float a) { o.x *= a, o.y *= a, o.z *= a, o.w *= a; }
+
+// A warp's first 4 J rows, whose queries are q, through one block of nk keys from key j0 on.
+template <int D, int J>
+__device__ __forceinline__ void block(Rows<D> &r, const float (*q)[D + 4], const float (*ks)[D + 4], const float (*vs)[D],
+                                      float (*ps)[kKeys + 8], int nk, int j0, float scale)
+{
+    constexpr int H = Rows<D>::H;
+    const int x = threadIdx.x & 7, y = (threadIdx.x & 31) >> 3;
+    float2 dot[4][J];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            dot[i][j] = make_float2(0.f, 0.f);
+    // (Past the last key or row it reads what lies there; those scores are not used.)
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 u[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            u[j] = *reinterpret_cast<const float4 *>(&q[y + 4 * j][c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 w = *reinterpret_cast<const float4 *>(&ks[x + 8 * i][c]);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                dot[i][j] = __ffma2_rn(make_float2(u[j].x, u[j].y), make_float2(w.x, w.y), dot[i][j]);
+                dot[i][j] = __ffma2_rn(make_float2(u[j].z, u[j].w), make_float2(w.z, w.w), dot[i][j]);
+            }
+        }
+    }
+    float sc[4][J], mx[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int lim = min(nk, r.see[j] - j0);
+        mx[j] = r.m[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sc[i][j] = x + 8 * i < lim ? (dot[i][j].x + dot[i][j].y) * scale : -INFINITY;
+            mx[j] = fmaxf(mx[j], sc[i][j]);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], d));
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const float base = mx[j] == -INFINITY ? 0.f : mx[j], alpha = expf(r.m[j] - base);
+        r.m[j] = mx[j];
+        r.l[j] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float pj = expf(sc[i][j] - base);
+            r.l[j] += pj;
+            ps[y + 4 * j][x + 8 * i] = pj;
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            scale_by(r.o[j][h], alpha);
+    }
+    __syncwarp();
+    int k = 0;
+#pragma unroll 1
+    for (; k + 4 <= nk; k += 4) {
+        float4 pk[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            pk[j] = *reinterpret_cast<const float4 *>(&ps[y + 4 * j][k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float4 v = *reinterpret_cast<const float4 *>(&vs[k + e][32 * h + 4 * x]);
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    add_product(r.o[j][h], e == 0 ? pk[j].x : (e == 1 ? pk[j].y : (e == 2 ? pk[j].z : pk[j].w)), v);
+            }
+    }
+#pragma unroll 1
+    for (; k < nk; ++k)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const float4 v = *reinterpret_cast<const float4 *>(&vs[k][32 * h + 4 * x]);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                add_product(r.o[j][h], ps[y + 4 * j][k], v);
+        }
+    __syncwarp();  // ps is written again with the next block
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_constant__ PrefixAttnParams p)
 {
-    constexpr int PER = D / 32;
+    constexpr int H = D / 32, kBlocks = Smem<D>::kBlocks, kTurn = Smem<D>::kTurn;
     extern __shared__ __align__(16) unsigned char raw[];
     Smem<D> &s = *reinterpret_cast<Smem<D> *>(raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane_x = threadIdx.x & 7, y = (threadIdx.x & 31) >> 3;
     const int G = p.G;
     const int worker = blockIdx.x;
     const float scale = 1.0f / sqrtf((float)D);
@@ -120,126 +233,111 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     Piece x;
     while (walk.next(p, x)) {
         const int rows = (int)x.ntok * G;
-        __syncthreads();  // the last piece's rows are done with q
+        __syncthreads();  // the last piece's rows are done with q, and with the ring
 #pragma unroll 4
         for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
             const int row = i / (D / 4), c = i % (D / 4) * 4;
             const int64_t at = (int64_t)(x.tok + row / G) * p.q_token_stride + (x.head * G + row % G) * p.q_head_stride + c;
             *reinterpret_cast<float4 *>(&s.q[row][c]) = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
         }
-        // Rows i * kWarps + warp of the unit, i < mine, and the keys they see.
-        const int mine = max(0, (rows - warp + kWarps - 1) / kWarps);
-        float m[kWarpRows], l[kWarpRows], o[kWarpRows][PER];
-        int64_t see[kWarpRows];
+        // kWarpRows rows a warp, or fewer, and as many key groups of such warps as there
+        // are warps and blocks for.
+        const int row_groups = (rows + kWarpRows - 1) / kWarpRows, per = (rows + row_groups - 1) / row_groups;
+        int key_groups = kBlocks;
+        while (row_groups * key_groups > kWarps)
+            key_groups >>= 1;
+        const int kg = warp / row_groups, row0 = (warp - kg * row_groups) * per;
+        const bool works = kg < key_groups;
+        Rows<D> r;
 #pragma unroll
-        for (int i = 0; i < kWarpRows; ++i) {
-            const int row = i * kWarps + warp;
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-            see[i] = row < rows ? min((int64_t)x.keys, x.see0 + row / G) : 0;
+        for (int j = 0; j < 2; ++j) {
+            const int row = row0 + y + 4 * j;
+            r.m[j] = -INFINITY;
+            r.l[j] = 0.f;
+            r.see[j] = row < rows ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + row / G)) : 0;
 #pragma unroll
-            for (int c = 0; c < PER; ++c)
-                o[i][c] = 0.f;
+            for (int h = 0; h < H; ++h)
+                r.o[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const int64_t most = min((int64_t)x.keys, x.see0 + (x.ntok - 1));  // the keys that any row sees
         const int64_t j1 = min(most, (int64_t)x.t1 * kTileKeys);
         const int64_t j00 = (int64_t)x.t0 * kTileKeys;
-        // Block b of 32 keys: this thread copies 16 bytes of kCopies keys, whose pages'
-        // ids it read a block before.  Keys past the last one are not copied.
-        constexpr int kPieces = D / 4, kCopies = kKeys * kPieces / kThreads;
+        // A turn: this thread copies 16 bytes of kCopies keys, whose pages' ids it read
+        // a turn before.  Keys past the last one are not copied.
+        constexpr int kPieces = D / 4, kCopies = kTurn * kPieces / kThreads, kStep = kThreads / kPieces;
         const int piece = threadIdx.x % kPieces, key0 = threadIdx.x / kPieces;
         int ids[kCopies];
-        look_up<kCopies>(p, x, j00 + key0, kThreads / kPieces, j1, ids);
-        fetch<D, kCopies>(p, x, s, 0, key0, piece, kThreads / kPieces, j00, j1, ids);
-        look_up<kCopies>(p, x, j00 + kKeys + key0, kThreads / kPieces, j1, ids);
+        look_up<kCopies>(p, x, j00 + key0, kStep, j1, ids);
+        fetch<D, kCopies>(p, x, s, 0, key0, piece, kStep, j00, j1, ids);
+        look_up<kCopies>(p, x, j00 + kTurn + key0, kStep, j1, ids);
         int buffer = 0;
-        for (int64_t j0 = j00; j0 < j1; j0 += kKeys, buffer ^= 1) {
-            const int nk = (int)min((int64_t)kKeys, j1 - j0);
-            fetch<D, kCopies>(p, x, s, buffer ^ 1, key0, piece, kThreads / kPieces, j0 + kKeys, j1, ids);
-            look_up<kCopies>(p, x, j0 + 2 * kKeys + key0, kThreads / kPieces, j1, ids);
+        for (int64_t j0 = j00; j0 < j1; j0 += kTurn, buffer ^= 1) {
+            fetch<D, kCopies>(p, x, s, buffer ^ 1, key0, piece, kStep, j0 + kTurn, j1, ids);
+            look_up<kCopies>(p, x, j0 + 2 * kTurn + key0, kStep, j1, ids);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncthreads();  // every thread's copies of this block
-            // (four chains of sums a row: a warp has few rows to hide their latency behind)
-            float4 dot[kWarpRows];
+            __syncthreads();  // every thread's copies of this turn
+            for (int b = works ? kg : kBlocks; b < kBlocks; b += key_groups) {
+                const int64_t jb = j0 + b * kKeys;
+                if (jb >= j1)
+                    break;
+                const int nk = (int)min((int64_t)kKeys, j1 - jb);
+                if (per <= 4)
+                    block<D, 1>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale);
+                else
+                    block<D, 2>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale);
+            }
+            __syncthreads();  // the turn is done with: its buffer is filled next
+        }
 #pragma unroll
-            for (int i = 0; i < kWarpRows; ++i)
-                dot[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (lane < nk) {
-#pragma unroll 4
-                for (int c = 0; c < D / 4; ++c) {
-                    const float4 w = *reinterpret_cast<const float4 *>(&s.k[buffer][lane][4 * c]);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < kWarpRows; ++i) {
-                        if (i >= mine)
-                            break;  // the same for the whole warp
-                        const float4 u = *reinterpret_cast<const float4 *>(&s.q[i * kWarps + warp][4 * c]);
-                        dot[i].x = fmaf(u.x, w.x, dot[i].x);
-                        dot[i].y = fmaf(u.y, w.y, dot[i].y);
-                        dot[i].z = fmaf(u.z, w.z, dot[i].z);
-                        dot[i].w = fmaf(u.w, w.w, dot[i].w);
+            for (int d = 1; d < 8; d <<= 1)
+                r.l[j] += __shfl_xor_sync(0xffffffffu, r.l[j], d);
+        // The key groups' rows are joined in their order, through the ring.
+        float(*scratch)[D + 4] = s.k[0];  // [key group - 1][row]: o, m, l
+        static_assert(sizeof s.k >= sizeof(float) * kRows * (D + 4), "scratch");
+        if (key_groups > 1) {
+            if (works && kg > 0) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = row0 + y + 4 * j;
+                    if (y + 4 * j >= per || row >= rows)
+                        continue;
+                    float *w = scratch[(kg - 1) * rows + row];
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        *reinterpret_cast<float4 *>(w + 32 * h + lane_x * 4) = r.o[j][h];
+                    if (lane_x == 0) {
+                        w[D] = r.m[j];
+                        w[D + 1] = r.l[j];
                     }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < kWarpRows; ++i) {
-                if (i >= mine)
-                    break;
-                const float sc = lane < min((int64_t)nk, see[i] - j0) ? ((dot[i].x + dot[i].y) + (dot[i].z + dot[i].w)) * scale : -INFINITY;
-                const float mn = fmaxf(m[i], warp_max(sc));
-                const float base = mn == -INFINITY ? 0.f : mn;
-                const float alpha = expf(m[i] - base), pj = expf(sc - base);
-                l[i] = l[i] * alpha + warp_sum(pj);
-                m[i] = mn;
-                s.p[i * kWarps + warp][lane] = pj;
-#pragma unroll
-                for (int c = 0; c < PER; ++c)
-                    o[i][c] *= alpha;
-            }
-            __syncwarp();
-            int k = 0;
-            for (; k + 4 <= nk; k += 4) {
-                float v[4][PER];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int c = 0; c < PER; ++c)
-                        v[e][c] = s.v[buffer][k + e][lane + 32 * c];
-#pragma unroll
-                for (int i = 0; i < kWarpRows; ++i) {
-                    if (i >= mine)
-                        break;
-                    const float4 pk = *reinterpret_cast<const float4 *>(&s.p[i * kWarps + warp][k]);
-#pragma unroll
-                    for (int c = 0; c < PER; ++c)
-                        o[i][c] = fmaf(pk.w, v[3][c], fmaf(pk.z, v[2][c], fmaf(pk.y, v[1][c], fmaf(pk.x, v[0][c], o[i][c]))));
-                }
-            }
-            for (; k < nk; ++k) {
-                float v[PER];
-#pragma unroll
-                for (int c = 0; c < PER; ++c)
-                    v[c] = s.v[buffer][k][lane + 32 * c];
-#pragma unroll
-                for (int i = 0; i < kWarpRows; ++i) {
-                    if (i >= mine)
-                        break;
-                    const float pk = s.p[i * kWarps + warp][k];
-#pragma unroll
-                    for (int c = 0; c < PER; ++c)
-                        o[i][c] = fmaf(pk, v[c], o[i][c]);
-                }
-            }
-            __syncthreads();  // the block is done with: its buffer is filled next
+            __syncthreads();
         }
+        if (kg > 0)
+            continue;
 #pragma unroll
-        for (int i = 0; i < kWarpRows; ++i) {
-            const int row = i * kWarps + warp;
-            if (row >= rows)
+        for (int j = 0; j < 2; ++j) {
+            const int row = row0 + y + 4 * j;
+            if (y + 4 * j >= per || row >= rows)
                 continue;
+            for (int g = 1; g < key_groups; ++g) {
+                const float *w = scratch[(g - 1) * rows + row];
+                const float mn = fmaxf(r.m[j], w[D]), base = mn == -INFINITY ? 0.f : mn;
+                const float a = expf(r.m[j] - base), b = expf(w[D] - base);
+                r.m[j] = mn;
+                r.l[j] = r.l[j] * a + w[D + 1] * b;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    scale_by(r.o[j][h], a);
+                    add_product(r.o[j][h], b, *reinterpret_cast<const float4 *>(w + 32 * h + lane_x * 4));
+                }
+            }
             const int token = x.tok + row / G;
             const int hq = x.head * G + row % G;
-            const bool empty = !(l[i] > 0.f) && l[i] == l[i];
-            const float inv = empty ? 0.f : 1.f / l[i];
+            const bool empty = !(r.l[j] > 0.f) && r.l[j] == r.l[j];
+            const float inv = empty ? 0.f : 1.f / r.l[j];
             const int64_t at = (int64_t)token * p.Hq + hq, slot = (int64_t)worker * kPrefixUnitRows + row;
             float *dst, *lse;
             if (is_result(p, x)) {
@@ -253,10 +351,12 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                 lse = p.slot_lse + slot;
             }
 #pragma unroll
-            for (int c = 0; c < PER; ++c)
-                dst[lane + 32 * c] = o[i][c] * inv;
-            if (lane == 0)
-                *lse = empty ? -INFINITY : m[i] + logf(l[i]);
+            for (int h = 0; h < H; ++h) {
+                scale_by(r.o[j][h], inv);
+                *reinterpret_cast<float4 *>(dst + 32 * h + lane_x * 4) = r.o[j][h];
+            }
+            if (lane_x == 0)
+                *lse = empty ? -INFINITY : r.m[j] + logf(r.l[j]);
         }
     }
 }
