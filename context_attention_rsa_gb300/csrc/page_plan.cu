@@ -13,7 +13,8 @@
 // finds its page in the old part of its table or, past that, straight in
 // free_pages, so no block reads a table entry that another one writes.  The
 // work is a few bytes a token: the launch and the scan's latency bound it at
-// any size a server sees.
+// any size a server sees (8 requests 7.0 us on the GPU, 4000 requests with 0.42
+// million rows 13.9 us, of which the 6.8 MB would take 1).
 #include "rsa_internal.h"
 
 namespace rsa {

@@ -12,7 +12,10 @@
 // over all tokens and heads.
 //
 // Bound by HBM: every element is read once and written once, about 10 (20
-// backward) operations apart.  A row of d elements lies across L = d * size / 16
+// backward) operations apart.  Measured, 64 + 8 heads of 128 in bf16: 32768 tokens
+// with their cache rows 224 us, 6.1 TB/s or 0.90 of a plain copy's rate; backward of
+// 8192 tokens 84 us, 5.4 TB/s, 0.80, with the sums' launch (the instructions take 0.6
+// of the issue slots); 1001 tokens of 8 + 8 heads of 64 in fp32, backward, 9.7 us.  A row of d elements lies across L = d * size / 16
 // lanes, its sums are shuffles among those.  A group of L lanes goes through a run
 // of items (kHeads heads of one token each): their rows come by 16-byte
 // asynchronous copies into a ring of kStages items in shared memory, so that the
