@@ -1,4 +1,5 @@
-"""In-tree build of librsa.so with nvcc for sm_103a.
+"""In-tree build of librsa.so with nvcc for sm_103a, and of the compiled part of
+the Python binding with the host compiler.
 
 Each .cu file is compiled to an object in parallel, then linked into
 ``context_attention_rsa_gb300/_build/librsa.so``.  A stamp of the sources,
@@ -11,6 +12,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -104,7 +107,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return lib
 
 
+BINDING = os.path.join(BUILD, "_paged.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the extension module of the paged calls (csrc/torch_paged.cpp) if
+    stale, against the running Python and PyTorch; returns its path."""
+    import torch
+    src, stamp = os.path.join(CSRC, "torch_paged.cpp"), os.path.join(BUILD, "_paged.stamp")
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(tdir, "include"), "-isystem", os.path.join(tdir, "include/torch/csrc/api/include"),
+           "-isystem", os.path.join(cuda, "include"), "-I", INCLUDE, src,
+           "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    h = hashlib.sha256(" ".join([torch.__version__, sys.version, *cmd]).encode())
+    for f in (src, os.path.join(INCLUDE, "rsa.h")):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    with _lock:
+        os.makedirs(BUILD, exist_ok=True)
+        if not force and os.path.exists(BINDING) and os.path.exists(stamp):
+            with open(stamp) as f:
+                if f.read().strip() == h.hexdigest():
+                    return BINDING
+        tmp = BINDING + f".tmp{os.getpid()}"
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("the binding's compiler failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+        os.replace(tmp, BINDING)
+        with open(stamp, "w") as f:
+            f.write(h.hexdigest())
+    return BINDING
+
+
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True,
                 extra_flags=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else []))
