@@ -121,7 +121,7 @@ def build_binding(force: bool = False) -> str:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(tdir, "include"), "-isystem", os.path.join(tdir, "include/torch/csrc/api/include"),
            "-isystem", os.path.join(cuda, "include"), "-I", INCLUDE, src,
-           "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     h = hashlib.sha256(" ".join([torch.__version__, sys.version, *cmd]).encode())
     for f in (src, os.path.join(INCLUDE, "rsa.h")):
         with open(f, "rb") as fh:

@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -130,7 +131,7 @@ public:
 
     at::Tensor make(at::IntArrayRef shape, at::ScalarType type)
     {
-        made_.push_back(at::empty(shape, at::TensorOptions().dtype(type).device(dev_)));
+        made_.push_back(at::detail::empty_cuda(shape, type, dev_, std::nullopt));
         return made_.back();
     }
 
