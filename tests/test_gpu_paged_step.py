@@ -2,6 +2,8 @@
 then captured decode steps, the plan feeding the cache write and the attention;
 the cache grows page by page behind a shared prefix.  Compared with attention
 over dense keys in 64 bits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -160,3 +162,77 @@ def test_host_tensors_are_refused_with_a_gpu_at_hand():
         rsa.qk_norm_rope(x, x.cpu(), None, None, None, None)
     with pytest.raises(TypeError):
         rsa.prefix_attn(x, x.view(1, 2, 1, 128).cpu(), x, i32(3), i32(2, 1), i32(2))
+
+
+def test_calls_of_two_threads_at_once():
+    # the calls let go of the interpreter while they launch; each thread has its stream and gets its own results
+    need_cuda()
+    T, Hq, Hkv, d, page = 40, 8, 2, 64, 32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    kc, vc = rand(60, Hkv, page, d), rand(60, Hkv, page, d)
+    cu, lens = i32(list(range(T + 1))), i32([1 + i for i in range(T)])
+    table = torch.arange(T * 2, device="cuda").view(T, 2).to(torch.int32) % 60
+    qs, cos_sin, pos = [rand(T, Hq, d) for _ in range(2)], rsa.rope_table(100, d), torch.arange(T, device="cuda")
+
+    def step(q):
+        x, _ = rsa.qk_norm_rope(q, q[:, :2], None, None, pos, cos_sin)
+        return rsa.prefix_attn(x, kc, vc, cu, table, lens, prefix_pages=table[3], prefix_len=50)
+    want = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    got[i].append(step(qs[i]))
+                    del got[i][:-3]
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+    rsa.check_device_error()
+
+
+def test_arguments_that_are_no_fitting_objects():
+    need_cuda()
+    q = torch.randn(3, 4, 64, device="cuda")
+    kc = torch.randn(4, 2, 16, 64, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (q, kc, kc.clone(), i32(0, 1, 3), torch.zeros(2, 2, dtype=torch.int32, device="cuda"), i32(5, 7))
+    out, lse = rsa.prefix_attn(*args)
+    n = rsa.prefix_attn_workspace_size(torch.float32, 3, 4, 2, 64, 2)
+    for bad, err in [(dict(stream=object()), TypeError), (dict(stream="0"), TypeError), (dict(prefix_len=1.5), TypeError),
+                     (dict(prefix_len=-1, prefix_pages=i32(0)), rsa.RsaError), (dict(prefix_len=10), TypeError),
+                     (dict(workspace=torch.zeros(2 * n, dtype=torch.uint8, device="cuda")[::2]), ValueError),
+                     (dict(workspace=torch.zeros(1, dtype=torch.uint8, device="cuda").expand(n)), ValueError),
+                     (dict(workspace=torch.zeros(n, dtype=torch.uint8)), TypeError), (dict(out=q.data_ptr()), TypeError),
+                     (dict(out=q), rsa.RsaError), (dict(lse=lse.t().contiguous().t()), ValueError)]:
+        with pytest.raises(err):
+            rsa.prefix_attn(*args, **bad)
+    pos, table = torch.arange(3, device="cuda"), rsa.rope_table(10, 64)
+    for bad, err in [(dict(sections=5), TypeError), (dict(sections=[]), ValueError), (dict(sections=[8] * 5), ValueError),
+                     (dict(sections=["a"]), TypeError), (dict(eps="x"), TypeError), (dict(eps=float("nan")), rsa.RsaError),
+                     (dict(eps=-1.0), rsa.RsaError)]:
+        with pytest.raises(err):
+            rsa.qk_norm_rope(q, q, None, None, pos, table, **bad)
+    with pytest.raises(TypeError):
+        rsa.qk_norm_rope(q, q, None, None, None, table)
+    # leaves of a graph are read like any tensor, and results have no history
+    leaf = torch.nn.Parameter(q)
+    a, b = rsa.qk_norm_rope(leaf, leaf, None, None, pos, table)
+    assert not a.requires_grad and torch.equal(a, rsa.qk_norm_rope(q, q, None, None, pos, table)[0])
+    out2, lse2 = rsa.prefix_attn(*args, stream=torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert rsa.prefix_attn(*args, out=out2, lse=lse2)[0] is out2
+    rsa.check_device_error()
