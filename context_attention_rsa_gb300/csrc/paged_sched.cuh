@@ -176,6 +176,34 @@ struct Piece {
     bool first, whole;     // it begins the unit; it is all of it
 };
 
+// Segments in ascending order for a warp that walks them: a lane each, 32 at a time,
+// so that a batch of short ones does not wait for its lengths request by request.
+struct Batch {
+    Segment mine;
+    int base = -64;
+
+    __device__ __forceinline__ Segment get(const PrefixAttnParams &p, int s)
+    {
+        const int lane = threadIdx.x & 31;
+        if (s - base >= 32) {
+            base = s;
+            mine = segment(p, min(s + lane, p.R));
+        }
+        const int from = s - base;
+        Segment g;
+        g.tok0 = __shfl_sync(0xffffffffu, mine.tok0, from);
+        g.ntok = __shfl_sync(0xffffffffu, mine.ntok, from);
+        g.keys = __shfl_sync(0xffffffffu, mine.keys, from);
+        g.pages = reinterpret_cast<const int32_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine.pages), from));
+        g.groups = __shfl_sync(0xffffffffu, mine.groups, from);
+        g.tiles = __shfl_sync(0xffffffffu, mine.tiles, from);
+        g.see0 = __shfl_sync(0xffffffffu, mine.see0, from);
+        g.cost = __shfl_sync(0xffffffffu, mine.cost, from);
+        g.line = __shfl_sync(0xffffffffu, mine.line, from);
+        return g;
+    }
+};
+
 // Walks a worker's pieces.  Roles of a CTA that walk by themselves see the same pieces.
 struct Walk {
     Segment g;
@@ -201,11 +229,17 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(const PrefixAttnParams &p, Piece &x)
     {
+        return next(p, x, [&](int s) { return segment(p, s); });
+    }
+    // With `segment_of` to say what a segment is.
+    template <class F>
+    __device__ __forceinline__ bool next(const PrefixAttnParams &p, Piece &x, F segment_of)
+    {
         while (left > 0) {
             if (head >= p.Hkv || g.line == 0) {
                 if (++seg > p.R)
                     return false;  // (only if the lengths changed meanwhile)
-                g = segment(p, seg);
+                g = segment_of(seg);
                 head = group = at = 0;
                 continue;
             }

@@ -435,10 +435,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             return __all_sync(0xffffffffu, ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
         };
         Walk walk;
+        Batch segments;
         walk.begin(st);
         Piece x;
         for (bool more = true; ok && more; ++pieces) {
-            more = walk.next(p, x);
+            more = walk.next(p, x, [&](int i) { return segments.get(p, i); });
             const Work f = work_of(x, p);
             const int at = pieces % C::kWork;
             if (pieces >= C::kWork)
@@ -455,26 +456,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (!more || f.tiles == 0)
                 continue;
             // What this lane loads of a tile: a page of a full tile, a group of 8 rows of
-            // the segment's last, shorter one.
-            auto find = [&](int tile, int &row, int &first) {
-                const int held = min(kTileKeys, x.keys - tile * kTileKeys);
-                const int step = held < kTileKeys ? 8 : page, key = lane * step;
-                row = none;
-                first = 0;
-                if (key >= held)
-                    return;  // (a group without keys: zeros)
-                const int id = x.pages[tile * per_tile + (key >> p.page_shift)];
-                if (id < 0 || id >= p.n_pages) {
-                    record_bad_index(p.err, 0x55, id);
-                    return;
-                }
-                row = id * p.Hkv + x.head;
-                // a group of v < 8 keys ends with them: its box starts 8 - v rows early, on
-                // rows of the same page or, before its first, on zeros
-                first = (key & (page - 1)) - max(0, key + 8 - held);
+            // the segment's last, shorter one.  Its page's id is read a tile ahead.
+            auto key_of = [&](int held) { return lane * (held < kTileKeys ? 8 : page); };
+            auto held_of = [&](int tile) { return min(kTileKeys, x.keys - tile * kTileKeys); };
+            auto look = [&](int tile) {
+                const int held = held_of(tile), key = key_of(held);
+                return key < held ? x.pages[tile * per_tile + (key >> p.page_shift)] : INT_MIN;
             };
-            int first, row;
-            find(x.t0, row, first);
+            int id = look(x.t0);
             const int q0 = f.two ? 0 : q_slot, q1 = f.two ? 2 : q_slot + 1;
 #pragma unroll 1
             for (int t = q0; ok && t < q1; ++t) {
@@ -493,10 +482,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (!f.two)
                 q_slot ^= 1;
             for (int i = 0; ok && i < f.tiles; ++i) {
-                const bool full = x.keys - (x.t0 + i) * kTileKeys >= kTileKeys;
-                int next_first = 0, next_row = none;
+                const int held = held_of(x.t0 + i), key = key_of(held);
+                const bool full = held == kTileKeys;
+                int row = none;  // (a group without keys, or of a page that is none: zeros)
+                if (id >= 0 && id < p.n_pages)
+                    row = id * p.Hkv + x.head;
+                else if (id != INT_MIN)
+                    record_bad_index(p.err, 0x55, id);
+                // a group of v < 8 keys ends with them: its box starts 8 - v rows early, on
+                // rows of the same page or, before its first, on zeros
+                const int first = (key & (page - 1)) - max(0, key + 8 - held);
                 if (i + 1 < f.tiles)
-                    find(x.t0 + i + 1, next_row, next_first);
+                    id = look(x.t0 + i + 1);
+                // (K of keys that are none is not brought: their scores are masked whatever they are)
+                const int k_groups = (held + 7) >> 3;
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v, ++ld) {
                     const int slot = ld & (C::kStages - 1);
@@ -506,21 +505,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     if (!ok)
                         break;
                     if (lane == 0)
-                        ptx::mbar_arrive_expect_tx(BAR(C::kKVF + slot), C::kTileBytes);
+                        ptx::mbar_arrive_expect_tx(BAR(C::kKVF + slot), v ? C::kTileBytes : k_groups * C::kGroupBytes);
                     __syncwarp();
                     const uint32_t dst = sKV + slot * C::kTileBytes;
                     if (full) {
                         if (lane < per_tile)
                             ptx::tma_load_5d(dst + lane * (page >> 3) * C::kGroupBytes, v ? &tm_v : &tm_k,
                                              BAR(C::kKVF + slot), 0, 0, 0, 0, row);
-                    } else if (lane < kTileKeys / 8) {
+                    } else if (lane < (v ? kTileKeys / 8 : k_groups)) {
                         ptx::tma_load_4d(dst + lane * C::kGroupBytes, v ? &tm_v8 : &tm_k8, BAR(C::kKVF + slot), 0, first, 0,
                                          row);
                     }
                     landed[slot] = use + 1;
                 }
-                row = next_row;
-                first = next_first;
             }
         }
         // Every copy this warp started lands before the CTA can exit.
