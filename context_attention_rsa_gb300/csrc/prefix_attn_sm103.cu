@@ -6,12 +6,16 @@
 //
 // One CTA on each SM takes an equal stretch of all key tiles (paged_sched.cuh)
 // and goes through its pieces.  Warp roles as in the block kernel:
-//   warp 8      producer: the piece's query rows (one 4-D TMA box a 128-row
-//               tile: G heads of floor(128 / G) tokens, so any group size is
-//               loaded without a gather), then K and V tiles through a ring of
-//               shared-memory slots, one TMA box a page, each lane loading the
-//               page whose id it read from the table one tile ahead.  It also
-//               walks the work for the others and hands them each piece.
+//   warp 8      producer of Q and K: the piece's query rows (one 4-D TMA box a
+//               128-row tile: G heads of floor(128 / G) tokens, so any group size is
+//               loaded without a gather), then K tiles into every other slot of a ring
+//               in shared memory, one box a page, each lane loading the page whose id
+//               it read from the table one tile ahead.  It also walks the work for
+//               the others and hands them each piece.
+//   warp 10     producer of V, the other slots, walking by itself: a box takes the
+//               issuing warp about 80 cycles, and one warp for K and V paced the loads
+//               (4 long contexts 447 -> 425 us, pages of 16 behind 100000 keys 278 ->
+//               254, short units 3 to 13 % less).
 //   warp 9      one thread issues the MMAs: S_t = Q K^T from shared memory,
 //               O_t += P_t V with P in TMEM.
 //   warps 0-7   softmax, two threads a row (warps w and w + 4), in turn on the
@@ -106,7 +110,8 @@ struct Cfg {
     static constexpr int kSoftmaxThreads = 256;
     static constexpr int kProducerWarp = 8;
     static constexpr int kMmaWarp = 9;
-    static constexpr int kThreads = 320;
+    static constexpr int kValueWarp = 10;
+    static constexpr int kThreads = 352;
     static constexpr int kHalves = D / 64;              // 128-byte halves of a row
     static constexpr uint32_t kTileBytes = kHalves * 128u * 128u;
     // A Q tile is two (d = 64: one) boxes of 128 rows x 128 bytes.  A K or V tile is
@@ -420,15 +425,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
     Work *work = reinterpret_cast<Work *>(gbase + C::kWorkOff);
 
-    if (warp == C::kProducerWarp) {
-        // ============================= producer =============================
+    if (warp == C::kProducerWarp || warp == C::kValueWarp) {
+        // ============================ producers =============================
+        const bool values = warp == C::kValueWarp;  // V; the other one brings Q and K and hands out the pieces
         const int page = 1 << p.page_shift, per_tile = kTileKeys >> p.page_shift;
         const int none = (int)(p.n_pages * p.Hkv);  // outside the maps: zeros
-        uint32_t ld = 0, q_use[2] = {0, 0};
+        uint32_t ld = values, q_use[2] = {0, 0};  // (a tile's K is load 2i, its V load 2i + 1)
         int q_slot = 0;
-        uint32_t landed[C::kStages];  // uses of each slot
-        for (int s = 0; s < C::kStages; ++s)
-            landed[s] = 0;
         uint32_t pieces = 0;
         bool ok = true;
         auto wait = [&](int bar, uint32_t phase, int site) {
@@ -441,17 +444,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (bool more = true; ok && more; ++pieces) {
             more = walk.next(p, x, [&](int i) { return segments.get(p, i); });
             const Work f = work_of(x, p);
-            const int at = pieces % C::kWork;
-            if (pieces >= C::kWork)
-                ok = wait(C::kWE + at, pieces / C::kWork - 1, 0x65);
-            if (!ok)
-                break;
-            if (lane == 0) {
-                if (more)
-                    work[at] = f;
-                else
-                    work[at].tiles = -1;
-                ptx::mbar_arrive(BAR(C::kWF + at));
+            if (!values) {
+                const int at = pieces % C::kWork;
+                if (pieces >= C::kWork)
+                    ok = wait(C::kWE + at, pieces / C::kWork - 1, 0x65);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    if (more)
+                        work[at] = f;
+                    else
+                        work[at].tiles = -1;
+                    ptx::mbar_arrive(BAR(C::kWF + at));
+                }
             }
             if (!more || f.tiles == 0)
                 continue;
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             int id = look(x.t0);
             const int q0 = f.two ? 0 : q_slot, q1 = f.two ? 2 : q_slot + 1;
 #pragma unroll 1
-            for (int t = q0; ok && t < q1; ++t) {
+            for (int t = q0; ok && !values && t < q1; ++t) {
                 if (q_use[t] > 0)
                     ok = wait(C::kQFree + t, q_use[t] - 1, 0x61);
                 if (!ok)
@@ -495,29 +500,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 if (i + 1 < f.tiles)
                     id = look(x.t0 + i + 1);
                 // (K of keys that are none is not brought: their scores are masked whatever they are)
-                const int k_groups = (held + 7) >> 3;
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v, ++ld) {
-                    const int slot = ld & (C::kStages - 1);
-                    const uint32_t use = ld >> C::kStageBits;
-                    if (use > 0)
-                        ok = wait(C::kKVE + slot, use - 1, 0x62);
-                    if (!ok)
-                        break;
-                    if (lane == 0)
-                        ptx::mbar_arrive_expect_tx(BAR(C::kKVF + slot), v ? C::kTileBytes : k_groups * C::kGroupBytes);
-                    __syncwarp();
-                    const uint32_t dst = sKV + slot * C::kTileBytes;
-                    if (full) {
-                        if (lane < per_tile)
-                            ptx::tma_load_5d(dst + lane * (page >> 3) * C::kGroupBytes, v ? &tm_v : &tm_k,
-                                             BAR(C::kKVF + slot), 0, 0, 0, 0, row);
-                    } else if (lane < (v ? kTileKeys / 8 : k_groups)) {
-                        ptx::tma_load_4d(dst + lane * C::kGroupBytes, v ? &tm_v8 : &tm_k8, BAR(C::kKVF + slot), 0, first, 0,
-                                         row);
-                    }
-                    landed[slot] = use + 1;
+                const int groups = values ? kTileKeys / 8 : (held + 7) >> 3;
+                const int slot = ld & (C::kStages - 1);
+                const uint32_t use = ld >> C::kStageBits;
+                if (use > 0)
+                    ok = wait(C::kKVE + slot, use - 1, values ? 0x63 : 0x62);
+                if (!ok)
+                    break;
+                if (lane == 0)
+                    ptx::mbar_arrive_expect_tx(BAR(C::kKVF + slot), groups * C::kGroupBytes);
+                __syncwarp();
+                const uint32_t dst = sKV + slot * C::kTileBytes;
+                if (full) {
+                    if (lane < per_tile)
+                        ptx::tma_load_5d(dst + lane * (page >> 3) * C::kGroupBytes, values ? &tm_v : &tm_k, BAR(C::kKVF + slot), 0, 0, 0,
+                                         0, row);
+                } else if (lane < groups) {
+                    ptx::tma_load_4d(dst + lane * C::kGroupBytes, values ? &tm_v8 : &tm_k8, BAR(C::kKVF + slot), 0, first, 0, row);
                 }
+                ld += 2;
             }
         }
         // Every copy this warp started lands before the CTA can exit.
@@ -525,9 +526,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (int t = 0; t < 2; ++t)
             if (q_use[t] > 0)
                 ptx::mbar_wait(BAR(C::kQF + t), (q_use[t] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
-        for (int s = 0; s < C::kStages; ++s)
-            if (landed[s])
-                ptx::mbar_wait(BAR(C::kKVF + s), (landed[s] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
+        for (uint32_t n = ld > C::kStages + values ? ld - C::kStages : values; n < ld; n += 2)  // the last load of each slot
+            ptx::mbar_wait(BAR(C::kKVF + (n & (C::kStages - 1))), n >> C::kStageBits & 1, lim_ns, &no_abort, p.err, 0x64);
         __syncwarp();
     } else if (warp == C::kMmaWarp) {
         // ============================ MMA issuer ============================
