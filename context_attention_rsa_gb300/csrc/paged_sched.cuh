@@ -42,7 +42,8 @@ struct Segment {
     int cost;              // places of a tile
     int64_t line;          // places on the line
 
-    __device__ __forceinline__ int64_t unit_line() const { return (int64_t)tiles * cost + kUnitCost; }
+    // (below 2^26: fewer than 2^24 tiles of 128 keys)
+    __device__ __forceinline__ int unit_line() const { return tiles * cost + kUnitCost; }
 };
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
@@ -208,7 +209,8 @@ struct Batch {
 struct Walk {
     Segment g;
     int seg, head, group;
-    int64_t at, left;  // the next place in the unit; places left
+    int at;        // the next place in the unit
+    int64_t left;  // places left
 
     __device__ __forceinline__ void begin(const Stretch &st)
     {
@@ -217,15 +219,16 @@ struct Walk {
             return;
         seg = st.seg;
         g = st.g;
-        const int64_t len = g.unit_line(), unit = st.off / len;
-        at = st.off - unit * len;
+        const int len = g.unit_line();
+        const int64_t unit = st.off / len;
+        at = (int)(st.off - unit * len);
         head = (int)(unit / g.groups);
         group = (int)(unit - (int64_t)head * g.groups);
     }
     // The first tile that begins at place `u` of the unit or later.
-    __device__ __forceinline__ int first_tile(int64_t u) const
+    __device__ __forceinline__ int first_tile(int u) const
     {
-        return u <= kUnitCost ? 0 : (int)((u - kUnitCost + g.cost - 1) / g.cost);
+        return u <= kUnitCost ? 0 : (u - kUnitCost + g.cost - 1) / g.cost;
     }
     __device__ __forceinline__ bool next(const PrefixAttnParams &p, Piece &x)
     {
@@ -243,7 +246,7 @@ struct Walk {
                 head = group = at = 0;
                 continue;
             }
-            const int64_t len = g.unit_line(), end = min(len, at + left);
+            const int len = g.unit_line(), end = (int)min((int64_t)len, at + left);
             const int i0 = group * p.unit_tokens;
             x.seg = seg;
             x.tok = g.tok0 + i0;

@@ -72,8 +72,9 @@ using namespace paged;
 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;  // log2 units the maximum may rise before O is rescaled
-// Places of a key tile (kUnitCost for a unit): measured next to one another, a tile
-// against two row tiles took 1.7 us, one against one 1.2 us, a unit 1.7 us more.
+// Places of a key tile (kUnitCost for a unit): a step of two row tiles takes 1.5 us, of
+// one 1.0, a short unit some 1.5 more.  Other weights (4:2:3, 3:3:4, 6:4:5, 4:4:6 for unit,
+// one and two row tiles) move single batches by up to 10 % either way and none all.
 constexpr int kLightTile = 2, kHeavyTile = 3;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -185,6 +186,7 @@ struct Issuer {
 
     __device__ __forceinline__ bool wait(int bar, uint32_t phase, int site)
     {
+        // (inlined here only: the issuer paces the short steps; the other roles' waits shrink the code by being called)
         return ptx::mbar_wait(bars + 8u * (uint32_t)bar, phase & 1, lim_ns, abort_flag, err, site);
     }
     __device__ __forceinline__ bool ready(int bar, uint32_t phase) { return ptx::mbar_test_wait(bars + 8u * (uint32_t)bar, phase & 1); }
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         uint32_t pieces = 0;
         bool ok = true;
         auto wait = [&](int bar, uint32_t phase, int site) {
-            return __all_sync(0xffffffffu, ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
+            return __all_sync(0xffffffffu, ptx::mbar_wait_called(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
         };
         Walk walk;
         Batch segments;
@@ -525,9 +527,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         volatile int no_abort = 0;
         for (int t = 0; t < 2; ++t)
             if (q_use[t] > 0)
-                ptx::mbar_wait(BAR(C::kQF + t), (q_use[t] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
+                ptx::mbar_wait_called(BAR(C::kQF + t), (q_use[t] - 1) & 1, lim_ns, &no_abort, p.err, 0x64);
         for (uint32_t n = ld > C::kStages + values ? ld - C::kStages : values; n < ld; n += 2)  // the last load of each slot
-            ptx::mbar_wait(BAR(C::kKVF + (n & (C::kStages - 1))), n >> C::kStageBits & 1, lim_ns, &no_abort, p.err, 0x64);
+            ptx::mbar_wait_called(BAR(C::kKVF + (n & (C::kStages - 1))), n >> C::kStageBits & 1, lim_ns, &no_abort, p.err, 0x64);
         __syncwarp();
     } else if (warp == C::kMmaWarp) {
         // ============================ MMA issuer ============================
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 // Every MMA this thread issued has finished before TMEM is freed.
                 mma.commit(C::kDrain);
                 volatile int no_abort = 0;
-                ptx::mbar_wait(BAR(C::kDrain), 0, lim_ns, &no_abort, p.err, 0x74);
+                ptx::mbar_wait_called(BAR(C::kDrain), 0, lim_ns, &no_abort, p.err, 0x74);
             }
         }
         __syncwarp();
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         int o_slot = 0;
         bool ok = true;
         auto wait = [&](int bar, uint32_t phase, int site) {
-            return __all_sync(0xffffffffu, ptx::mbar_wait(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
+            return __all_sync(0xffffffffu, ptx::mbar_wait_called(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
         };
 
         // The last piece's rows, whose O is still being computed while the next piece's
