@@ -43,15 +43,17 @@
 //
 // Measured (64 query heads over 8 key heads of 128; GB/s of the keys and values that
 // have to be read, TFLOP/s of the visible pairs):
-//   4 requests of 131072 to 262144 own keys       446 us, 6.64 TB/s, 0.98 of a copy
+//   4 requests of 131072 to 262144 own keys       426 us, 6.95 TB/s, the rate of a copy
 //   8 requests of 4 tokens, 32 key heads, behind
-//     100000 keys in pages of 16                   288 us, 5.8 TB/s
-//   608 requests behind 262144 keys               3190 us, 1638 TFLOP/s (a key tile
-//     against two row tiles 1.56 us, 0.87 of the cuBLAS rate; the block kernel 1.47)
-//   64 requests of 4 to 2000 keys behind 32768     102 us: 42 us of two-tile steps and
-//     18 of short units if perfectly shared, the rest the scan, the pieces' ends (20 MB
-//     of partials written and read) and the joining launch
-//   1 request of 1000 keys                        14.4 us, nearly all latency
+//     100000 keys in pages of 16                   255 us, 6.5 TB/s, 0.96 of a copy
+//   608 requests behind 262144 keys               3131 us, 1668 TFLOP/s, 0.88 of cuBLAS
+//   64 requests of 4 to 2000 keys behind 32768      94 us: 40 us of two-tile steps and
+//     18 of short units if perfectly shared; the scan 2, the first loads 5, a piece's end
+//     6 (its 256 rows, 16 bytes a lane and store) and the joining launch 5 us
+//   1 request of 1000 keys                        14.5 us, nearly all latency
+// The kernel's code is about as large as the instruction cache that two neighbouring
+// SMs share: a step takes 2850 cycles, 4400 next to a CTA that runs short units, and
+// what made short units faster by more code made the whole slower.
 // P is rounded to bf16 for the MMA (2^-8 of each probability at most; the sum l takes it
 // before that): with the result's own rounding 0.0021 to 0.0024 from the 64-bit
 // answer, where rounding that answer alone gives 0.0017.
