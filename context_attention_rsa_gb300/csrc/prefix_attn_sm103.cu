@@ -32,8 +32,9 @@
 //               cost little and HBM is the bound.
 // Rows past the keys are not trusted: a score of such a key is masked, but its
 // 0 * NaN would reach O through V.  So they are never loaded: the segment's last,
-// shorter tile is brought in groups of 8 rows; groups without keys lie outside the
-// tensor map, which fills them with zeros, and the box of a group of v < 8 keys
+// shorter tile is brought in groups of 8 rows; V's groups without keys lie outside the
+// tensor map, which fills them with zeros (K's stay what they were: masked whatever
+// they are), and the box of a group of v < 8 keys
 // starts 8 - v rows early, on keys that are there already or before the page, on
 // zeros.  The softmax masks those columns; the keys' order within a tile does not
 // matter to it.
@@ -236,13 +237,12 @@ struct Issuer {
                         (acc || kk > 0) ? 1u : 0u);
     }
     // Key tile j of n against two row tiles, the piece's first tile being `done`: PV of
-    // both, each followed by its S of the next tile.  The slots are known at compile
-    // time, K(j) and V(j) in pair kPair of the ring and K(j + 1) in the next one, so
-    // that the descriptors are constants of the kernel.
-    template <int kPair>
+    // both, each followed by its S of the next tile.  (One copy for all slots: with the
+    // descriptors as constants, a copy for each pair of slots, a step was no faster and
+    // the code 2 KB larger.)
     __device__ __forceinline__ bool step(uint32_t done, int j, int n)
     {
-        constexpr int kV = 2 * kPair + 1, kK = 2 * ((kPair + 1) % C::kPairs);
+        const int pair = (done + j) & (C::kPairs - 1), kV = 2 * pair + 1, kK = 2 * ((pair + 1) & (C::kPairs - 1));
         const uint32_t tile = done + j;
         const bool more = j + 1 < n;
         if (!wait(C::kKVF + kV, tile >> C::kPairBits, 0x71) || !p_full(0))
@@ -612,17 +612,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         mma.q_free();
                     ok = mma.o_free(0) && mma.o_free(1);
                     for (int j = 0; ok && j < n; ++j) {
-                        const int pair = (done + j) & (C::kPairs - 1);
-                        if (pair == 0)
-                            ok = mma.template step<0>(done, j, n);
-                        else if (pair == 1)
-                            ok = mma.template step<1>(done, j, n);
-                        if constexpr (C::kPairs == 4) {
-                            if (pair == 2)
-                                ok = mma.template step<2>(done, j, n);
-                            else if (pair == 3)
-                                ok = mma.template step<3>(done, j, n);
-                        }
+                        ok = mma.step(done, j, n);
                     }
                     done += n;
                     ahead = done;
