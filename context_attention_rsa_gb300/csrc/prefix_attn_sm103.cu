@@ -47,8 +47,8 @@
 //   4 requests of 131072 to 262144 own keys       426 us, 6.95 TB/s, the rate of a copy
 //   8 requests of 4 tokens, 32 key heads, behind
 //     100000 keys in pages of 16                   255 us, 6.5 TB/s, 0.96 of a copy
-//   608 requests behind 262144 keys               3131 us, 1668 TFLOP/s, 0.88 of cuBLAS
-//   64 requests of 4 to 2000 keys behind 32768      94 us: 40 us of two-tile steps and
+//   608 requests behind 262144 keys               3120 us, 1674 TFLOP/s, 0.89 of cuBLAS
+//   64 requests of 4 to 2000 keys behind 32768      91 us: 40 us of two-tile steps and
 //     18 of short units if perfectly shared; the scan 2, the first loads 5, a piece's end
 //     6 (its 256 rows, 16 bytes a lane and store) and the joining launch 5 us
 //   1 request of 1000 keys                        14.5 us, nearly all latency
