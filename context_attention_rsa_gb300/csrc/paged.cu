@@ -89,6 +89,100 @@ rsa_status check_result(const rsa_heads &h, rsa_dtype dt, int64_t T, int H, int 
 
 HeadRows rows(const rsa_heads &h) { return HeadRows{h.data, h.token_stride, h.head_stride}; }
 
+// The memory of an operand: T x H rows of `row` bytes, `token` and `head` bytes apart
+// (a plain array is one row; nothing at 0).
+struct Region {
+    const char *name;
+    int kind;  // a result may lie exactly on an input of the same kind (0: on none)
+    int64_t at, T, H, token, head, row;
+};
+
+constexpr int64_t kMostBytes = 1ll << 60;  // (more than an address space: sums and differences stay in 64 bits)
+
+Region region(const char *name, const void *p, int64_t count, int64_t size)
+{
+    if (!p)
+        return Region{};
+    const int64_t bytes = count > kMostBytes / size ? kMostBytes : count * size;
+    return Region{name, 0, (int64_t) reinterpret_cast<uintptr_t>(p), 1, 1, bytes, bytes, bytes};
+}
+
+Region region(const char *name, int kind, const rsa_heads &h, rsa_dtype dt, int64_t T, int64_t H, int d)
+{
+    const int64_t size = dt == RSA_F32 ? 4 : 2;
+    auto bytes = [&](int64_t n) { return n > kMostBytes / size ? kMostBytes : n * size; };
+    return Region{name, kind, (int64_t) reinterpret_cast<uintptr_t>(h.data), T, H, bytes(h.token_stride), bytes(h.head_stride),
+                  d * size};
+}
+
+bool same_rows(const Region &a, const Region &b)
+{
+    return a.at == b.at && a.T == b.T && a.H == b.H && (a.T == 1 || a.token == b.token) && (a.H == 1 || a.head == b.head);
+}
+
+// From the first row's beginning to the last one's end.
+int64_t span(const Region &a)
+{
+    const __int128 n = (__int128)(a.T - 1) * a.token + (__int128)(a.H - 1) * a.head + a.row;
+    return n > kMostBytes ? kMostBytes : (int64_t)n;
+}
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether a row of one lies on a row of the other.  Exact for rows with common strides,
+// as cut from one packed buffer; of other regions that reach into one another it says yes.
+bool shares(Region a, Region b)
+{
+    const int64_t na = span(a), nb = span(b);
+    if (!a.at || !b.at || a.at >= b.at + nb || b.at >= a.at + na)
+        return false;
+    if (na == kMostBytes || nb == kMostBytes)
+        return true;
+    for (Region *r : {&a, &b}) {  // heads side by side are one row, tokens too
+        if (r->head == r->row && r->H > 1) {
+            r->row *= r->H;
+            r->H = 1;
+        }
+        if (r->token == r->row && r->T > 1) {
+            r->row *= r->T;
+            r->T = 1;
+        }
+    }
+    // the stride of a single token or head says nothing
+    const int64_t token = a.T > 1 ? a.token : b.token, head = a.H > 1 ? a.head : b.head;
+    if ((b.T > 1 && b.token != token) || (b.H > 1 && b.head != head))
+        return true;
+    // Row (t, h) of a lies on row (u, i) of b if -a.row < off + (t - u) token + (h - i) head < b.row.
+    const int64_t off = a.at - b.at;
+    auto meet = [&](int64_t x0, int64_t x1, int64_t x_stride, int64_t y0, int64_t y1, int64_t y_stride) {
+        for (int64_t x = x0; x <= x1; ++x) {
+            const int64_t at = off + x * x_stride;
+            const int64_t lo = -floor_div(a.row - 1 + at, y_stride), hi = floor_div(b.row - 1 - at, y_stride);
+            if (lo <= hi && lo <= y1 && hi >= y0)
+                return true;
+        }
+        return false;
+    };
+    if (a.H + b.H <= a.T + b.T)
+        return meet(1 - b.H, a.H - 1, head, 1 - b.T, a.T - 1, token);
+    return meet(1 - b.T, a.T - 1, token, 1 - b.H, a.H - 1, head);
+}
+
+// No result shares memory with another operand, except exactly with its own input.
+template <int kOut, int kIn>
+rsa_status check_apart(const Region (&out)[kOut], const Region (&in)[kIn])
+{
+    for (int i = 0; i < kOut; ++i) {
+        for (const Region &r : in)
+            if (shares(out[i], r) && !(r.kind && r.kind == out[i].kind && same_rows(out[i], r)))
+                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, r.name);
+        for (int j = 0; j < i; ++j)
+            if (shares(out[i], out[j]))
+                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return RSA_OK;
+}
+
 rsa_status check_cache(int page_size, int64_t n_pages, int Hkv)
 {
     if (page_shift_of(page_size) < 0)
@@ -310,6 +404,18 @@ rsa_status rsa_qk_norm_rope_fwd(const rsa_qk_norm_rope_args *args, rsa_heads q_o
         p.n_pages = n_pages;
         p.page_shift = page_shift_of(page_size);
     }
+    // Rows are fetched some items ahead while other groups write theirs.
+    const rsa_dtype dt = args->dt;
+    const int64_t size = dt == RSA_F32 ? 4 : 2, T = args->T, cache = slot_map ? n_pages * args->Hkv * page_size * args->d : 0;
+    const Region outs[] = {region("q_out", 1, q_out, dt, T, args->Hq, args->d), region("k_out", 2, k_out, dt, T, args->Hkv, args->d),
+                           region("k_cache", p.k_cache, cache, size), region("v_cache", p.v_cache, cache, size)};
+    const Region ins[] = {region("q", 1, args->q, dt, T, args->Hq, args->d), region("k", 2, args->k, dt, T, args->Hkv, args->d),
+                          region("v", 0, slot_map ? v : rsa_heads{}, dt, T, args->Hkv, args->d),
+                          region("q_weight", args->q_weight, args->d, size), region("k_weight", args->k_weight, args->d, size),
+                          region("positions", args->rot ? args->positions : nullptr, args->n_axes * T, 8),
+                          region("cos_sin", args->rot ? args->cos_sin : nullptr, args->max_pos, 4ll * args->rot),
+                          region("slot_map", slot_map, T, 8)};
+    RSA_TRY(check_apart(outs, ins));
     RSA_TRY(device_error_word(&p.err));
     rsa_status inj;
     if (injected_failure("head norm launch", &inj))
@@ -355,6 +461,17 @@ rsa_status rsa_qk_norm_rope_bwd(const rsa_qk_norm_rope_args *args, rsa_heads dq_
     p.partial = static_cast<float *>(workspace);
     p.dq_weight = dq_weight;
     p.dk_weight = dk_weight;
+    const rsa_dtype dt = args->dt;
+    const int64_t size = dt == RSA_F32 ? 4 : 2, T = args->T;
+    const Region outs[] = {region("dq", 1, dq, dt, T, args->Hq, args->d), region("dk", 2, dk, dt, T, args->Hkv, args->d),
+                           region("dq_weight", dq_weight, args->d, 4), region("dk_weight", dk_weight, args->d, 4),
+                           region("workspace", workspace, (int64_t)need, 1)};
+    const Region ins[] = {region("q", 1, args->q, dt, T, args->Hq, args->d), region("k", 2, args->k, dt, T, args->Hkv, args->d),
+                          region("dq_out", 1, dq_out, dt, T, args->Hq, args->d), region("dk_out", 2, dk_out, dt, T, args->Hkv, args->d),
+                          region("q_weight", args->q_weight, args->d, size), region("k_weight", args->k_weight, args->d, size),
+                          region("positions", args->rot ? args->positions : nullptr, args->n_axes * T, 8),
+                          region("cos_sin", args->rot ? args->cos_sin : nullptr, args->max_pos, 4ll * args->rot)};
+    RSA_TRY(check_apart(outs, ins));
     RSA_TRY(device_error_word(&p.err));
     rsa_status inj;
     if (injected_failure("head norm backward launch", &inj))

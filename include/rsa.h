@@ -516,7 +516,10 @@ typedef struct {
 
 /*
  * Forward: q_out [T, Hq, d] and k_out [T, Hkv, d], dtype dt; each may be its
- * input, otherwise the two do not overlap.  With slot_map [T] the results of k
+ * input (the same rows: address and strides).  What is written, the caches
+ * too, shares no other memory with an operand: such calls are refused.  (Rows
+ * between one another's, of one packed buffer, share none; their strides have
+ * to be the same then.)  With slot_map [T] the results of k
  * and the rows of v (v [T, Hkv, d], copied) are also written to slots
  * slot_map[t] of k_cache and v_cache, and k_out.data may then be NULL.  Rows
  * with a negative slot are not written; other slots are left as they were.
@@ -532,8 +535,10 @@ rsa_status rsa_qk_norm_rope_fwd(const rsa_qk_norm_rope_args *args, rsa_heads q_o
  *   g = R(pos)^T dy, c = w o g
  *   dx = (c - xhat mean(c o xhat)) / sqrt(mean(x^2) + eps)
  *   dw = sum over tokens and heads of g o xhat          [d], fp32
- * dq, dk have dtype dt; dq may be dq_out and dk may be dk_out.  dq_weight or
- * dk_weight may be NULL (not wanted).  The sums run in a fixed order.
+ * dq, dk have dtype dt; dq may be dq_out or q and dk may be dk_out or k (the
+ * same rows); what is written, workspace too, shares no other memory with an
+ * operand, as above.  dq_weight or dk_weight may be NULL (not wanted).  The
+ * sums run in a fixed order.
  * workspace: rsa_qk_norm_rope_bwd_workspace_size() bytes.  Two launches.
  */
 rsa_status rsa_qk_norm_rope_bwd_workspace_size(int d, size_t *bytes);
