@@ -522,16 +522,19 @@ rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_
     RSA_TRY(check_ptr(workspace, "workspace"));
     if (ws_bytes < lay.total)
         return fail(RSA_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", ws_bytes, lay.total);
-    // Rows are read again after others have been written.
+    // Rows are read again after others have been written; page ids are read while other
+    // pieces' results are written, and the lengths by the joining launch again.
     const int64_t size = dt == RSA_F32 ? 4 : 2, cache = n_pages * Hkv * page_size * d * size;
     const struct {
         const void *p;
         int64_t n;
         const char *name;
     } bufs[] = {{q, ((T - 1) * q_token_stride + (Hq - 1) * q_head_stride + d) * size, "q"}, {k_cache, cache, "k_cache"},
-                {v_cache, cache, "v_cache"}, {out, T * Hq * d * size, "out"}, {lse, T * Hq * 4, "lse"},
-                {workspace, (int64_t)lay.total, "workspace"}};
-    for (int i = 3; i < 6; ++i)  // what is written
+                {v_cache, cache, "v_cache"}, {cu_q, (R + 1) * 4ll, "cu_q"}, {kv_len, R * 4ll, "kv_len"},
+                {block_table, ((R - 1) * table_stride + max_pages) * 4, "block_table"},
+                {prefix_len > 0 ? prefix_pages : nullptr, ((prefix_len + page_size - 1) >> shift) * 4, "prefix_pages"},
+                {out, T * Hq * d * size, "out"}, {lse, T * Hq * 4, "lse"}, {workspace, (int64_t)lay.total, "workspace"}};
+    for (int i = 7; i < 10; ++i)  // what is written
         for (int j = 0; j < i; ++j)
             if (overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n))
                 return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", bufs[i].name, bufs[j].name);

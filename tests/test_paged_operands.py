@@ -160,3 +160,35 @@ def test_rows_between_rows_against_counting():
         elif meet:
             assert code == INVALID, (n, hq, hkv, sq, sk, hex(k_at))
     assert min(seen.values()) > 100
+
+
+# ---- attention --------------------------------------------------------------------------
+
+R, MAX_PAGES, STRIDE = 4, 8, 9
+PREFIX = 100
+ATTN_AT = dict(q=0x1000000, k_cache=0x2000000, v_cache=0x3000000, out=0x4000000, lse=0x5000000, cu_q=0x5100000, kv_len=0x5200000,
+               block_table=0x5300000, prefix_pages=0x5400000, workspace=0x10000000)
+
+
+def attention(prefix=PREFIX, **kw):
+    a = {**ATTN_AT, **kw}
+    return stopped(lambda lib: lib.rsa_prefix_attn_fwd(a["q"], HQ * D, D, a["k_cache"], a["v_cache"], 1, T, HQ, HKV, D, PAGE, PAGES,
+                                                       a["cu_q"], a["kv_len"], R, a["block_table"], STRIDE, MAX_PAGES,
+                                                       a["prefix_pages"], prefix, a["out"], a["lse"], a["workspace"], 1 << 30, None))
+
+
+@pytest.mark.parametrize("out", ["out", "lse", "workspace"])
+@pytest.mark.parametrize("index,entries", [("cu_q", R + 1), ("kv_len", R), ("block_table", (R - 1) * STRIDE + MAX_PAGES),
+                                           ("prefix_pages", -(-PREFIX // PAGE))])
+def test_attention_refuses_results_over_its_lengths_and_tables(out, index, entries):
+    code, text = attention(**{index: ATTN_AT[out]})
+    assert code == INVALID and f"{out} overlaps {index}" in text.decode()
+    code, text = attention(**{index: ATTN_AT[out] - 4 * (entries - 1)})       # its last entry
+    assert code == INVALID and f"{out} overlaps {index}" in text.decode()
+    assert attention(**{index: ATTN_AT[out] - 4 * entries})[0] == STOPPED     # right before
+
+
+def test_attention_takes_operands_of_their_own():
+    assert attention()[0] == STOPPED
+    assert attention(cu_q=ATTN_AT["kv_len"])[0] == STOPPED                    # only read
+    assert attention(prefix=0, prefix_pages=ATTN_AT["out"])[0] == STOPPED     # not read
