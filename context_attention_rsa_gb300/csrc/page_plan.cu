@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const __grid_consta
             if (from[k] && page[k] >= 0 && page[k] < p.n_pages)
                 slot[k] = ((long long)page[k] << p.page_shift) + (at[k] & (P - 1));
             else if (from[k])
-                record_bad_index(p.err, 0x50, page[k]);
+                record_bad_index(p.err, kSitePlanPage, page[k]);
         }
         if (i0 + kTokensPerThread <= p.max_tokens) {
 #pragma unroll

@@ -67,10 +67,12 @@ __device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, boo
         g.pages = p.block_table + r * p.table_stride;
         g.see0 = g.keys - g.ntok + 1;
         if (report) {
-            if (g.tok0 != a || g.tok0 + g.ntok != b)
-                record_bad_index(p.err, 0x53, b);
+            if (g.tok0 != a)
+                record_bad_index(p.err, kSiteQueryRows, a);
+            else if (g.tok0 + g.ntok != b)
+                record_bad_index(p.err, kSiteQueryRows, b);
             if (g.keys != n)
-                record_bad_index(p.err, 0x54, n);
+                record_bad_index(p.err, kSiteKvLen, n);
         }
     }
     g.groups = (int)(((int64_t)g.ntok + p.unit_tokens - 1) / p.unit_tokens);

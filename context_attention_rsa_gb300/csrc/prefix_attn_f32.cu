@@ -103,7 +103,7 @@ __device__ __forceinline__ void fetch(const PrefixAttnParams &p, const Piece &x,
         if (j < j1) {
             const bool there = ids[i] >= 0 && ids[i] < p.n_pages;  // (the keys of another id count as zeros)
             if (!there)
-                record_bad_index(p.err, 0x55, ids[i]);
+                record_bad_index(p.err, kSiteCachePage, ids[i]);
             const int64_t row = (((int64_t)(there ? ids[i] : 0) * p.Hkv + x.head) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
             copy_async(&s.k[buffer][key][piece * 4], kc + row * D + piece * 4, there);
             copy_async(&s.v[buffer][key][piece * 4], vc + row * D + piece * 4, there);

@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 if (id >= 0 && id < p.n_pages)
                     row = id * p.Hkv + x.head;
                 else if (id != INT_MIN)
-                    record_bad_index(p.err, 0x55, id);
+                    record_bad_index(p.err, kSiteCachePage, id);
                 // a group of v < 8 keys ends with them: its box starts 8 - v rows early, on
                 // rows of the same page or, before its first, on zeros
                 const int first = (key & (page - 1)) - max(0, key + 8 - held);

@@ -140,7 +140,7 @@ __device__ __forceinline__ Turn<N, kLayout> load_turn(const NormRopeParams &p, i
     auto row = [&](int axis) {
         int64_t pos = p.positions[axis * p.T + t];
         if (pos < 0 || pos >= p.max_pos) {
-            record_bad_index(p.err, 0x51, pos);
+            record_bad_index(p.err, kSitePosition, pos);
             pos = 0;
         }
         return p.cos_sin + pos * p.rot;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 cache = static_cast<E *>(x.what == 1 ? p.k_cache : p.v_cache) + (page * p.Hkv + x.h0) * head_step +
                         (slot & ((1 << p.page_shift) - 1)) * D;
             else
-                record_bad_index(p.err, 0x52, slot);
+                record_bad_index(p.err, kSiteSlot, slot);
         }
         const HeadRows &out = x.what == 0 ? p.q_out : p.k_out;
         const bool keep = x.what != 2 && out.data;

@@ -946,8 +946,8 @@ rsa_status rsa_check_device_error(rsa_stream_t stream)
     if (v & kDevErrTimeout)
         return fail(RSA_ERR_TIMEOUT, "a device wait exceeded its limit (site code 0x%02x)", v & 0xffu);
     if (v & kDevErrBounds)
-        return fail(RSA_ERR_CUDA, "a device bounds check failed (site code 0x%02x, first bad index %lld)", v & 0xffu,
-                    (long long)rec.bad_index_plus1 - 1);
+        return fail(RSA_ERR_CUDA, "a device bounds check failed (site code 0x%02x, first bad index %lld)", rec.bad_site,
+                    rec.bad_index);
     return fail(RSA_ERR_CUDA, "device error word 0x%x", v);
 }
 

@@ -18,26 +18,29 @@
 
 namespace rsa {
 
-// Device error word values (OR-ed with a site code in the low byte).
-constexpr unsigned int kDevErrTimeout = 0x100u;
-constexpr unsigned int kDevErrBounds = 0x200u;  // a bounds check failed (RSA_DEBUG build, or index data)
+// Device error word values.
+constexpr unsigned int kDevErrTimeout = 0x100u;  // OR-ed with the wait's site code in the low byte
+constexpr unsigned int kDevErrBounds = 0x200u;   // a bounds check failed (RSA_DEBUG build, or index data)
 
 // The device-side error record.  Kernels get a pointer to `word` and OR codes
-// into it; builds with RSA_DEBUG also keep the first out-of-range index (plus
-// one, so that 0 means none) of a failed bounds check.
+// into it.  The first failed bounds check since the record was cleared also
+// leaves its site (never 0) and its index.
 struct DeviceError {
     unsigned int word;
-    unsigned int pad;
-    unsigned long long bad_index_plus1;
+    unsigned int bad_site;
+    long long bad_index;
 };
 
-// Record an index that lies outside its range: the site code and the first
-// such index (plus one).  For index data that only the device sees (lengths,
-// page ids, slots, positions), in every build; the caller skips the access.
+// Record an index that lies outside its range: the first one's site code and
+// value (any: -1 is as likely as another).  For index data that only the device
+// sees (lengths, page ids, slots, positions), in every build; the caller skips
+// the access.
 __device__ __forceinline__ void record_bad_index(unsigned int *err, unsigned int site, long long idx)
 {
-    atomicOr(err, kDevErrBounds | site);
-    atomicCAS(&reinterpret_cast<DeviceError *>(err)->bad_index_plus1, 0ull, (unsigned long long)idx + 1ull);
+    DeviceError *e = reinterpret_cast<DeviceError *>(err);
+    if (atomicCAS(&e->bad_site, 0u, site) == 0u)
+        e->bad_index = idx;
+    atomicOr(&e->word, kDevErrBounds);
 }
 
 #ifdef RSA_DEBUG
@@ -53,6 +56,10 @@ __device__ __forceinline__ bool debug_check(bool ok, unsigned int *err, unsigned
 #else
 #define RSA_DCHECK(cond, err, site, idx) true
 #endif
+
+// Sites of index data (rsa.h names them; the other kernels' codes are all below 0x90).
+constexpr unsigned int kSitePlanPage = 0x90, kSitePosition = 0x91, kSiteSlot = 0x92, kSiteQueryRows = 0x93, kSiteKvLen = 0x94,
+                       kSiteCachePage = 0x95;
 
 // Position axes of a rotation (time, height, width, one more).
 constexpr int kMaxRopeAxes = 4;

@@ -431,8 +431,8 @@ rsa_status rsa_decode_attn_fwd(const void *q, const void *k, const void *v, rsa_
  * Lengths, page ids, slots and positions are data of the device, so that a
  * captured step can be replayed with other lengths.  They are checked there:
  * a value outside its range is forced into it or its access skipped, and
- * rsa_check_device_error reports RSA_ERR_CUDA with the value; the results of
- * the rows concerned are then unspecified.
+ * rsa_check_device_error reports RSA_ERR_CUDA with the first such value; the
+ * results of the rows concerned are then unspecified.
  */
 
 /*
@@ -659,8 +659,10 @@ int rsa_debug_checks(void);
  * Synchronise `stream`, then read and clear the device error word of the
  * current device: RSA_OK, RSA_ERR_TIMEOUT if a kernel gave up on a wait, or
  * RSA_ERR_CUDA if a bounds check failed, of an RSA_DEBUG build or of index data
- * that only the device sees (the text gives the site code and the first bad
- * index).
+ * that only the device sees.  The text gives the site code and the index of one
+ * failure, the first to be recorded.  Site codes of index data: 0x90 a page id in
+ * rsa_page_plan; 0x91 a position, 0x92 a slot; 0x93 cu_q, 0x94 kv_len, 0x95 a
+ * page id in rsa_prefix_attn_fwd.
  */
 rsa_status rsa_check_device_error(rsa_stream_t stream);
 
