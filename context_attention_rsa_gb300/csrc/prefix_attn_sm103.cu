@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             auto held_of = [&](int tile) { return min(kTileKeys, x.keys - tile * kTileKeys); };
             auto look = [&](int tile) {
                 const int held = held_of(tile), key = key_of(held);
-                return key < held ? x.pages[tile * per_tile + (key >> p.page_shift)] : INT_MIN;
+                return key < held ? x.pages[tile * per_tile + (key >> p.page_shift)] : 0;
             };
             int id = look(x.t0);
             const int q0 = f.two ? 0 : q_slot, q1 = f.two ? 2 : q_slot + 1;
@@ -494,10 +494,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const int held = held_of(x.t0 + i), key = key_of(held);
                 const bool full = held == kTileKeys;
                 int row = none;  // (a group without keys, or of a page that is none: zeros)
-                if (id >= 0 && id < p.n_pages)
-                    row = id * p.Hkv + x.head;
-                else if (id != INT_MIN)
-                    record_bad_index(p.err, kSiteCachePage, id);
+                if (key < held) {
+                    if (id >= 0 && id < p.n_pages)
+                        row = id * p.Hkv + x.head;
+                    else
+                        record_bad_index(p.err, kSiteCachePage, id);
+                }
                 // a group of v < 8 keys ends with them: its box starts 8 - v rows early, on
                 // rows of the same page or, before its first, on zeros
                 const int first = (key & (page - 1)) - max(0, key + 8 - held);

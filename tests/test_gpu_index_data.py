@@ -3,7 +3,6 @@ value in rsa_check_device_error's text, and every other row as it would have bee
 import pytest
 import torch
 
-import paged_reference as ref
 import context_attention_rsa_gb300 as rsa
 from gpu_helpers import need_cuda
 from test_gpu_prefix_attn import Batch
@@ -82,3 +81,18 @@ def test_the_first_of_two_is_kept():
     attend(cu=-1)       # 0x93 and, as the lengths no longer fit, perhaps others
     attend(length=-5)
     assert "site code 0x93, first bad index -1)" in reported()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf", "f"])
+@pytest.mark.parametrize("where", [1, 9], ids=["full tile", "short tile"])
+@pytest.mark.parametrize("page", [INT_MIN, INT_MIN + 1, -1, INT_MAX])
+def test_any_page_id_out_of_range_is_reported(dtype, where, page):
+    # 150 keys in pages of 16: a tile of 128, and a shorter one of 22
+    need_cuda()
+    b = Batch([1, 1, 1], [40, 150, 60], 30, 4, 2, 64, 16, dtype)
+    want, wl = b.check()
+    b.table[1, where] = page
+    out, lse = b.run()
+    assert f"site code 0x95, first bad index {page})" in reported()
+    keep = [0, 2]
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], wl[keep])
