@@ -408,22 +408,27 @@ PyObject *qk_norm_rope(PyObject *const *a)
     return results(st, {qt, kt});
 }
 
-// ..., dq_out, dk_out, dq, dk, workspace, stream
+// ..., dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, stream
 PyObject *qk_norm_rope_bwd(PyObject *const *a)
 {
     const at::Tensor *q, *k;
     const rsa_qk_norm_rope_args args = norm_rope_args(a, &q, &k);
     const c10::Device dev = q->device();
     const rsa_heads gq = rows("dq_out", a[9], q->scalar_type(), dev, q), gk = rows("dk_out", a[10], q->scalar_type(), dev, k);
-    Call call(dev, a[14]);
-    at::Tensor dq, dk, dwq, dwk, ws;
+    Call call(dev, a[16]);
+    at::Tensor dq, dk, dw[2], ws;
     const rsa_heads dqo = result_rows(call, "dq", a[11], *q, &dq), dko = result_rows(call, "dk", a[12], *k, &dk);
-    if (args.q_weight)
-        dwq = call.make({args.d}, at::kFloat);
-    if (args.k_weight)
-        dwk = call.make({args.d}, at::kFloat);
-    if (a[13] != Py_None) {
-        ws = workspace(a[13], dev);
+    for (int i = 0; i < 2; ++i) {
+        if (a[13 + i] != Py_None) {
+            dw[i] = check(i ? "dk_weight" : "dq_weight", a[13 + i], 1, at::kFloat, dev);
+            if (dw[i].size(0) != args.d)
+                value_error("dq_weight and dk_weight must hold d=" + std::to_string(args.d) + " values");
+        } else if (i ? args.k_weight : args.q_weight) {
+            dw[i] = call.make({args.d}, at::kFloat);
+        }
+    }
+    if (a[15] != Py_None) {
+        ws = workspace(a[15], dev);
     } else {
         size_t n = 0;
         const rsa_status st = rope_bwd_size_fn(args.d, &n);
@@ -433,10 +438,10 @@ PyObject *qk_norm_rope_bwd(PyObject *const *a)
     }
     const rsa_stream_t stream = call.stream();
     const rsa_status st = launch([&] {
-        return rope_bwd_fn(&args, gq, gk, dqo, dko, dwq.defined() ? dwq.data_ptr<float>() : nullptr,
-                           dwk.defined() ? dwk.data_ptr<float>() : nullptr, ws.data_ptr(), ws.nbytes(), stream);
+        return rope_bwd_fn(&args, gq, gk, dqo, dko, dw[0].defined() ? dw[0].data_ptr<float>() : nullptr,
+                           dw[1].defined() ? dw[1].data_ptr<float>() : nullptr, ws.data_ptr(), ws.nbytes(), stream);
     });
-    return results(st, {dq, dk, dwq, dwk});
+    return results(st, {dq, dk, dw[0], dw[1]});
 }
 
 // q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages, prefix_len, out, lse, workspace, stream
@@ -542,7 +547,7 @@ PyObject *bind(PyObject *const *a)
 
 #define RSA_ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {RSA_ENTRY(bind, 7),          RSA_ENTRY(page_plan, 11),       RSA_ENTRY(qk_norm_rope, 16),
-                         RSA_ENTRY(qk_norm_rope_bwd, 15), RSA_ENTRY(prefix_attn, 12), {nullptr, nullptr, 0, nullptr}};
+                         RSA_ENTRY(qk_norm_rope_bwd, 17), RSA_ENTRY(prefix_attn, 12), {nullptr, nullptr, 0, nullptr}};
 #undef RSA_ENTRY
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods};

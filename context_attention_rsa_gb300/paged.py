@@ -137,12 +137,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, eps: float = 1e-6,
                      interleaved: bool = False, sections: Optional[Sequence[int]] = None, dq=None, dk=None,
-                     workspace=None, stream=None):
+                     workspace=None, stream=None, dq_weight=None, dk_weight=None):
     """Gradients of qk_norm_rope (rsa_qk_norm_rope_bwd) from those of its
     results: (dq, dk in q's dtype, dq_weight, dk_weight fp32 [d], None for a
-    weight that is None).  dq may be dq_out and dk may be dk_out."""
+    weight that is None).  dq may be dq_out or q, and dk dk_out or k; dq,
+    dk, dq_weight and dk_weight are made if they are not given."""
     r = (_native or _load_native()).qk_norm_rope_bwd(q, k, q_weight, k_weight, positions, cos_sin, eps, interleaved, sections,
-                                                     dq_out, dk_out, dq, dk, workspace, stream)
+                                                     dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, stream)
     if r.__class__ is int:
         raise _error("rsa_qk_norm_rope_bwd", r)
     return r
