@@ -54,3 +54,44 @@ def test_weight_gradients_that_the_caller_passes():
         with pytest.raises(err):
             rsa.qk_norm_rope_bwd(*args, dq_weight=bad)
     rsa.check_device_error()
+
+
+def test_tensors_that_a_call_makes_are_filled_where_pytorch_fills_them():
+    # rows behind the batch are left as they were: in deterministic mode that is what torch.empty gives there
+    need_cuda()
+    from torch.utils.deterministic import fill_uninitialized_memory
+    assert fill_uninitialized_memory
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(4, 4, 64, generator=g, device="cuda")
+    kc, vc = (torch.randn(6, 2, 16, 64, generator=g, device="cuda") for _ in range(2))
+    args = (q, kc, vc, i32([0, 1]), i32([[0, 1, 2]]), i32([40]))
+    want, wl = rsa.prefix_attn(*args)
+    mode = torch.are_deterministic_algorithms_enabled()
+    try:
+        torch.use_deterministic_algorithms(True)
+        out, lse = rsa.prefix_attn(*args)
+    finally:
+        torch.use_deterministic_algorithms(mode)
+    assert torch.equal(out[0], want[0]) and torch.equal(lse[0], wl[0])
+    assert out[1:].isnan().all() and lse[1:].isnan().all()
+
+
+def test_tensors_that_a_call_makes_are_seen_by_a_mode():
+    need_cuda()
+    from torch.utils._python_dispatch import TorchDispatchMode
+    seen = []
+
+    class Seen(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            r = func(*args, **(kwargs or {}))
+            seen.append((func, tuple(r.shape) if isinstance(r, torch.Tensor) else None))
+            return r
+    args = step_of()
+    with Seen():
+        dq, dk, dwq, dwk = rsa.qk_norm_rope_bwd(*args)
+    made = [s for f, s in seen if f is torch.ops.aten.empty.memory_format]
+    for t in (dq, dk, dwq, dwk):
+        assert tuple(t.shape) in made
+    for x, y in zip((dq, dk, dwq, dwk), rsa.qk_norm_rope_bwd(*args)):
+        assert torch.equal(x, y)
+    rsa.check_device_error()
