@@ -96,3 +96,15 @@ def test_any_page_id_out_of_range_is_reported(dtype, where, page):
     assert f"site code 0x95, first bad index {page})" in reported()
     keep = [0, 2]
     assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], wl[keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf", "f"])
+def test_rows_that_do_not_ascend_leave_the_others_right(dtype):
+    # request 1 is forced to the batch's end, where request 2 then has no rows: request 0 is as it was
+    need_cuda()
+    b = Batch([1, 1, 1], [40, 50, 60], 30, 4, 2, 64, 16, dtype)
+    want, wl = b.check()
+    b.cu = torch.tensor([0, 1, 1 << 30, 3], dtype=torch.int32)
+    out, lse = b.run()
+    assert "site code 0x93, first bad index" in reported()
+    assert torch.equal(out[0], want[0]) and torch.equal(lse[0], wl[0])

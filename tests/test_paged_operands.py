@@ -6,6 +6,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import context_attention_rsa_gb300 as rsa
 from context_attention_rsa_gb300 import paged
@@ -192,3 +193,11 @@ def test_attention_takes_operands_of_their_own():
     assert attention()[0] == STOPPED
     assert attention(cu_q=ATTN_AT["kv_len"])[0] == STOPPED                    # only read
     assert attention(prefix=0, prefix_pages=ATTN_AT["out"])[0] == STOPPED     # not read
+
+
+@pytest.mark.parametrize("n", [29, 30, 31, 62])
+def test_attention_workspace_has_a_plan_of_requests_and_two_words(n):
+    # 8 bytes each, rounded up to 256: 30 requests are the most that one such unit holds
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    rest = 2 * (up(T * HQ * D * 4) + up(T * HQ * 4)) + up(160 * 256 * D * 4) + up(160 * 256 * 4)
+    assert rsa.prefix_attn_workspace_size(torch.bfloat16, T, HQ, HKV, D, n) == up((n + 2) * 8) + rest
