@@ -94,7 +94,8 @@ HeadRows rows(const rsa_heads &h) { return HeadRows{h.data, h.token_stride, h.he
 struct Region {
     const char *name;
     int kind;  // a result may lie exactly on an input of the same kind (0: on none)
-    int64_t at, T, H, token, head, row;
+    int64_t at, end;  // the first row's beginning, the last one's end
+    int64_t T, H, token, head, row;
 };
 
 constexpr int64_t kMostBytes = 1ll << 60;  // (more than an address space: sums and differences stay in 64 bits)
@@ -103,15 +104,18 @@ Region region(const char *name, const void *p, int64_t count, int64_t size)
 {
     if (!p)
         return Region{};
-    const int64_t bytes = count > kMostBytes / size ? kMostBytes : count * size;
-    return Region{name, 0, (int64_t) reinterpret_cast<uintptr_t>(p), 1, 1, bytes, bytes, bytes};
+    const int64_t bytes = count > kMostBytes / size ? kMostBytes : count * size, at = (int64_t) reinterpret_cast<uintptr_t>(p);
+    return Region{name, 0, at, at + bytes, 1, 1, bytes, bytes, bytes};
 }
 
 Region region(const char *name, int kind, const rsa_heads &h, rsa_dtype dt, int64_t T, int64_t H, int d)
 {
-    const int64_t size = dt == RSA_F32 ? 4 : 2;
-    auto bytes = [&](int64_t n) { return n > kMostBytes / size ? kMostBytes : n * size; };
-    return Region{name, kind, (int64_t) reinterpret_cast<uintptr_t>(h.data), T, H, bytes(h.token_stride), bytes(h.head_stride),
+    if (!h.data)
+        return Region{};
+    const int64_t size = dt == RSA_F32 ? 4 : 2, at = (int64_t) reinterpret_cast<uintptr_t>(h.data);
+    const __int128 n = ((__int128)(T - 1) * h.token_stride + (__int128)(H - 1) * h.head_stride + d) * size;
+    auto bytes = [&](int64_t x) { return x > kMostBytes / size ? kMostBytes : x * size; };
+    return Region{name, kind, at, at + (n > kMostBytes ? kMostBytes : (int64_t)n), T, H, bytes(h.token_stride), bytes(h.head_stride),
                   d * size};
 }
 
@@ -120,23 +124,13 @@ bool same_rows(const Region &a, const Region &b)
     return a.at == b.at && a.T == b.T && a.H == b.H && (a.T == 1 || a.token == b.token) && (a.H == 1 || a.head == b.head);
 }
 
-// From the first row's beginning to the last one's end.
-int64_t span(const Region &a)
-{
-    const __int128 n = (__int128)(a.T - 1) * a.token + (__int128)(a.H - 1) * a.head + a.row;
-    return n > kMostBytes ? kMostBytes : (int64_t)n;
-}
-
 int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
 
 // Whether a row of one lies on a row of the other.  Exact for rows with common strides,
 // as cut from one packed buffer; of other regions that reach into one another it says yes.
-bool shares(Region a, Region b)
+bool rows_meet(Region a, Region b)
 {
-    const int64_t na = span(a), nb = span(b);
-    if (!a.at || !b.at || a.at >= b.at + nb || b.at >= a.at + na)
-        return false;
-    if (na == kMostBytes || nb == kMostBytes)
+    if (a.end - a.at == kMostBytes || b.end - b.at == kMostBytes)
         return true;
     for (Region *r : {&a, &b}) {  // heads side by side are one row, tokens too
         if (r->head == r->row && r->H > 1) {
@@ -166,6 +160,11 @@ bool shares(Region a, Region b)
     if (a.H + b.H <= a.T + b.T)
         return meet(1 - b.H, a.H - 1, head, 1 - b.T, a.T - 1, token);
     return meet(1 - b.T, a.T - 1, token, 1 - b.H, a.H - 1, head);
+}
+
+bool shares(const Region &a, const Region &b)
+{
+    return a.at < b.end && b.at < a.end && rows_meet(a, b);  // (what is not there ends at 0)
 }
 
 // No result shares memory with another operand, except exactly with its own input.

@@ -129,17 +129,21 @@ const at::Tensor &workspace(PyObject *o, const c10::Device &dev)
 // One call: its device, its stream, and the tensors that it made.
 class Call {
 public:
-    Call(const c10::Device &dev, PyObject *stream) : dev_(dev), guard_(dev), stream_(stream) {}
-
     // Straight from the allocator, 1 to 2 us a call less than by way of the dispatcher,
     // unless that would do more: a mode sees the tensor, or its memory is filled.
-    at::Tensor make(at::IntArrayRef shape, at::ScalarType type)
+    Call(const c10::Device &dev, PyObject *stream) : dev_(dev), guard_(dev), stream_(stream)
     {
         const at::Context &c = at::globalContext();
-        const bool plain = !c10::impl::TorchDispatchModeTLS::any_modes_set() &&
-                           !(c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory());
-        made_.push_back(plain ? at::Tensor(at::detail::empty_cuda(shape, type, dev_, std::nullopt))
-                              : at::empty(shape, at::TensorOptions(dev_).dtype(type)));
+        plain_ = !c10::impl::TorchDispatchModeTLS::any_modes_set() &&
+                 !(c.deterministicAlgorithms() && c.deterministicFillUninitializedMemory());
+    }
+
+    at::Tensor make(at::IntArrayRef shape, at::ScalarType type)
+    {
+        if (plain_)
+            made_.push_back(at::detail::empty_cuda(shape, type, dev_, std::nullopt));
+        else
+            made_.push_back(at::empty(shape, at::TensorOptions(dev_).dtype(type)));
         return made_.back();
     }
 
@@ -185,6 +189,7 @@ private:
     c10::Device dev_;
     c10::cuda::CUDAGuard guard_;
     PyObject *stream_;
+    bool plain_;
     std::vector<at::Tensor> made_;
 };
 
