@@ -13,8 +13,8 @@
 // finds its page in the old part of its table or, past that, straight in
 // free_pages, so no block reads a table entry that another one writes.  The
 // work is a few bytes a token: the launch and the scan's latency bound it at
-// any size a server sees (8 requests 7.0 us on the GPU, 4000 requests with 0.42
-// million rows 12.7 us, of which the 6.8 MB would take 1).
+// any size a server sees (8 requests 6.3 us on the GPU, 4000 requests with 0.42
+// million rows 13.1 us, of which the 6.8 MB would take 1).
 #include "rsa_internal.h"
 
 namespace rsa {
@@ -233,7 +233,7 @@ cudaError_t launch(const PagePlanParams &p, int most, cudaStream_t s)
 
 }  // namespace
 
-// Many requests: a block on each SM, wide enough to scan them (16000 requests 16.4 us;
+// Many requests: a block on each of 152 SMs, wide enough to scan them (16000 requests 16.4 us;
 // with two on each 22.5, with 256 threads 28.8).  Else narrower blocks, which wait less
 // for one another: 1000 requests 8.2 us instead of 10.2.
 cudaError_t launch_page_plan(const PagePlanParams &p, cudaStream_t s)

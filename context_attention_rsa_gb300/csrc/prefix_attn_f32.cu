@@ -12,16 +12,19 @@
 // turn ahead of the arithmetic, in blocks of 32 keys.  A warp takes up to 8 rows of
 // the unit through a block: lane (x, y) of 8 x 4 scores keys x, x + 8, .. for rows y
 // and y + 4, and owns columns 4x.. of each 32 of the same rows of the output, so that
-// every value read from shared memory, which is the bound, serves several products
+// every value read from shared memory serves several products
 // and a row's maximum and factors stay in its lanes.  A unit of few rows leaves warps
 // over: they are then cut into 2 or 4 key groups, which take the turn's blocks in
 // parallel and join their rows at the end of the piece.
-// Measured: 5 requests of 2 tokens, 4 key heads of 64, behind 4097 keys 22.6 us (4 key
+// Measured: 5 requests of 2 tokens, 4 key heads of 64, behind 4097 keys 21.3 us (4 key
 // groups and these tiles; with one row or two a warp, every block through all 16, it
-// took 41); one row of 100000 keys 68 us, 3.0 TB/s; 20-row units of d = 128 21 TFLOP/s.
+// took 41); one row of 4 heads of 64 over 100000 keys 62 us, 3.3 TB/s; 8 heads of 128 over
+// 60000 keys with 20 rows each 312 us, 15.8 TFLOP/s, and 512 rows over 4608 keys 343 us, 26.6
+// TFLOP/s of the visible pairs (a step of 4 columns is six 16-byte shared loads for 32
+// products a lane; which of the two pipes binds has not been counted).
 // A unit of few rows is bound by one warp's way through a block, not by the loads: the
-// same with a producer warp and TMA, which brings them earlier, took 82 us for the
-// 100000 keys.
+// same with a producer warp and TMA, which brings them earlier, took 82 us for a row of
+// 100000 keys that took 68.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
             locate(i0 + lane, o, at);
             lse = *at;
         }
-        // The first rows of o are under way before their weights are known, eight at a time.
+        // The first rows of o are under way before their weights are known, kAhead at a time.
         float v[kAhead][PER];
         auto fetch_rows = [&](int i) {
 #pragma unroll

@@ -47,14 +47,17 @@
 //   4 requests of 131072 to 262144 own keys       426 us, 6.95 TB/s, the rate of a copy
 //   8 requests of 4 tokens, 32 key heads, behind
 //     100000 keys in pages of 16                   255 us, 6.5 TB/s, 0.96 of a copy
-//   608 requests behind 262144 keys               3120 us, 1674 TFLOP/s, 0.89 of cuBLAS
+//   608 requests behind 262144 keys               3760 us, 1389 TFLOP/s, 0.74 of cuBLAS (ten calls;
+//     after a hundred, power-capped, 4080 us; keys of zeros, which cost less power, 3235 us)
+//   512 new tokens with 32768 before them          421 us, 1316 TFLOP/s; a prompt of 8192 without
+//     a past 1673 us, 657 TFLOP/s: its places count tiles that its rows do not see
 //   64 requests of 4 to 2000 keys behind 32768      91 us: 40 us of two-tile steps and
 //     18 of short units if perfectly shared; the scan 2, the first loads 5, a piece's end
 //     6 (its 256 rows, 16 bytes a lane and store) and the joining launch 5 us
 //   1 request of 1000 keys                        14.5 us, nearly all latency
-// The kernel's code is about as large as the instruction cache that two neighbouring
-// SMs share: a step takes 2850 cycles, 4400 next to a CTA that runs short units, and
-// what made short units faster by more code made the whole slower.
+// A step takes 2850 cycles, 4400 next to a CTA that runs short units, and what made short
+// units faster by more code made the whole slower: as if two neighbouring SMs shared an
+// instruction cache that the kernel's code fills (read from timings, not from a counter).
 // P is rounded to bf16 for the MMA (2^-8 of each probability at most; the sum l takes it
 // before that): with the result's own rounding 0.0021 to 0.0024 from the 64-bit
 // answer, where rounding that answer alone gives 0.0017.

@@ -15,6 +15,14 @@ binding they only check and marshal arguments, here in an extension module
 Caches are [n_pages, Hkv, page_size, d]; a step's rows are packed [T, H, d].
 Nothing synchronises, so a step can be captured into a CUDA graph and replayed
 with other lengths: what depends on them is read on the device.
+
+No call takes part in autograd, as in the rest of the binding: inputs that
+require a gradient are read like any others and results have no history.  A
+training loop calls qk_norm_rope_bwd itself, for instance from the backward of
+a torch.autograd.Function of its own.
+
+Heads, NormRopeArgs and SIGS describe the C ABI for ctypes: load() types the
+library's functions with them, for callers of the C calls themselves.
 """
 from __future__ import annotations
 

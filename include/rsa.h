@@ -557,19 +557,22 @@ rsa_status rsa_qk_norm_rope_bwd(const rsa_qk_norm_rope_args *args, rsa_heads dq_
  *   out [T, Hq, d] (dtype dt) = softmax(q K^T / sqrt(d)) V, lse [T, Hq] fp32
  * over both together.  A row that sees nothing gets out = 0, lse = -inf; rows
  * of no request (before cu_q[0], from cu_q[R] on) are left as they were.  The keys
- * and values of the prefix are read once for the whole batch, not once for
- * each request; prefix_len = 0 is plain attention over a paged cache.  Entries
+ * and values of the prefix are read once for up to 256 query rows of a key head
+ * (fp32: 128) together, of whichever requests, not once for each request;
+ * prefix_len = 0 is plain attention over a paged cache.  Entries
  * of block_table past a request's keys are not read, and cache rows past
  * kv_len or prefix_len may hold anything; rows within them have to be finite
  * (a token's row that a request's earlier new tokens do not see yet is still
  * multiplied, by zero).
  * Hq / Hkv is at most 128.  What is written (out, lse, workspace) overlaps
  * nothing else.  prefix_len is the call's own: a captured call keeps it, while
- * its lengths, tables and page ids may change.  Meant for steps whose new tokens are few next to
- * the keys: a request's keys are shared out as if all its new tokens saw all
- * of them, which costs up to twice the time for a prompt without a past (the
- * ring is the call for that).  `workspace` holds
- * rsa_prefix_attn_workspace_size() bytes: calls that may run at the same time
+ * its lengths, tables and page ids may change.  Meant for steps whose new
+ * tokens are few next to the keys: a request's keys are shared out as if all
+ * its new tokens saw all of them, so that a prompt without a past takes up to
+ * twice the time (the ring has no such loss, but takes neither pages nor
+ * grouped heads nor requests of several lengths).  `workspace` holds
+ * rsa_prefix_attn_workspace_size() bytes, two fp32 partials for every row and
+ * some 10 (d = 64) or 21 MB: calls that may run at the same time
  * (two streams, two captured graphs) each need their own.  Two launches; the
  * work is shared out on the device, from the lengths that it finds there.
  */
