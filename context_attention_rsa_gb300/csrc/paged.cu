@@ -1,5 +1,6 @@
 // C ABI of the paged-cache operators: a step's plan, the norm and rotation of
-// its heads with the cache write, and attention behind a shared prefix.
+// its heads with the cache write, attention behind a shared prefix, drafted
+// tokens, and the keeping of pages.
 #include <cmath>
 #include <cstring>
 
@@ -297,6 +298,187 @@ rsa_status check_prefix_shape(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, i
     return RSA_OK;
 }
 
+rsa_status check_words(int words)
+{
+    if (words < 1 || words > kTreeMaxWords)
+        return fail(RSA_ERR_INVALID_ARG, "words=%d must be in [1, %d]", words, kTreeMaxWords);
+    return RSA_OK;
+}
+
+// A memory range of a call, for the check that nothing written lies in another one.
+struct Buffer {
+    const void *p;
+    int64_t n;
+    const char *name;
+};
+
+template <int kOut, int kIn>
+rsa_status check_buffers(const Buffer (&out)[kOut], const Buffer (&in)[kIn])
+{
+    for (int i = 0; i < kOut; ++i) {
+        for (const Buffer &b : in)
+            if (overlap(out[i].p, out[i].n, b.p, b.n))
+                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, b.name);
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return RSA_OK;
+}
+
+rsa_status check_table(const int32_t *block_table, int64_t table_stride, int max_pages, int page_size)
+{
+    RSA_TRY(check_i32_ptr(block_table, "block_table"));
+    if (max_pages < 1 || table_stride < max_pages || table_stride > 0x7fffffffLL || (int64_t)max_pages * page_size > 0x7fffffffLL)
+        return fail(RSA_ERR_INVALID_ARG,
+                    "max_pages=%d (rows %lld apart): at least 1, at most the row and 2^31-1 keys are wanted", max_pages,
+                    (long long)table_stride);
+    return RSA_OK;
+}
+
+rsa_status check_requests(int R)
+{
+    if (R < 1)
+        return fail(RSA_ERR_INVALID_ARG, "R=%d must be >= 1", R);
+    if (R > kPagePlanMaxRequests)
+        return fail(RSA_ERR_UNSUPPORTED, "R=%d exceeds %d requests", R, kPagePlanMaxRequests);
+    return RSA_OK;
+}
+
+rsa_status check_layers(const rsa_cache *a, CacheLayers *c)
+{
+    if (!a)
+        return fail(RSA_ERR_INVALID_ARG, "cache is NULL");
+    RSA_TRY(check_dtype(a->dt));
+    if (a->layers < 1 || a->Hkv < 1)
+        return fail(RSA_ERR_INVALID_ARG, "layers and Hkv must be >= 1 (got %d, %d)", a->layers, a->Hkv);
+    RSA_TRY(check_head_dim(a->d));
+    RSA_TRY(check_cache(a->page_size, a->n_pages, a->Hkv));
+    if ((int64_t)a->layers * a->Hkv > 32767)
+        return fail(RSA_ERR_UNSUPPORTED, "layers=%d of Hkv=%d key heads: more than 32767", a->layers, a->Hkv);
+    RSA_TRY(check_ptr(a->k_cache, "k_cache"));
+    RSA_TRY(check_ptr(a->v_cache, "v_cache"));
+    c->data[0] = static_cast<char *>(a->k_cache);
+    c->data[1] = static_cast<char *>(a->v_cache);
+    c->row = a->d * (a->dt == RSA_F32 ? 4 : 2);
+    c->layers = a->layers;
+    c->n_pages = a->n_pages;
+    c->Hkv = a->Hkv;
+    c->page_shift = page_shift_of(a->page_size);
+    c->layer_bytes = a->n_pages * a->Hkv * a->page_size * c->row;  // (below 2^47)
+    return RSA_OK;
+}
+
+// Both attention calls; `drafted`: with a mask.
+rsa_status paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache, const void *v_cache,
+                      rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int page_size, int64_t n_pages, const int32_t *cu_q,
+                      const int32_t *kv_len, int R, const int32_t *block_table, int64_t table_stride, int max_pages,
+                      const int32_t *prefix_pages, int64_t prefix_len, bool drafted, const uint32_t *mask, int64_t mask_stride,
+                      int words, void *out, float *lse, void *workspace, size_t ws_bytes, rsa_stream_t stream)
+{
+    RSA_TRY(check_prefix_shape(dt, T, Hq, Hkv, d, R));
+    RSA_TRY(check_cache(page_size, n_pages, Hkv));
+    const int shift = page_shift_of(page_size);
+    RSA_TRY(check_ptr(q, "q"));
+    RSA_TRY(check_strides(dt, q_token_stride, q_head_stride, d, "q"));
+    RSA_TRY(check_ptr(k_cache, "k_cache"));
+    RSA_TRY(check_ptr(v_cache, "v_cache"));
+    RSA_TRY(check_ptr(out, "out"));
+    RSA_TRY(check_ptr(lse, "lse"));
+    RSA_TRY(check_i32_ptr(cu_q, "cu_q"));
+    RSA_TRY(check_i32_ptr(kv_len, "kv_len"));
+    RSA_TRY(check_i32_ptr(block_table, "block_table"));
+    if (max_pages < 1 || table_stride < max_pages || ((int64_t)max_pages << shift) > 0x7fffffffLL)
+        return fail(RSA_ERR_INVALID_ARG,
+                    "max_pages=%d (rows %lld apart): at least 1, at most the row and 2^31-1 keys are wanted", max_pages,
+                    (long long)table_stride);
+    if (prefix_len < 0 || prefix_len > (1ll << 31) - 128)  // (a tile's last key is still an int)
+        return fail(RSA_ERR_INVALID_ARG, "prefix_len=%lld must be in [0, 2^31-128]", (long long)prefix_len);
+    if (prefix_len > 0)
+        RSA_TRY(check_i32_ptr(prefix_pages, "prefix_pages"));
+    if (drafted) {
+        RSA_TRY(check_i32_ptr(mask, "mask"));
+        RSA_TRY(check_words(words));
+        if (mask_stride < words || mask_stride > (1ll << 30))
+            return fail(RSA_ERR_INVALID_ARG, "mask_stride=%lld must be at least words=%d and at most 2^30", (long long)mask_stride,
+                        words);
+    }
+    const PrefixLayout lay = prefix_layout(T, Hq, d, R);
+    RSA_TRY(check_ptr(workspace, "workspace"));
+    if (ws_bytes < lay.total)
+        return fail(RSA_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", ws_bytes, lay.total);
+    // Rows are read again after others have been written; page ids are read while other
+    // pieces' results are written, and the lengths by the joining launch again.
+    const int64_t size = dt == RSA_F32 ? 4 : 2, cache = n_pages * Hkv * page_size * d * size;
+    const struct {
+        const void *p;
+        int64_t n;
+        const char *name;
+    } bufs[] = {{q, ((T - 1) * q_token_stride + (Hq - 1) * q_head_stride + d) * size, "q"}, {k_cache, cache, "k_cache"},
+                {v_cache, cache, "v_cache"}, {cu_q, (R + 1) * 4ll, "cu_q"}, {kv_len, R * 4ll, "kv_len"},
+                {block_table, ((R - 1) * table_stride + max_pages) * 4, "block_table"},
+                {prefix_len > 0 ? prefix_pages : nullptr, ((prefix_len + page_size - 1) >> shift) * 4, "prefix_pages"},
+                {drafted ? mask : nullptr, ((T - 1) * mask_stride + words) * 4, "mask"},
+                {out, T * Hq * d * size, "out"}, {lse, T * Hq * 4, "lse"}, {workspace, (int64_t)lay.total, "workspace"}};
+    for (int i = 8; i < 11; ++i)  // what is written
+        for (int j = 0; j < i; ++j)
+            if (overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n))
+                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", bufs[i].name, bufs[j].name);
+    RSA_TRY(check_device_for(dt));
+    PrefixAttnParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q;
+    p.q_token_stride = q_token_stride;
+    p.q_head_stride = q_head_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.d = d;
+    p.f32 = dt == RSA_F32;
+    p.n_pages = n_pages;
+    p.page_shift = shift;
+    p.cu_q = cu_q;
+    p.kv_len = kv_len;
+    p.R = R;
+    p.block_table = block_table;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.prefix_pages = prefix_pages;
+    p.prefix_len = prefix_len;
+    p.mask = drafted ? mask : nullptr;
+    p.mask_stride = mask_stride;
+    p.words = words;
+    p.out = out;
+    p.lse = lse;
+    char *w = static_cast<char *>(workspace);
+    auto take = [&](size_t n) {
+        char *at = w;
+        w += n;
+        return at;
+    };
+    p.plan = reinterpret_cast<int64_t *>(take(lay.plan));
+    for (int i = 0; i < 2; ++i) {
+        p.home_o[i] = reinterpret_cast<float *>(take(lay.home_o));
+        p.home_lse[i] = reinterpret_cast<float *>(take(lay.home_lse));
+    }
+    p.slot_o = reinterpret_cast<float *>(take(lay.slot_o));
+    p.slot_lse = reinterpret_cast<float *>(take(lay.slot_lse));
+    RSA_TRY(worker_count(&p.workers));
+    p.wait_limit_ns = wait_limit_ns();
+    RSA_TRY(device_error_word(&p.err));
+    rsa_status inj;
+    const char *name = drafted ? "tree attention launch" : "prefix attention launch";
+    if (injected_failure(name, &inj))
+        return inj;
+    cudaError_t e = dt == RSA_BF16 ? launch_prefix_attn_bf16(p, stream) : launch_prefix_attn_f32(p, stream);
+    if (e != cudaSuccess)
+        return fail(RSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    return RSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -497,94 +679,205 @@ rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_
                                const int32_t *prefix_pages, int64_t prefix_len, void *out, float *lse, void *workspace,
                                size_t ws_bytes, rsa_stream_t stream)
 {
-    RSA_TRY(check_prefix_shape(dt, T, Hq, Hkv, d, R));
-    RSA_TRY(check_cache(page_size, n_pages, Hkv));
-    const int shift = page_shift_of(page_size);
-    RSA_TRY(check_ptr(q, "q"));
-    RSA_TRY(check_strides(dt, q_token_stride, q_head_stride, d, "q"));
-    RSA_TRY(check_ptr(k_cache, "k_cache"));
-    RSA_TRY(check_ptr(v_cache, "v_cache"));
-    RSA_TRY(check_ptr(out, "out"));
-    RSA_TRY(check_ptr(lse, "lse"));
-    RSA_TRY(check_i32_ptr(cu_q, "cu_q"));
+    return paged_attn(q, q_token_stride, q_head_stride, k_cache, v_cache, dt, T, Hq, Hkv, d, page_size, n_pages, cu_q, kv_len, R,
+                      block_table, table_stride, max_pages, prefix_pages, prefix_len, false, nullptr, 0, 0, out, lse, workspace,
+                      ws_bytes, stream);
+}
+
+rsa_status rsa_tree_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
+                             const void *v_cache, rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int page_size,
+                             int64_t n_pages, const int32_t *cu_q, const int32_t *kv_len, int R, const int32_t *block_table,
+                             int64_t table_stride, int max_pages, const int32_t *prefix_pages, int64_t prefix_len,
+                             const uint32_t *mask, int64_t mask_stride, int words, void *out, float *lse, void *workspace,
+                             size_t ws_bytes, rsa_stream_t stream)
+{
+    return paged_attn(q, q_token_stride, q_head_stride, k_cache, v_cache, dt, T, Hq, Hkv, d, page_size, n_pages, cu_q, kv_len, R,
+                      block_table, table_stride, max_pages, prefix_pages, prefix_len, true, mask, mask_stride, words, out, lse,
+                      workspace, ws_bytes, stream);
+}
+
+rsa_status rsa_tree_plan(const int32_t *parent, int64_t T, const int32_t *cu_new, const int32_t *kv_len, int R, int words,
+                         int64_t pos0, int64_t *positions, uint32_t *mask, rsa_stream_t stream)
+{
+    if (T < 1 || R < 1)
+        return fail(RSA_ERR_INVALID_ARG, "T and R must be >= 1 (got %lld, %d)", (long long)T, R);
+    if (T > (1ll << 30) || R > (1 << 30))
+        return fail(RSA_ERR_UNSUPPORTED, "T=%lld tokens or R=%d requests: more than 2^30", (long long)T, R);
+    RSA_TRY(check_words(words));
+    if (pos0 < 0)
+        return fail(RSA_ERR_INVALID_ARG, "pos0=%lld must be >= 0", (long long)pos0);
+    RSA_TRY(check_i32_ptr(parent, "parent"));
+    RSA_TRY(check_i32_ptr(cu_new, "cu_new"));
     RSA_TRY(check_i32_ptr(kv_len, "kv_len"));
-    RSA_TRY(check_i32_ptr(block_table, "block_table"));
-    if (max_pages < 1 || table_stride < max_pages || ((int64_t)max_pages << shift) > 0x7fffffffLL)
-        return fail(RSA_ERR_INVALID_ARG,
-                    "max_pages=%d (rows %lld apart): at least 1, at most the row and 2^31-1 keys are wanted", max_pages,
-                    (long long)table_stride);
-    if (prefix_len < 0 || prefix_len > (1ll << 31) - 128)  // (a tile's last key is still an int)
-        return fail(RSA_ERR_INVALID_ARG, "prefix_len=%lld must be in [0, 2^31-128]", (long long)prefix_len);
-    if (prefix_len > 0)
-        RSA_TRY(check_i32_ptr(prefix_pages, "prefix_pages"));
-    const PrefixLayout lay = prefix_layout(T, Hq, d, R);
-    RSA_TRY(check_ptr(workspace, "workspace"));
-    if (ws_bytes < lay.total)
-        return fail(RSA_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", ws_bytes, lay.total);
-    // Rows are read again after others have been written; page ids are read while other
-    // pieces' results are written, and the lengths by the joining launch again.
-    const int64_t size = dt == RSA_F32 ? 4 : 2, cache = n_pages * Hkv * page_size * d * size;
-    const struct {
-        const void *p;
-        int64_t n;
-        const char *name;
-    } bufs[] = {{q, ((T - 1) * q_token_stride + (Hq - 1) * q_head_stride + d) * size, "q"}, {k_cache, cache, "k_cache"},
-                {v_cache, cache, "v_cache"}, {cu_q, (R + 1) * 4ll, "cu_q"}, {kv_len, R * 4ll, "kv_len"},
-                {block_table, ((R - 1) * table_stride + max_pages) * 4, "block_table"},
-                {prefix_len > 0 ? prefix_pages : nullptr, ((prefix_len + page_size - 1) >> shift) * 4, "prefix_pages"},
-                {out, T * Hq * d * size, "out"}, {lse, T * Hq * 4, "lse"}, {workspace, (int64_t)lay.total, "workspace"}};
-    for (int i = 7; i < 10; ++i)  // what is written
-        for (int j = 0; j < i; ++j)
-            if (overlap(bufs[i].p, bufs[i].n, bufs[j].p, bufs[j].n))
-                return fail(RSA_ERR_INVALID_ARG, "%s overlaps %s", bufs[i].name, bufs[j].name);
-    RSA_TRY(check_device_for(dt));
-    PrefixAttnParams p;
+    RSA_TRY(check_index_ptr(positions, "positions"));
+    RSA_TRY(check_i32_ptr(mask, "mask"));
+    const Buffer ins[] = {{parent, T * 4, "parent"}, {cu_new, (R + 1ll) * 4, "cu_new"}, {kv_len, R * 4ll, "kv_len"}},
+                 outs[] = {{positions, T * 8, "positions"}, {mask, T * words * 4, "mask"}};
+    RSA_TRY(check_buffers(outs, ins));
+    TreePlanParams p;
     memset(&p, 0, sizeof p);
-    p.q = q;
-    p.q_token_stride = q_token_stride;
-    p.q_head_stride = q_head_stride;
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
+    p.parent = parent;
     p.T = T;
-    p.Hq = Hq;
-    p.Hkv = Hkv;
-    p.G = Hq / Hkv;
-    p.d = d;
-    p.f32 = dt == RSA_F32;
-    p.n_pages = n_pages;
-    p.page_shift = shift;
-    p.cu_q = cu_q;
+    p.cu_new = cu_new;
     p.kv_len = kv_len;
     p.R = R;
+    p.words = words;
+    p.pos0 = pos0;
+    p.positions = positions;
+    p.mask = mask;
+    RSA_TRY(device_error_word(&p.err));
+    rsa_status inj;
+    if (injected_failure("tree plan launch", &inj))
+        return inj;
+    cudaError_t e = launch_tree_plan(p, stream);
+    if (e != cudaSuccess)
+        return fail(RSA_ERR_CUDA, "tree plan launch: %s", cudaGetErrorString(e));
+    return RSA_OK;
+}
+
+rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table, int64_t table_stride, int max_pages,
+                             const int32_t *cached_len, const int32_t *kv_len, int R, const int32_t *keep, int64_t keep_stride,
+                             int max_keep, const int32_t *keep_len, int32_t *new_len, rsa_stream_t stream)
+{
+    CompactParams p;
+    memset(&p, 0, sizeof p);
+    RSA_TRY(check_layers(cache, &p.c));
+    if (R < 1 || max_keep < 1)
+        return fail(RSA_ERR_INVALID_ARG, "R and max_keep must be >= 1 (got %d, %d)", R, max_keep);
+    RSA_TRY(check_table(block_table, table_stride, max_pages, cache->page_size));
+    if (keep_stride < max_keep || keep_stride > 0x7fffffffLL)
+        return fail(RSA_ERR_INVALID_ARG, "keep_stride=%lld must be in [max_keep=%d, 2^31-1]", (long long)keep_stride, max_keep);
+    RSA_TRY(check_i32_ptr(cached_len, "cached_len"));
+    RSA_TRY(check_i32_ptr(kv_len, "kv_len"));
+    RSA_TRY(check_i32_ptr(keep, "keep"));
+    RSA_TRY(check_i32_ptr(keep_len, "keep_len"));
+    RSA_TRY(check_i32_ptr(new_len, "new_len"));
+    const int64_t bytes = p.c.layer_bytes * p.c.layers;
+    const Buffer ins[] = {{block_table, ((R - 1) * table_stride + max_pages) * 4, "block_table"}, {cached_len, R * 4ll, "cached_len"},
+                          {kv_len, R * 4ll, "kv_len"}, {keep, ((R - 1) * keep_stride + max_keep) * 4, "keep"},
+                          {keep_len, R * 4ll, "keep_len"}},
+                 outs[] = {{p.c.data[0], bytes, "k_cache"}, {p.c.data[1], bytes, "v_cache"}, {new_len, R * 4ll, "new_len"}};
+    RSA_TRY(check_buffers(outs, ins));
     p.block_table = block_table;
     p.table_stride = table_stride;
     p.max_pages = max_pages;
-    p.prefix_pages = prefix_pages;
-    p.prefix_len = prefix_len;
-    p.out = out;
-    p.lse = lse;
-    char *w = static_cast<char *>(workspace);
-    auto take = [&](size_t n) {
-        char *at = w;
-        w += n;
-        return at;
-    };
-    p.plan = reinterpret_cast<int64_t *>(take(lay.plan));
-    for (int i = 0; i < 2; ++i) {
-        p.home_o[i] = reinterpret_cast<float *>(take(lay.home_o));
-        p.home_lse[i] = reinterpret_cast<float *>(take(lay.home_lse));
-    }
-    p.slot_o = reinterpret_cast<float *>(take(lay.slot_o));
-    p.slot_lse = reinterpret_cast<float *>(take(lay.slot_lse));
-    RSA_TRY(worker_count(&p.workers));
-    p.wait_limit_ns = wait_limit_ns();
+    p.cached_len = cached_len;
+    p.kv_len = kv_len;
+    p.R = R;
+    p.keep = keep;
+    p.keep_stride = keep_stride;
+    p.max_keep = max_keep;
+    p.keep_len = keep_len;
+    p.new_len = new_len;
     RSA_TRY(device_error_word(&p.err));
     rsa_status inj;
-    if (injected_failure("prefix attention launch", &inj))
+    if (injected_failure("cache compaction launch", &inj))
         return inj;
-    cudaError_t e = dt == RSA_BF16 ? launch_prefix_attn_bf16(p, stream) : launch_prefix_attn_f32(p, stream);
+    cudaError_t e = launch_cache_compact(p, stream);
     if (e != cudaSuccess)
-        return fail(RSA_ERR_CUDA, "prefix attention launch: %s", cudaGetErrorString(e));
+        return fail(RSA_ERR_CUDA, "cache compaction launch: %s", cudaGetErrorString(e));
+    return RSA_OK;
+}
+
+rsa_status rsa_page_fork(const rsa_cache *cache, int32_t *block_table, int64_t table_stride, int max_pages, int32_t *kv_len, int R,
+                         const int32_t *src, const int32_t *dst, int F, const int32_t *free_pages, int64_t n_free,
+                         const int64_t *free_start, int32_t *shares, int64_t *info, rsa_stream_t stream)
+{
+    PageForkParams p;
+    memset(&p, 0, sizeof p);
+    RSA_TRY(check_layers(cache, &p.c));
+    RSA_TRY(check_requests(R));
+    if (F < 1 || F > R)
+        return fail(RSA_ERR_INVALID_ARG, "F=%d must be in [1, R=%d]", F, R);
+    RSA_TRY(check_table(block_table, table_stride, max_pages, cache->page_size));
+    if ((int64_t)F * max_pages > 0x7fffffffLL)
+        return fail(RSA_ERR_UNSUPPORTED, "F=%d rows of max_pages=%d: more than 2^31-1 entries", F, max_pages);
+    if (n_free < 0 || n_free > 0x7fffffffLL)
+        return fail(RSA_ERR_INVALID_ARG, "n_free=%lld must be in [0, 2^31-1]", (long long)n_free);
+    RSA_TRY(check_i32_ptr(kv_len, "kv_len"));
+    RSA_TRY(check_i32_ptr(src, "src"));
+    RSA_TRY(check_i32_ptr(dst, "dst"));
+    if (n_free > 0)
+        RSA_TRY(check_i32_ptr(free_pages, "free_pages"));
+    if (free_start)
+        RSA_TRY(check_index_ptr(free_start, "free_start"));
+    if (shares)
+        RSA_TRY(check_i32_ptr(shares, "shares"));
+    RSA_TRY(check_index_ptr(info, "info"));
+    const int64_t bytes = p.c.layer_bytes * p.c.layers;
+    const Buffer ins[] = {{src, F * 4ll, "src"}, {dst, F * 4ll, "dst"}, {free_pages, n_free * 4, "free_pages"},
+                          {free_start, 8, "free_start"}},
+                 outs[] = {{p.c.data[0], bytes, "k_cache"}, {p.c.data[1], bytes, "v_cache"},
+                           {block_table, ((R - 1) * table_stride + max_pages) * 4, "block_table"}, {kv_len, R * 4ll, "kv_len"},
+                           {shares, p.c.n_pages * 4, "shares"}, {info, 32, "info"}};
+    RSA_TRY(check_buffers(outs, ins));
+    p.block_table = block_table;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.kv_len = kv_len;
+    p.R = R;
+    p.src = src;
+    p.dst = dst;
+    p.F = F;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.free_start = free_start;
+    p.shares = shares;
+    p.info = info;
+    RSA_TRY(device_error_word(&p.err));
+    rsa_status inj;
+    if (injected_failure("page fork launch", &inj))
+        return inj;
+    cudaError_t e = launch_page_fork(p, stream);
+    if (e != cudaSuccess)
+        return fail(RSA_ERR_CUDA, "page fork launch: %s", cudaGetErrorString(e));
+    return RSA_OK;
+}
+
+rsa_status rsa_page_free(const int32_t *block_table, int64_t table_stride, int max_pages, const int32_t *kv_len,
+                         const int32_t *keep_len, int R, int page_size, int64_t n_pages, int32_t *free_pages, int64_t n_free,
+                         const int64_t *free_start, int32_t *shares, int64_t *info, rsa_stream_t stream)
+{
+    RSA_TRY(check_requests(R));
+    RSA_TRY(check_cache(page_size, n_pages, 1));
+    if (n_pages > kPageFreeMaxPages)
+        return fail(RSA_ERR_UNSUPPORTED, "n_pages=%lld exceeds %lld pages", (long long)n_pages, (long long)kPageFreeMaxPages);
+    RSA_TRY(check_table(block_table, table_stride, max_pages, page_size));
+    if (n_free < 1 || n_free > 0x7fffffffLL)
+        return fail(RSA_ERR_INVALID_ARG, "n_free=%lld must be in [1, 2^31-1]", (long long)n_free);
+    RSA_TRY(check_i32_ptr(kv_len, "kv_len"));
+    RSA_TRY(check_i32_ptr(keep_len, "keep_len"));
+    RSA_TRY(check_i32_ptr(free_pages, "free_pages"));
+    RSA_TRY(check_index_ptr(free_start, "free_start"));
+    if (shares)
+        RSA_TRY(check_i32_ptr(shares, "shares"));
+    RSA_TRY(check_index_ptr(info, "info"));
+    const Buffer ins[] = {{block_table, ((R - 1) * table_stride + max_pages) * 4, "block_table"}, {kv_len, R * 4ll, "kv_len"},
+                          {keep_len, R * 4ll, "keep_len"}, {free_start, 8, "free_start"}},
+                 outs[] = {{free_pages, n_free * 4, "free_pages"}, {shares, n_pages * 4, "shares"}, {info, 32, "info"}};
+    RSA_TRY(check_buffers(outs, ins));
+    PageFreeParams p;
+    memset(&p, 0, sizeof p);
+    p.block_table = block_table;
+    p.table_stride = table_stride;
+    p.max_pages = max_pages;
+    p.kv_len = kv_len;
+    p.keep_len = keep_len;
+    p.R = R;
+    p.page_shift = page_shift_of(page_size);
+    p.n_pages = n_pages;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.free_start = free_start;
+    p.shares = shares;
+    p.info = info;
+    RSA_TRY(device_error_word(&p.err));
+    rsa_status inj;
+    if (injected_failure("page free launch", &inj))
+        return inj;
+    cudaError_t e = launch_page_free(p, stream);
+    if (e != cudaSuccess)
+        return fail(RSA_ERR_CUDA, "page free launch: %s", cudaGetErrorString(e));
     return RSA_OK;
 }
 

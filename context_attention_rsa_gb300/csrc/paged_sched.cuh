@@ -175,6 +175,7 @@ struct Piece {
     int keys;              // the segment's keys
     const int32_t *pages;
     int64_t see0;          // unit token i sees keys [0, min(keys, see0 + i))
+    int drafted;           // the segment's keys from here on are its tokens' own (the prefix: none); may be negative
     int t0, t1;
     bool first, whole;     // it begins the unit; it is all of it
 };
@@ -257,6 +258,7 @@ struct Walk {
             x.keys = g.keys;
             x.pages = g.pages;
             x.see0 = seg == 0 ? g.keys : (int64_t)g.see0 + i0;
+            x.drafted = seg == 0 ? g.keys : g.see0 - 1;
             x.t0 = first_tile(at);
             x.t1 = first_tile(end);
             x.first = x.t0 == 0;
@@ -276,6 +278,13 @@ struct Walk {
         return false;
     }
 };
+
+// 32 bits of a row's mask from drafted token j on; tokens before the first count as set.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t *row, int words, int j)
+{
+    auto word = [&](int w) { return w < 0 ? 0xffffffffu : (w < words ? row[w] : 0u); };
+    return __funnelshift_r(word(j >> 5), word((j >> 5) + 1), j & 31);
+}
 
 // The piece is all there is for its rows: its (o, lse) is the result.
 __device__ __forceinline__ bool is_result(const PrefixAttnParams &p, const Piece &x)

@@ -122,6 +122,7 @@ struct Rows {
     float m[2], l[2];  // (l: of this lane's keys)
     float4 o[2][H];
     int see[2];  // they see keys [0, see) of the segment
+    const uint32_t *mask[2];  // ... and of those from the piece's `drafted` on the ones that are set here
 };
 
 __device__ __forceinline__ void add_product(float4 &o, float p, const float4 &v)
@@ -135,9 +136,9 @@ __device__ __forceinline__ void add_product(float4 &o, float p, const float4 &v)
 __device__ __forceinline__ void scale_by(float4 &o, float a) { o.x *= a, o.y *= a, o.z *= a, o.w *= a; }
 
 // A warp's first 4 J rows, whose queries are q, through one block of nk keys from key j0 on.
-template <int D, int J>
+template <int D, int J, bool kTree>
 __device__ __forceinline__ void block(Rows<D> &r, const float (*q)[D + 4], const float (*ks)[D + 4], const float (*vs)[D],
-                                      float (*ps)[kKeys + 8], int nk, int j0, float scale)
+                                      float (*ps)[kKeys + 8], int nk, int j0, float scale, int drafted, int words)
 {
     constexpr int H = Rows<D>::H;
     const int x = threadIdx.x & 7, y = (threadIdx.x & 31) >> 3;
@@ -168,10 +169,13 @@ __device__ __forceinline__ void block(Rows<D> &r, const float (*q)[D + 4], const
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int lim = min(nk, r.see[j] - j0);
+        uint32_t bits = 0xffffffffu;
+        if (kTree && j0 + kKeys > drafted && lim > 0)
+            bits = mask_bits(r.mask[j], words, j0 - drafted);
         mx[j] = r.m[j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            sc[i][j] = x + 8 * i < lim ? (dot[i][j].x + dot[i][j].y) * scale : -INFINITY;
+            sc[i][j] = x + 8 * i < lim && (!kTree || (bits >> (x + 8 * i) & 1)) ? (dot[i][j].x + dot[i][j].y) * scale : -INFINITY;
             mx[j] = fmaxf(mx[j], sc[i][j]);
         }
     }
@@ -225,7 +229,7 @@ __device__ __forceinline__ void block(Rows<D> &r, const float (*q)[D + 4], const
     __syncwarp();  // ps is written again with the next block
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_constant__ PrefixAttnParams p)
 {
     constexpr int H = D / 32, kBlocks = Smem<D>::kBlocks, kTurn = Smem<D>::kTurn;
@@ -265,6 +269,8 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
             r.m[j] = -INFINITY;
             r.l[j] = 0.f;
             r.see[j] = row < rows ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + row / G)) : 0;
+            if (kTree)  // (a row that is none sees no key, and reads none)
+                r.mask[j] = p.mask + (x.tok + row / G) * p.mask_stride;
 #pragma unroll
             for (int h = 0; h < H; ++h)
                 r.o[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -292,9 +298,11 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                     break;
                 const int nk = (int)min((int64_t)kKeys, j1 - jb);
                 if (per <= 4)
-                    block<D, 1>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale);
+                    block<D, 1, kTree>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale,
+                                       x.drafted, p.words);
                 else
-                    block<D, 2>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale);
+                    block<D, 2, kTree>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale,
+                                       x.drafted, p.words);
             }
             __syncthreads();  // the turn is done with: its buffer is filled next
         }
@@ -566,11 +574,11 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
     PrefixAttnParams p = p_in;
     p.unit_tokens = p.light_tokens = kRows / p.G;
     p.light_tile = p.heavy_tile = 2;
-    cudaError_t e =
-        cudaFuncSetAttribute(prefix_attn_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
+    auto kernel = p.mask ? prefix_attn_f32_kernel<D, true> : prefix_attn_f32_kernel<D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)
         return e;
-    prefix_attn_f32_kernel<D><<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
+    kernel<<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }

@@ -91,6 +91,7 @@ struct Work {
     int t0, keys;         // its first tile; the segment's keys
     int64_t see0;         // unit token i sees keys [0, min(keys, see0 + i))
     int tok, ntok, head;  // the unit's tokens and key head
+    int drafted;          // keys from here on go by the rows' masks
     int to;               // where its rows go: kHome + (0 prefix, 1 own), kSlot or kResult
 };
 constexpr int kHome = 0, kSlot = 2, kResult = 3;
@@ -108,6 +109,7 @@ __device__ __forceinline__ Work work_of(const Piece &x, const PrefixAttnParams &
     w.tok = x.tok;
     w.ntok = x.ntok;
     w.head = x.head;
+    w.drafted = x.drafted;
     w.to = !x.first ? kSlot : (is_result(p, x) ? kResult : kHome + (x.seg > 0));
     return w;
 }
@@ -282,18 +284,25 @@ struct Row {
 
 // The scores of this thread's 64 keys of a tile (half h of it), masked; their
 // maximum is returned.  lim: keys of the tile that the row sees; held: keys of the
-// tile.
-__device__ __forceinline__ float read_scores(uint32_t tS, int h, int lim, int held, uint32_t (&s)[64])
+// tile; with kTree, bits: those of the 64 that its mask lets it see.
+template <bool kTree>
+__device__ __forceinline__ float read_scores(uint32_t tS, int h, int lim, int held, uint64_t bits, uint32_t (&s)[64])
 {
     ptx::tc_fence_after();
     ptx::tmem_ld64(tS + 64 * h, s);
     ptx::tmem_ld_wait64(s);
-    if (lim < kTileKeys) {
+    if (lim < kTileKeys || (kTree && bits != ~0ull)) {
         // Column c is key c, except in the last group of 8 of a shorter tile: its
         // keys end where the group ends (see the producer).
         const int last = (held - 1) & ~7, gap = last + 8 - held;
-        const uint64_t seen = columns(min(lim, last) - 64 * h) |
-                              (columns(min(lim + gap, last + 8) - 64 * h) & ~columns(last + gap - 64 * h));
+        uint64_t seen;
+        if constexpr (kTree) {
+            const uint64_t keys = columns(lim - 64 * h) & bits, whole = columns(last - 64 * h);
+            seen = (keys & whole) | ((keys & ~whole) << gap);
+        } else {
+            seen = columns(min(lim, last) - 64 * h) |
+                   (columns(min(lim + gap, last + 8) - 64 * h) & ~columns(last + gap - 64 * h));
+        }
         const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -371,7 +380,8 @@ __device__ __forceinline__ void write_probabilities(uint32_t tS, int h, float sl
     r.l += a.x + a.y;
 }
 
-template <int D>
+// kTree: keys from the piece's `drafted` on are seen by the rows whose mask says so.
+template <int D, bool kTree>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k8,
@@ -755,6 +765,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 break;
             const Work &f = work[at];  // given back when its rows have been written
             const int tiles = max(f.tiles, 0), t0 = f.t0, keys = f.keys;
+            // The mask's bits for this thread's 64 keys of the tile from key0 on, read while
+            // the tile's scores are still to come.
+            const int drafted = f.drafted, tok = f.tok, ntok = f.ntok;
+            auto mask_of = [&](int key0, int e) -> uint64_t {
+                const int ti = row_tok + e * TT;
+                if (!kTree || drafted - key0 >= kTileKeys || row_tok >= TT || ti >= ntok)
+                    return ~0ull;
+                const uint32_t *m = p.mask + (tok + ti) * p.mask_stride;
+                const int j = key0 + 64 * h - drafted;
+                return (uint64_t)mask_bits(m, p.words, j + 32) << 32 | mask_bits(m, p.words, j);
+            };
             const bool two = f.two != 0, last = f.tiles < 0;
             Row r[2];  // of the two row tiles; with one, of it
             uint32_t s[64];
@@ -775,10 +796,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                     for (int t = 0; t < 2; ++t) {
                         const bool busy = __any_sync(0xffffffffu, r[t].allowed != INT_MAX);
                         float mx = -INFINITY;
+                        const uint64_t bits = mask_of(key0, t);
                         const bool got = wait(C::kSF + t, (t ? s_use1 : s_use0) + j, 0x80);
                         if (got && busy) {
-                            mx = read_scores(lanes + (t ? C::kColS1 : C::kColS0), h, r[t].allowed - key0,
-                                             min(kTileKeys, keys - key0), s);
+                            mx = read_scores<kTree>(lanes + (t ? C::kColS1 : C::kColS0), h, r[t].allowed - key0,
+                                                    min(kTileKeys, keys - key0), bits, s);
                             xch[(t * 2 + h) * 128 + row] = mx;
                         }
                         // Both halves of the rows have read S before P is written over it.
@@ -808,9 +830,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                         const int key0 = (t0 + j) * kTileKeys, t = (done + j) & 1;
                         const uint32_t tS = lanes + (t ? C::kColS1 : C::kColS0);
                         float mx = -INFINITY;
+                        const uint64_t bits = mask_of(key0, 0);
                         const bool got = wait(C::kSF + t, t ? s_use1++ : s_use0++, 0x80);
                         if (got && busy) {
-                            mx = read_scores(tS, h, r[0].allowed - key0, min(kTileKeys, keys - key0), s);
+                            mx = read_scores<kTree>(tS, h, r[0].allowed - key0, min(kTileKeys, keys - key0), bits, s);
                             xch[(t * 2 + h) * 128 + row] = mx;
                         }
                         ptx::tc_fence_before();
@@ -886,11 +909,11 @@ cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
         !make_bf16_map_sw128(&mv, p.v_cache, 5, kd, ks, kb) || !make_bf16_map_sw128(&mk8, p.k_cache, 4, gd, gs, gb) ||
         !make_bf16_map_sw128(&mv8, p.v_cache, 4, gd, gs, gb))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Cfg<D>::kSmemBytes);
+    auto kernel = p.mask ? prefix_attn_kernel<D, true> : prefix_attn_kernel<D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    prefix_attn_kernel<D><<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, mk8, mv8, p);
+    kernel<<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, mk8, mv8, p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }

@@ -59,7 +59,9 @@ __device__ __forceinline__ bool debug_check(bool ok, unsigned int *err, unsigned
 
 // Sites of index data (rsa.h names them; the other kernels' codes are all below 0x90).
 constexpr unsigned int kSitePlanPage = 0x90, kSitePosition = 0x91, kSiteSlot = 0x92, kSiteQueryRows = 0x93, kSiteKvLen = 0x94,
-                       kSiteCachePage = 0x95;
+                       kSiteCachePage = 0x95, kSiteTreeRows = 0x96, kSiteTreeLen = 0x97, kSiteParent = 0x98, kSiteTreeSize = 0x99,
+                       kSiteCompactLen = 0x9a, kSiteKeep = 0x9b, kSiteCompactPage = 0x9c, kSiteForkPage = 0x9d,
+                       kSiteFreePage = 0x9e, kSiteFreeTwice = 0x9f;
 
 // Position axes of a rotation (time, height, width, one more).
 constexpr int kMaxRopeAxes = 4;
@@ -199,6 +201,9 @@ struct PrefixAttnParams {
     int max_pages;
     const int32_t *prefix_pages;
     int64_t prefix_len;
+    const uint32_t *mask;        // drafted tokens (rsa_tree_attn_fwd): [T, words], rows mask_stride apart; else NULL
+    int64_t mask_stride;
+    int words;
     void *out;                   // [T, Hq, d]
     float *lse;                  // [T, Hq]
     // workspace (see paged_sched.cuh)
@@ -216,6 +221,78 @@ struct PrefixAttnParams {
 constexpr int kPrefixMaxWorkers = 160;   // CTAs of the attention launch: one on each SM
 constexpr int kPrefixUnitRows = 256;     // query rows of one unit at most
 constexpr int kPrefixMaxGroup = 128;     // query heads per key head at most
+
+// Positions and ancestor masks of drafted tokens (rsa_tree_plan).
+constexpr int kTreeMaxWords = 32;
+struct TreePlanParams {
+    const int32_t *parent;  // [T]
+    int64_t T;
+    const int32_t *cu_new, *kv_len;
+    int R, words;
+    int64_t pos0;
+    int64_t *positions;
+    uint32_t *mask;         // [T, words]
+    unsigned int *err;
+};
+
+// The caches of several layers (rsa_cache): rows of `row` bytes.
+struct CacheLayers {
+    char *data[2];        // keys, values: [layers, n_pages, Hkv, page, row]
+    int64_t layer_bytes;
+    int64_t n_pages;
+    int layers, Hkv, page_shift, row;
+};
+
+// Kept rows moved together (rsa_cache_compact).
+struct CompactParams {
+    CacheLayers c;
+    const int32_t *block_table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t *cached_len, *kv_len;
+    int R;
+    const int32_t *keep;  // [R, max_keep], rows keep_stride apart
+    int64_t keep_stride;
+    int max_keep;
+    const int32_t *keep_len;
+    int32_t *new_len;
+    unsigned int *err;
+};
+
+// Forks of requests (rsa_page_fork).
+struct PageForkParams {
+    CacheLayers c;
+    int32_t *block_table;
+    int64_t table_stride;
+    int max_pages;
+    int32_t *kv_len;
+    int R;
+    const int32_t *src, *dst;
+    int F;
+    const int32_t *free_pages;
+    int64_t n_free;
+    const int64_t *free_start;
+    int32_t *shares;      // [n_pages] or NULL: every page is copied
+    int64_t *info;
+    unsigned int *err;
+};
+
+// Pages given back (rsa_page_free).
+constexpr int64_t kPageFreeMaxPages = 1 << 23;
+struct PageFreeParams {
+    const int32_t *block_table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t *kv_len, *keep_len;
+    int R, page_shift;
+    int64_t n_pages;
+    int32_t *free_pages;
+    int64_t n_free;
+    const int64_t *free_start;
+    int32_t *shares;      // [n_pages] or NULL: one user a page
+    int64_t *info;
+    unsigned int *err;
+};
 
 // Launchers (no validation; the C ABI layer validates).  They return the
 // cudaError_t of the launch.
@@ -236,6 +313,10 @@ cudaError_t launch_prefix_attn_bf16(const PrefixAttnParams &p, cudaStream_t s);
 cudaError_t launch_prefix_attn_f32(const PrefixAttnParams &p, cudaStream_t s);
 // Joins the pieces of every row: the second launch of the attention.
 cudaError_t launch_prefix_join(const PrefixAttnParams &p, cudaStream_t s);
+cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s);
+cudaError_t launch_cache_compact(const CompactParams &p, cudaStream_t s);
+cudaError_t launch_page_fork(const PageForkParams &p, cudaStream_t s);
+cudaError_t launch_page_free(const PageFreeParams &p, cudaStream_t s);
 cudaError_t launch_selftest_wait(uint64_t limit_ns, unsigned int *err, cudaStream_t s);
 // Two-pass ring self-attention (bf16, d = 128, T/N a multiple of 128): per
 // query chunk, score pass into S [BH, Tc, T] fp32 (and per-tile row

@@ -33,6 +33,11 @@ decltype(&rsa_qk_norm_rope_bwd) rope_bwd_fn;
 decltype(&rsa_qk_norm_rope_bwd_workspace_size) rope_bwd_size_fn;
 decltype(&rsa_prefix_attn_fwd) attn_fn;
 decltype(&rsa_prefix_attn_workspace_size) attn_size_fn;
+decltype(&rsa_tree_plan) tree_plan_fn;
+decltype(&rsa_tree_attn_fwd) tree_attn_fn;
+decltype(&rsa_cache_compact) compact_fn;
+decltype(&rsa_page_fork) fork_fn;
+decltype(&rsa_page_free) free_fn;
 PyObject *share_fn;  // (stream, device index, tensors): memory of the current stream used on another one
 
 // A Python exception to raise.
@@ -457,8 +462,9 @@ PyObject *qk_norm_rope_bwd(PyObject *const *a)
     return results(st, {dq, dk, dw[0], dw[1]});
 }
 
-// q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages, prefix_len, out, lse, workspace, stream
-PyObject *prefix_attn(PyObject *const *a)
+// q, k_cache, v_cache, cu_q, block_table, kv_len, then those of `b`: prefix_pages, prefix_len, out, lse, workspace,
+// stream; with a mask (mask_arg) for drafted tokens, or none (NULL).
+PyObject *attention(PyObject *const *a, PyObject *mask_arg, PyObject *const *b)
 {
     rsa_dtype dt;
     const at::Tensor &q = queries(a[0], &dt);
@@ -479,33 +485,45 @@ PyObject *prefix_attn(PyObject *const *a)
         value_error("cu_q [R + 1], kv_len [R] and block_table [R, max_pages] must agree");
     if (std::max({Hq, Hkv, d, page_size, R, max_pages}) > INT32_MAX)
         value_error("a dimension does not fit 32 bits");
-    const int64_t stride = table_stride(table), prefix_len = integer(a[7]);
+    const int64_t stride = table_stride(table), prefix_len = integer(b[1]);
     const int32_t *prefix = nullptr;
     if (prefix_len != 0) {
-        const at::Tensor &t = check("prefix_pages", a[6], 1, at::kInt, dev);
+        const at::Tensor &t = check("prefix_pages", b[0], 1, at::kInt, dev);
         if (t.size(0) < prefix_len / std::max<int64_t>(page_size, 1) + (prefix_len % std::max<int64_t>(page_size, 1) > 0))
             value_error("prefix_pages hold " + std::to_string(t.size(0) * page_size) + " tokens, prefix_len is " +
                         std::to_string(prefix_len));
         prefix = t.data_ptr<int>();
     }
-    Call call(dev, a[11]);
+    const uint32_t *mask = nullptr;
+    int64_t mask_stride = 0, words = 0;
+    if (mask_arg) {
+        const at::Tensor &t = check("tree_mask", mask_arg, 2, at::kInt, dev, false);
+        if (t.size(0) != T)
+            value_error("tree_mask must hold T=" + std::to_string(T) + " rows");
+        if (t.stride(1) != 1 && t.size(1) > 1)
+            value_error("rows of tree_mask must be contiguous");
+        mask = static_cast<const uint32_t *>(t.data_ptr());
+        words = std::min<int64_t>(t.size(1), INT32_MAX);
+        mask_stride = T == 1 ? words : t.stride(0);
+    }
+    Call call(dev, b[5]);
     at::Tensor out, lse, ws;
-    if (a[8] == Py_None) {
+    if (b[2] == Py_None) {
         out = call.make(q.sizes(), type);
     } else {
-        out = check("out", a[8], 3, type, dev);
+        out = check("out", b[2], 3, type, dev);
         if (out.sizes() != q.sizes())
             value_error("out must have q's shape");
     }
-    if (a[9] == Py_None) {
+    if (b[3] == Py_None) {
         lse = call.make({T, Hq}, at::kFloat);
     } else {
-        lse = check("lse", a[9], 2, at::kFloat, dev);
+        lse = check("lse", b[3], 2, at::kFloat, dev);
         if (lse.size(0) != T || lse.size(1) != Hq)
             value_error("lse must be [T, Hq]");
     }
-    if (a[10] != Py_None) {
-        ws = workspace(a[10], dev);
+    if (b[4] != Py_None) {
+        ws = workspace(b[4], dev);
     } else {
         size_t n = 0;
         const rsa_status st = attn_size_fn(dt, T, (int)Hq, (int)Hkv, (int)d, (int)R, &n);
@@ -515,11 +533,199 @@ PyObject *prefix_attn(PyObject *const *a)
     }
     const rsa_stream_t stream = call.stream();
     const rsa_status st = launch([&] {
+        if (mask_arg)
+            return tree_attn_fn(qh.data, qh.token_stride, qh.head_stride, kc->data_ptr(), vc->data_ptr(), dt, T, (int)Hq, (int)Hkv,
+                                (int)d, (int)page_size, n_pages, cu.data_ptr<int>(), kv.data_ptr<int>(), (int)R,
+                                table.data_ptr<int>(), stride, (int)max_pages, prefix, prefix_len, mask, mask_stride, (int)words,
+                                out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), ws.nbytes(), stream);
         return attn_fn(qh.data, qh.token_stride, qh.head_stride, kc->data_ptr(), vc->data_ptr(), dt, T, (int)Hq, (int)Hkv, (int)d,
                        (int)page_size, n_pages, cu.data_ptr<int>(), kv.data_ptr<int>(), (int)R, table.data_ptr<int>(), stride,
                        (int)max_pages, prefix, prefix_len, out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(), ws.nbytes(), stream);
     });
     return results(st, {out, lse});
+}
+
+PyObject *prefix_attn(PyObject *const *a) { return attention(a, nullptr, a + 6); }
+
+// ..., kv_len, tree_mask, prefix_pages, ...
+PyObject *tree_attn(PyObject *const *a) { return attention(a, a[6], a + 7); }
+
+// A result of `n` entries: the caller's, or a new one.
+at::Tensor result_list(Call &call, const char *name, PyObject *given, int64_t n, at::ScalarType type, const c10::Device &dev)
+{
+    if (given == Py_None)
+        return call.make({n}, type);
+    const at::Tensor &t = check(name, given, 1, type, dev);
+    if (t.size(0) != n)
+        value_error(std::string(name) + " must hold " + std::to_string(n) + " entries");
+    return t;
+}
+
+// A list of `n` (any, if negative) 32-bit integers.
+const at::Tensor &list(const char *name, PyObject *o, int64_t n, const c10::Device &dev)
+{
+    const at::Tensor &t = check(name, o, 1, at::kInt, dev);
+    if (n >= 0 && t.size(0) != n)
+        value_error(std::string(name) + " must hold " + std::to_string(n) + " entries");
+    return t;
+}
+
+const int64_t *free_start(PyObject *o, const c10::Device &dev)
+{
+    if (o == Py_None)
+        return nullptr;
+    const at::Tensor &t = check("free_start", o, 1, at::kLong, dev);
+    if (t.size(0) < 1)
+        value_error("free_start must hold one entry");
+    return t.data_ptr<int64_t>();
+}
+
+c10::Device device_of(const char *name, PyObject *o)
+{
+    if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda())
+        type_error(std::string(name) + " must be a CUDA tensor");
+    return THPVariable_Unpack(o).device();
+}
+
+// block_table, whose rows and pages fit 32 bits.
+const at::Tensor &tables(PyObject *o, const c10::Device &dev)
+{
+    const at::Tensor &t = check("block_table", o, 2, at::kInt, dev, false);
+    if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX)
+        value_error("block_table is too large");
+    return t;
+}
+
+// Caches of one layer [n_pages, Hkv, page_size, d] or of several [layers, n_pages, ...].
+rsa_cache layers(PyObject *ko, PyObject *vo, const c10::Device &dev)
+{
+    rsa_cache c = {};
+    const at::Tensor &k = on_device("k_cache", ko, dev), &v = on_device("v_cache", vo, dev);
+    if ((k.dim() != 4 && k.dim() != 5) || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type())
+        value_error("k_cache and v_cache must both be [n_pages, Hkv, page_size, d] or [layers, n_pages, Hkv, page_size, d]");
+    if (!k.is_contiguous() || !v.is_contiguous())
+        value_error("k_cache and v_cache must be contiguous");
+    if (k.scalar_type() == at::kFloat)
+        c.dt = RSA_F32;
+    else if (k.scalar_type() == at::kBFloat16)
+        c.dt = RSA_BF16;
+    else
+        type_error(std::string("unsupported dtype ") + c10::toString(k.scalar_type()) + " (float32 or bfloat16)");
+    for (int64_t n : k.sizes())
+        if (n > INT32_MAX)
+            value_error("a dimension does not fit 32 bits");
+    const int64_t *s = k.sizes().data() + (k.dim() - 4);
+    c.k_cache = k.data_ptr();
+    c.v_cache = v.data_ptr();
+    c.layers = k.dim() == 5 ? (int)k.size(0) : 1;
+    c.n_pages = s[0];
+    c.Hkv = (int)s[1];
+    c.page_size = (int)s[2];
+    c.d = (int)s[3];
+    return c;
+}
+
+// parent, cu_new, kv_len, max_tree, pos0, out, stream
+PyObject *tree_plan(PyObject *const *a)
+{
+    const c10::Device dev = device_of("parent", a[0]);
+    const at::Tensor &parent = list("parent", a[0], -1, dev), &kv = list("kv_len", a[2], -1, dev);
+    const int64_t T = parent.size(0), R = kv.size(0);
+    if (R >= INT32_MAX)
+        value_error("kv_len is too large");
+    const at::Tensor &cu = list("cu_new", a[1], R + 1, dev);
+    const int64_t most = integer(a[3]), pos0 = integer(a[4]);
+    if (most < 1 || most > 1024)
+        value_error("max_tree=" + std::to_string(most) + " must be in [1, 1024]");
+    const int64_t words = (most + 31) / 32;
+    Call call(dev, a[6]);
+    at::Tensor pos, mask;
+    if (a[5] == Py_None) {
+        pos = call.make({T}, at::kLong);
+        mask = call.make({T, words}, at::kInt);
+    } else {
+        if (!PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 2)
+            type_error("out must be a TreePlan");
+        pos = result_list(call, "out.positions", PyTuple_GET_ITEM(a[5], 0), T, at::kLong, dev);
+        mask = check("out.mask", PyTuple_GET_ITEM(a[5], 1), 2, at::kInt, dev);
+        if (mask.size(0) != T || mask.size(1) != words)
+            value_error("out.mask must be [" + std::to_string(T) + ", " + std::to_string(words) + "]");
+    }
+    const rsa_stream_t stream = call.stream();
+    const rsa_status st = launch([&] {
+        return tree_plan_fn(parent.data_ptr<int>(), T, cu.data_ptr<int>(), kv.data_ptr<int>(), (int)R, (int)words, pos0,
+                            pos.data_ptr<int64_t>(), static_cast<uint32_t *>(mask.data_ptr()), stream);
+    });
+    return results(st, {pos, mask});
+}
+
+// k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_len, out, stream
+PyObject *cache_compact(PyObject *const *a)
+{
+    const c10::Device dev = device_of("k_cache", a[0]);
+    const rsa_cache c = layers(a[0], a[1], dev);
+    const at::Tensor &table = tables(a[2], dev);
+    const int64_t R = table.size(0), stride = table_stride(table);
+    const at::Tensor &cached = list("cached_len", a[3], R, dev), &kv = list("kv_len", a[4], R, dev);
+    const at::Tensor &keep = check("keep", a[5], 2, at::kInt, dev, false), &n = list("keep_len", a[6], R, dev);
+    if (keep.size(0) != R || keep.size(1) > INT32_MAX || (keep.stride(1) != 1 && keep.size(1) > 1))
+        value_error("keep must hold a contiguous row for each of block_table's " + std::to_string(R) + " requests");
+    const int64_t keep_stride = R == 1 ? keep.size(1) : keep.stride(0);
+    Call call(dev, a[8]);
+    const at::Tensor out = result_list(call, "out", a[7], R, at::kInt, dev);
+    const rsa_stream_t stream = call.stream();
+    const rsa_status st = launch([&] {
+        return compact_fn(&c, table.data_ptr<int>(), stride, (int)table.size(1), cached.data_ptr<int>(), kv.data_ptr<int>(), (int)R,
+                          keep.data_ptr<int>(), keep_stride, (int)keep.size(1), n.data_ptr<int>(), out.data_ptr<int>(), stream);
+    });
+    return results(st, {out});
+}
+
+// k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_start, shares, out, stream
+PyObject *page_fork(PyObject *const *a)
+{
+    const c10::Device dev = device_of("k_cache", a[0]);
+    const rsa_cache c = layers(a[0], a[1], dev);
+    const at::Tensor &table = tables(a[2], dev);
+    const int64_t R = table.size(0), stride = table_stride(table);
+    const at::Tensor &kv = list("kv_len", a[3], R, dev), &src = list("src", a[4], -1, dev);
+    const at::Tensor &dst = list("dst", a[5], src.size(0), dev), &pages = list("free_pages", a[6], -1, dev);
+    if (src.size(0) > INT32_MAX)
+        value_error("src is too large");
+    const int64_t *start = free_start(a[7], dev);
+    int32_t *shares = a[8] == Py_None ? nullptr : list("shares", a[8], c.n_pages, dev).data_ptr<int>();
+    Call call(dev, a[10]);
+    const at::Tensor info = result_list(call, "out", a[9], 4, at::kLong, dev);
+    const rsa_stream_t stream = call.stream();
+    const rsa_status st = launch([&] {
+        return fork_fn(&c, table.data_ptr<int>(), stride, (int)table.size(1), kv.data_ptr<int>(), (int)R, src.data_ptr<int>(),
+                       dst.data_ptr<int>(), (int)src.size(0), pages.data_ptr<int>(), pages.size(0), start, shares,
+                       info.data_ptr<int64_t>(), stream);
+    });
+    return results(st, {info});
+}
+
+// block_table, kv_len, keep_len, free_pages, free_start, page_size, n_pages, shares, out, stream
+PyObject *page_free(PyObject *const *a)
+{
+    const c10::Device dev = device_of("block_table", a[0]);
+    const at::Tensor &table = tables(a[0], dev);
+    const int64_t R = table.size(0), stride = table_stride(table);
+    const at::Tensor &kv = list("kv_len", a[1], R, dev), &keep = list("keep_len", a[2], R, dev), &pages = list("free_pages", a[3], -1, dev);
+    if (a[4] == Py_None)
+        type_error("free_start must be a CUDA tensor on " + dev.str());
+    const int64_t *start = free_start(a[4], dev);
+    const int page_size = small_integer(a[5], "page_size");
+    const int64_t n_pages = integer(a[6]);
+    int32_t *shares = a[7] == Py_None ? nullptr : list("shares", a[7], n_pages, dev).data_ptr<int>();
+    Call call(dev, a[9]);
+    const at::Tensor info = result_list(call, "out", a[8], 4, at::kLong, dev);
+    const rsa_stream_t stream = call.stream();
+    const rsa_status st = launch([&] {
+        return free_fn(table.data_ptr<int>(), stride, (int)table.size(1), kv.data_ptr<int>(), keep.data_ptr<int>(), (int)R, page_size,
+                       n_pages, pages.data_ptr<int>(), pages.size(0), start, shares, info.data_ptr<int64_t>(), stream);
+    });
+    return results(st, {info});
 }
 
 // A function of N arguments; C++ exceptions become Python's.
@@ -542,11 +748,11 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// The addresses of the six calls, and share_fn.
+// The addresses of the eleven functions, and share_fn.
 PyObject *bind(PyObject *const *a)
 {
-    void *p[6];
-    for (int i = 0; i < 6; ++i)
+    void *p[11];
+    for (int i = 0; i < 11; ++i)
         p[i] = reinterpret_cast<void *>(integer(a[i]));
     page_plan_fn = reinterpret_cast<decltype(page_plan_fn)>(p[0]);
     rope_fn = reinterpret_cast<decltype(rope_fn)>(p[1]);
@@ -554,13 +760,19 @@ PyObject *bind(PyObject *const *a)
     rope_bwd_size_fn = reinterpret_cast<decltype(rope_bwd_size_fn)>(p[3]);
     attn_fn = reinterpret_cast<decltype(attn_fn)>(p[4]);
     attn_size_fn = reinterpret_cast<decltype(attn_size_fn)>(p[5]);
-    Py_XSETREF(share_fn, Py_NewRef(a[6]));
+    tree_plan_fn = reinterpret_cast<decltype(tree_plan_fn)>(p[6]);
+    tree_attn_fn = reinterpret_cast<decltype(tree_attn_fn)>(p[7]);
+    compact_fn = reinterpret_cast<decltype(compact_fn)>(p[8]);
+    fork_fn = reinterpret_cast<decltype(fork_fn)>(p[9]);
+    free_fn = reinterpret_cast<decltype(free_fn)>(p[10]);
+    Py_XSETREF(share_fn, Py_NewRef(a[11]));
     Py_RETURN_NONE;
 }
 
 #define RSA_ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {RSA_ENTRY(bind, 7),          RSA_ENTRY(page_plan, 11),       RSA_ENTRY(qk_norm_rope, 16),
-                         RSA_ENTRY(qk_norm_rope_bwd, 17), RSA_ENTRY(prefix_attn, 12), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {RSA_ENTRY(bind, 12),       RSA_ENTRY(page_plan, 11),    RSA_ENTRY(qk_norm_rope, 16), RSA_ENTRY(qk_norm_rope_bwd, 17),
+                         RSA_ENTRY(prefix_attn, 12), RSA_ENTRY(tree_plan, 7),     RSA_ENTRY(tree_attn, 13),    RSA_ENTRY(cache_compact, 9),
+                         RSA_ENTRY(page_fork, 11),   RSA_ENTRY(page_free, 10),    {nullptr, nullptr, 0, nullptr}};
 #undef RSA_ENTRY
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods};

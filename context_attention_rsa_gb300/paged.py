@@ -1,5 +1,6 @@
 """Serving over a paged KV cache: a step's plan, the norm and rotation of its
-heads with the cache write, and attention behind a shared prefix.
+heads with the cache write, attention behind a shared prefix, drafted tokens,
+and the keeping of pages.
 
 The calls of ``include/rsa.h`` with the same names; as in the rest of the
 binding they only check and marshal arguments, here in an extension module
@@ -11,6 +12,16 @@ binding they only check and marshal arguments, here in an extension module
                             k_cache=k_cache, v_cache=v_cache)
         out, lse = prefix_attn(q, k_cache, v_cache, plan.cu_new, block_table, plan.kv_len,
                                prefix_pages=prefix_pages, prefix_len=prefix_len)
+
+With a tree of drafted tokens for every request (parent: each token's parent):
+
+    plan = page_plan(...)
+    tree = tree_plan(parent, plan.cu_new, plan.kv_len, max_tree, pos0=prefix_len)
+    for each layer: qk_norm_rope as above with tree.positions, then
+        out, lse = tree_attn(q, k_cache, v_cache, plan.cu_new, block_table, plan.kv_len, tree.mask, ...)
+    new_len = cache_compact(k_caches, v_caches, block_table, cached_len, plan.kv_len, accepted, n_accepted)
+    info = page_free(block_table, plan.kv_len, new_len, free_pages, plan.info[3:], page_size, n_pages)
+    # the next step: cached_len = new_len, free_start = info[3:]
 
 Caches are [n_pages, Hkv, page_size, d]; a step's rows are packed [T, H, d].
 Nothing synchronises, so a step can be captured into a CUDA graph and replayed
@@ -37,7 +48,7 @@ import torch
 from . import RSA_BF16, RSA_F32, RsaError, _build, load
 
 PLAN_STATUS = {0: "ok", 1: "negative length", 2: "block table row too short", 3: "too few free pages",
-               4: "more tokens than max_tokens"}
+               4: "more tokens than max_tokens", 5: "a fork's requests", 6: "no room for the free pages"}
 
 
 class Heads(ctypes.Structure):
@@ -64,6 +75,18 @@ class PagePlan(NamedTuple):
     info: torch.Tensor
 
 
+class TreePlan(NamedTuple):
+    """What tree_plan leaves for the step (device tensors)."""
+    positions: torch.Tensor
+    mask: torch.Tensor
+
+
+class Cache(ctypes.Structure):
+    """rsa_cache."""
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("dt", ctypes.c_int), ("layers", ctypes.c_int),
+                ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int), ("page_size", ctypes.c_int), ("d", ctypes.c_int)]
+
+
 _p, _i32, _i64, _size = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 SIGS = {
     "rsa_page_plan": [_p, _p, _i32, _i32, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _p],
@@ -73,6 +96,12 @@ SIGS = {
     "rsa_prefix_attn_workspace_size": [_i32, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_size)],
     "rsa_prefix_attn_fwd": [_p, _i64, _i64, _p, _p, _i32, _i64, _i32, _i32, _i32, _i32, _i64, _p, _p, _i32, _p, _i64, _i32,
                             _p, _i64, _p, _p, _p, _size, _p],
+    "rsa_tree_plan": [_p, _i64, _p, _p, _i32, _i32, _i64, _p, _p, _p],
+    "rsa_tree_attn_fwd": [_p, _i64, _i64, _p, _p, _i32, _i64, _i32, _i32, _i32, _i32, _i64, _p, _p, _i32, _p, _i64, _i32,
+                          _p, _i64, _p, _i64, _i32, _p, _p, _p, _size, _p],
+    "rsa_cache_compact": [_p, _p, _i64, _i32, _p, _p, _i32, _p, _i64, _i32, _p, _p, _p],
+    "rsa_page_fork": [_p, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _p, _i64, _p, _p, _p, _p],
+    "rsa_page_free": [_p, _i64, _i32, _p, _p, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p],
 }
 
 _DT = {torch.float32: RSA_F32, torch.bfloat16: RSA_BF16}
@@ -100,7 +129,8 @@ def _load_native():
             spec.loader.exec_module(m)
             m.bind(*(ctypes.cast(getattr(lib, n), _p).value for n in (
                 "rsa_page_plan", "rsa_qk_norm_rope_fwd", "rsa_qk_norm_rope_bwd", "rsa_qk_norm_rope_bwd_workspace_size",
-                "rsa_prefix_attn_fwd", "rsa_prefix_attn_workspace_size")), _share)
+                "rsa_prefix_attn_fwd", "rsa_prefix_attn_workspace_size", "rsa_tree_plan", "rsa_tree_attn_fwd", "rsa_cache_compact",
+                "rsa_page_fork", "rsa_page_free")), _share)
             _native = m
     return _native
 
@@ -190,3 +220,72 @@ def prefix_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages=Non
     if r.__class__ is int:
         raise _error("rsa_prefix_attn_fwd", r)
     return r
+
+
+def tree_plan(parent: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor, max_tree: int, pos0: int = 0,
+              out: Optional[TreePlan] = None, stream=None) -> TreePlan:
+    """Positions and ancestor masks of a step's drafted tokens (rsa_tree_plan).
+    parent [T] int32: for each row of the step (page_plan's, cu_new and kv_len with
+    it) the index of the token's parent among its request's new tokens, -1 for one that
+    follows the cached tokens; a token comes after its parent.  max_tree: the most
+    drafted tokens of a request, up to 1024.  positions int64 [T] take the place of
+    page_plan's; mask int32 [T, ceil(max_tree / 32)] is for tree_attn."""
+    r = (_native or _load_native()).tree_plan(parent, cu_new, kv_len, max_tree, pos0, out, stream)
+    if r.__class__ is int:
+        raise _error("rsa_tree_plan", r)
+    return TreePlan._make(r) if out is None else out
+
+
+def tree_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, tree_mask, prefix_pages=None, prefix_len: int = 0, out=None,
+              lse=None, workspace=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """prefix_attn for drafted tokens (rsa_tree_attn_fwd): row i of request r's n
+    sees the prefix, the request's own tokens before its drafted ones, and those of
+    its drafted tokens j <= i whose bit (bit j mod 32 of word j // 32) is set in the
+    row of tree_mask, int32 [T, words]; the mask is tree_plan's or the caller's
+    own.  The workspace is prefix_attn's (prefix_attn_workspace_size)."""
+    r = (_native or _load_native()).tree_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, tree_mask, prefix_pages, prefix_len, out,
+                                              lse, workspace, stream)
+    if r.__class__ is int:
+        raise _error("rsa_tree_attn_fwd", r)
+    return r
+
+
+def cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_len, out=None, stream=None) -> torch.Tensor:
+    """Keeps some of each request's newest tokens and closes the gaps
+    (rsa_cache_compact): own token cached_len[r] + i takes the rows of own token
+    cached_len[r] + keep[r, i], i < keep_len[r], in every layer of k_cache and v_cache
+    [n_pages, Hkv, page_size, d] or [layers, n_pages, Hkv, page_size, d].  keep
+    [R, max_keep] int32, strictly ascending in a row's first keep_len[r] entries.
+    Returns the new lengths, int32 [R]: cached_len + keep_len."""
+    r = (_native or _load_native()).cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_len, out, stream)
+    if r.__class__ is int:
+        raise _error("rsa_cache_compact", r)
+    return r[0]
+
+
+def page_fork(k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_start: Optional[torch.Tensor] = None, shares=None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Request dst[f] becomes a copy of request src[f] (rsa_page_fork): with shares
+    [n_pages] int32 (users of a page beyond the first; zeros to begin with) full
+    pages are shared and the partial last one is copied, without every page is.
+    block_table, kv_len and shares are updated in place, rows are copied in every layer
+    of the caches (as in cache_compact); fresh pages come from free_pages as in
+    page_plan.  Returns info, int64 [4]: status (PLAN_STATUS), entries shared, pages
+    taken, first free entry after them.  Forks that cannot all be made change nothing."""
+    r = (_native or _load_native()).page_fork(k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_start, shares, out, stream)
+    if r.__class__ is int:
+        raise _error("rsa_page_fork", r)
+    return r[0]
+
+
+def page_free(block_table, kv_len, keep_len, free_pages, free_start: torch.Tensor, page_size: int, n_pages: int, shares=None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Requests keep their first keep_len [R] of kv_len tokens (0: the request ends)
+    and give the pages behind them back (rsa_page_free): those without another user,
+    by shares if given, go to free_pages before entry free_start[0], ascending.  Returns
+    info, int64 [4]: status (PLAN_STATUS), pages freed, entries given back, the new
+    free_start.  What cannot all be given back changes nothing."""
+    r = (_native or _load_native()).page_free(block_table, kv_len, keep_len, free_pages, free_start, page_size, n_pages, shares, out, stream)
+    if r.__class__ is int:
+        raise _error("rsa_page_free", r)
+    return r[0]

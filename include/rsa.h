@@ -467,7 +467,9 @@ enum {
     RSA_PLAN_BAD_LENGTH = 1,
     RSA_PLAN_TABLE_FULL = 2,
     RSA_PLAN_NO_PAGES = 3,
-    RSA_PLAN_TOO_MANY_TOKENS = 4
+    RSA_PLAN_TOO_MANY_TOKENS = 4,
+    RSA_PLAN_BAD_REQUEST = 5, /* (rsa_page_fork) */
+    RSA_PLAN_NO_ROOM = 6      /* (rsa_page_free) */
 };
 rsa_status rsa_page_plan(const int32_t *cached_len, const int32_t *new_len, int R, int page_size, int64_t n_pages,
                          int32_t *block_table, int64_t table_stride, int max_pages, const int32_t *free_pages,
@@ -585,6 +587,138 @@ rsa_status rsa_prefix_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_
                                size_t ws_bytes, rsa_stream_t stream);
 
 /*
+ * Drafted tokens.  A step may verify a tree of drafted tokens for every request
+ * at once: its new tokens are the tree's, in an order in which a token comes
+ * after its parent.  rsa_page_plan gives them their cache slots as it does any
+ * new tokens, rsa_tree_plan their positions (a token is as far behind the cached
+ * ones as it is deep in the tree) and what each of them sees, rsa_tree_attn_fwd
+ * takes the place of rsa_prefix_attn_fwd, and of the tokens that the model agrees
+ * with rsa_cache_compact moves the rows together; rsa_page_free takes back the
+ * pages behind them.
+ */
+
+/*
+ * Positions and ancestor masks of a step's drafted tokens.  Request r's tokens
+ * are rows [cu_new[r], cu_new[r + 1]) of the step, n of them, the newest of its
+ * kv_len[r] own tokens.  parent[row] is the index among them of the token's
+ * parent, -1 for a token that follows the cached ones (several may), less than
+ * the token's own index i.  Then
+ *   positions[row] = pos0 + kv_len[r] - n + (the number of the token's ancestors)
+ *   mask[row]: bit j (bit j mod 32 of word j / 32) is set for j = i and for
+ *     every ancestor j of the token, and for no other
+ * mask is [T, words]: up to 32 * words tokens a request, words in 1..32.  Rows of
+ * no request (before cu_new[0], from cu_new[R] on: a padded batch) get position 0
+ * and an empty mask.  A parent that is none of -1..i-1 counts as -1, and a token
+ * of index 32 * words or more gets position 0 and an empty mask; both are
+ * reported by rsa_check_device_error.  No output may overlap an input or the
+ * other output.  One launch.
+ */
+rsa_status rsa_tree_plan(const int32_t *parent, int64_t T, const int32_t *cu_new, const int32_t *kv_len, int R, int words,
+                         int64_t pos0, int64_t *positions, uint32_t *mask, rsa_stream_t stream);
+
+/*
+ * rsa_prefix_attn_fwd for drafted tokens: row i of request r's n sees
+ *   the whole prefix,
+ *   its request's own tokens [0, kv_len[r] - n), and
+ *   own token kv_len[r] - n + j for every j <= i whose bit is set in the row's mask
+ * (mask [T, words], rows mask_stride words apart; bits past 32 * words count as not
+ * set).  The mask may be any: rsa_tree_plan's, or a caller's own in which a row
+ * does not see itself, or nothing.  All else is as for rsa_prefix_attn_fwd, whose
+ * workspace size is this call's too.
+ */
+rsa_status rsa_tree_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
+                             const void *v_cache, rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int page_size,
+                             int64_t n_pages, const int32_t *cu_q, const int32_t *kv_len, int R,
+                             const int32_t *block_table, int64_t table_stride, int max_pages,
+                             const int32_t *prefix_pages, int64_t prefix_len, const uint32_t *mask, int64_t mask_stride,
+                             int words, void *out, float *lse, void *workspace, size_t ws_bytes, rsa_stream_t stream);
+
+/*
+ * The caches of several layers that share their block tables, for the two calls
+ * below, which move rows of all of them in one launch: k_cache and v_cache
+ * [layers, n_pages, Hkv, page_size, d] (a layer's part is what the other calls
+ * take).
+ */
+typedef struct {
+    void *k_cache, *v_cache;
+    rsa_dtype dt;
+    int layers;
+    int64_t n_pages;
+    int Hkv, page_size, d;
+} rsa_cache;
+
+/*
+ * Keeps some of each request's newest tokens and closes the gaps: own token
+ * cached_len[r] + i takes the rows of own token cached_len[r] + keep[r][i], for i in
+ * [0, keep_len[r]), and new_len[r] = cached_len[r] + keep_len[r].  keep is
+ * [R, max_keep], rows keep_stride apart, a row's first keep_len[r] entries strictly
+ * ascending in [0, kv_len[r] - cached_len[r]): the accepted tokens of a drafted tree,
+ * or what is to be kept of a long cache.  Rows behind new_len[r] keep what they
+ * hold or held.  A request whose lengths, list or pages are outside their ranges is
+ * left as it is, with new_len[r] = cached_len[r], and is reported by
+ * rsa_check_device_error.  The pages that rows move within are the request's
+ * own: no other request's moves may touch them in the same call.  Keys are moved
+ * as they are, rotated for the position that they had: right for accepted
+ * tokens, whose positions were those already.  No buffer written may overlap
+ * another operand.  One launch.
+ */
+rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table, int64_t table_stride, int max_pages,
+                             const int32_t *cached_len, const int32_t *kv_len, int R, const int32_t *keep,
+                             int64_t keep_stride, int max_keep, const int32_t *keep_len, int32_t *new_len,
+                             rsa_stream_t stream);
+
+/*
+ * Pages that several requests' tables share are counted in shares [n_pages]: for
+ * each page the number of its users beyond the first, 0 for a page that one
+ * request has for itself (what rsa_page_plan hands out is, so it needs no
+ * counts).  A shared page is not written again: rsa_page_fork shares full ones
+ * alone.  (A request that is cut back into a shared page and then grows would
+ * write to it: fork it first.)
+ *
+ * Forks: for f in [0, F) request dst[f] becomes a copy of request src[f], whose
+ * kv_len[src[f]] tokens lie in ceil(kv_len / page_size) pages.
+ *   - with shares, dst's row of block_table gets src's full pages, each counted once
+ *     more, and for a partial last page a fresh one with the same rows;
+ *   - without (NULL) a fresh page for every page, with the same rows;
+ *   - kv_len[dst[f]] = kv_len[src[f]].
+ * Fresh pages are the next entries of free_pages from entry *free_start on (0 if
+ * free_start is NULL), in the forks' order.  The rows are copied in all layers.  What
+ * dst's row held before is not freed.  dst has no request twice and none that is in
+ * src; src may name a request several times.
+ *   info [4]: status, entries shared, pages taken, first free entry after them.
+ * Forks that cannot all be made change nothing: RSA_PLAN_BAD_REQUEST (a request
+ * outside [0, R), or twice in dst, or in both), RSA_PLAN_BAD_LENGTH (kv_len of a
+ * source negative or beyond its row), RSA_PLAN_NO_PAGES; the first that
+ * applies.  A page id outside [0, n_pages) in a source's row is copied, but neither
+ * counted nor its rows copied; it and such an entry of free_pages are reported
+ * by rsa_check_device_error.  No buffer written may overlap another operand.  R at
+ * most 16384.  One launch.
+ */
+rsa_status rsa_page_fork(const rsa_cache *cache, int32_t *block_table, int64_t table_stride, int max_pages, int32_t *kv_len,
+                         int R, const int32_t *src, const int32_t *dst, int F, const int32_t *free_pages, int64_t n_free,
+                         const int64_t *free_start, int32_t *shares, int64_t *info, rsa_stream_t stream);
+
+/*
+ * Requests that end or are cut back give their pages back: request r, with
+ * kv_len[r] tokens, keeps its first keep_len[r] (0: it ends), and entries
+ * [ceil(keep_len / P), ceil(kv_len / P)) of its row of block_table are given
+ * back.  A page given back as often as it has users (once, without shares; else
+ * shares + 1 times) is free; a shared one is counted down.  The n pages that
+ * become free are written to free_pages [start - n, start), in ascending order,
+ * with start = *free_start: entries that rsa_page_plan has taken before.
+ *   info [4]: status, pages freed, entries given back, start - n (the next step's
+ * free_start).  Status RSA_PLAN_BAD_LENGTH (not 0 <= keep_len <= kv_len, or kv_len
+ * beyond the row) or RSA_PLAN_NO_ROOM (start is not in [n, n_free]): nothing is
+ * changed.  An id outside [0, n_pages) is skipped, and a page given back more often
+ * than it has users is freed once; both are reported by rsa_check_device_error.  Rows
+ * of block_table stay as they are.  No buffer written may overlap another operand.
+ * At most 16384 requests and 2^23 pages.  One launch.
+ */
+rsa_status rsa_page_free(const int32_t *block_table, int64_t table_stride, int max_pages, const int32_t *kv_len,
+                         const int32_t *keep_len, int R, int page_size, int64_t n_pages, int32_t *free_pages, int64_t n_free,
+                         const int64_t *free_start, int32_t *shares, int64_t *info, rsa_stream_t stream);
+
+/*
  * Two-pass Ring Self-Attention ([P3] "How It Works", steps 1-2), the form that
  * keeps whole score rows: for each query chunk n in turn, the score pass
  * visits the key chunks in ring order (n - r) mod N and fills the full score
@@ -665,7 +799,10 @@ int rsa_debug_checks(void);
  * that only the device sees.  The text gives the site code and the index of one
  * failure, the first to be recorded.  Site codes of index data: 0x90 a page id in
  * rsa_page_plan; 0x91 a position, 0x92 a slot; 0x93 cu_q, 0x94 kv_len, 0x95 a
- * page id in rsa_prefix_attn_fwd.
+ * page id in rsa_prefix_attn_fwd and rsa_tree_attn_fwd; 0x96 cu_new, 0x97 kv_len, 0x98
+ * a parent, 0x99 the index of a token past the mask in rsa_tree_plan; 0x9a a length, 0x9b
+ * an entry of keep, 0x9c a page id in rsa_cache_compact; 0x9d a page id in
+ * rsa_page_fork; 0x9e a page id, 0x9f a page given back too often in rsa_page_free.
  */
 rsa_status rsa_check_device_error(rsa_stream_t stream);
 
