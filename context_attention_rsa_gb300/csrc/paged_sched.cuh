@@ -10,8 +10,7 @@
 // All tiles of all units lie on one line: segments in order, in a segment the
 // key heads, in a head the token groups, in a unit its tiles.  A tile takes
 // light_tile places, or heavy_tile where its unit has many rows, and a unit
-// kUnitCost places before its first tile, for what it costs to begin and to end
-// one, so that a place takes about the same time everywhere.  The line is cut
+// some places before its first tile, for what it costs to begin and to end one, so that a place takes about the same time everywhere.  The line is cut
 // into `workers` equal stretches, one for each CTA, so that one long request,
 // many short ones and a prefix all fill the GPU alike.  The tiles of a unit that
 // begin in a stretch are a piece; it leaves a partial (o, lse) for its rows: in
@@ -31,19 +30,17 @@ namespace rsa {
 namespace paged {
 
 constexpr int kTileKeys = 128;
-constexpr int kUnitCost = 3;
-
 struct Segment {
     int tok0, ntok;        // its query tokens
     int keys;              // its keys
     const int32_t *pages;  // their pages
     int groups, tiles;     // token groups; key tiles of a unit
     int see0;              // token i of the segment sees keys [0, min(keys, see0 + i)): all of the prefix
-    int cost;              // places of a tile
+    int cost, unit;        // places of a tile; of a unit before its first one
     int64_t line;          // places on the line
 
     // (below 2^26: fewer than 2^24 tiles of 128 keys)
-    __device__ __forceinline__ int unit_line() const { return tiles * cost + kUnitCost; }
+    __device__ __forceinline__ int unit_line() const { return tiles * cost + unit; }
 };
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
@@ -78,6 +75,7 @@ __device__ __forceinline__ Segment segment(const PrefixAttnParams &p, int s, boo
     g.groups = (int)(((int64_t)g.ntok + p.unit_tokens - 1) / p.unit_tokens);
     g.tiles = (int)(((int64_t)g.keys + kTileKeys - 1) / kTileKeys);
     g.cost = g.ntok > p.light_tokens ? p.heavy_tile : p.light_tile;
+    g.unit = p.unit + (min(g.ntok, p.unit_tokens) * p.G >> p.unit_shift);
     g.line = g.tiles > 0 ? (int64_t)g.groups * p.Hkv * g.unit_line() : 0;
     return g;
 }
@@ -203,6 +201,7 @@ struct Batch {
         g.tiles = __shfl_sync(0xffffffffu, mine.tiles, from);
         g.see0 = __shfl_sync(0xffffffffu, mine.see0, from);
         g.cost = __shfl_sync(0xffffffffu, mine.cost, from);
+        g.unit = __shfl_sync(0xffffffffu, mine.unit, from);
         g.line = __shfl_sync(0xffffffffu, mine.line, from);
         return g;
     }
@@ -231,7 +230,7 @@ struct Walk {
     // The first tile that begins at place `u` of the unit or later.
     __device__ __forceinline__ int first_tile(int u) const
     {
-        return u <= kUnitCost ? 0 : (u - kUnitCost + g.cost - 1) / g.cost;
+        return u <= g.unit ? 0 : (u - g.unit + g.cost - 1) / g.cost;
     }
     __device__ __forceinline__ bool next(const PrefixAttnParams &p, Piece &x)
     {

@@ -27,10 +27,12 @@
 // 100000 keys that took 68.
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <cmath>
 
 #include "paged_sched.cuh"
 #include "ptx_sm103.cuh"
+#include "tc_common.cuh"
 
 namespace rsa {
 namespace {
@@ -41,7 +43,6 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = kJoinWarps * 32;
-constexpr int kAhead = 4;             // partial rows that a joining warp has in flight
 constexpr int kRows = 128;            // rows of a unit
 constexpr int kWarpRows = 8;
 constexpr int kKeys = 32;             // keys of a block
@@ -62,8 +63,27 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-__device__ __forceinline__ void store(float *p, float x) { *p = x; }
-__device__ __forceinline__ void store(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+// 2 or 4 values side by side.
+template <int N>
+__device__ __forceinline__ void store(float *p, const float (&x)[N])
+{
+    if constexpr (N == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+}
+template <int N>
+__device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[N])
+{
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+        w[i] = tc::pack_bf16(x[2 * i], x[2 * i + 1]);
+    if constexpr (N == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+}
 
 // 16 bytes to shared memory; zeros if not `there`.
 __device__ __forceinline__ void copy_async(void *dst, const void *src, bool there)
@@ -386,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
 __device__ __forceinline__ int request_of(const PrefixAttnParams &p, int token)
 {
     const int lane = threadIdx.x & 31;
-    if (token >= p.cu_q[p.R])
+    if (token >= p.cu_q[p.R] || token < p.cu_q[0])
         return -1;
     int64_t lo = 0, n = p.R;  // the answer is in [lo, lo + n)
     while (n > 1) {
@@ -394,7 +414,7 @@ __device__ __forceinline__ int request_of(const PrefixAttnParams &p, int token)
         const bool below = lane * step < n && p.cu_q[lo + lane * step] <= token;
         const unsigned vote = __ballot_sync(0xffffffffu, below);
         if (!vote)
-            return -1;  // (rows before cu_q[0])
+            return -1;  // (only where cu_q does not ascend)
         const int k = 31 - __clz(vote);
         n = min(step, n - k * step);
         lo += k * step;
@@ -402,16 +422,193 @@ __device__ __forceinline__ int request_of(const PrefixAttnParams &p, int token)
     return (int)lo;
 }
 
-// A row's pieces in one segment: its home, then one slot for each worker after the first.
+// The same for each lane's own token, by two levels of 32: every 32nd part's first row and
+// then, of each lane's part, its own.
+__device__ __forceinline__ int lane_request_of(const PrefixAttnParams &p, int token)
+{
+    const int lane = threadIdx.x & 31;
+    if (!__any_sync(0xffffffffu, token < p.cu_q[p.R]))
+        return -1;
+    int64_t lo = 0, n = p.R;  // this lane's answer is in [lo, lo + n)
+    // the first level is the same for all lanes: they read its 32 rows together
+    const int64_t step = (n + 31) / 32;
+    const int begin = lane * step < n ? p.cu_q[lane * step] : INT_MAX;
+    int part = -1;
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        part += __shfl_sync(0xffffffffu, begin, k) <= token;
+    const bool there = part >= 0 && token < p.cu_q[p.R];
+    lo = max(part, 0) * step;
+    n = min(step, n - lo);
+    while (n > 1) {  // (with up to 1024 requests five reads of a few lines)
+        const int64_t half = (n + 1) / 2;
+        if (p.cu_q[lo + half] <= token)
+            lo += half, n -= half;
+        else
+            n = half;
+    }
+    return there ? (int)lo : -1;
+}
+
+// Places of the line before request r's segment and in all, where the R < 32 requests'
+// segments are a lane each: follows from the lengths alone, so a warp can work it out
+// while the attention launch still computes (2 us less for a short call).  With more
+// requests that would cost every warp a scan, and it takes the sums that worker 0 has left.
+struct Line {
+    int64_t upto, total;  // of segments [0, lane]
+
+    __device__ __forceinline__ explicit Line(const PrefixAttnParams &p)
+    {
+        const int lane = threadIdx.x & 31;
+        upto = lane <= p.R ? segment(p, lane).line : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += y;
+        }
+        total = __shfl_sync(0xffffffffu, upto, 31);
+    }
+};
+
+// The pieces of one key head's rows of a token in one segment: their home, then one
+// slot for each worker after the first.
 struct Pieces {
-    const float *o, *lse;  // home
-    int64_t slot;          // row of the first slot; the next are kPrefixUnitRows apart
+    int64_t slot;  // row of the first query head's first slot; the next worker's are kPrefixUnitRows further
     int n;
 };
 
-// kParts warps a row (token, query head), each with a run of its pieces.  Lane i
-// brings the lse of piece i, so that all of them are in flight together, and with
-// them the first rows of o.  Lane c owns columns [c * PER, (c + 1) * PER).
+// Segment g, which begins at place `at` of the line.
+__device__ __forceinline__ Pieces pieces_of(const PrefixAttnParams &p, const Segment &g, int64_t at, int token, int head, int64_t share)
+{
+    const int i = token - g.tok0;
+    if (g.line == 0 || i < 0 || i >= g.ntok)  // (outside: only where cu_q does not ascend)
+        return Pieces{0, 0};
+    const int64_t unit = (int64_t)head * g.groups + i / p.unit_tokens;
+    at += unit * g.unit_line() + g.unit;  // the unit's first tile
+    const int64_t w0 = at / share, w1 = (at + (int64_t)(g.tiles - 1) * g.cost) / share;
+    return Pieces{(w0 + 1) * kPrefixUnitRows + (i % p.unit_tokens) * p.G, (int)(w1 - w0) + 1};
+}
+
+// Where piece i of a row lies: (o, lse).
+struct Locate {
+    const PrefixAttnParams &p;
+    int64_t row;
+    int g;          // query head within the key head
+    Pieces pc[2];   // prefix, own
+
+    __device__ __forceinline__ void operator()(int i, int d, const float *&o, const float *&lse) const
+    {
+        const int s = i >= pc[0].n;
+        const int k = i - (s ? pc[0].n : 0);
+        const int64_t slot = (s ? pc[1].slot : pc[0].slot) + g + (int64_t)(k - 1) * kPrefixUnitRows;
+        o = k == 0 ? (s ? p.home_o[1] : p.home_o[0]) + row * d : p.slot_o + slot * d;
+        lse = k == 0 ? (s ? p.home_lse[1] : p.home_lse[0]) + row : p.slot_lse + slot;
+    }
+};
+
+// Pieces [from, end) of kR rows that follow one another, for the whole warp.  Lane i brings
+// the rows' lse of piece i, so that all of them are in flight together, and with them the first
+// kAhead rows of o.  Lane c owns columns [c * PER, (c + 1) * PER).
+template <int D, int kR, int kAhead>
+struct Fold {
+    static constexpr int PER = D / 32;
+    float M[kR], L[kR], acc[kR][PER];
+
+    __device__ __forceinline__ void pieces(int from, int end, const Locate &locate)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int q = 0; q < kR; ++q) {
+            M[q] = -INFINITY;
+            L[q] = 0.f;
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                acc[q][c] = 0.f;
+        }
+        for (int i0 = from; i0 < end; i0 += 32) {
+            const int m = min(32, end - i0);
+            const float *o = nullptr, *at = nullptr;
+            float lse[kR];
+            if (lane < m)
+                locate(i0 + lane, D, o, at);
+#pragma unroll
+            for (int q = 0; q < kR; ++q)
+                lse[q] = lane < m ? at[q] : -INFINITY;
+            // The first rows of o are under way before their weights are known, kAhead at a time.
+            float v[kAhead][kR][PER];
+            auto fetch_rows = [&](int i) {
+#pragma unroll
+                for (int e = 0; e < kAhead; ++e) {
+                    const float *oi = reinterpret_cast<const float *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (i + e) & 31));
+                    if (i + e >= m)
+                        continue;
+#pragma unroll
+                    for (int q = 0; q < kR; ++q) {
+                        if constexpr (PER == 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(oi + q * D + lane * 4);
+                            v[e][q][0] = x.x, v[e][q][1] = x.y, v[e][q][2] = x.z, v[e][q][3] = x.w;
+                        } else {
+                            const float2 x = *reinterpret_cast<const float2 *>(oi + q * D + lane * 2);
+                            v[e][q][0] = x.x, v[e][q][1] = x.y;
+                        }
+                    }
+                }
+            };
+            fetch_rows(0);
+            float w[kR];
+#pragma unroll
+            for (int q = 0; q < kR; ++q) {
+                const float mn = fmaxf(M[q], warp_max(lse[q]));
+                const float base = mn == -INFINITY ? 0.f : mn;
+                const float a = expf(M[q] - base);
+                w[q] = expf(lse[q] - base);
+                L[q] = L[q] * a + warp_sum(w[q]);
+                M[q] = mn;
+#pragma unroll
+                for (int c = 0; c < PER; ++c)
+                    acc[q][c] *= a;
+            }
+#pragma unroll 1
+            for (int i = 0;;) {
+#pragma unroll
+                for (int e = 0; e < kAhead; ++e)
+#pragma unroll
+                    for (int q = 0; q < kR; ++q) {
+                        const float wi = __shfl_sync(0xffffffffu, w[q], (i + e) & 31);
+                        if (i + e < m)
+#pragma unroll
+                            for (int c = 0; c < PER; ++c)
+                                acc[q][c] = fmaf(wi, v[e][q][c], acc[q][c]);
+                    }
+                i += kAhead;
+                if (i >= m)
+                    break;
+                fetch_rows(i);
+            }
+        }
+    }
+    template <class E>
+    __device__ __forceinline__ void write(const PrefixAttnParams &p, int64_t row) const
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int q = 0; q < kR; ++q) {
+            const bool empty = !(L[q] > 0.f) && L[q] == L[q];  // (a NaN stays one)
+            const float inv = empty ? 0.f : 1.f / L[q];
+            float y[PER];
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                y[c] = acc[q][c] * inv;
+            store(static_cast<E *>(p.out) + (row + q) * D + lane * PER, y);
+            if (lane == 0)
+                p.lse[row + q] = empty ? -INFINITY : M[q] + logf(L[q]);
+        }
+    }
+};
+
+// Few rows: kParts warps a row (token, query head), each with a run of its pieces.
 template <class E, int D, int kParts>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ PrefixAttnParams p)
 {
@@ -424,122 +621,41 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     const int hq = (int)(row - (int64_t)token * p.Hq), head = hq / p.G;
     const int r = request_of(p, token);
     const Segment g[2] = {segment(p, 0), r < 0 ? Segment() : segment(p, 1 + r)};
-    // Where the row's pieces are follows from the lengths alone.  With up to 31
-    // requests, one segment a lane, the warp works it out itself, all of it while the
-    // attention launch still computes (2 us less for a short call); with more that
-    // would cost every row a scan, and it takes the sums that worker 0 has left.
-    int64_t total, before = 0;
+    int64_t total, before;
     const bool few = p.R < 32;
     if (few) {
-        const int64_t line = lane <= p.R ? segment(p, lane).line : 0;
-        total = line;
-        before = lane <= r ? line : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-        }
+        const Line line(p);
+        total = line.total;
+        before = __shfl_sync(0xffffffffu, line.upto, max(r, 0));
     } else {
         ptx::wait_for_launch_before();
         total = p.plan[p.R + 1];
         before = p.plan[1 + max(r, 0)];
     }
     const int64_t share = share_of(p, total);
-    bool whole = false;
-    Pieces pc[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        pc[s].n = 0;
-        const int i = token - g[s].tok0;
-        if (r < 0 || g[s].line == 0 || i < 0 || i >= g[s].ntok)
-            continue;  // (outside: only where cu_q does not ascend)
-        const int64_t unit = (int64_t)head * g[s].groups + i / p.unit_tokens;
-        const int64_t at = (s == 0 ? 0 : before) + unit * g[s].unit_line() + kUnitCost;  // the unit's first tile
-        const int64_t w0 = at / share, w1 = (at + (int64_t)(g[s].tiles - 1) * g[s].cost) / share;
-        whole = s == 1 && w0 == w1 && p.prefix_len == 0;
-        pc[s].o = p.home_o[s] + row * D;
-        pc[s].lse = p.home_lse[s] + row;
-        pc[s].slot = (w0 + 1) * kPrefixUnitRows + (i % p.unit_tokens) * p.G + (hq - head * p.G);
-        pc[s].n = (int)(w1 - w0) + 1;
+    Locate locate{p, row, hq - head * p.G, {{0, 0}, {0, 0}}};
+    if (r >= 0) {
+        locate.pc[0] = pieces_of(p, g[0], 0, token, head, share);
+        locate.pc[1] = pieces_of(p, g[1], before, token, head, share);
     }
     // Every thread waits, also where it has nothing to join: the launch after this one
     // waits only for this one.
     if (few)
         ptx::wait_for_launch_before();
-    if (r < 0 || whole)
+    if (r < 0 || (locate.pc[1].n == 1 && p.prefix_len == 0))
         return;  // a row behind the last request stays as it is; a single piece went straight to out
-    const int n = pc[0].n + pc[1].n, run = (n + kParts - 1) / kParts, end = min(n, (part + 1) * run);
-    auto locate = [&](int i, const float *&o, const float *&lse) {  // piece i of the row
-        const int s = i >= pc[0].n;
-        const int k = i - (s ? pc[0].n : 0);
-        const int64_t slot = (s ? pc[1].slot : pc[0].slot) + (int64_t)(k - 1) * kPrefixUnitRows;
-        o = k == 0 ? (s ? pc[1].o : pc[0].o) : p.slot_o + slot * D;
-        lse = k == 0 ? (s ? pc[1].lse : pc[0].lse) : p.slot_lse + slot;
-    };
-    float M = -INFINITY, L = 0.f, acc[PER];
-#pragma unroll
-    for (int c = 0; c < PER; ++c)
-        acc[c] = 0.f;
-    for (int i0 = part * run; i0 < end; i0 += 32) {
-        const int m = min(32, end - i0);
-        const float *o = nullptr, *at = nullptr;
-        float lse = -INFINITY;
-        if (lane < m) {
-            locate(i0 + lane, o, at);
-            lse = *at;
-        }
-        // The first rows of o are under way before their weights are known, kAhead at a time.
-        float v[kAhead][PER];
-        auto fetch_rows = [&](int i) {
-#pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
-                const float *oi = reinterpret_cast<const float *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (i + e) & 31));
-                if (i + e >= m)
-                    continue;
-                if constexpr (PER == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(oi + lane * 4);
-                    v[e][0] = x.x, v[e][1] = x.y, v[e][2] = x.z, v[e][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(oi + lane * 2);
-                    v[e][0] = x.x, v[e][1] = x.y;
-                }
-            }
-        };
-        fetch_rows(0);
-        const float mn = fmaxf(M, warp_max(lse));
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float w = expf(lse - base), a = expf(M - base);
-        L = L * a + warp_sum(w);
-        M = mn;
-#pragma unroll
-        for (int c = 0; c < PER; ++c)
-            acc[c] *= a;
-#pragma unroll 1
-        for (int i = 0;;) {
-#pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
-                const float wi = __shfl_sync(0xffffffffu, w, (i + e) & 31);
-                if (i + e < m)
-#pragma unroll
-                    for (int c = 0; c < PER; ++c)
-                        acc[c] = fmaf(wi, v[e][c], acc[c]);
-            }
-            i += kAhead;
-            if (i >= m)
-                break;
-            fetch_rows(i);
-        }
-    }
+    const int n = locate.pc[0].n + locate.pc[1].n, run = (n + kParts - 1) / kParts, end = min(n, (part + 1) * run);
+    Fold<D, 1, 4> f;
+    f.pieces(part * run, end, locate);
     if constexpr (kParts > 1) {
         __shared__ float s_part[kJoinWarps][D + 2];
         if (part > 0) {
 #pragma unroll
             for (int c = 0; c < PER; ++c)
-                s_part[warp][lane * PER + c] = acc[c];
+                s_part[warp][lane * PER + c] = f.acc[0][c];
             if (lane == 0) {
-                s_part[warp][D] = M;
-                s_part[warp][D + 1] = L;
+                s_part[warp][D] = f.M[0];
+                s_part[warp][D + 1] = f.L[0];
             }
         }
         // (named barriers of one row's warps: another row's may have returned)
@@ -547,25 +663,93 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         if (part > 0)
             return;
 #pragma unroll
-        for (int g = 1; g < kParts; ++g) {
-            const float *w = s_part[warp + g];
-            const float mn = fmaxf(M, w[D]), base = mn == -INFINITY ? 0.f : mn;
-            const float a = expf(M - base), b = expf(w[D] - base);
-            M = mn;
-            L = L * a + w[D + 1] * b;
+        for (int i = 1; i < kParts; ++i) {
+            const float *w = s_part[warp + i];
+            const float mn = fmaxf(f.M[0], w[D]), base = mn == -INFINITY ? 0.f : mn;
+            const float a = expf(f.M[0] - base), b = expf(w[D] - base);
+            f.M[0] = mn;
+            f.L[0] = f.L[0] * a + w[D + 1] * b;
 #pragma unroll
             for (int c = 0; c < PER; ++c)
-                acc[c] = acc[c] * a + w[lane * PER + c] * b;
+                f.acc[0][c] = f.acc[0][c] * a + w[lane * PER + c] * b;
         }
     }
-    const bool empty = !(L > 0.f) && L == L;  // (a NaN stays one)
-    const float inv = empty ? 0.f : 1.f / L;
-    E *out = static_cast<E *>(p.out) + row * D + lane * PER;
-#pragma unroll
-    for (int c = 0; c < PER; ++c)
-        store(out + c, acc[c] * inv);
-    if (lane == 0)
-        p.lse[row] = empty ? -INFINITY : M + logf(L);
+    f.template write<E>(p, row);
+}
+
+// Many rows: an item is up to kJoinRows rows of a (token, key head), and a warp takes every
+// so-manieth.  Where the pieces of its next 32 items lie its lanes work out at once: done row
+// by row, that search and its divisions took most of the launch's time (46080 rows of 3
+// pieces 56 us, 622592 rows with nothing to join 365 us).
+template <class E, int D, int kJoinRows, int kAhead, int kBlocks>
+__global__ void __launch_bounds__(kJoinThreads, kBlocks) prefix_join_rows_kernel(const __grid_constant__ PrefixAttnParams p)
+{
+    const int lane = threadIdx.x & 31, cuts = (p.G + kJoinRows - 1) / kJoinRows;
+    const int64_t items = p.T * p.Hkv * cuts, warps = (int64_t)gridDim.x * kJoinWarps;
+    const int64_t first = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const bool few = p.R < 32;
+    int64_t upto = 0, total = 0;
+    if (few) {
+        const Line line(p);
+        upto = line.upto;
+        total = line.total;
+    }
+    const Segment prefix = segment(p, 0);
+    bool waited = false;
+    for (int64_t i0 = first; i0 < items; i0 += 32 * warps) {
+        const int64_t item = i0 + lane * warps;
+        const bool there = item < items;
+        const int64_t head_row = (there ? item : items - 1) / cuts;  // token * Hkv + head
+        const int g0 = (int)((there ? item : items - 1) - head_row * cuts) * kJoinRows;
+        const int token = (int)(head_row / p.Hkv), head = (int)(head_row - (int64_t)token * p.Hkv);
+        const int r = lane_request_of(p, token);
+        const Segment g = segment(p, 1 + max(r, 0));
+        int64_t before;
+        if (few) {
+            before = __shfl_sync(0xffffffffu, upto, max(r, 0));
+        } else {
+            if (!waited)
+                ptx::wait_for_launch_before();
+            waited = true;
+            total = p.plan[p.R + 1];
+            before = p.plan[1 + max(r, 0)];
+        }
+        const int64_t share = share_of(p, total);
+        Pieces pre{0, 0}, own{0, 0};
+        if (r >= 0) {
+            pre = pieces_of(p, prefix, 0, token, head, share);
+            own = pieces_of(p, g, before, token, head, share);
+        }
+        if (!waited)
+            ptx::wait_for_launch_before();
+        waited = true;
+        // (rows behind the last request stay as they are; a single piece went straight to out)
+        const unsigned todo = __ballot_sync(0xffffffffu, there && r >= 0 && !(own.n == 1 && p.prefix_len == 0));
+#pragma unroll 1
+        for (unsigned left = todo; left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const int64_t row0 = __shfl_sync(0xffffffffu, head_row * p.G + g0, k);
+            Locate locate{p, row0, __shfl_sync(0xffffffffu, g0, k),
+                          {{__shfl_sync(0xffffffffu, pre.slot, k), __shfl_sync(0xffffffffu, pre.n, k)},
+                           {__shfl_sync(0xffffffffu, own.slot, k), __shfl_sync(0xffffffffu, own.n, k)}}};
+            const int n = locate.pc[0].n + locate.pc[1].n;
+            int rows = min(kJoinRows, p.G - locate.g);
+            if (rows == kJoinRows) {
+                Fold<D, kJoinRows, kAhead> f;
+                f.pieces(0, n, locate);
+                f.template write<E>(p, locate.row);
+                continue;
+            }
+#pragma unroll 1
+            for (; rows > 0; --rows, ++locate.g, ++locate.row) {
+                Fold<D, 1, 4> f;
+                f.pieces(0, n, locate);
+                f.template write<E>(p, locate.row);
+            }
+        }
+    }
+    if (!waited)
+        ptx::wait_for_launch_before();
 }
 
 template <int D>
@@ -574,6 +758,8 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
     PrefixAttnParams p = p_in;
     p.unit_tokens = p.light_tokens = kRows / p.G;
     p.light_tile = p.heavy_tile = 2;
+    p.unit = 3;
+    p.unit_shift = 31;
     auto kernel = p.mask ? prefix_attn_f32_kernel<D, true> : prefix_attn_f32_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)
@@ -583,13 +769,10 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
     return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }
 
-template <class E, int D, int kParts>
-cudaError_t join(const PrefixAttnParams &p, cudaStream_t s)
+// The launch begins while the attention still computes.
+template <class K, class... A>
+cudaError_t launch_early(K kernel, int64_t blocks, cudaStream_t s, const A &...args)
 {
-    constexpr int kRowsPerBlock = kJoinWarps / kParts;
-    const int64_t blocks = (p.T * p.Hq + kRowsPerBlock - 1) / kRowsPerBlock;
-    if (blocks > 0x7fffffffLL)
-        return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
@@ -599,16 +782,28 @@ cudaError_t join(const PrefixAttnParams &p, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_join_kernel<E, D, kParts>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class E, int D, int kJoinRows, int kAhead, int kBlocks>
+cudaError_t join_rows(const PrefixAttnParams &p, cudaStream_t s)
+{
+    const int64_t items = p.T * p.Hkv * ((p.G + kJoinRows - 1) / kJoinRows), blocks = (items + kJoinWarps - 1) / kJoinWarps;
+    return launch_early(prefix_join_rows_kernel<E, D, kJoinRows, kAhead, kBlocks>, blocks < 152 * kBlocks ? blocks : 152 * kBlocks, s, p);
 }
 
 // Up to a row for each SM: four warps a row, since the fewer the rows, the more pieces
 // has each (19 pieces a row in 64 rows, a call of 24.7 us takes 22.4; with 5 pieces a
-// row in 256 it would take 20.0 instead of 19.1).
+// row in 256 it would take 20.0 instead of 19.1).  Then a row a warp while the SMs hold
+// them at once, else four rows together, for the loads in flight.
 template <class E, int D>
 cudaError_t join_any(const PrefixAttnParams &p, cudaStream_t s)
 {
-    return p.T * p.Hq <= 152 ? join<E, D, 4>(p, s) : join<E, D, 1>(p, s);
+    constexpr int kParts = 4;
+    const int64_t rows = p.T * p.Hq;
+    if (rows <= 152)
+        return launch_early(prefix_join_kernel<E, D, kParts>, (rows * kParts + kJoinWarps - 1) / kJoinWarps, s, p);
+    return rows <= 152 * 24 ? join_rows<E, D, 1, 4, 3>(p, s) : join_rows<E, D, 4, 3, 2>(p, s);
 }
 
 }  // namespace

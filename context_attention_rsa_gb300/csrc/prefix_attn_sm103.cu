@@ -78,10 +78,11 @@ using namespace paged;
 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;  // log2 units the maximum may rise before O is rescaled
-// Places of a key tile (kUnitCost for a unit): a step of two row tiles takes 1.5 us, of
+// Places of a key tile (kUnit for a unit): a step of two row tiles takes 1.5 us, of
 // one 1.0, a short unit some 1.5 more.  Other weights (4:2:3, 3:3:4, 6:4:5, 4:4:6 for unit,
 // one and two row tiles) move single batches by up to 10 % either way and none all.
-constexpr int kLightTile = 2, kHeavyTile = 3;
+constexpr int kLightTile = 2, kHeavyTile = 3, kUnit = 3;
+constexpr int kTreeUnit = 6, kTreeUnitShift = 5;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // A piece as the producer hands it to the other roles.
@@ -893,6 +894,8 @@ cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
     p.light_tokens = TT;
     p.light_tile = kLightTile;
     p.heavy_tile = kHeavyTile;
+    p.unit = p.mask ? kTreeUnit : kUnit;
+    p.unit_shift = p.mask ? kTreeUnitShift : 31;
     CUtensorMap mq, mk, mv, mk8, mv8;
     const uint64_t page = 1ull << p.page_shift, heads = (uint64_t)(p.n_pages * p.Hkv), halves = D / 64;
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.T};

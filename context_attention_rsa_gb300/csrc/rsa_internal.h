@@ -215,6 +215,7 @@ struct PrefixAttnParams {
     int unit_tokens;             // query tokens of a unit at most
     int light_tokens;            // a unit of more tokens than this costs heavy_tile places a key tile, else light_tile
     int light_tile, heavy_tile;
+    int unit, unit_shift;        // places of a unit before its first tile: unit + (rows >> unit_shift)
     uint64_t wait_limit_ns;
     unsigned int *err;
 };
@@ -260,6 +261,7 @@ struct CompactParams {
 };
 
 // Forks of requests (rsa_page_fork).
+constexpr int kPageForkMost = 8192;
 struct PageForkParams {
     CacheLayers c;
     int32_t *block_table;

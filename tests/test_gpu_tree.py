@@ -191,15 +191,17 @@ def test_random_trees(dtype, seed):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("case", [c for c in CASES if c[7] == BF and c[5] == 128][:9], ids=lambda c: f"n{sum(c[0])}P{c[2]}")
-def test_a_chain_has_the_bits_of_the_causal_attention(case, d):
-    # every token the child of the one before, and a mask of ones (bits of later tokens are none of a row's)
+def test_a_chain_sees_what_the_causal_attention_sees(case, d):
+    # every token the child of the one before, and a mask of ones (bits of later tokens are none of a row's): the causal
+    # definition, and the same bits whichever way it is said
     need_cuda()
     case = (*case[:5], d, *case[6:])
-    want = Batch(*case).run()
+    want, n, first = Batch(*case).reference(), int(sum(case[0])), None
     for kw in (dict(width=1), dict(mask=-1), dict(mask=-1, words=32)):
         got = TreeBatch(*case, **kw).run()
-        n = int(sum(case[0]))
-        assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:n], want[1][:n])
+        ref.assert_prefix_attn(*got, want, BF, n)
+        first = first or got
+        assert torch.equal(got[0][:n], first[0][:n]) and torch.equal(got[1][:n], first[1][:n])
     rsa.check_device_error()
 
 
@@ -214,6 +216,26 @@ def test_rows_that_see_nothing_and_rows_behind_the_batch(dtype):
         assert (out[13:] == 7).all() and (lse[13:] == 8).all()
         if prefix == 0 and lens[0] == 6:
             assert torch.isneginf(lse[:13]).all() and (out[:13] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
+@pytest.mark.parametrize("rows", [2, 60, 900])
+def test_one_request_whose_rows_begin_later(dtype, rows):
+    # rows before the first request are none of its, with one request as with several
+    need_cuda()
+    for cls in (Batch, TreeBatch):
+        for prefix in (0, 40):
+            b = cls([rows], [rows + 50], prefix, 6, 2, 64, 32, dtype, extra=5)
+            b.cu += 3
+            out, lse = torch.full((rows + 5, 6, 64), 7.0, dtype=dtype, device="cuda"), torch.full((rows + 5, 6), 8.0, device="cuda")
+            if cls is TreeBatch:
+                b.mask[3:rows + 3] = b.mask[:rows].clone()
+            b.run(out=out, lse=lse)
+            rsa.check_device_error()
+            if rows < 100:
+                ref.assert_prefix_attn(out[3:rows + 3], lse[3:rows + 3], tuple(x[3:rows + 3] for x in b.reference()), dtype)
+            for at in (slice(0, 3), slice(rows + 3, None)):
+                assert (out[at] == 7).all() and (lse[at] == 8).all()
 
 
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
