@@ -16,11 +16,9 @@
 namespace rsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kDepth = 8;  // rows that a thread has in flight
-
 struct Cut {
-    int cols;        // 16-byte columns of a row
+    int cols;        // 16-byte columns of a row that a block takes
+    int parts;       // blocks that share a row
     int row_lanes;   // threads that share a column, each with kDepth rows of a batch
     int slabs;       // (layer, head, keys or values) of a block
 };
@@ -30,15 +28,16 @@ struct Move {
     int64_t from, to;
 };
 
-__device__ __forceinline__ int64_t row_of(const CompactParams &p, int r, int token)
+__device__ __forceinline__ int64_t row_of(const CompactParams &p, int page, int token)
 {
-    const int page = p.block_table[r * p.table_stride + (token >> p.c.page_shift)];
     return (((int64_t)page * p.c.Hkv) << p.c.page_shift) + (token & ((1 << p.c.page_shift) - 1));
 }
 
+// kDepth: rows that a thread has in flight.  kOnce: no list is longer than a batch.
+template <int kThreads, int kDepth, bool kOnce>
 __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_constant__ CompactParams p, const Cut cut)
 {
-    extern __shared__ Move s_move[];  // of a batch
+    extern __shared__ Move s_move[];  // of a batch (of three, in turn)
     const int r = blockIdx.x, tid = threadIdx.x, batch = cut.row_lanes * kDepth;
     const int base = p.cached_len[r], all = p.kv_len[r], m = p.keep_len[r];
     const int32_t *keep = p.keep + r * p.keep_stride;
@@ -59,8 +58,11 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
                 bad = 1;
                 continue;
             }
-            if (k == i)
+            if (k == i) {
+                if (i < batch)
+                    s_move[i] = Move{-1, -1};
                 continue;
+            }
             const int32_t *table = p.block_table + r * p.table_stride;
             const int from = table[(base + k) >> p.c.page_shift];
             const int to = i < all - base ? table[(base + i) >> p.c.page_shift] : -1;  // (i >= all - base: the list does not ascend)
@@ -68,6 +70,8 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
                 if (tell)
                     record_bad_index(p.err, kSiteCompactPage, from < 0 || from >= p.c.n_pages ? from : to);
                 bad = 1;
+            } else if (i < batch) {
+                s_move[i] = Move{row_of(p, from, base + k), row_of(p, to, base + i)};
             }
         }
     ok = !__syncthreads_or(bad) && ok;
@@ -78,48 +82,86 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
 
     // ---- the moves -----------------------------------------------------------------
     const int col = tid % cut.cols, lane = tid / cut.cols % cut.row_lanes, slab0 = tid / (cut.cols * cut.row_lanes);
-    const int slab = blockIdx.y * cut.slabs + slab0;
+    const int group = blockIdx.y / cut.parts, part = blockIdx.y - group * cut.parts;
+    const int slab = group * cut.slabs + slab0;
     const bool works = slab < 2 * p.c.layers * p.c.Hkv;
     const int head = slab % p.c.Hkv, kv = slab / p.c.Hkv & 1, layer = works ? slab / (2 * p.c.Hkv) : 0;
-    char *at = p.c.data[kv] + layer * p.c.layer_bytes + (((int64_t)head << p.c.page_shift) * p.c.row) + col * 16;
+    char *at = p.c.data[kv] + layer * p.c.layer_bytes + (((int64_t)head << p.c.page_shift) * p.c.row) +
+               (part * cut.cols + col) * 16;
+    uint4 x[kDepth];
+    auto read = [&](const Move *list, int n) {
+#pragma unroll
+        for (int e = 0; e < kDepth; ++e) {
+            const int i = e * cut.row_lanes + lane;
+            if (works && i < n && list[i].from >= 0)
+                x[e] = *reinterpret_cast<const uint4 *>(at + list[i].from * p.c.row);
+        }
+    };
+    auto write = [&](const Move *list, int n) {
+#pragma unroll
+        for (int e = 0; e < kDepth; ++e) {
+            const int i = e * cut.row_lanes + lane;
+            if (works && i < n && list[i].from >= 0)
+                *reinterpret_cast<uint4 *>(at + list[i].to * p.c.row) = x[e];
+        }
+    };
+    if constexpr (kOnce) {
+        read(s_move, m);
+        __syncthreads();  // all has been read
+        write(s_move, m);
+        return;
+    }
+    // Three lists in turn: one is written while the batch before it is read, and the one before
+    // that may still be being written back.
+    const int32_t *table = p.block_table + r * p.table_stride;
+    Move *list = s_move, *next = s_move + batch, *after = next + batch;
     for (int i0 = 0; i0 < m; i0 += batch) {
-        for (int i = tid; i < batch && i0 + i < m; i += kThreads) {
-            const int k = keep[i0 + i];
-            s_move[i] = k == i0 + i ? Move{-1, -1} : Move{row_of(p, r, base + k), row_of(p, r, base + i0 + i)};
+        read(list, m - i0);
+        for (int i = tid; i < batch && i0 + batch + i < m; i += kThreads) {
+            const int to = i0 + batch + i, k = keep[to];
+            next[i] = Move{-1, -1};
+            if (k != to)
+                next[i] = Move{row_of(p, table[(base + k) >> p.c.page_shift], base + k),
+                               row_of(p, table[(base + to) >> p.c.page_shift], base + to)};
         }
-        __syncthreads();
-        uint4 x[kDepth];
-#pragma unroll
-        for (int e = 0; e < kDepth; ++e) {
-            const int i = e * cut.row_lanes + lane;
-            if (works && i0 + i < m && s_move[i].from >= 0)
-                x[e] = *reinterpret_cast<const uint4 *>(at + s_move[i].from * p.c.row);
-        }
-        __syncthreads();  // the batch has been read
-#pragma unroll
-        for (int e = 0; e < kDepth; ++e) {
-            const int i = e * cut.row_lanes + lane;
-            if (works && i0 + i < m && s_move[i].from >= 0)
-                *reinterpret_cast<uint4 *>(at + s_move[i].to * p.c.row) = x[e];
-        }
-        __syncthreads();  // s_move is written again
+        __syncthreads();  // the batch has been read, the next one's list is there
+        write(list, m - i0);
+        Move *const done = list;
+        list = next;
+        next = after;
+        after = done;
     }
 }
 
-}  // namespace
-
-cudaError_t launch_cache_compact(const CompactParams &p, cudaStream_t s)
+template <int kThreads, int kDepth, bool kOnce>
+cudaError_t launch(const CompactParams &p, cudaStream_t s)
 {
     Cut cut;
+    const int64_t slabs = 2ll * p.c.layers * p.c.Hkv;
     cut.cols = p.c.row / 16;
+    cut.parts = 1;
+    // (where blocks are few, several share a row, down to 64 bytes each, for longer batches)
+    for (; !kOnce && cut.cols > 4 && p.R * slabs * cut.parts * 2 <= 152; cut.cols /= 2)
+        cut.parts *= 2;
     cut.row_lanes = 1;
     while (cut.row_lanes * kDepth < p.max_keep && cut.row_lanes * cut.cols < kThreads)
         cut.row_lanes *= 2;
     cut.slabs = kThreads / (cut.cols * cut.row_lanes);
-    const int64_t slabs = 2ll * p.c.layers * p.c.Hkv, groups = (slabs + cut.slabs - 1) / cut.slabs;
-    const size_t smem = sizeof(Move) * cut.row_lanes * kDepth;  // (at most 4 KB)
-    cache_compact_kernel<<<dim3((unsigned)p.R, (unsigned)groups), kThreads, smem, s>>>(p, cut);
+    const int64_t groups = (slabs + cut.slabs - 1) / cut.slabs * cut.parts;  // (below 2^16)
+    const size_t smem = (kOnce ? 1 : 3) * sizeof(Move) * cut.row_lanes * kDepth;  // (at most 24 KB)
+    cache_compact_kernel<kThreads, kDepth, kOnce><<<dim3((unsigned)p.R, (unsigned)groups), kThreads, smem, s>>>(p, cut);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+// Short lists fit a batch of 256 threads (64 requests with up to 6 rows in 16 layers 8.2 us;
+// by the loop 10.2).  Long ones go through batches of 128 rows of a head at least: whole rows
+// of whole pages (4 caches of 8192 rows in 4 layers 180 us, 6.0 TB/s, 0.88 of a copy; with
+// 256 threads of 8 rows 194, with blocks that share rows by columns 191 to 330).
+cudaError_t launch_cache_compact(const CompactParams &p, cudaStream_t s)
+{
+    return p.max_keep <= 8 * 256 / (p.c.row / 16) ? launch<256, 8, true>(p, s) : launch<512, 4, false>(p, s);
 }
 
 }  // namespace rsa
