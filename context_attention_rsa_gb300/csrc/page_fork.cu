@@ -6,16 +6,18 @@
 // does its share of the table entries and of the rows.  Nothing that any block reads
 // is written by another: sources and destinations are different rows, and a copy's
 // destination comes from free_pages.
-// A page's rows of one key head lie side by side: a warp copies them, 16 bytes a lane.
-// The copies go layer by layer, so that the forks of one request read its page
-// from L2 after the first.
+// A page's rows of one key head lie side by side: a warp reads 4 KB of them, 16 bytes a lane,
+// and writes them for every fork of the request.
+#include <climits>
+
 #include "rsa_internal.h"
 
 namespace rsa {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kDepth = 8;  // 16-byte pieces that a lane has in flight
+constexpr int kDepth = 8;             // 16-byte loads that a lane has in flight
+constexpr int kPiece = kDepth * 512;  // bytes that a warp copies at once
 
 // Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
 __device__ __forceinline__ int last_not_above(const int *a, int n, int x)
@@ -71,37 +73,43 @@ __device__ __forceinline__ long long exclusive_sums(int *a, int n, long long *s_
 __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_constant__ PageForkParams p)
 {
     extern __shared__ int smem[];
-    int *s_len = smem;                 // [F]
-    int *s_pages = s_len + p.F;        // [F + 1] table entries before each fork
-    int *s_fresh = s_pages + p.F + 1;  // [F + 1] fresh pages before each fork
-    unsigned *s_used = reinterpret_cast<unsigned *>(s_fresh + p.F + 1);  // a bit for each request: it is in dst
+    int *s_pages = smem;                // [F + 1] table entries before each fork; then pages to copy before each
+    int *s_fresh = s_pages + p.F + 1;   // [F + 1] fresh pages before each fork
+    int *s_first = s_fresh + p.F + 1;   // [R] the first fork of each source
+    int *s_forks = s_first + p.R;       // [R] its forks
+    unsigned *s_used = reinterpret_cast<unsigned *>(s_forks + p.R);  // a bit for each request: it is in dst
     __shared__ long long s_warp[kWarps];
+    __shared__ int s_list[kWarps][32];
     const int tid = threadIdx.x, P = 1 << p.c.page_shift, F = p.F;
     const bool shared = p.shares != nullptr;
 
     // ---- the forks, and what makes them impossible ---------------------------------------
+    for (int i = tid; i < p.R; i += kThreads) {
+        s_first[i] = INT_MAX;
+        s_forks[i] = 0;
+    }
     for (int i = tid; i < (p.R + 31) / 32; i += kThreads)
         s_used[i] = 0;
     __syncthreads();
     int bad = 0;
     for (int f = tid; f < F; f += kThreads) {
         const int a = p.src[f], b = p.dst[f];
-        if (a < 0 || a >= p.R || b < 0 || b >= p.R || (atomicOr(&s_used[b >> 5], 1u << (b & 31)) >> (b & 31) & 1))
+        if (a < 0 || a >= p.R || b < 0 || b >= p.R || (atomicOr(&s_used[b >> 5], 1u << (b & 31)) >> (b & 31) & 1)) {
             bad = 1;
+            continue;
+        }
+        atomicMin(&s_first[a], f);
+        atomicAdd(&s_forks[a], 1);
     }
     bad = __syncthreads_or(bad);
     int bad_len = 0;
     for (int f = tid; f < F && !bad; f += kThreads) {
-        const int a = p.src[f];
-        if (s_used[a >> 5] >> (a & 31) & 1) {
+        const int a = p.src[f], n = p.kv_len[a];
+        if (s_used[a >> 5] >> (a & 31) & 1)
             bad = 1;
-            break;
-        }
-        const int n = p.kv_len[a];
         if (n < 0 || n > (int64_t)p.max_pages << p.c.page_shift)
             bad_len = 1;
         const int pages = bad_len ? 0 : (int)(((int64_t)n + P - 1) >> p.c.page_shift);
-        s_len[f] = n;
         s_pages[f] = pages;
         s_fresh[f] = shared ? (n & (P - 1)) != 0 : pages;
     }
@@ -129,15 +137,16 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
     }
     if (code)
         return;
+    // (dst's lengths and rows of the table are written, src's are read: no request is in both)
     for (long long f = g0; f < F; f += gn)
-        p.kv_len[p.dst[f]] = s_len[f];
+        p.kv_len[p.dst[f]] = p.kv_len[p.src[f]];
 
     // ---- table entries -------------------------------------------------------------------
     for (long long i = g0; i < entries; i += gn) {
-        const int f = last_not_above(s_pages, F, (int)i), j = (int)i - s_pages[f], full = s_len[f] >> p.c.page_shift;
+        const int f = last_not_above(s_pages, F, (int)i), j = (int)i - s_pages[f], a = p.src[f];
         int id;
-        if (shared && j < full) {
-            id = p.block_table[(int64_t)p.src[f] * p.table_stride + j];
+        if (shared && j < p.kv_len[a] >> p.c.page_shift) {
+            id = p.block_table[a * p.table_stride + j];
             if (id >= 0 && id < p.c.n_pages)
                 atomicAdd(&p.shares[id], 1);
             else
@@ -145,41 +154,88 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
         } else {
             id = p.free_pages[start + s_fresh[f] + (shared ? 0 : j)];
         }
-        p.block_table[(int64_t)p.dst[f] * p.table_stride + j] = id;
+        p.block_table[p.dst[f] * p.table_stride + j] = id;
     }
 
     // ---- rows ------------------------------------------------------------------------------
-    // A warp takes one copied page's rows of one key head, of keys or values, in a layer.
-    const int lane = tid & 31;
-    const long long heads = 2ll * p.c.Hkv, items = fresh * heads * p.c.layers;
-    for (long long i = (long long)blockIdx.x * kWarps + (tid >> 5); i < items; i += (long long)gridDim.x * kWarps) {
-        const int layer = (int)(i / (fresh * heads));
-        const long long in_layer = i - layer * (fresh * heads);
-        const int c = (int)(in_layer / heads), slab = (int)(in_layer - c * heads), head = slab >> 1;
-        const int f = last_not_above(s_fresh, F, c);
-        const int j = shared ? s_len[f] >> p.c.page_shift : c - s_fresh[f];
-        const int rows = min(P, s_len[f] - (j << p.c.page_shift));
-        const int from = p.block_table[(int64_t)p.src[f] * p.table_stride + j], to = p.free_pages[start + c];
-        if (from < 0 || from >= p.c.n_pages || to < 0 || to >= p.c.n_pages) {
+    // The forks of one source copy the same pages: the first of them stands for all.
+    __syncthreads();
+    for (int f = tid; f < F; f += kThreads)
+        s_pages[f] = s_first[p.src[f]] == f ? s_fresh[f + 1] - s_fresh[f] : 0;
+    __syncthreads();
+    const long long pages = exclusive_sums(s_pages, F, s_warp);
+    // A warp takes up to kPiece bytes of such a page's rows of one key head, of keys or values, in
+    // a layer, reads them once and writes them for every fork.
+    const int lane = tid & 31, warp = tid >> 5, heads = 2 * p.c.Hkv, page_bytes = p.c.row << p.c.page_shift;
+    const int pieces = (page_bytes + kPiece - 1) / kPiece;
+    const long long items = pages * heads * pieces * p.c.layers;
+    for (long long i = (long long)blockIdx.x * kWarps + warp; i < items; i += (long long)gridDim.x * kWarps) {
+        // (layer, piece, page, head), the head fastest
+        int c, slab, piece, layer;
+        if (items <= UINT_MAX) {
+            const unsigned q = (unsigned)i / (unsigned)heads, u = q / (unsigned)pages;
+            slab = (int)((unsigned)i - q * heads), c = (int)(q - u * (unsigned)pages), layer = (int)(u / (unsigned)pieces);
+            piece = (int)(u - (unsigned)layer * pieces);
+        } else {
+            const long long q = i / heads, u = q / pages;
+            slab = (int)(i - q * heads), c = (int)(q - u * pages), layer = (int)(u / pieces);
+            piece = (int)(u - (long long)layer * pieces);
+        }
+        const int f = last_not_above(s_pages, F, c), a = p.src[f], len = p.kv_len[a];
+        const int j = shared ? len >> p.c.page_shift : c - s_pages[f];
+        const int first = piece * kPiece / 16, n = min((piece + 1) * kPiece, min(P, len - (j << p.c.page_shift)) * p.c.row) / 16;
+        if (first >= n)
+            continue;
+        const int from = p.block_table[a * p.table_stride + j];
+        if (from < 0 || from >= p.c.n_pages) {
             if (lane == 0)
-                record_bad_index(p.err, kSiteForkPage, from < 0 || from >= p.c.n_pages ? from : to);
+                record_bad_index(p.err, kSiteForkPage, from);
             continue;
         }
-        char *data = p.c.data[slab & 1] + layer * p.c.layer_bytes;
-        const int64_t bytes = (int64_t)p.c.row << p.c.page_shift;
-        const uint4 *x = reinterpret_cast<const uint4 *>(data + ((int64_t)from * p.c.Hkv + head) * bytes);
-        uint4 *y = reinterpret_cast<uint4 *>(data + ((int64_t)to * p.c.Hkv + head) * bytes);
-        const int n = rows * (p.c.row / 16);
-        for (int k0 = lane; k0 < n; k0 += 32 * kDepth) {
-            uint4 v[kDepth];
+        char *data = p.c.data[slab & 1] + layer * p.c.layer_bytes + (int64_t)(slab >> 1) * page_bytes;
+        const int64_t stride = (int64_t)p.c.Hkv * page_bytes;
+        const uint4 *x = reinterpret_cast<const uint4 *>(data + from * stride);
+        uint4 v[kDepth];
 #pragma unroll
-            for (int e = 0; e < kDepth; ++e)
-                if (k0 + 32 * e < n)
-                    v[e] = x[k0 + 32 * e];
+        for (int e = 0; e < kDepth; ++e)
+            if (first + lane + 32 * e < n)
+                v[e] = x[first + lane + 32 * e];
+        // 32 forks at a time: each lane finds the fresh page of one
+        for (int next = f, left = s_forks[a]; left > 0;) {
+            int found = 0;
+            __syncwarp();
+            for (; found < min(left, 32); next += 32) {
+                const bool mine = next + lane < F && p.src[next + lane] == a;
+                const unsigned who = __ballot_sync(0xffffffffu, mine);
+                const int at = found + __popc(who & ((1u << lane) - 1));
+                if (mine && at < 32)
+                    s_list[warp][at] = next + lane;
+                found += __popc(who);
+                if (found > 32) {  // the others of these 32 in the next turn
+                    next = __shfl_sync(0xffffffffu, next + lane, __ffs(__ballot_sync(0xffffffffu, mine && at == 32)) - 1) - 32;
+                    found = 32;
+                }
+            }
+            __syncwarp();
+            int to = -1;
+            if (lane < found) {
+                to = p.free_pages[start + s_fresh[s_list[warp][lane]] + (shared ? 0 : j)];
+                if (to < 0 || to >= p.c.n_pages) {
+                    record_bad_index(p.err, kSiteForkPage, to);
+                    to = -1;
+                }
+            }
+            for (int k = 0; k < found; ++k) {
+                const int page = __shfl_sync(0xffffffffu, to, k);
+                if (page < 0)
+                    continue;
+                uint4 *y = reinterpret_cast<uint4 *>(data + page * stride);
 #pragma unroll
-            for (int e = 0; e < kDepth; ++e)
-                if (k0 + 32 * e < n)
-                    y[k0 + 32 * e] = v[e];
+                for (int e = 0; e < kDepth; ++e)
+                    if (first + lane + 32 * e < n)
+                        y[first + lane + 32 * e] = v[e];
+            }
+            left -= found;
         }
     }
 }
@@ -188,18 +244,19 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
 
 cudaError_t launch_page_fork(const PageForkParams &p, cudaStream_t s)
 {
-    const size_t smem = (3ull * p.F + 2) * 4 + (p.R + 31) / 32 * 4;
-    if (smem > 48 * 1024 - 1024) {
+    const size_t smem = (2ull * p.F + 2 + 2ull * p.R + (p.R + 31) / 32) * 4;  // (at most 199 KB)
+    if (smem > 48 * 1024 - 2048) {
         cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;
     }
-    // As many warps as there are rows to copy for them, at most what the SMs hold.
-    const int64_t items = (int64_t)p.F * (p.shares ? 1 : p.max_pages) * 2 * p.c.Hkv * p.c.layers;
+    // As many warps as there may be pieces to copy, at most what the SMs hold.
+    const int64_t pieces = (((int64_t)p.c.row << p.c.page_shift) + kPiece - 1) / kPiece;
+    const int64_t items = (int64_t)p.F * (p.shares ? 1 : p.max_pages) * 2 * p.c.Hkv * pieces * p.c.layers;
     int64_t blocks = (items + kWarps - 1) / kWarps;
     const int64_t entries = ((int64_t)p.F * p.max_pages + kThreads - 1) / kThreads;
     blocks = blocks > entries ? blocks : entries;
-    blocks = blocks < 1 ? 1 : (blocks > 608 ? 608 : blocks);
+    blocks = blocks < 1 ? 1 : (blocks > 304 ? 304 : blocks);
     page_fork_kernel<<<(unsigned)blocks, kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
