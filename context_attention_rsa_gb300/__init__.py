@@ -30,8 +30,8 @@ __all__ = [
     "workspace_size", "ring_schedule", "set_block_kernel",
     "set_wait_limit_ns", "check_device_error", "selftest_wait_timeout", "version",
     "page_plan", "PagePlan", "PLAN_STATUS", "qk_norm_rope", "qk_norm_rope_bwd", "rope_table", "prefix_attn",
-    "prefix_attn_workspace_size", "tree_plan", "TreePlan", "tree_attn", "cache_compact", "page_fork", "page_free", "RSA_F32",
-    "RSA_BF16",
+    "prefix_attn_workspace_size", "tree_plan", "TreePlan", "tree_attn", "tree_attn_workspace_size", "cache_compact", "page_fork",
+    "page_free", "RSA_F32", "RSA_BF16",
 ]
 
 RSA_F32 = 0
@@ -581,4 +581,5 @@ def selftest_wait_timeout(stream=None) -> None:
 
 
 from .paged import (PLAN_STATUS, PagePlan, TreePlan, cache_compact, page_fork, page_free, page_plan,  # noqa: E402
-                    prefix_attn, prefix_attn_workspace_size, qk_norm_rope, qk_norm_rope_bwd, rope_table, tree_attn, tree_plan)
+                    prefix_attn, prefix_attn_workspace_size, qk_norm_rope, qk_norm_rope_bwd, rope_table, tree_attn,
+                    tree_attn_workspace_size, tree_plan)

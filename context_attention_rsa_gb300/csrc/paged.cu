@@ -265,19 +265,20 @@ rsa_status worker_count(int *n)
 }
 
 struct PrefixLayout {
-    size_t plan, home_o, home_lse, slot_o, slot_lse, total;
+    size_t plan, pair_plan, home_o, home_lse, slot_o, slot_lse, total;
 };
 
-PrefixLayout prefix_layout(int64_t T, int Hq, int d, int R)
+PrefixLayout prefix_layout(int64_t T, int Hq, int d, int R, bool drafted)
 {
     PrefixLayout w;
     const size_t rows_ = (size_t)T * Hq, slots = (size_t)kPrefixMaxWorkers * kPrefixUnitRows;
     w.plan = align256(((size_t)R + 2) * 8);
+    w.pair_plan = drafted ? w.plan : 0;
     w.home_o = align256(rows_ * d * 4);
     w.home_lse = align256(rows_ * 4);
     w.slot_o = align256(slots * d * 4);
     w.slot_lse = align256(slots * 4);
-    w.total = w.plan + 2 * (w.home_o + w.home_lse) + w.slot_o + w.slot_lse;
+    w.total = w.plan + w.pair_plan + 2 * (w.home_o + w.home_lse) + w.slot_o + w.slot_lse;
     return w;
 }
 
@@ -403,7 +404,7 @@ rsa_status paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stri
             return fail(RSA_ERR_INVALID_ARG, "mask_stride=%lld must be at least words=%d and at most 2^30", (long long)mask_stride,
                         words);
     }
-    const PrefixLayout lay = prefix_layout(T, Hq, d, R);
+    const PrefixLayout lay = prefix_layout(T, Hq, d, R, drafted);
     RSA_TRY(check_ptr(workspace, "workspace"));
     if (ws_bytes < lay.total)
         return fail(RSA_ERR_INVALID_ARG, "workspace holds %zu bytes, %zu needed", ws_bytes, lay.total);
@@ -460,6 +461,7 @@ rsa_status paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stri
         return at;
     };
     p.plan = reinterpret_cast<int64_t *>(take(lay.plan));
+    p.pair_plan = reinterpret_cast<int64_t *>(take(lay.pair_plan));
     for (int i = 0; i < 2; ++i) {
         p.home_o[i] = reinterpret_cast<float *>(take(lay.home_o));
         p.home_lse[i] = reinterpret_cast<float *>(take(lay.home_lse));
@@ -668,7 +670,16 @@ rsa_status rsa_prefix_attn_workspace_size(rsa_dtype dt, int64_t T, int Hq, int H
     if (!bytes)
         return fail(RSA_ERR_INVALID_ARG, "bytes is NULL");
     RSA_TRY(check_prefix_shape(dt, T, Hq, Hkv, d, R));
-    *bytes = prefix_layout(T, Hq, d, R).total;
+    *bytes = prefix_layout(T, Hq, d, R, false).total;
+    return RSA_OK;
+}
+
+rsa_status rsa_tree_attn_workspace_size(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int R, size_t *bytes)
+{
+    if (!bytes)
+        return fail(RSA_ERR_INVALID_ARG, "bytes is NULL");
+    RSA_TRY(check_prefix_shape(dt, T, Hq, Hkv, d, R));
+    *bytes = prefix_layout(T, Hq, d, R, true).total;
     return RSA_OK;
 }
 

@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     const int worker = blockIdx.x;
     const float scale = 1.0f / sqrtf((float)D);
 
-    const Stretch st = find_stretch<kThreads>(p, worker, s.sum, &s.st);
+    const Stretch st = find_stretch<kThreads, false>(p, worker, s.sum, &s.st);
     ptx::launch_dependents();
-    Walk walk;
-    walk.begin(st);
+    Walk<false> walk;
+    walk.begin(p, st, worker);
     Piece x;
     while (walk.next(p, x)) {
         const int rows = (int)x.ntok * G;
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                 r.o[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const int64_t most = min((int64_t)x.keys, x.see0 + (x.ntok - 1));  // the keys that any row sees
-        const int64_t j1 = min(most, (int64_t)x.t1 * kTileKeys);
-        const int64_t j00 = (int64_t)x.t0 * kTileKeys;
+        const int64_t j1 = min(most, (int64_t)x.t1 << p.tile_shift);
+        const int64_t j00 = (int64_t)x.t0 << p.tile_shift;
         // A turn: this thread copies 16 bytes of kCopies keys, whose pages' ids it read
         // a turn before.  Keys past the last one are not copied.
         constexpr int kPieces = D / 4, kCopies = kTurn * kPieces / kThreads, kStep = kThreads / kPieces;
@@ -454,20 +454,47 @@ __device__ __forceinline__ int lane_request_of(const PrefixAttnParams &p, int to
 // segments are a lane each: follows from the lengths alone, so a warp can work it out
 // while the attention launch still computes (2 us less for a short call).  With more
 // requests that would cost every warp a scan, and it takes the sums that worker 0 has left.
-struct Line {
-    int64_t upto, total;  // of segments [0, lane]
+struct Sums {
+    int64_t before, total;            // of this lane's request; of all
+    int64_t pairs_before, all_pairs;  // the same for the even groups
 
-    __device__ __forceinline__ explicit Line(const PrefixAttnParams &p)
+    // r: this lane's request; few: R < 32.
+    __device__ __forceinline__ Sums(const PrefixAttnParams &p, int r, bool few)
     {
         const int lane = threadIdx.x & 31;
-        upto = lane <= p.R ? segment(p, lane).line : 0;
+        pairs_before = all_pairs = 0;
+        r = max(r, 0);
+        if (few) {
+            int64_t x = 0, y = 0;
+            if (lane <= p.R) {
+                const Segment g = segment<true>(p, lane);
+                x = g.line;
+                y = g.pair_line;
+            }
+            scan(x, r, before, total);
+            if (p.side_by_side)
+                scan(y, r, pairs_before, all_pairs);
+        } else {
+            total = p.plan[p.R + 1];
+            before = p.plan[1 + r];
+            if (p.side_by_side) {
+                all_pairs = p.pair_plan[p.R + 1];
+                pairs_before = p.pair_plan[1 + r];
+            }
+        }
+    }
+    // x: of the lane's segment.
+    __device__ __forceinline__ static void scan(int64_t x, int r, int64_t &before, int64_t &total)
+    {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o)
-                upto += y;
+                x += y;
         }
-        total = __shfl_sync(0xffffffffu, upto, 31);
+        before = __shfl_sync(0xffffffffu, x, r);  // (segments 0 to r lie before 1 + r)
+        total = __shfl_sync(0xffffffffu, x, 31);
     }
 };
 
@@ -478,15 +505,25 @@ struct Pieces {
     int n;
 };
 
-// Segment g, which begins at place `at` of the line.
-__device__ __forceinline__ Pieces pieces_of(const PrefixAttnParams &p, const Segment &g, int64_t at, int token, int head, int64_t share)
+// Segment g, before which lie `before` and `pairs_before` places of its parts of the line.
+__device__ __forceinline__ Pieces pieces_of(const PrefixAttnParams &p, const Segment &g, int64_t before, int64_t pairs_before,
+                                            const Line &line, int token, int head)
 {
     const int i = token - g.tok0;
-    if (g.line == 0 || i < 0 || i >= g.ntok)  // (outside: only where cu_q does not ascend)
+    if (g.tiles == 0 || i < 0 || i >= g.ntok)  // (outside: only where cu_q does not ascend)
         return Pieces{0, 0};
-    const int64_t unit = (int64_t)head * g.groups + i / p.unit_tokens;
-    at += unit * g.unit_line() + g.unit;  // the unit's first tile
-    const int64_t w0 = at / share, w1 = (at + (int64_t)(g.tiles - 1) * g.cost) / share;
+    const int group = i / p.unit_tokens;
+    int64_t at;
+    if (group < 2 * g.pairs) {
+        at = (group & 1 ? line.odd : 0) + pairs_before + ((int64_t)head * g.pairs + (group >> 1)) * g.unit_line();
+    } else {
+        const int64_t unit = (int64_t)head * g.singles + (group - 2 * g.pairs) - g.skip;
+        if (unit < 0)
+            return Pieces{0, 1};  // a whole unit that is not on the line
+        at = line.rest + before + unit * g.unit_line();
+    }
+    at += g.unit;  // the unit's first tile
+    const int64_t w0 = at / line.share, w1 = (at + (int64_t)(g.tiles - 1) * g.cost) / line.share;
     return Pieces{(w0 + 1) * kPrefixUnitRows + (i % p.unit_tokens) * p.G, (int)(w1 - w0) + 1};
 }
 
@@ -620,23 +657,16 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     const int token = (int)(row / p.Hq);
     const int hq = (int)(row - (int64_t)token * p.Hq), head = hq / p.G;
     const int r = request_of(p, token);
-    const Segment g[2] = {segment(p, 0), r < 0 ? Segment() : segment(p, 1 + r)};
-    int64_t total, before;
+    const Segment g[2] = {segment<true>(p, 0), r < 0 ? Segment() : segment<true>(p, 1 + r)};
     const bool few = p.R < 32;
-    if (few) {
-        const Line line(p);
-        total = line.total;
-        before = __shfl_sync(0xffffffffu, line.upto, max(r, 0));
-    } else {
+    if (!few)
         ptx::wait_for_launch_before();
-        total = p.plan[p.R + 1];
-        before = p.plan[1 + max(r, 0)];
-    }
-    const int64_t share = share_of(p, total);
+    const Sums sums(p, r, few);
+    const Line line(p, sums.all_pairs, sums.total);
     Locate locate{p, row, hq - head * p.G, {{0, 0}, {0, 0}}};
     if (r >= 0) {
-        locate.pc[0] = pieces_of(p, g[0], 0, token, head, share);
-        locate.pc[1] = pieces_of(p, g[1], before, token, head, share);
+        locate.pc[0] = pieces_of(p, g[0], 0, 0, line, token, head);
+        locate.pc[1] = pieces_of(p, g[1], sums.before, sums.pairs_before, line, token, head);
     }
     // Every thread waits, also where it has nothing to join: the launch after this one
     // waits only for this one.
@@ -688,13 +718,7 @@ __global__ void __launch_bounds__(kJoinThreads, kBlocks) prefix_join_rows_kernel
     const int64_t items = p.T * p.Hkv * cuts, warps = (int64_t)gridDim.x * kJoinWarps;
     const int64_t first = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     const bool few = p.R < 32;
-    int64_t upto = 0, total = 0;
-    if (few) {
-        const Line line(p);
-        upto = line.upto;
-        total = line.total;
-    }
-    const Segment prefix = segment(p, 0);
+    const Segment prefix = segment<true>(p, 0);
     bool waited = false;
     for (int64_t i0 = first; i0 < items; i0 += 32 * warps) {
         const int64_t item = i0 + lane * warps;
@@ -703,22 +727,17 @@ __global__ void __launch_bounds__(kJoinThreads, kBlocks) prefix_join_rows_kernel
         const int g0 = (int)((there ? item : items - 1) - head_row * cuts) * kJoinRows;
         const int token = (int)(head_row / p.Hkv), head = (int)(head_row - (int64_t)token * p.Hkv);
         const int r = lane_request_of(p, token);
-        const Segment g = segment(p, 1 + max(r, 0));
-        int64_t before;
-        if (few) {
-            before = __shfl_sync(0xffffffffu, upto, max(r, 0));
-        } else {
-            if (!waited)
-                ptx::wait_for_launch_before();
+        const Segment g = segment<true>(p, 1 + max(r, 0));
+        if (!few && !waited) {
+            ptx::wait_for_launch_before();
             waited = true;
-            total = p.plan[p.R + 1];
-            before = p.plan[1 + max(r, 0)];
         }
-        const int64_t share = share_of(p, total);
+        const Sums sums(p, r, few);
+        const Line line(p, sums.all_pairs, sums.total);
         Pieces pre{0, 0}, own{0, 0};
         if (r >= 0) {
-            pre = pieces_of(p, prefix, 0, token, head, share);
-            own = pieces_of(p, g, before, token, head, share);
+            pre = pieces_of(p, prefix, 0, 0, line, token, head);
+            own = pieces_of(p, g, sums.before, sums.pairs_before, line, token, head);
         }
         if (!waited)
             ptx::wait_for_launch_before();
@@ -742,7 +761,7 @@ __global__ void __launch_bounds__(kJoinThreads, kBlocks) prefix_join_rows_kernel
             }
 #pragma unroll 1
             for (; rows > 0; --rows, ++locate.g, ++locate.row) {
-                Fold<D, 1, 4> f;
+                Fold<D, 1, kAhead> f;
                 f.pieces(0, n, locate);
                 f.template write<E>(p, locate.row);
             }
@@ -757,9 +776,21 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
 {
     PrefixAttnParams p = p_in;
     p.unit_tokens = p.light_tokens = kRows / p.G;
+    p.tile_shift = kTileShift;
     p.light_tile = p.heavy_tile = 2;
     p.unit = 3;
     p.unit_shift = 31;
+    p.side_by_side = 0;
+    if (p.mask) {
+        // Trees are short calls: tiles of 32 keys, which even out what the SMs get (40 tokens of 8
+        // heads behind 4097 keys 43 -> 33 us, 2 requests of 16 tokens behind 2000 31.6 -> 20.6;
+        // tiles of 64 36 and 23).  A unit of over 64 rows takes a block's time twice.
+        p.tile_shift = 5;
+        p.light_tokens = 64 / p.G;
+        p.light_tile = 1;
+        p.heavy_tile = 2;
+        p.unit = 4;
+    }
     auto kernel = p.mask ? prefix_attn_f32_kernel<D, true> : prefix_attn_f32_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)
@@ -803,7 +834,7 @@ cudaError_t join_any(const PrefixAttnParams &p, cudaStream_t s)
     const int64_t rows = p.T * p.Hq;
     if (rows <= 152)
         return launch_early(prefix_join_kernel<E, D, kParts>, (rows * kParts + kJoinWarps - 1) / kJoinWarps, s, p);
-    return rows <= 152 * 24 ? join_rows<E, D, 1, 4, 3>(p, s) : join_rows<E, D, 4, 3, 2>(p, s);
+    return rows <= 152 * 32 ? join_rows<E, D, 1, 8, 2>(p, s) : join_rows<E, D, 4, 3, 2>(p, s);
 }
 
 }  // namespace

@@ -138,7 +138,7 @@ struct Cfg {
     static constexpr uint32_t kXchOff = kBarOff + 512;  // [2 S tiles][2 halves][128 rows] maxima, then sums
     static constexpr uint32_t kSumOff = kXchOff + 2 * 2048;
     static constexpr int kWork = 8;                       // pieces handed out and not yet taken by every role
-    static constexpr uint32_t kWorkOff = kSumOff + 256;   // their descriptions
+    static constexpr uint32_t kWorkOff = kSumOff + 320;   // their descriptions
     static constexpr uint32_t kSmemBytes = kWorkOff + kWork * sizeof(Work) + 1024;
     static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
     static constexpr int kQF = 0;            // one for each Q tile
@@ -154,7 +154,7 @@ struct Cfg {
     static constexpr int kDrain = kWE + kWork;
     static constexpr int kNumBars = kDrain + 1;
     static_assert(kNumBars * 8 + 8 <= 512, "barrier area");
-    static_assert(sizeof(Stretch) + 8 * (kThreads / 32) <= 256, "scan area");
+    static_assert(sizeof(Stretch) + 16 * (kThreads / 32) <= 320, "scan area");
 };
 
 // The two warps that share rows (w and w + 4, pair w mod 4): named barriers 2 to
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
     }
     int64_t *s_sum = reinterpret_cast<int64_t *>(gbase + C::kSumOff);
-    const Stretch st = find_stretch<C::kThreads>(p, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + C::kThreads / 32));
+    const Stretch st = find_stretch<C::kThreads, kTree>(p, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + 2 * (C::kThreads / 32)));
     ptx::launch_dependents();  // the joining launch finds its rows' pieces while this one computes
     ptx::tc_fence_before();
     __syncthreads();
@@ -455,9 +455,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         auto wait = [&](int bar, uint32_t phase, int site) {
             return __all_sync(0xffffffffu, ptx::mbar_wait_called(BAR(bar), phase & 1, lim_ns, abort_flag, p.err, site)) != 0;
         };
-        Walk walk;
-        Batch segments;
-        walk.begin(st);
+        Walk<kTree> walk;
+        Batch<kTree> segments;
+        walk.begin(p, st, worker);
         Piece x;
         for (bool more = true; ok && more; ++pieces) {
             more = walk.next(p, x, [&](int i) { return segments.get(p, i); });
@@ -890,12 +890,14 @@ cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
 {
     PrefixAttnParams p = p_in;
     const int TT = 128 / p.G;
+    p.tile_shift = kTileShift;
     p.unit_tokens = 2 * TT;
     p.light_tokens = TT;
     p.light_tile = kLightTile;
     p.heavy_tile = kHeavyTile;
     p.unit = p.mask ? kTreeUnit : kUnit;
     p.unit_shift = p.mask ? kTreeUnitShift : 31;
+    p.side_by_side = p.mask ? -1 : 0;
     CUtensorMap mq, mk, mv, mk8, mv8;
     const uint64_t page = 1ull << p.page_shift, heads = (uint64_t)(p.n_pages * p.Hkv), halves = D / 64;
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.T};

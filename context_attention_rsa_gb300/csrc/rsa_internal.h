@@ -208,14 +208,17 @@ struct PrefixAttnParams {
     float *lse;                  // [T, Hq]
     // workspace (see paged_sched.cuh)
     int64_t *plan;               // [R + 2]
+    int64_t *pair_plan;          // [R + 2] (only with side_by_side)
     float *home_o[2], *home_lse[2];  // [T * Hq, d] and [T * Hq]: a row's first piece of the prefix, of its own keys
     float *slot_o, *slot_lse;    // [workers, 256, d] and [workers, 256]: a worker's first piece, begun by another
     // how the launcher's kernel cuts the work
     int workers;
+    int tile_shift;              // keys of a tile, log2
     int unit_tokens;             // query tokens of a unit at most
     int light_tokens;            // a unit of more tokens than this costs heavy_tile places a key tile, else light_tile
     int light_tile, heavy_tile;
     int unit, unit_shift;        // places of a unit before its first tile: unit + (rows >> unit_shift)
+    int side_by_side;            // all ones: units of the same keys are taken side by side; 0: in order
     uint64_t wait_limit_ns;
     unsigned int *err;
 };

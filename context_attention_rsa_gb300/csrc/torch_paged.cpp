@@ -35,6 +35,7 @@ decltype(&rsa_prefix_attn_fwd) attn_fn;
 decltype(&rsa_prefix_attn_workspace_size) attn_size_fn;
 decltype(&rsa_tree_plan) tree_plan_fn;
 decltype(&rsa_tree_attn_fwd) tree_attn_fn;
+decltype(&rsa_tree_attn_workspace_size) tree_attn_size_fn;
 decltype(&rsa_cache_compact) compact_fn;
 decltype(&rsa_page_fork) fork_fn;
 decltype(&rsa_page_free) free_fn;
@@ -526,7 +527,7 @@ PyObject *attention(PyObject *const *a, PyObject *mask_arg, PyObject *const *b)
         ws = workspace(b[4], dev);
     } else {
         size_t n = 0;
-        const rsa_status st = attn_size_fn(dt, T, (int)Hq, (int)Hkv, (int)d, (int)R, &n);
+        const rsa_status st = (mask_arg ? tree_attn_size_fn : attn_size_fn)(dt, T, (int)Hq, (int)Hkv, (int)d, (int)R, &n);
         if (st != RSA_OK)
             return PyLong_FromLong(st);
         ws = call.make({(int64_t)n}, at::kByte);
@@ -748,11 +749,11 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// The addresses of the eleven functions, and share_fn.
+// The addresses of the twelve functions, and share_fn.
 PyObject *bind(PyObject *const *a)
 {
-    void *p[11];
-    for (int i = 0; i < 11; ++i)
+    void *p[12];
+    for (int i = 0; i < 12; ++i)
         p[i] = reinterpret_cast<void *>(integer(a[i]));
     page_plan_fn = reinterpret_cast<decltype(page_plan_fn)>(p[0]);
     rope_fn = reinterpret_cast<decltype(rope_fn)>(p[1]);
@@ -765,12 +766,13 @@ PyObject *bind(PyObject *const *a)
     compact_fn = reinterpret_cast<decltype(compact_fn)>(p[8]);
     fork_fn = reinterpret_cast<decltype(fork_fn)>(p[9]);
     free_fn = reinterpret_cast<decltype(free_fn)>(p[10]);
-    Py_XSETREF(share_fn, Py_NewRef(a[11]));
+    tree_attn_size_fn = reinterpret_cast<decltype(tree_attn_size_fn)>(p[11]);
+    Py_XSETREF(share_fn, Py_NewRef(a[12]));
     Py_RETURN_NONE;
 }
 
 #define RSA_ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {RSA_ENTRY(bind, 12),       RSA_ENTRY(page_plan, 11),    RSA_ENTRY(qk_norm_rope, 16), RSA_ENTRY(qk_norm_rope_bwd, 17),
+PyMethodDef methods[] = {RSA_ENTRY(bind, 13),       RSA_ENTRY(page_plan, 11),    RSA_ENTRY(qk_norm_rope, 16), RSA_ENTRY(qk_norm_rope_bwd, 17),
                          RSA_ENTRY(prefix_attn, 12), RSA_ENTRY(tree_plan, 7),     RSA_ENTRY(tree_attn, 13),    RSA_ENTRY(cache_compact, 9),
                          RSA_ENTRY(page_fork, 11),   RSA_ENTRY(page_free, 10),    {nullptr, nullptr, 0, nullptr}};
 #undef RSA_ENTRY

@@ -99,6 +99,7 @@ SIGS = {
     "rsa_tree_plan": [_p, _i64, _p, _p, _i32, _i32, _i64, _p, _p, _p],
     "rsa_tree_attn_fwd": [_p, _i64, _i64, _p, _p, _i32, _i64, _i32, _i32, _i32, _i32, _i64, _p, _p, _i32, _p, _i64, _i32,
                           _p, _i64, _p, _i64, _i32, _p, _p, _p, _size, _p],
+    "rsa_tree_attn_workspace_size": [_i32, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_size)],
     "rsa_cache_compact": [_p, _p, _i64, _i32, _p, _p, _i32, _p, _i64, _i32, _p, _p, _p],
     "rsa_page_fork": [_p, _p, _i64, _i32, _p, _i32, _p, _p, _i32, _p, _i64, _p, _p, _p, _p],
     "rsa_page_free": [_p, _i64, _i32, _p, _p, _i32, _i32, _i64, _p, _i64, _p, _p, _p, _p],
@@ -130,7 +131,7 @@ def _load_native():
             m.bind(*(ctypes.cast(getattr(lib, n), _p).value for n in (
                 "rsa_page_plan", "rsa_qk_norm_rope_fwd", "rsa_qk_norm_rope_bwd", "rsa_qk_norm_rope_bwd_workspace_size",
                 "rsa_prefix_attn_fwd", "rsa_prefix_attn_workspace_size", "rsa_tree_plan", "rsa_tree_attn_fwd", "rsa_cache_compact",
-                "rsa_page_fork", "rsa_page_free")), _share)
+                "rsa_page_fork", "rsa_page_free", "rsa_tree_attn_workspace_size")), _share)
             _native = m
     return _native
 
@@ -197,13 +198,17 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda") -> 
     return torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
 
 
-def prefix_attn_workspace_size(dtype: torch.dtype, T: int, Hq: int, Hkv: int, d: int, R: int) -> int:
+def _workspace_size(fn: str, dtype: torch.dtype, *shape: int) -> int:
     n = ctypes.c_size_t(0)
     lib = load()
-    st = lib.rsa_prefix_attn_workspace_size(_DT.get(dtype, -1), T, Hq, Hkv, d, R, ctypes.byref(n))
+    st = getattr(lib, fn)(_DT.get(dtype, -1), *shape, ctypes.byref(n))
     if st != 0:
-        raise RsaError("rsa_prefix_attn_workspace_size", st, lib.rsa_last_error_string().decode())
+        raise RsaError(fn, st, lib.rsa_last_error_string().decode())
     return int(n.value)
+
+
+def prefix_attn_workspace_size(dtype: torch.dtype, T: int, Hq: int, Hkv: int, d: int, R: int) -> int:
+    return _workspace_size("rsa_prefix_attn_workspace_size", dtype, T, Hq, Hkv, d, R)
 
 
 def prefix_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, prefix_pages=None, prefix_len: int = 0, out=None,
@@ -242,12 +247,16 @@ def tree_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, tree_mask, prefix_
     sees the prefix, the request's own tokens before its drafted ones, and those of
     its drafted tokens j <= i whose bit (bit j mod 32 of word j // 32) is set in the
     row of tree_mask, int32 [T, words]; the mask is tree_plan's or the caller's
-    own.  The workspace is prefix_attn's (prefix_attn_workspace_size)."""
+    own.  workspace: tree_attn_workspace_size bytes."""
     r = (_native or _load_native()).tree_attn(q, k_cache, v_cache, cu_q, block_table, kv_len, tree_mask, prefix_pages, prefix_len, out,
                                               lse, workspace, stream)
     if r.__class__ is int:
         raise _error("rsa_tree_attn_fwd", r)
     return r
+
+
+def tree_attn_workspace_size(dtype: torch.dtype, T: int, Hq: int, Hkv: int, d: int, R: int) -> int:
+    return _workspace_size("rsa_tree_attn_workspace_size", dtype, T, Hq, Hkv, d, R)
 
 
 def cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_len, out=None, stream=None) -> torch.Tensor:

@@ -623,9 +623,10 @@ rsa_status rsa_tree_plan(const int32_t *parent, int64_t T, const int32_t *cu_new
  *   own token kv_len[r] - n + j for every j <= i whose bit is set in the row's mask
  * (mask [T, words], rows mask_stride words apart; bits past 32 * words count as not
  * set).  The mask may be any: rsa_tree_plan's, or a caller's own in which a row
- * does not see itself, or nothing.  All else is as for rsa_prefix_attn_fwd, whose
- * workspace size is this call's too.
+ * does not see itself, or nothing.  All else is as for rsa_prefix_attn_fwd; the
+ * workspace holds rsa_tree_attn_workspace_size() bytes.
  */
+rsa_status rsa_tree_attn_workspace_size(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int R, size_t *bytes);
 rsa_status rsa_tree_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
                              const void *v_cache, rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int page_size,
                              int64_t n_pages, const int32_t *cu_q, const int32_t *kv_len, int R,

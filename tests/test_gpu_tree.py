@@ -174,6 +174,34 @@ def test_attn_matches_the_definition(case, mask):
     TreeBatch(*case, mask=mask).check()
 
 
+@pytest.mark.parametrize("case", [
+    ([152], [160], 300, 256, 2, 64, 64, BF),                # a unit of the prefix for every SM, none over
+    ([101, 60], [110, 300], 140, 256, 2, 128, 16, BF),      # ... and a few over
+    ([300, 20, 1], [300, 25, 200], 129, 256, 2, 64, 32, BF),  # two for every SM
+    ([7, 9, 2, 1, 4], [7, 300, 140, 1, 5], 0, 256, 2, 64, 16, BF),       # pairs of token groups with and without one over
+    ([64, 0, 33, 5, 96], [2064, 3, 700, 5, 129], 0, 16, 2, 128, 64, BF),
+    ([70] * 9, [70 + 90 * i for i in range(9)], 20, 8, 1, 128, 32, BF),
+    ([5] * 40, [6 + 7 * i for i in range(40)], 0, 128, 1, 64, 16, BF),    # more requests than a warp
+], ids=lambda c: f"R{len(c[0])}n{sum(c[0])}P{c[2]}")
+@pytest.mark.parametrize("mask", [None, "random"], ids=["tree", "any"])
+def test_units_side_by_side(case, mask):
+    need_cuda()
+    b = TreeBatch(*case, mask=mask)
+    first = b.check()
+    again = b.run()
+    assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_more_requests_than_threads_with_pairs(prefix):
+    # the blocks look at the lengths in several turns
+    need_cuda()
+    rng = np.random.default_rng(8)
+    new = rng.integers(0, 6, 800)
+    lens = new + rng.integers(0, 40, 800)
+    TreeBatch(new.tolist(), lens.tolist(), prefix, 128, 1, 64, 16, BF).check()
+
+
 @pytest.mark.parametrize("dtype", [BF, F], ids=["bf", "f"])
 @pytest.mark.parametrize("seed", range(10))
 def test_random_trees(dtype, seed):
@@ -287,7 +315,7 @@ def test_same_bits_whatever_the_workspace_held_and_on_streams():
     b = TreeBatch(*CASES[9])
     dev = b.device()
     kw = dict(prefix_pages=dev[7], prefix_len=b.prefix)
-    n = rsa.prefix_attn_workspace_size(BF, *b.q.shape[:2], CASES[9][4], CASES[9][5], len(b.lens))
+    n = rsa.tree_attn_workspace_size(BF, *b.q.shape[:2], CASES[9][4], CASES[9][5], len(b.lens))
     want = b.run(workspace=torch.zeros(n, dtype=torch.uint8, device="cuda"))
     for fill in (255, 127):
         got = b.run(workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
