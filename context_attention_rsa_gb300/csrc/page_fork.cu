@@ -33,39 +33,48 @@ __device__ __forceinline__ int last_not_above(const int *a, int n, int x)
     return lo;
 }
 
-// Exclusive sums of a[0..n) in place, a[n] the total (64 bits: also returned), by the whole block.
-__device__ __forceinline__ long long exclusive_sums(int *a, int n, long long *s_warp)
+// What is counted of a fork.
+struct Counts {
+    int entries, fresh, copies;  // table entries; fresh pages; pages copied, where it is the first fork of its source
+
+    __device__ __forceinline__ void add(const Counts &x) { entries += x.entries, fresh += x.fresh, copies += x.copies; }
+};
+
+// Exclusive sums of the three lists in place, with the totals behind them, by the whole block.
+// (They stay below 2^31.)
+__device__ __forceinline__ Counts exclusive_sums(int *entries, int *fresh, int *copies, int n, Counts *s_warp)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = (n + kThreads - 1) / kThreads | 1;
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    long long mine = 0;
+    Counts mine{0, 0, 0};
     for (int i = i0; i < i1; ++i)
-        mine += a[i];
-    long long x = mine;
+        mine.add(Counts{entries[i], fresh[i], copies[i]});
+    Counts x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const Counts y{__shfl_up_sync(0xffffffffu, x.entries, o), __shfl_up_sync(0xffffffffu, x.fresh, o),
+                       __shfl_up_sync(0xffffffffu, x.copies, o)};
         if (lane >= o)
-            x += y;
+            x.add(y);
     }
     if (lane == 31)
         s_warp[warp] = x;
     __syncthreads();
-    long long before = x - mine, total = 0;
+    Counts before{x.entries - mine.entries, x.fresh - mine.fresh, x.copies - mine.copies}, total{0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp)
-            before += s_warp[w];
-        total += s_warp[w];
+            before.add(s_warp[w]);
+        total.add(s_warp[w]);
     }
     for (int i = i0; i < i1; ++i) {
-        const int v = a[i];
-        a[i] = (int)before;  // (wraps only where the forks are refused)
-        before += v;
+        const Counts v{entries[i], fresh[i], copies[i]};
+        entries[i] = before.entries, fresh[i] = before.fresh, copies[i] = before.copies;
+        before.add(v);
     }
     if (tid == 0)
-        a[n] = (int)total;
+        entries[n] = total.entries, fresh[n] = total.fresh, copies[n] = total.copies;
     __syncthreads();
     return total;
 }
@@ -73,12 +82,13 @@ __device__ __forceinline__ long long exclusive_sums(int *a, int n, long long *s_
 __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_constant__ PageForkParams p)
 {
     extern __shared__ int smem[];
-    int *s_pages = smem;                // [F + 1] table entries before each fork; then pages to copy before each
+    int *s_pages = smem;                // [F + 1] table entries before each fork
     int *s_fresh = s_pages + p.F + 1;   // [F + 1] fresh pages before each fork
-    int *s_first = s_fresh + p.F + 1;   // [R] the first fork of each source
+    int *s_copies = s_fresh + p.F + 1;  // [F + 1] pages to copy before each fork, the forks of one source counted once
+    int *s_first = s_copies + p.F + 1;  // [R] the first fork of each source
     int *s_forks = s_first + p.R;       // [R] its forks
     unsigned *s_used = reinterpret_cast<unsigned *>(s_forks + p.R);  // a bit for each request: it is in dst
-    __shared__ long long s_warp[kWarps];
+    __shared__ Counts s_warp[kWarps];
     __shared__ int s_list[kWarps][32];
     const int tid = threadIdx.x, P = 1 << p.c.page_shift, F = p.F;
     const bool shared = p.shares != nullptr;
@@ -112,15 +122,15 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
         const int pages = bad_len ? 0 : (int)(((int64_t)n + P - 1) >> p.c.page_shift);
         s_pages[f] = pages;
         s_fresh[f] = shared ? (n & (P - 1)) != 0 : pages;
+        s_copies[f] = s_first[a] == f ? s_fresh[f] : 0;
     }
     bad = __syncthreads_or(bad);
     bad_len = __syncthreads_or(bad_len);
     const long long start = p.free_start ? *p.free_start : 0;
-    long long entries = 0, fresh = 0;
-    if (!bad && !bad_len) {
-        entries = exclusive_sums(s_pages, F, s_warp);
-        fresh = exclusive_sums(s_fresh, F, s_warp);
-    }
+    Counts all{0, 0, 0};
+    if (!bad && !bad_len)
+        all = exclusive_sums(s_pages, s_fresh, s_copies, F, s_warp);
+    const int entries = all.entries, fresh = all.fresh, pages = all.copies;
     int code = 0;
     if (bad)
         code = RSA_PLAN_BAD_REQUEST;
@@ -159,16 +169,11 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
 
     // ---- rows ------------------------------------------------------------------------------
     // The forks of one source copy the same pages: the first of them stands for all.
-    __syncthreads();
-    for (int f = tid; f < F; f += kThreads)
-        s_pages[f] = s_first[p.src[f]] == f ? s_fresh[f + 1] - s_fresh[f] : 0;
-    __syncthreads();
-    const long long pages = exclusive_sums(s_pages, F, s_warp);
     // A warp takes up to kPiece bytes of such a page's rows of one key head, of keys or values, in
     // a layer, reads them once and writes them for every fork.
     const int lane = tid & 31, warp = tid >> 5, heads = 2 * p.c.Hkv, page_bytes = p.c.row << p.c.page_shift;
     const int pieces = (page_bytes + kPiece - 1) / kPiece;
-    const long long items = pages * heads * pieces * p.c.layers;
+    const long long items = (long long)pages * heads * pieces * p.c.layers;
     for (long long i = (long long)blockIdx.x * kWarps + warp; i < items; i += (long long)gridDim.x * kWarps) {
         // (layer, piece, page, head), the head fastest
         int c, slab, piece, layer;
@@ -181,8 +186,8 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
             slab = (int)(i - q * heads), c = (int)(q - u * pages), layer = (int)(u / pieces);
             piece = (int)(u - (long long)layer * pieces);
         }
-        const int f = last_not_above(s_pages, F, c), a = p.src[f], len = p.kv_len[a];
-        const int j = shared ? len >> p.c.page_shift : c - s_pages[f];
+        const int f = last_not_above(s_copies, F, c), a = p.src[f], len = p.kv_len[a];
+        const int j = shared ? len >> p.c.page_shift : c - s_copies[f];
         const int first = piece * kPiece / 16, n = min((piece + 1) * kPiece, min(P, len - (j << p.c.page_shift)) * p.c.row) / 16;
         if (first >= n)
             continue;
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
 
 cudaError_t launch_page_fork(const PageForkParams &p, cudaStream_t s)
 {
-    const size_t smem = (2ull * p.F + 2 + 2ull * p.R + (p.R + 31) / 32) * 4;  // (at most 199 KB)
+    const size_t smem = (3ull * p.F + 3 + 2ull * p.R + (p.R + 31) / 32) * 4;  // (at most 224 KB)
     if (smem > 48 * 1024 - 2048) {
         cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)

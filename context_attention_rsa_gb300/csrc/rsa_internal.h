@@ -264,7 +264,7 @@ struct CompactParams {
 };
 
 // Forks of requests (rsa_page_fork).
-constexpr int kPageForkMost = 8192;
+constexpr int kPageForkMost = 8000;
 struct PageForkParams {
     CacheLayers c;
     int32_t *block_table;

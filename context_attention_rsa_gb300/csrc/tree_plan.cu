@@ -3,7 +3,8 @@
 //   A_i = {i} + A_parent(i),  depth_i = |A_i| - 1,  pos_i = pos0 + cached + depth_i
 //
 // A thread takes a row and walks up its ancestors, whose indices descend, so that it
-// finishes one word of the mask after the other and holds only one.  The parents
+// finishes one word of the mask after the other and holds only one (up to two: both, since
+// lanes that finish a word at different steps make all of them wait).  The parents
 // lie in shared memory, those of the block's rows and of as many rows before them as
 // a mask has bits.  A row's request comes from a 32-way search of cu_new by its warp.
 // The work is a few bytes a token: the launch, two or three dependent reads and one
@@ -36,6 +37,8 @@ __device__ __forceinline__ int request_of(const TreePlanParams &p, int64_t row)
     return (int)lo;
 }
 
+// kShort: masks of one or two words, held whole.
+template <bool kShort>
 __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_constant__ TreePlanParams p)
 {
     extern __shared__ int s_parent[];  // of rows [first, row0 + kThreads)
@@ -45,86 +48,101 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
     for (int64_t t = first + tid; t < min(p.T, row0 + kThreads); t += kThreads)
         s_parent[t - first] = p.parent[t];
 
+    // (a request for each row to look at: read early, told about late)
+    int64_t look = row;
+    int look_a = look <= p.R ? p.cu_new[look] : 0, look_b = look <= p.R ? p.cu_new[min(look + 1, (int64_t)p.R)] : 0;
+
     // ---- the row's request: the warp's first row's, or one after it --------------------
-    const int64_t rows = min((int64_t)max(p.cu_new[p.R], 0), p.T);
-    if (row == 0 && p.cu_new[p.R] != rows)
-        record_bad_index(p.err, kSiteTreeRows, p.cu_new[p.R]);
-    for (int64_t i = row; i < p.R; i += (int64_t)gridDim.x * kThreads)
-        if (p.cu_new[i + 1] < p.cu_new[i])
-            record_bad_index(p.err, kSiteTreeRows, p.cu_new[i + 1]);
+    // Its window of 32 requests comes in one read, with their lengths; more of them begin within
+    // the warp's rows only where some have one row or none.
     const int64_t warp_row = row0 + (tid & ~31);
-    int r = -1;
-    if (warp_row < rows) {
-        r = request_of(p, warp_row);
-        // (the requests that begin within the warp's rows; more than 31, those of one or
-        // no row among them, in several turns)
-        for (int from = r + 1;; from += 32) {
-            const int begin = from + lane < p.R ? p.cu_new[from + lane] : INT_MAX;
-            const unsigned in = __ballot_sync(0xffffffffu, begin < warp_row + 32);
-            for (unsigned left = in; left; left &= left - 1) {
-                const int k = __ffs(left) - 1;
-                if (__shfl_sync(0xffffffffu, begin, k) <= row)
-                    r = from + k;
-            }
-            if (in != 0xffffffffu)
-                break;
+    int64_t begin = 0, end = 0, all = 0;
+    for (int from = max(request_of(p, warp_row), 0);; from += 32) {
+        const bool there = from + lane < p.R;
+        const int a = there ? p.cu_new[from + lane] : INT_MAX, b = there ? p.cu_new[from + lane + 1] : INT_MAX;
+        const int n = there ? p.kv_len[from + lane] : 0;
+        const unsigned in = __ballot_sync(0xffffffffu, a < warp_row + 32);
+        for (unsigned left = in; left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const int ak = __shfl_sync(0xffffffffu, a, k), bk = __shfl_sync(0xffffffffu, b, k), nk = __shfl_sync(0xffffffffu, n, k);
+            if (ak <= row)  // (requests without rows share their successor's: the last one has them)
+                begin = ak, end = bk, all = nk;
         }
+        if (in != 0xffffffffu)
+            break;
     }
     __syncthreads();
+    while (look <= p.R) {
+        if (look_a < 0 || look_a > p.T || look_b < look_a)
+            record_bad_index(p.err, kSiteTreeRows, look_a < 0 || look_a > p.T ? look_a : look_b);
+        look += (int64_t)gridDim.x * kThreads;
+        if (look <= p.R) {
+            look_a = p.cu_new[look];
+            look_b = p.cu_new[min(look + 1, (int64_t)p.R)];
+        }
+    }
     if (row >= p.T)
         return;
 
     // ---- its index, and the way up -----------------------------------------------------
     uint32_t *mask = p.mask + row * p.words;
-    int64_t begin = 0, pos = 0;
-    bool on = r >= 0 && row < rows;
-    if (on) {
-        const int64_t a = p.cu_new[r], b = p.cu_new[r + 1];
-        begin = max(a, (int64_t)0);
-        const int64_t n = b - a, cached = (int64_t)p.kv_len[r] - n;
-        on = row < b;
-        if (on && row == begin) {
-            if (a < 0 || b > p.T)
-                record_bad_index(p.err, kSiteTreeRows, a < 0 ? a : b);
-            if (cached < 0)
-                record_bad_index(p.err, kSiteTreeLen, p.kv_len[r]);
-        }
-        pos = p.pos0 + max(cached, (int64_t)0);
-    }
+    bool on = row < end;
+    const int64_t cached = all - (end - begin);
+    if (on && row == max(begin, (int64_t)0) && cached < 0)
+        record_bad_index(p.err, kSiteTreeLen, all);
+    begin = max(begin, (int64_t)0);
+    int64_t pos = p.pos0 + max(cached, (int64_t)0);
     int i = on ? (int)(row - begin) : 0;
     if (on && i >= most) {
         if (i == most)
             record_bad_index(p.err, kSiteTreeSize, i);
         on = false;
     }
-    int at = p.words - 1;  // the word to be written next
-    uint32_t bits = 0;
-    if (on) {
-        const int base = (int)(begin - first);  // (the row's own index is below `most`: all before it is there)
-        for (int depth = 0;; ++depth) {
-            for (const int w = i >> 5; at > w; --at) {
-                mask[at] = bits;
-                bits = 0;
-            }
-            bits |= 1u << (i & 31);
-            int up = s_parent[base + i];
-            if (up < -1 || up >= i) {
-                if (depth == 0)
-                    record_bad_index(p.err, kSiteParent, up);
-                up = -1;
-            }
-            if (up < 0) {
-                pos += depth;
-                break;
-            }
+    const int *parent = s_parent + (begin - first);  // (the row's own index is below `most`: all before it is there)
+    int up = on ? parent[i] : -1, depth = 0;
+    if (on && (up < -1 || up >= i))
+        record_bad_index(p.err, kSiteParent, up);
+    // (-1 and what is no earlier token end the walk)
+    if constexpr (kShort) {
+        uint32_t word[2] = {0, 0};
+        auto set = [&] {
+            const uint32_t bit = 1u << (i & 31);
+            word[0] |= i < 32 ? bit : 0;
+            word[1] |= i < 32 ? 0 : bit;
+        };
+        if (on)
+            set();
+        while ((unsigned)up < (unsigned)i) {
             i = up;
+            up = parent[i];
+            ++depth;
+            set();
+        }
+        mask[0] = word[0];
+        if (p.words > 1)
+            mask[1] = word[1];
+    } else {
+        int at = p.words - 1;  // the word to be written next
+        uint32_t bits = 0;
+        if (on) {
+            for (; at > i >> 5; --at)
+                mask[at] = 0;
+            for (bits = 1u << (i & 31); (unsigned)up < (unsigned)i; bits |= 1u << (i & 31)) {
+                i = up;
+                up = parent[i];
+                ++depth;
+                for (; at > i >> 5; --at) {
+                    mask[at] = bits;
+                    bits = 0;
+                }
+            }
+        }
+        for (; at >= 0; --at) {
+            mask[at] = bits;
+            bits = 0;
         }
     }
-    p.positions[row] = on ? pos : 0;
-    for (; at >= 0; --at) {
-        mask[at] = bits;
-        bits = 0;
-    }
+    p.positions[row] = on ? pos + depth : 0;
 }
 
 }  // namespace
@@ -132,7 +150,8 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
 cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s)
 {
     const size_t smem = (size_t)(kThreads + 32 * p.words) * 4;  // (at most 4.6 KB)
-    tree_plan_kernel<<<(unsigned)((p.T + kThreads - 1) / kThreads), kThreads, smem, s>>>(p);
+    auto kernel = p.words <= 2 ? tree_plan_kernel<true> : tree_plan_kernel<false>;
+    kernel<<<(unsigned)((p.T + kThreads - 1) / kThreads), kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -693,7 +693,7 @@ rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table,
  * applies.  A page id outside [0, n_pages) in a source's row is copied, but neither
  * counted nor its rows copied; it and such an entry of free_pages are reported
  * by rsa_check_device_error.  No buffer written may overlap another operand.  At most
- * 16384 requests and 8192 forks.  One launch.
+ * 16384 requests and 8000 forks.  One launch.
  */
 rsa_status rsa_page_fork(const rsa_cache *cache, int32_t *block_table, int64_t table_stride, int max_pages, int32_t *kv_len,
                          int R, const int32_t *src, const int32_t *dst, int F, const int32_t *free_pages, int64_t n_free,
