@@ -154,7 +154,7 @@ struct Cfg {
     static constexpr int kDrain = kWE + kWork;
     static constexpr int kNumBars = kDrain + 1;
     static_assert(kNumBars * 8 + 8 <= 512, "barrier area");
-    static_assert(sizeof(Stretch) + 16 * (kThreads / 32) <= 320, "scan area");
+    static_assert(sizeof(Stretch) + 16 * (kThreads / 32) <= 320 && 2 * sizeof(Stretch) <= 320, "scan area");
 };
 
 // The two warps that share rows (w and w + 4, pair w mod 4): named barriers 2 to
@@ -434,7 +434,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
     }
     int64_t *s_sum = reinterpret_cast<int64_t *>(gbase + C::kSumOff);
-    const Stretch st = find_stretch<C::kThreads, kTree>(p, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + 2 * (C::kThreads / 32)));
+    Stretch st;
+    if (!kTree || p.R >= 32)
+        st = find_stretch<C::kThreads, kTree>(p, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + 2 * (C::kThreads / 32)));
+    else if (warp == C::kProducerWarp || warp == C::kValueWarp)
+        st = few_stretch<kTree>(p, worker, reinterpret_cast<Stretch *>(s_sum) + (warp == C::kValueWarp), warp == C::kProducerWarp);
     ptx::launch_dependents();  // the joining launch finds its rows' pieces while this one computes
     ptx::tc_fence_before();
     __syncthreads();
