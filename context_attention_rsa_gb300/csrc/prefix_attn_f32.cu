@@ -142,7 +142,18 @@ struct Rows {
     float m[2], l[2];  // (l: of this lane's keys)
     float4 o[2][H];
     int see[2];  // they see keys [0, see) of the segment
-    const uint32_t *mask[2];  // ... and of those from the piece's `drafted` on the ones that are set here
+};
+
+// What the rows' masks say of the keys from the piece's `drafted` on.
+struct Masks {
+    const PrefixAttnParams &p;
+    int tok, row0, drafted;  // the piece's first token, the warp's first row
+
+    // 32 bits of row row0 + i, from key j on.
+    __device__ __forceinline__ uint32_t bits(int i, int j) const
+    {
+        return mask_bits(p.mask + (tok + (row0 + i) / p.G) * p.mask_stride, p.words, j - drafted);
+    }
 };
 
 __device__ __forceinline__ void add_product(float4 &o, float p, const float4 &v)
@@ -158,7 +169,7 @@ __device__ __forceinline__ void scale_by(float4 &o, float a) { o.x *= a, o.y *= 
 // A warp's first 4 J rows, whose queries are q, through one block of nk keys from key j0 on.
 template <int D, int J, bool kTree>
 __device__ __forceinline__ void block(Rows<D> &r, const float (*q)[D + 4], const float (*ks)[D + 4], const float (*vs)[D],
-                                      float (*ps)[kKeys + 8], int nk, int j0, float scale, int drafted, int words)
+                                      float (*ps)[kKeys + 8], int nk, int j0, float scale, const Masks &masks)
 {
     constexpr int H = Rows<D>::H;
     const int x = threadIdx.x & 7, y = (threadIdx.x & 31) >> 3;
@@ -190,8 +201,8 @@ __device__ __forceinline__ void block(Rows<D> &r, const float (*q)[D + 4], const
     for (int j = 0; j < J; ++j) {
         const int lim = min(nk, r.see[j] - j0);
         uint32_t bits = 0xffffffffu;
-        if (kTree && j0 + kKeys > drafted && lim > 0)
-            bits = mask_bits(r.mask[j], words, j0 - drafted);
+        if (kTree && j0 + kKeys > masks.drafted && lim > 0)  // (a row that is none sees no key)
+            bits = masks.bits(y + 4 * j, j0);
         mx[j] = r.m[j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -282,6 +293,7 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
             key_groups >>= 1;
         const int kg = warp / row_groups, row0 = (warp - kg * row_groups) * per;
         const bool works = kg < key_groups;
+        const Masks masks{p, x.tok, row0, x.drafted};
         Rows<D> r;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -289,8 +301,6 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
             r.m[j] = -INFINITY;
             r.l[j] = 0.f;
             r.see[j] = row < rows ? (int)max((int64_t)0, min((int64_t)x.keys, x.see0 + row / G)) : 0;
-            if (kTree)  // (a row that is none sees no key, and reads none)
-                r.mask[j] = p.mask + (x.tok + row / G) * p.mask_stride;
 #pragma unroll
             for (int h = 0; h < H; ++h)
                 r.o[j][h] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -318,11 +328,9 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
                     break;
                 const int nk = (int)min((int64_t)kKeys, j1 - jb);
                 if (per <= 4)
-                    block<D, 1, kTree>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale,
-                                       x.drafted, p.words);
+                    block<D, 1, kTree>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale, masks);
                 else
-                    block<D, 2, kTree>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale,
-                                       x.drafted, p.words);
+                    block<D, 2, kTree>(r, &s.q[row0], &s.k[buffer][b * kKeys], &s.v[buffer][b * kKeys], s.p[warp], nk, (int)jb, scale, masks);
             }
             __syncthreads();  // the turn is done with: its buffer is filled next
         }
