@@ -4,8 +4,7 @@
 // entries are looked at: a bitmap of all pages in shared memory takes it, and reading
 // the bitmap in order gives the pages ascending.  Users of a page are counted down by
 // atomics; of those that count one down in the same call exactly one finds 0.
-// One launch of one CTA, or of one cluster where there is more to do.  Every CTA sums up all
-// requests' entries (8 bytes a request, from L2) and marks the pages of its share of the
+// One launch of one cluster.  Every CTA sums up all requests' entries (8 bytes a request, from L2) and marks the pages of its share of the
 // entries; then each reads a part of the bitmap.  Where a bitmap of all pages fits a CTA's
 // shared memory (780000 pages), each marks one of its own, and the parts are put
 // together through distributed shared memory; else each CTA holds a part and the others
@@ -22,7 +21,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMostCtas = 8;
+constexpr int kCtas = 8;  // of the cluster
 
 // Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
 __device__ __forceinline__ int last_not_above(const int *a, int n, int x)
@@ -97,7 +96,7 @@ struct Entries {
     }
 };
 
-// kWhole: every CTA has a bitmap of all pages (ctas parts of `words` words), else its part.
+// kWhole: every CTA has a bitmap of all pages (kCtas parts of `words` words), else its part.
 // kBatch: lengths or entries that a thread has in flight.  spare: words of shared memory behind
 // all else.
 template <int kThreads, bool kWhole, int kBatch>
@@ -105,13 +104,13 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
 {
     extern __shared__ int smem[];
     cg::cluster_group cluster = cg::this_cluster();
-    const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
-    const int held = kWhole ? words * ctas : words;
+    const int tid = threadIdx.x, rank = (int)cluster.block_rank();
+    const int held = kWhole ? words * kCtas : words;
     unsigned *s_bits = reinterpret_cast<unsigned *>(smem);  // [held]
     int *s_before = smem + held;                            // [R + 1]
     int *s_kept = kWhole ? s_before + p.R + 1 : nullptr;    // [R]
     __shared__ int s_warp[32];
-    __shared__ int s_freed[kMostCtas], s_marked[kMostCtas];  // pages in each CTA's part; entries that each has marked
+    __shared__ int s_freed[kCtas], s_marked[kCtas];  // pages in each CTA's part; entries that each has marked
     const int R = p.R, P = 1 << p.page_shift;
 
     for (int i = tid; i < held; i += kThreads)
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
         cluster.sync();  // every part of the bitmap is empty
 
     // ---- what becomes free ---------------------------------------------------------------
-    const int run = (entries + ctas * kThreads - 1) / (ctas * kThreads);
+    const int run = (entries + kCtas * kThreads - 1) / (kCtas * kThreads);
     const int first = min((int64_t)entries, (int64_t)(rank * kThreads + tid) * run), last = min(entries - first, run) + first;
     int marked = 0;
     if (first < last) {
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     }
     int in_cta;
     block_sum<kThreads>(marked, s_warp, &in_cta);
-    if (tid < ctas)
+    if (tid < kCtas)
         *cluster.map_shared_rank(&s_marked[rank], tid) = in_cta;
     cluster.sync();  // the bitmap is complete
 
@@ -216,22 +215,21 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     const int wper = (words + kThreads - 1) / kThreads, w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
     int count = 0;
     for (int w = w0; w < w1; ++w) {
-        if (kWhole && ctas > 1) {
+        if (kWhole) {
             unsigned x = 0;
 #pragma unroll
-            for (int c = 0; c < kMostCtas; ++c)
-                if (c < ctas)
-                    x |= cluster.map_shared_rank(part, c)[w];
+            for (int c = 0; c < kCtas; ++c)
+                x |= cluster.map_shared_rank(part, c)[w];
             part[w] = x;  // (no other CTA reads this part)
         }
         count += __popc(part[w]);
     }
     const int mine0 = block_sum<kThreads>(count, s_warp, &in_cta);  // this thread's first page among the CTA's
-    if (tid < ctas)
+    if (tid < kCtas)
         *cluster.map_shared_rank(&s_freed[rank], tid) = in_cta;
     cluster.sync();
     int freed = 0, marks = 0, before = 0;
-    for (int c = 0; c < ctas; ++c) {
+    for (int c = 0; c < kCtas; ++c) {
         if (c < rank)
             before += s_freed[c];
         freed += s_freed[c];
@@ -298,10 +296,10 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
 }
 
 template <int kThreads, bool kWhole, int kBatch>
-cudaError_t launch(const PageFreeParams &p, int ctas, cudaStream_t s)
+cudaError_t launch(const PageFreeParams &p, cudaStream_t s)
 {
-    const int64_t words = ((p.n_pages + 31) / 32 + ctas - 1) / ctas;
-    const size_t used = (kWhole ? (size_t)words * ctas + 2 * p.R + 1 : (size_t)words + p.R + 1) * 4;
+    const int64_t words = ((p.n_pages + 31) / 32 + kCtas - 1) / kCtas;
+    const size_t used = (kWhole ? (size_t)words * kCtas + 2 * p.R + 1 : (size_t)words + p.R + 1) * 4;
     const size_t spare = kWhole && used <= 200 * 1024 ? 8 * 1024 : 0, smem = used + spare;
     if (smem > 48 * 1024 - 1024) {
         cudaError_t e =
@@ -311,10 +309,10 @@ cudaError_t launch(const PageFreeParams &p, int ctas, cudaStream_t s)
     }
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = (unsigned)ctas;
+    cluster.val.clusterDim.x = kCtas;
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.gridDim = dim3(kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -329,15 +327,13 @@ cudaError_t launch_page_free(const PageFreeParams &p, cudaStream_t s)
 {
     constexpr int64_t kMostWhole = 780000;  // 98 KB of bitmap beside 128 KB of sums and kept pages
     if (p.n_pages > kMostWhole)
-        return launch<1024, false, 4>(p, kMostCtas, s);
-    // Few entries: one CTA (8 requests' few pages, called one after the other, 6.2 us; with more
-    // entries in flight a thread, which is more code, or in a cluster, 8.2).
-    if ((int64_t)p.R * p.max_pages <= 8192 && p.n_pages <= 1 << 18)
-        return launch<256, true, 4>(p, 1, s);
-    // (40 requests of up to 250 pages 8.2 us; with 1024 threads 10.2)
-    if ((int64_t)p.R * p.max_pages <= 65536)
-        return launch<512, true, 4>(p, kMostCtas, s);
-    return launch<1024, true, 4>(p, kMostCtas, s);
+        return launch<1024, false, 4>(p, s);
+    // Fewer threads where there is less to do, for shorter barriers and scans (300 requests of 75000
+    // entries in all, a tenth given back, 6.2 us against 6.9; 8 requests 5.0 against 5.9).  One CTA
+    // gains 0.1 us where next to nothing is given back and loses 4 where 2000 entries are.
+    if ((int64_t)p.R * p.max_pages <= 131072)
+        return launch<256, true, 4>(p, s);
+    return launch<1024, true, 4>(p, s);
 }
 
 }  // namespace rsa
