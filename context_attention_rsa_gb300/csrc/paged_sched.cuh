@@ -10,9 +10,10 @@
 // All tiles of all units lie on one line: segments in order, in a segment the
 // key heads, in a head the token groups, in a unit its tiles.  A tile takes
 // light_tile places, or heavy_tile where its unit has many rows, and a unit
-// some places before its first tile, for what it costs to begin and to end one, so that a place takes about the same time everywhere.  The line is cut
-// into `workers` equal stretches, one for each CTA, so that one long request,
-// many short ones and a prefix all fill the GPU alike.  The tiles of a unit that
+// some places before its first tile, for what it costs to begin and to end one,
+// so that a place takes about the same time everywhere.  The line is cut into
+// `workers` equal stretches, one for each CTA, so that one long request, many
+// short ones and a prefix all fill the GPU alike.  The tiles of a unit that
 // begin in a stretch are a piece; it leaves a partial (o, lse) for its rows: in
 // the rows' own place (home) if the piece begins the unit, else in the worker's
 // slot, as only a worker's first piece can begin inside a unit.  Workspace:
@@ -40,6 +41,7 @@ namespace rsa {
 namespace paged {
 
 constexpr int kTileShift = 7, kTileKeys = 1 << kTileShift;
+
 struct Segment {
     int tok0, ntok;        // its query tokens
     int keys;              // its keys

@@ -22,6 +22,9 @@
 // 60000 keys with 20 rows each 312 us, 15.8 TFLOP/s, and 512 rows over 4608 keys 343 us, 26.6
 // TFLOP/s of the visible pairs (a step of 4 columns is six 16-byte shared loads for 32
 // products a lane; which of the two pipes binds has not been counted).
+// Drafted tokens (kTree) in tiles of 32 keys: 5 requests of 3 to 13 tokens, 4 key heads of 64, behind
+// 4097 keys 30.2 us (with tiles of 128 43).  Four rows a lane instead of two would read shared memory
+// less but spilled (32 us).
 // A unit of few rows is bound by one warp's way through a block, not by the loads: the
 // same with a producer warp and TMA, which brings them earlier, took 82 us for a row of
 // 100000 keys that took 68.

@@ -55,6 +55,16 @@
 //     18 of short units if perfectly shared; the scan 2, the first loads 5, a piece's end
 //     6 (its 256 rows, 16 bytes a lane and store) and the joining launch 5 us
 //   1 request of 1000 keys                        14.5 us, nearly all latency
+// Drafted tokens (kTree): keys from the piece's `drafted` on are masked by the rows' bits, in the
+// last tiles only; the words come while the tile's scores are still being computed.  Their
+// units lie on the line in another order (side by side, paged_sched.cuh) and weigh by
+// their rows:
+//   48 requests of 5 to 25 tokens behind 32768     596 us, 1335 TFLOP/s (837 at first: the short units
+//     weighed too little, 260 us, and the joining launch took 56 instead of 20)
+//   16 requests of 64 tokens, 8192 to 32768 keys   444 us, 1311 TFLOP/s; HBM reads 1.17 GB, each key once
+//     (2.3 GB with the two halves of a request's rows at different times)
+//   38 requests of 16 tokens behind 131072        1650 us, 1585 TFLOP/s, 0.84 of cuBLAS (2003 with the
+//     prefix read from HBM by every unit)
 // A step takes 2850 cycles, 4400 next to a CTA that runs short units, and what made short
 // units faster by more code made the whole slower: as if two neighbouring SMs shared an
 // instruction cache that the kernel's code fills (read from timings, not from a counter).
@@ -79,7 +89,8 @@ using namespace paged;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescale = 8.0f;  // log2 units the maximum may rise before O is rescaled
 // Places of a key tile (kUnit for a unit): a step of two row tiles takes 1.5 us, of
-// one 1.0, a short unit some 1.5 more.  Other weights (4:2:3, 3:3:4, 6:4:5, 4:4:6 for unit,
+// one 1.0, a short unit some 1.5 more.  (Drafted tokens: a unit of 8 rows 2.2, of 128 rows 3,
+// of 256 rows 5.5 more, and as much again where a partial is written.)  Other weights (4:2:3, 3:3:4, 6:4:5, 4:4:6 for unit,
 // one and two row tiles) move single batches by up to 10 % either way and none all.
 constexpr int kLightTile = 2, kHeavyTile = 3, kUnit = 3;
 constexpr int kTreeUnit = 6, kTreeUnitShift = 5;

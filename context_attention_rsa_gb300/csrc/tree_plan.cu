@@ -8,7 +8,8 @@
 // lie in shared memory, those of the block's rows and of as many rows before them as
 // a mask has bits.  A row's request comes from a 32-way search of cu_new by its warp.
 // The work is a few bytes a token: the launch, two or three dependent reads and one
-// shared-memory access for each generation of the deepest tree bound it.
+// shared-memory access for each generation of the deepest tree bound it (8 trees of 16
+// 2.6 us on the GPU; 1000 of up to 64, 33000 rows, 3.6, the same as chains 4.5).
 #include <climits>
 
 #include "rsa_internal.h"
