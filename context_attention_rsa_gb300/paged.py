@@ -278,7 +278,7 @@ def page_fork(k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_
     [n_pages] int32 (users of a page beyond the first; zeros to begin with) full
     pages are shared and the partial last one is copied, without every page is.
     block_table, kv_len and shares are updated in place, rows are copied in every layer
-    of the caches (as in cache_compact); fresh pages come from free_pages as in
+    of the caches (as in cache_compact; a fork is one call, with all layers); fresh pages come from free_pages as in
     page_plan.  Returns info, int64 [4]: status (PLAN_STATUS), entries shared, pages
     taken, first free entry after them.  Forks that cannot all be made change nothing."""
     r = (_native or _load_native()).page_fork(k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_start, shares, out, stream)

@@ -683,7 +683,8 @@ rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table,
  *   - without (NULL) a fresh page for every page, with the same rows;
  *   - kv_len[dst[f]] = kv_len[src[f]].
  * Fresh pages are the next entries of free_pages from entry *free_start on (0 if
- * free_start is NULL), in the forks' order.  The rows are copied in all layers.  What
+ * free_start is NULL), in the forks' order.  The rows are copied in all layers of
+ * the call: a fork is one call, with the caches of every layer.  What
  * dst's row held before is not freed.  dst has no request twice and none that is in
  * src; src may name a request several times.
  *   info [4]: status, entries shared, pages taken, first free entry after them.
