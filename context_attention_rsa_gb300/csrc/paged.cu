@@ -265,7 +265,7 @@ rsa_status worker_count(int *n)
 }
 
 struct PrefixLayout {
-    size_t plan, pair_plan, home_o, home_lse, slot_o, slot_lse, total;
+    size_t slack, plan, pair_plan, home_o, home_lse, slot_o, slot_lse, total;
 };
 
 PrefixLayout prefix_layout(int64_t T, int Hq, int d, int R, bool drafted)
@@ -278,7 +278,8 @@ PrefixLayout prefix_layout(int64_t T, int Hq, int d, int R, bool drafted)
     w.home_lse = align256(rows_ * 4);
     w.slot_o = align256(slots * d * 4);
     w.slot_lse = align256(slots * 4);
-    w.total = w.plan + w.pair_plan + 2 * (w.home_o + w.home_lse) + w.slot_o + w.slot_lse;
+    w.slack = drafted ? 256 : 0;  // its partials begin on 256 bytes wherever the workspace does
+    w.total = w.slack + w.plan + w.pair_plan + 2 * (w.home_o + w.home_lse) + w.slot_o + w.slot_lse;
     return w;
 }
 
@@ -455,6 +456,8 @@ rsa_status paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stri
     p.out = out;
     p.lse = lse;
     char *w = static_cast<char *>(workspace);
+    if (drafted)
+        w = reinterpret_cast<char *>(align256(reinterpret_cast<uintptr_t>(w)));
     auto take = [&](size_t n) {
         char *at = w;
         w += n;

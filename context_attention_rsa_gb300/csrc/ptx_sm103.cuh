@@ -514,6 +514,16 @@ __device__ __forceinline__ void wait_for_launch_before()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ---- wide stores ---------------------------------------------------------------
+
+// 32 bytes, a whole sector, to an address that is a multiple of 32.
+__device__ __forceinline__ void store8(float *p, const float *v)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                 "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 // ---- special functions ---------------------------------------------------------
 
 __device__ __forceinline__ float ex2(float x)

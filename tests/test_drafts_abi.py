@@ -81,10 +81,10 @@ def test_tree_attn_refuses(kw, code, what):
 
 
 def test_tree_attn_workspace_size():
-    # prefix_attn's and the sums of the pairs of token groups
+    # prefix_attn's, the sums of the pairs of token groups, and room to begin on 256 bytes
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     for T, Hq, Hkv, d, R in ((17, 40, 8, 128, 9), (1, 1, 1, 64, 1), (1000, 64, 8, 64, 500)):
-        want = rsa.prefix_attn_workspace_size(torch.bfloat16, T, Hq, Hkv, d, R) + up((R + 2) * 8)
+        want = rsa.prefix_attn_workspace_size(torch.bfloat16, T, Hq, Hkv, d, R) + up((R + 2) * 8) + 256
         assert rsa.tree_attn_workspace_size(torch.bfloat16, T, Hq, Hkv, d, R) == want
         shape = dict(T=T, Hq=Hq, Hkv=Hkv, d=d, R=R, qt=Hq * d, qh=d, q=1 << 40, kc=2 << 40, vc=3 << 40, out=4 << 40, lse=5 << 40, ws=6 << 40,
                      mask=7 << 40, plen=0)

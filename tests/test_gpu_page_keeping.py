@@ -221,6 +221,54 @@ def test_fork_without_a_start_and_with_bad_pages():
             k.assert_caches(k.plain())
 
 
+def test_most_requests_and_forks():
+    need_cuda()
+    R, F, page = 16384, 8000, 16
+    g = torch.Generator(device="cuda").manual_seed(0)
+    n_pages = R - F + F
+    kc, vc = (torch.randn(n_pages, 1, page, 64, generator=g, device="cuda").to(BF) for _ in range(2))
+    order = torch.randperm(R, generator=g, device="cuda")
+    dst, rest = order[:F], order[F:]
+    table = torch.full((R, 1), -1, dtype=torch.int32, device="cuda")
+    table[rest, 0] = torch.arange(R - F, dtype=torch.int32, device="cuda")
+    kv = torch.zeros(R, dtype=torch.int32, device="cuda")
+    kv[rest] = torch.randint(1, page, (R - F,), generator=g, device="cuda", dtype=torch.int32)
+    src = rest[torch.randint(0, R - F, (F,), generator=g, device="cuda")]
+    free = torch.arange(R - F, n_pages, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    shares = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    was = kc.clone(), vc.clone()
+    info = rsa.page_fork(kc, vc, table, kv, src.int(), dst.int(), free, shares=shares)
+    rsa.check_device_error()
+    assert info.tolist() == [0, 0, F, F] and not shares.any()
+    assert torch.equal(kv[dst], kv[src]) and torch.equal(table[dst, 0], free)
+    rows = torch.arange(page, device="cuda") < kv[dst][:, None]
+    for c, w in zip((kc, vc), was):
+        w[free.long()] = torch.where(rows[:, None, :, None], w[table[src, 0].long()], w[free.long()])
+        assert torch.equal(c, w)
+    with pytest.raises(rsa.RsaError):
+        rsa.page_fork(kc, vc, table, kv, order[:8001].int(), order[:8001].int(), free)
+
+
+@pytest.mark.parametrize("n_pages", [780000, 780001])
+def test_most_requests_with_the_most_pages_that_fit(n_pages):
+    # the two forms of the bitmap meet at 780000 pages; all of shared memory is in use there
+    need_cuda()
+    R = 16384
+    g = torch.Generator(device="cuda").manual_seed(1)
+    table = torch.randperm(n_pages, generator=g, device="cuda")[:R * 40].int().view(R, 40).contiguous()
+    kv = torch.randint(0, 641, (R,), generator=g, device="cuda", dtype=torch.int32)
+    keep = (kv * torch.rand(R, generator=g, device="cuda")).int()
+    col = torch.arange(40, device="cuda")
+    gone = table[(col >= (keep[:, None] + 15) // 16) & (col < (kv[:, None] + 15) // 16)]
+    for shares in (None, torch.zeros(n_pages, dtype=torch.int32, device="cuda")):
+        free = torch.full((n_pages,), -1, dtype=torch.int32, device="cuda")
+        info = rsa.page_free(table, kv, keep, free, i64([n_pages]), 16, n_pages, shares=shares)
+        rsa.check_device_error()
+        n = gone.numel()
+        assert info.tolist() == [0, n, n, n_pages - n]
+        assert torch.equal(free[n_pages - n:], gone.sort().values) and (free[:n_pages - n] == -1).all()
+
+
 def test_fork_refusals():
     need_cuda()
     k = Keeper([40, 20], 16)

@@ -320,6 +320,9 @@ def test_same_bits_whatever_the_workspace_held_and_on_streams():
     for fill in (255, 127):
         got = b.run(workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+    for shift in (16, 48, 240):  # (a workspace need not begin on more than 16 bytes)
+        got = b.run(workspace=torch.zeros(n + shift, dtype=torch.uint8, device="cuda")[shift:])
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
     s = [torch.cuda.Stream(), torch.cuda.Stream()]
     got = [rsa.tree_attn(*dev[:7], **kw, stream=s[i % 2]) for i in range(8)]
     torch.cuda.synchronize()
