@@ -11,6 +11,7 @@
 // stay where they are (an accepted path's first tokens) are not touched.
 // A block checks all of its request's list, and the pages in it, before it moves
 // anything, so that all blocks of a request agree.
+#include "ptx_sm103.cuh"
 #include "rsa_internal.h"
 
 namespace rsa {
@@ -39,6 +40,7 @@ __global__ void __launch_bounds__(kThreads) cache_compact_kernel(const __grid_co
 {
     extern __shared__ Move s_move[];  // of a batch (of three, in turn)
     const int r = blockIdx.x, tid = threadIdx.x, batch = cut.row_lanes * kDepth;
+    ptx::wait_for_launch_before();
     const int base = p.cached_len[r], all = p.kv_len[r], m = p.keep_len[r];
     const int32_t *keep = p.keep + r * p.keep_stride;
 
@@ -149,8 +151,7 @@ cudaError_t launch(const CompactParams &p, cudaStream_t s)
     cut.slabs = kThreads / (cut.cols * cut.row_lanes);
     const int64_t groups = (slabs + cut.slabs - 1) / cut.slabs * cut.parts;  // (below 2^16)
     const size_t smem = (kOnce ? 1 : 3) * sizeof(Move) * cut.row_lanes * kDepth;  // (at most 24 KB)
-    cache_compact_kernel<kThreads, kDepth, kOnce><<<dim3((unsigned)p.R, (unsigned)groups), kThreads, smem, s>>>(p, cut);
-    return cudaGetLastError();
+    return launch_early(cache_compact_kernel<kThreads, kDepth, kOnce>, dim3((unsigned)p.R, (unsigned)groups), kThreads, smem, s, 1, p, cut);
 }
 
 }  // namespace

@@ -12,6 +12,7 @@
 // takes 267).
 #include <climits>
 
+#include "ptx_sm103.cuh"
 #include "rsa_internal.h"
 
 namespace rsa {
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
         s_used[i] = 0;
     if (tid == 0)
         s_bad = 0;
+    ptx::wait_for_launch_before();
     const long long start = p.free_start ? *p.free_start : 0;
     __syncthreads();
     for (int f = tid; f < F; f += kThreads) {
@@ -270,8 +272,7 @@ cudaError_t launch_page_fork(const PageForkParams &p, cudaStream_t s)
     const int64_t entries = ((int64_t)p.F * p.max_pages + kThreads - 1) / kThreads;
     blocks = blocks > entries ? blocks : entries;
     blocks = blocks < 1 ? 1 : (blocks > 304 ? 304 : blocks);
-    page_fork_kernel<<<(unsigned)blocks, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(page_fork_kernel, dim3((unsigned)blocks), kThreads, smem, s, 1, p);
 }
 
 }  // namespace rsa

@@ -14,6 +14,7 @@
 // the cluster's barriers one after the other.
 #include <cooperative_groups.h>
 
+#include "ptx_sm103.cuh"
 #include "rsa_internal.h"
 
 namespace rsa {
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     for (int i = tid; i < held; i += kThreads)
         s_bits[i] = 0;
     // ---- the requests' entries -----------------------------------------------------------
+    ptx::wait_for_launch_before();
     const long long start = *p.free_start;
     int bad = 0;
     for (int rb = tid; rb < R; rb += kThreads * kBatch) {
@@ -307,18 +309,7 @@ cudaError_t launch(const PageFreeParams &p, cudaStream_t s)
         if (e != cudaSuccess)
             return e;
     }
-    cudaLaunchAttribute cluster;
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = kCtas;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCtas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &cluster;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, page_free_kernel<kThreads, kWhole, kBatch>, p, (int)words, (int)spare / 4);
+    return launch_early(page_free_kernel<kThreads, kWhole, kBatch>, dim3(kCtas), kThreads, smem, s, kCtas, p, (int)words, (int)spare / 4);
 }
 
 }  // namespace

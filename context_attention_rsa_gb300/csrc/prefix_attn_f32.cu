@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(kThreads) prefix_attn_f32_kernel(const __grid_
     const int worker = blockIdx.x;
     const float scale = 1.0f / sqrtf((float)D);
 
+    if constexpr (kTree)
+        ptx::wait_for_launch_before();
     const Stretch st = find_stretch<kThreads, false>(p, worker, s.sum, &s.st);
     ptx::launch_dependents();
     Walk<false> walk;
@@ -806,32 +808,20 @@ cudaError_t simt(const PrefixAttnParams &p_in, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>));
     if (e != cudaSuccess)
         return e;
-    kernel<<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
-    e = cudaGetLastError();
+    if (p.mask) {
+        e = launch_early(kernel, dim3((unsigned)p.workers), kThreads, sizeof(Smem<D>), s, 1, p);
+    } else {
+        kernel<<<p.workers, kThreads, sizeof(Smem<D>), s>>>(p);
+        e = cudaGetLastError();
+    }
     return e != cudaSuccess ? e : launch_prefix_join(p, s);
-}
-
-// The launch begins while the attention still computes.
-template <class K, class... A>
-cudaError_t launch_early(K kernel, int64_t blocks, cudaStream_t s, const A &...args)
-{
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <class E, int D, int kJoinRows, int kAhead, int kBlocks>
 cudaError_t join_rows(const PrefixAttnParams &p, cudaStream_t s)
 {
     const int64_t items = p.T * p.Hkv * ((p.G + kJoinRows - 1) / kJoinRows), blocks = (items + kJoinWarps - 1) / kJoinWarps;
-    return launch_early(prefix_join_rows_kernel<E, D, kJoinRows, kAhead, kBlocks>, blocks < 152 * kBlocks ? blocks : 152 * kBlocks, s, p);
+    return launch_early(prefix_join_rows_kernel<E, D, kJoinRows, kAhead, kBlocks>, dim3((unsigned)(blocks < 152 * kBlocks ? blocks : 152 * kBlocks)), kJoinThreads, 0, s, 1, p);
 }
 
 // Up to a row for each SM: four warps a row, since the fewer the rows, the more pieces
@@ -844,7 +834,7 @@ cudaError_t join_any(const PrefixAttnParams &p, cudaStream_t s)
     constexpr int kParts = 4;
     const int64_t rows = p.T * p.Hq;
     if (rows <= 152)
-        return launch_early(prefix_join_kernel<E, D, kParts>, (rows * kParts + kJoinWarps - 1) / kJoinWarps, s, p);
+        return launch_early(prefix_join_kernel<E, D, kParts>, dim3((unsigned)((rows * kParts + kJoinWarps - 1) / kJoinWarps)), kJoinThreads, 0, s, 1, p);
     return rows <= 152 * 32 ? join_rows<E, D, 1, 8, 2>(p, s) : join_rows<E, D, 4, 3, 2>(p, s);
 }
 

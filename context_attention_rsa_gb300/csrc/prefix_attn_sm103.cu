@@ -445,6 +445,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
     }
     int64_t *s_sum = reinterpret_cast<int64_t *>(gbase + C::kSumOff);
+    if constexpr (kTree)
+        ptx::wait_for_launch_before();
     Stretch st;
     if (!kTree || p.R >= 32)
         st = find_stretch<C::kThreads, kTree>(p, worker, s_sum, reinterpret_cast<Stretch *>(s_sum + 2 * (C::kThreads / 32)));
@@ -939,8 +941,12 @@ cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::kSmemBytes);
     if (e != cudaSuccess)
         return e;
-    kernel<<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, mk8, mv8, p);
-    e = cudaGetLastError();
+    if (p.mask) {
+        e = launch_early(kernel, dim3((unsigned)p.workers), Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s, 1, mq, mk, mv, mk8, mv8, p);
+    } else {
+        kernel<<<p.workers, Cfg<D>::kThreads, Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, mk8, mv8, p);
+        e = cudaGetLastError();
+    }
     return e != cudaSuccess ? e : launch_prefix_join(p, s);
 }
 

@@ -371,6 +371,28 @@ rsa_status check_device_for(rsa_dtype dt);
 // A device pointer argument: not NULL and 16-byte aligned.
 rsa_status check_ptr(const void *p, const char *name);
 
+// Launches a kernel that may begin while the one before it on the stream ends.  The kernel
+// waits for that one (ptx::wait_for_launch_before) before it reads or writes memory, in every thread.
+// (0.3 us less a launch in a replayed graph.)  cluster: CTAs of a cluster.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, const A &...args)
+{
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Set the thread's last-error text and return `st`.

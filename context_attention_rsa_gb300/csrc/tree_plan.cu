@@ -12,6 +12,7 @@
 // 2.6 us on the GPU; 1000 of up to 64, 33000 rows, 3.6, the same as chains 4.5).
 #include <climits>
 
+#include "ptx_sm103.cuh"
 #include "rsa_internal.h"
 
 namespace rsa {
@@ -42,10 +43,12 @@ __device__ __forceinline__ int request_of(const TreePlanParams &p, int64_t row)
 template <bool kShort>
 __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_constant__ TreePlanParams p)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ int s_parent[];  // of rows [first, row0 + kThreads)
     const int tid = threadIdx.x, lane = tid & 31, most = 32 * p.words;
     const int64_t row0 = (int64_t)blockIdx.x * kThreads, row = row0 + tid;
     const int64_t first = max((int64_t)0, row0 - (most - 1));
+    ptx::wait_for_launch_before();
     for (int64_t t = first + tid; t < min(p.T, row0 + kThreads); t += kThreads)
         s_parent[t - first] = p.parent[t];
 
@@ -152,8 +155,17 @@ cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s)
 {
     const size_t smem = (size_t)(kThreads + 32 * p.words) * 4;  // (at most 4.6 KB)
     auto kernel = p.words <= 2 ? tree_plan_kernel<true> : tree_plan_kernel<false>;
-    kernel<<<(unsigned)((p.T + kThreads - 1) / kThreads), kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.T + kThreads - 1) / kThreads));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace rsa
