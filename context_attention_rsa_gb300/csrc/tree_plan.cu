@@ -3,13 +3,15 @@
 //   A_i = {i} + A_parent(i),  depth_i = |A_i| - 1,  pos_i = pos0 + cached + depth_i
 //
 // A thread takes a row and walks up its ancestors, whose indices descend, so that it
-// finishes one word of the mask after the other and holds only one (up to two: both, since
-// lanes that finish a word at different steps make all of them wait).  The parents
+// finishes one word of the mask after the other.  Of one or two words it holds both;
+// of more only the last, and those done go to shared memory, whence the block writes
+// them (lanes end a word at different steps, and a loop that fills words with zeros
+// there holds up the whole warp: 17 trees of up to 177, 11.2 us, so 5.0).  The parents
 // lie in shared memory, those of the block's rows and of as many rows before them as
 // a mask has bits.  A row's request comes from a 32-way search of cu_new by its warp.
 // The work is a few bytes a token: the launch, two or three dependent reads and one
 // shared-memory access for each generation of the deepest tree bound it (8 trees of 16
-// 2.6 us on the GPU; 1000 of up to 64, 33000 rows, 3.6, the same as chains 4.5).
+// 2.2 us on the GPU; 1000 of up to 64, 33000 rows, 3.3; four chains of 1024, 36).
 #include <climits>
 
 #include "ptx_sm103.cuh"
@@ -43,11 +45,14 @@ __device__ __forceinline__ int request_of(const TreePlanParams &p, int64_t row)
 template <bool kShort>
 __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_constant__ TreePlanParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     extern __shared__ int s_parent[];  // of rows [first, row0 + kThreads)
+    uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_parent + kThreads + 32 * p.words);  // [kThreads][words + 1] (not kShort)
     const int tid = threadIdx.x, lane = tid & 31, most = 32 * p.words;
     const int64_t row0 = (int64_t)blockIdx.x * kThreads, row = row0 + tid;
     const int64_t first = max((int64_t)0, row0 - (most - 1));
+    if (!kShort)
+        for (int k = tid; k < kThreads * (p.words + 1); k += kThreads)
+            s_mask[k] = 0;
     ptx::wait_for_launch_before();
     for (int64_t t = first + tid; t < min(p.T, row0 + kThreads); t += kThreads)
         s_parent[t - first] = p.parent[t];
@@ -85,17 +90,14 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
             look_b = p.cu_new[min(look + 1, (int64_t)p.R)];
         }
     }
-    if (row >= p.T)
-        return;
 
     // ---- its index, and the way up -----------------------------------------------------
-    uint32_t *mask = p.mask + row * p.words;
-    bool on = row < end;
+    bool on = row < end && row < p.T;
     const int64_t cached = all - (end - begin);
     if (on && row == max(begin, (int64_t)0) && cached < 0)
         record_bad_index(p.err, kSiteTreeLen, all);
     begin = max(begin, (int64_t)0);
-    int64_t pos = p.pos0 + max(cached, (int64_t)0);
+    const int64_t pos = p.pos0 + max(cached, (int64_t)0);
     int i = on ? (int)(row - begin) : 0;
     if (on && i >= most) {
         if (i == most)
@@ -122,50 +124,46 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
             ++depth;
             set();
         }
-        mask[0] = word[0];
-        if (p.words > 1)
-            mask[1] = word[1];
+        if (row < p.T) {
+            uint32_t *mask = p.mask + row * p.words;
+            mask[0] = word[0];
+            if (p.words > 1)
+                mask[1] = word[1];
+        }
     } else {
-        int at = p.words - 1;  // the word to be written next
-        uint32_t bits = 0;
-        if (on) {
-            for (; at > i >> 5; --at)
-                mask[at] = 0;
-            for (bits = 1u << (i & 31); (unsigned)up < (unsigned)i; bits |= 1u << (i & 31)) {
-                i = up;
-                up = parent[i];
-                ++depth;
-                for (; at > i >> 5; --at) {
-                    mask[at] = bits;
-                    bits = 0;
-                }
+        // a word is put away when the next one begins
+        uint32_t *mine = s_mask + tid * (p.words + 1), bits = 1u << (i & 31);
+        int w = i >> 5;
+        while ((unsigned)up < (unsigned)i) {
+            i = up;
+            up = parent[i];
+            ++depth;
+            if (i >> 5 != w) {
+                mine[w] = bits;
+                bits = 0;
+                w = i >> 5;
             }
+            bits |= 1u << (i & 31);
         }
-        for (; at >= 0; --at) {
-            mask[at] = bits;
-            bits = 0;
-        }
+        if (on)
+            mine[w] = bits;
+        __syncthreads();
+        const int n = (int)min((int64_t)kThreads, p.T - row0) * p.words;
+        uint32_t *mask = p.mask + row0 * p.words;
+        for (int k = tid; k < n; k += kThreads)
+            mask[k] = s_mask[k + k / p.words];
     }
-    p.positions[row] = on ? pos + depth : 0;
+    if (row < p.T)
+        p.positions[row] = on ? pos + depth : 0;
 }
 
 }  // namespace
 
 cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s)
 {
-    const size_t smem = (size_t)(kThreads + 32 * p.words) * 4;  // (at most 4.6 KB)
+    const size_t smem = (size_t)(kThreads + 32 * p.words + (p.words > 2 ? kThreads * (p.words + 1) : 0)) * 4;  // (at most 21 KB)
     auto kernel = p.words <= 2 ? tree_plan_kernel<true> : tree_plan_kernel<false>;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.T + kThreads - 1) / kThreads));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return launch_early(kernel, dim3((unsigned)((p.T + kThreads - 1) / kThreads)), kThreads, smem, s, 1, p);
 }
 
 }  // namespace rsa
