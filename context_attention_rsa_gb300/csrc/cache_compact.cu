@@ -156,9 +156,10 @@ cudaError_t launch(const CompactParams &p, cudaStream_t s)
 
 }  // namespace
 
-// Short lists fit a batch of 256 threads (64 requests with up to 6 rows in 16 layers 8.2 us;
-// by the loop 10.2).  Long ones go through batches of 128 rows of a head at least: whole rows
-// of whole pages (4 caches of 8192 rows in 4 layers 180 us, 6.0 TB/s, 0.88 of a copy; with
+// Short lists fit a batch of 256 threads (64 requests with up to 6 rows in 16 layers 6.0 us;
+// by the loop, when launches cost 2 us more, 10.2 against 8.2).  Long ones go through
+// batches of 128 rows of a head at least: whole rows of whole pages (4 caches of 8192 rows
+// in 4 layers 178 us, 6.0 TB/s, 0.88 of a copy; with
 // 256 threads of 8 rows 194, with blocks that share rows by columns 191 to 330).
 cudaError_t launch_cache_compact(const CompactParams &p, cudaStream_t s)
 {

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     }
     int32_t *to = p.free_pages + (start - freed) + before;
     // Each thread lists its words' pages; in shared memory first, where they fit what is no longer
-    // needed, so that they are written side by side (33000 pages 15.0 -> 12.2 us): the other parts
+    // needed, so that they are written side by side (33000 pages 15.0 -> 12.2 us, now 11.3): the other parts
     // of the bitmap, the sums and what lies behind them.
     const bool staged = kWhole && marks == freed && in_cta <= held - words + 2 * R + 1 + spare;
     auto stage = [&](int i) -> int & { return smem[i < rank * words ? i : i + words]; };
@@ -320,7 +320,7 @@ cudaError_t launch_page_free(const PageFreeParams &p, cudaStream_t s)
     if (p.n_pages > kMostWhole)
         return launch<1024, false, 4>(p, s);
     // Fewer threads where there is less to do, for shorter barriers and scans (300 requests of 75000
-    // entries in all, a tenth given back, 6.2 us against 6.9; 8 requests 5.0 against 5.9).  One CTA
+    // entries in all, a tenth given back, 6.2 us against 6.9; 8 requests 5.0 against 5.9, now 4.2).  One CTA
     // gains 0.1 us where next to nothing is given back and loses 4 where 2000 entries are.
     if ((int64_t)p.R * p.max_pages <= 131072)
         return launch<256, true, 4>(p, s);
