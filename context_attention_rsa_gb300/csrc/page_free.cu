@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
         }
     }
     bad = __syncthreads_or(bad);
-    // (a row has at most max_pages entries, and all rows below 2^31)
+    // (a row has at most max_pages entries, and all rows 2^30)
     const int per = (R + kThreads - 1) / kThreads | 1, r0 = min(R, tid * per), r1 = min(R, r0 + per);
     int mine = 0, entries;
     for (int r = r0; r < r1; ++r)

@@ -859,8 +859,8 @@ rsa_status rsa_page_free(const int32_t *block_table, int64_t table_stride, int m
     if (n_pages > kPageFreeMaxPages)
         return fail(RSA_ERR_UNSUPPORTED, "n_pages=%lld exceeds %lld pages", (long long)n_pages, (long long)kPageFreeMaxPages);
     RSA_TRY(check_table(block_table, table_stride, max_pages, page_size));
-    if ((int64_t)R * max_pages > 0x7fffffffLL)
-        return fail(RSA_ERR_UNSUPPORTED, "R=%d rows of max_pages=%d: more than 2^31-1 entries", R, max_pages);
+    if ((int64_t)R * max_pages > (1 << 30))  // (an entry's number and the threads' shares behind it are ints)
+        return fail(RSA_ERR_UNSUPPORTED, "R=%d rows of max_pages=%d: more than 2^30 entries", R, max_pages);
     if (n_free < 1 || n_free > 0x7fffffffLL)
         return fail(RSA_ERR_INVALID_ARG, "n_free=%lld must be in [1, 2^31-1]", (long long)n_free);
     RSA_TRY(check_i32_ptr(kv_len, "kv_len"));

@@ -714,7 +714,7 @@ rsa_status rsa_page_fork(const rsa_cache *cache, int32_t *block_table, int64_t t
  * changed.  An id outside [0, n_pages) is skipped, and a page given back more often
  * than it has users is freed once; both are reported by rsa_check_device_error.  Rows
  * of block_table stay as they are.  No buffer written may overlap another operand.
- * At most 16384 requests, 2^23 pages and 2^31 - 1 entries (R * max_pages).  One launch.
+ * At most 16384 requests, 2^23 pages and 2^30 entries (R * max_pages).  One launch.
  */
 rsa_status rsa_page_free(const int32_t *block_table, int64_t table_stride, int max_pages, const int32_t *kv_len,
                          const int32_t *keep_len, int R, int page_size, int64_t n_pages, int32_t *free_pages, int64_t n_free,

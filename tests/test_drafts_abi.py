@@ -214,3 +214,12 @@ def test_plain_page_keeping_by_hand():
     assert c[0][0, 5, 0, :, 0].tolist() == [4, 5, 22, 23]
     free, sh, info = dr.free_pages(t, [6, 6], [0, 0], np.array([7, 7, 7, 7]), 3, sh, page, 6)
     assert free.tolist() == [1, 3, 5, 7] and sh.tolist() == [0] * 6 and info == [0, 3, 4, 0]
+
+
+@pytest.mark.parametrize("R,max_pages,code", [(16384, 1 << 16, None), (16384, (1 << 16) + 1, UNSUPPORTED), (8192, 1 << 17, None),
+                                              (16384, (1 << 17) - 1, UNSUPPORTED)])
+def test_entries_of_a_page_free(R, max_pages, code):
+    # (a table of up to 8 GB, and what else there is behind it)
+    at = {k: v + (1 << 40) for k, v in AT.items() if k != "table"}
+    st, text = free_call(R=R, max_pages=max_pages, stride=max_pages, page=16, **at)
+    assert st == (code or STOPPED), text
