@@ -758,6 +758,8 @@ rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table,
     RSA_TRY(check_layers(cache, &p.c));
     if (R < 1 || max_keep < 1)
         return fail(RSA_ERR_INVALID_ARG, "R and max_keep must be >= 1 (got %d, %d)", R, max_keep);
+    if (max_keep > (1 << 30))  // (so that a step behind the list's end is still an int)
+        return fail(RSA_ERR_UNSUPPORTED, "max_keep=%d exceeds 2^30", max_keep);
     RSA_TRY(check_table(block_table, table_stride, max_pages, cache->page_size));
     if (keep_stride < max_keep || keep_stride > 0x7fffffffLL)
         return fail(RSA_ERR_INVALID_ARG, "keep_stride=%lld must be in [max_keep=%d, 2^31-1]", (long long)keep_stride, max_keep);

@@ -661,7 +661,7 @@ typedef struct {
  * own: no other request's moves may touch them in the same call.  Keys are moved
  * as they are, rotated for the position that they had: right for accepted
  * tokens, whose positions were those already.  No buffer written may overlap
- * another operand.  One launch.
+ * another operand.  max_keep is at most 2^30.  One launch.
  */
 rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table, int64_t table_stride, int max_pages,
                              const int32_t *cached_len, const int32_t *kv_len, int R, const int32_t *keep,

@@ -223,3 +223,9 @@ def test_entries_of_a_page_free(R, max_pages, code):
     at = {k: v + (1 << 40) for k, v in AT.items() if k != "table"}
     st, text = free_call(R=R, max_pages=max_pages, stride=max_pages, page=16, **at)
     assert st == (code or STOPPED), text
+
+
+@pytest.mark.parametrize("max_keep,code", [(1 << 30, None), ((1 << 30) + 1, UNSUPPORTED), ((1 << 31) - 1, UNSUPPORTED)])
+def test_longest_list_of_a_compaction(max_keep, code):
+    st, text = compact_call(R=1, max_keep=max_keep, ks=max_keep, keep=1 << 40)
+    assert st == (code or STOPPED), text
