@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     __shared__ int s_freed[kCtas], s_marked[kCtas];  // pages in each CTA's part; entries that each has marked
     const int R = p.R, P = 1 << p.page_shift;
 
+    if (kWhole)
+        ptx::cluster_begin_arrive();
     for (int i = tid; i < held; i += kThreads)
         s_bits[i] = 0;
     // ---- the requests' entries -----------------------------------------------------------
@@ -155,6 +157,8 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     }
     if (tid == 0)
         s_before[R] = entries;
+    if (kWhole)
+        ptx::cluster_begin_wait();
     if (bad) {  // (the same in every CTA)
         if (rank == 0 && tid == 0) {
             p.info[0] = RSA_PLAN_BAD_LENGTH;

@@ -421,6 +421,17 @@ __device__ __forceinline__ void cluster_sync()
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of a wait until every CTA of the cluster has begun, before which none may
+// touch another's shared memory.  Each by all threads, once, one after the other.
+__device__ __forceinline__ void cluster_begin_arrive()
+{
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begin_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Arrive on a barrier given by its cluster address (this CTA's or the peer's),
 // with the default CTA-scope release.  The kernels use it for "this thread's
 // tcgen05.st data is in its own CTA's TMEM" (already completed by
