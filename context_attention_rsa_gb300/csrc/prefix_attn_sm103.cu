@@ -61,7 +61,7 @@
 // their rows:
 //   48 requests of 5 to 25 tokens behind 32768     587 us, 1355 TFLOP/s (837 at first: the short units
 //     weighed too little, 260 us, and the joining launch took 56 instead of 18)
-//   16 requests of 64 tokens, 8192 to 32768 keys   426 us, 1409 TFLOP/s; HBM reads 1.17 GB, each key once
+//   16 requests of 64 tokens, 8192 to 32768 keys   426 us, 1367 TFLOP/s; HBM reads 1.17 GB, each key once
 //     (2.3 GB with the two halves of a request's rows at different times)
 //   38 requests of 16 tokens behind 131072        1650 us, 1585 TFLOP/s, 0.84 of cuBLAS (2003 with the
 //     prefix read from HBM by every unit)
