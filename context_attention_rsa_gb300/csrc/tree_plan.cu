@@ -6,12 +6,15 @@
 // finishes one word of the mask after the other.  Of one or two words it holds both;
 // of more only the last, and those done go to shared memory, whence the block writes
 // them (lanes end a word at different steps, and a loop that fills words with zeros
-// there holds up the whole warp: 17 trees of up to 177, 11.2 us, so 5.0).  The parents
+// there holds up the whole warp: 17 trees of up to 177, 11.2 us, so 5.0).  Where more than
+// half of a block's tokens are children of the one before them, a step goes over up to
+// 32 of those (four chains of 1024 36 -> 6.6 us); where few are it would take 1.5 times
+// as long, its steps being twice as dear.  The parents
 // lie in shared memory, those of the block's rows and of as many rows before them as
 // a mask has bits.  A row's request comes from a 32-way search of cu_new by its warp.
 // The work is a few bytes a token: the launch, two or three dependent reads and one
 // shared-memory access for each generation of the deepest tree bound it (8 trees of 16
-// 2.2 us on the GPU; 1000 of up to 64, 33000 rows, 3.3; four chains of 1024, 36).
+// 2.2 us on the GPU; 1000 of up to 64, 33000 rows, 3.3).
 #include <climits>
 
 #include "ptx_sm103.cuh"
@@ -47,6 +50,8 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
 {
     extern __shared__ int s_parent[];  // of rows [first, row0 + kThreads)
     uint32_t *s_mask = reinterpret_cast<uint32_t *>(s_parent + kThreads + 32 * p.words);  // [kThreads][words + 1] (not kShort)
+    uint32_t *s_follow = s_mask + kThreads * (p.words + 1);  // [words + kThreads / 32], from row row0 - 32 words on (not kShort)
+    __shared__ int64_t s_begin;  // of the first row's request
     const int tid = threadIdx.x, lane = tid & 31, most = 32 * p.words;
     const int64_t row0 = (int64_t)blockIdx.x * kThreads, row = row0 + tid;
     const int64_t first = max((int64_t)0, row0 - (most - 1));
@@ -80,6 +85,8 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
         if (in != 0xffffffffu)
             break;
     }
+    if (!kShort && tid == 0)
+        s_begin = max(begin, (int64_t)0);
     __syncthreads();
     while (look <= p.R) {
         if (look_a < 0 || look_a > p.T || look_b < look_a)
@@ -131,19 +138,61 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
                 mask[1] = word[1];
         }
     } else {
-        // a word is put away when the next one begins
-        uint32_t *mine = s_mask + tid * (p.words + 1), bits = 1u << (i & 31);
+        // A word of the mask is put away when the next one begins.
+        uint32_t *mine = s_mask + tid * (p.words + 1), bits = 0;
         int w = i >> 5;
-        while ((unsigned)up < (unsigned)i) {
-            i = up;
-            up = parent[i];
-            ++depth;
-            if (i >> 5 != w) {
-                mine[w] = bits;
-                bits = 0;
-                w = i >> 5;
+        const bool follows = on && i > 0 && up == i - 1;  // (the token is the child of the one before it)
+        const int rows = __syncthreads_count(on);
+        if (2 * __syncthreads_count(follows) > rows) {
+            // ---- mostly chains: up to 32 tokens in a row at a time, by a bit for each that follows
+            const unsigned vote = __ballot_sync(0xffffffffu, follows);
+            if (lane == 0)
+                s_follow[p.words + tid / 32] = vote;
+            for (int k = tid; k < most; k += kThreads) {  // (whole warps; of the rows before the block's)
+                const int64_t t = row0 - most + k;
+                const unsigned v = __ballot_sync(0xffffffffu, t >= first && t > s_begin && s_parent[t - first] == t - s_begin - 1);
+                if (lane == 0)
+                    s_follow[k / 32] = v;
             }
-            bits |= 1u << (i & 31);
+            __syncthreads();
+            const int off = on ? (int)(begin - row0) + most : 0;  // of token 0 in s_follow's bits
+            for (bool more = on; more;) {
+                const int at = off + i, k = at >> 5;
+                const uint32_t x = __funnelshift_rc(k > 0 ? s_follow[k - 1] : 0, s_follow[k], (at & 31) + 1);
+                // token i is behind `run` others in a row (never more than there are, also where cu_new does not ascend)
+                const int run = min(__clz(~x), i), low = i - run;
+                depth += run;
+                if (i >> 5 != w) {
+                    mine[w] = bits;
+                    bits = 0;
+                    w = i >> 5;
+                }
+                uint32_t set = ~0u >> (31 - (i & 31));
+                if (low >> 5 != w) {
+                    mine[w] = bits | set;
+                    bits = 0;
+                    --w;
+                    set = ~0u;
+                }
+                bits |= set & ~0u << (low & 31);
+                up = parent[low];
+                more = (unsigned)up < (unsigned)low;
+                i = up;
+                depth += more;
+            }
+        } else {
+            bits = 1u << (i & 31);
+            while ((unsigned)up < (unsigned)i) {
+                i = up;
+                up = parent[i];
+                ++depth;
+                if (i >> 5 != w) {
+                    mine[w] = bits;
+                    bits = 0;
+                    w = i >> 5;
+                }
+                bits |= 1u << (i & 31);
+            }
         }
         if (on)
             mine[w] = bits;
@@ -161,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
 
 cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s)
 {
-    const size_t smem = (size_t)(kThreads + 32 * p.words + (p.words > 2 ? kThreads * (p.words + 1) : 0)) * 4;  // (at most 21 KB)
+    const size_t smem = (size_t)(kThreads + 32 * p.words + (p.words > 2 ? kThreads * (p.words + 1) + p.words + kThreads / 32 : 0)) * 4;  // (at most 22 KB)
     auto kernel = p.words <= 2 ? tree_plan_kernel<true> : tree_plan_kernel<false>;
     return launch_early(kernel, dim3((unsigned)((p.T + kThreads - 1) / kThreads)), kThreads, smem, s, 1, p);
 }

@@ -107,6 +107,36 @@ def test_plan_reports_what_it_cannot_follow():
     assert got.positions[0] == 0  # (row 1 lies in [0, 2) and in [1, 4): either may have it)
 
 
+@pytest.mark.parametrize("sizes", [[100], [60, 300, 5], [1000, 90]])
+def test_plan_of_long_trees_with_runs_and_bad_parents(sizes):
+    # chains that break off at many places, among them parents that are none, across words and blocks
+    need_cuda()
+    rng = np.random.default_rng(sum(sizes))
+    for often in (0.02, 0.3):
+        parent, good = [], []
+        for n in sizes:
+            for i in range(n):
+                j = i - 1 if rng.random() > often else int(rng.integers(-1, i)) if i else -1
+                bad = rng.random() < 0.02
+                parent.append(int(rng.choice([i, i + 1, 2000, -2, -(1 << 31)])) if bad else j)
+                good.append(-1 if bad else j)
+        cu, lens = np.concatenate([[0], np.cumsum(sizes)]), [n + 7 for n in sizes]
+        want = dr.tree_plan(good, cu.tolist(), lens, -(-max(sizes) // 32), len(parent))
+        got = rsa.tree_plan(i32(parent), i32(cu.tolist()), i32(lens), max(sizes))
+        assert_plan(got, want)
+        assert parent == good or "site code 0x98" in reported()
+
+
+def test_long_plans_whose_rows_do_not_ascend():
+    # what is right of it does not matter, but nothing else is read or written, and it is reported
+    need_cuda()
+    parent = i32(list(range(-1, 299)))
+    for cu in ([0, 290, 40, 300], [200, 290, 0, 300], [300, 0, 250, 10], [0, 130, 129, 300]):
+        got = rsa.tree_plan(parent, i32(cu), i32([400] * 3), 300)
+        assert "site code 0x9" in reported()  # (0x96; or 0x98 first, a parent that is none among the rows of another request)
+        assert (got.positions >= 0).all() and (got.positions < 700).all()
+
+
 # ---- tree_attn ---------------------------------------------------------------------------
 
 class TreeBatch(Batch):
