@@ -259,9 +259,13 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
 
 cudaError_t launch_page_fork(const PageForkParams &p, cudaStream_t s)
 {
-    const size_t smem = (3ull * p.F + 3 + 2ull * p.R + (p.R + 31) / 32) * 4;  // (at most 224 KB)
+    auto smem_of = [](int64_t F, int64_t R) constexpr { return (size_t)(3 * F + 3 + 2 * R + (R + 31) / 32) * 4; };
+    constexpr size_t kMost = smem_of(kPageForkMost, kPagePlanMaxRequests);  // 224 KB
+    const size_t smem = smem_of(p.F, p.R);
+    // (always the most: the limit is the kernel's, not the call's, and another thread may launch it
+    // between this one's two calls)
     if (smem > 48 * 1024 - 2048) {
-        cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = cudaFuncSetAttribute(page_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess)
             return e;
     }

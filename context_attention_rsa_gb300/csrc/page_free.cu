@@ -301,26 +301,40 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     cluster.sync();  // no CTA ends while others look at its part
 }
 
+constexpr int64_t kMostWhole = 780000;  // pages: 98 KB of bitmap beside 128 KB of sums and kept pages
+
+// Words of a part of the bitmap, and bytes of shared memory without the spare ones.
+constexpr int64_t words_of(int64_t n_pages) { return ((n_pages + 31) / 32 + kCtas - 1) / kCtas; }
+template <bool kWhole>
+constexpr size_t smem_of(int64_t n_pages, int64_t R)
+{
+    return (size_t)(kWhole ? words_of(n_pages) * kCtas + 2 * R + 1 : words_of(n_pages) + R + 1) * 4;
+}
+
 template <int kThreads, bool kWhole, int kBatch>
 cudaError_t launch(const PageFreeParams &p, cudaStream_t s)
 {
-    const int64_t words = ((p.n_pages + 31) / 32 + kCtas - 1) / kCtas;
-    const size_t used = (kWhole ? (size_t)words * kCtas + 2 * p.R + 1 : (size_t)words + p.R + 1) * 4;
-    const size_t spare = kWhole && used <= 200 * 1024 ? 8 * 1024 : 0, smem = used + spare;
+    constexpr size_t kMost = smem_of<kWhole>(kWhole ? kMostWhole : kPageFreeMaxPages, kPagePlanMaxRequests);
+    constexpr size_t kSpare = 8 * 1024, kSpareUpTo = 200 * 1024;
+    static_assert(kMost <= 226 * 1024 && (!kWhole || kSpareUpTo + kSpare <= kMost), "shared memory");
+    const size_t used = smem_of<kWhole>(p.n_pages, p.R);
+    const size_t spare = kWhole && used <= kSpareUpTo ? kSpare : 0, smem = used + spare;
+    // (always the most: the limit is the kernel's, not the call's, and another thread may launch it
+    // between this one's two calls)
     if (smem > 48 * 1024 - 1024) {
         cudaError_t e =
-            cudaFuncSetAttribute(page_free_kernel<kThreads, kWhole, kBatch>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(page_free_kernel<kThreads, kWhole, kBatch>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess)
             return e;
     }
-    return launch_early(page_free_kernel<kThreads, kWhole, kBatch>, dim3(kCtas), kThreads, smem, s, kCtas, p, (int)words, (int)spare / 4);
+    return launch_early(page_free_kernel<kThreads, kWhole, kBatch>, dim3(kCtas), kThreads, smem, s, kCtas, p, (int)words_of(p.n_pages),
+                        (int)spare / 4);
 }
 
 }  // namespace
 
 cudaError_t launch_page_free(const PageFreeParams &p, cudaStream_t s)
 {
-    constexpr int64_t kMostWhole = 780000;  // 98 KB of bitmap beside 128 KB of sums and kept pages
     if (p.n_pages > kMostWhole)
         return launch<1024, false, 4>(p, s);
     // Fewer threads where there is less to do, for shorter barriers and scans (300 requests of 75000
