@@ -22,8 +22,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kDepth = 8;             // 16-byte loads that a lane has in flight
 constexpr int kPiece = kDepth * 512;  // bytes that a warp copies at once
 
-constexpr int kBadRequest = 1, kBadLength = 2;
-
 // Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
 __device__ __forceinline__ int last_not_above(const int *a, int n, int x)
 {
@@ -95,7 +93,6 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
     unsigned *s_used = reinterpret_cast<unsigned *>(s_forks + p.R);  // a bit for each request: it is in dst
     __shared__ Counts s_warp[kWarps];
     __shared__ int s_list[kWarps][32];
-    __shared__ int s_bad;
     const int tid = threadIdx.x, P = 1 << p.c.page_shift, F = p.F;
     const bool shared = p.shares != nullptr;
 
@@ -106,37 +103,37 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
     }
     for (int i = tid; i < (p.R + 31) / 32; i += kThreads)
         s_used[i] = 0;
-    if (tid == 0)
-        s_bad = 0;
     ptx::wait_for_launch_before();
     const long long start = p.free_start ? *p.free_start : 0;
     __syncthreads();
+    // (what is wrong is told at barriers, so that all threads take the same ways)
+    int bad = 0, bad_len = 0;
     for (int f = tid; f < F; f += kThreads) {
         const int a = p.src[f], b = p.dst[f];
         if (a < 0 || a >= p.R || b < 0 || b >= p.R || (atomicOr(&s_used[b >> 5], 1u << (b & 31)) >> (b & 31) & 1)) {
-            atomicOr(&s_bad, kBadRequest);
+            bad = 1;
             continue;
         }
         s_pages[f] = p.kv_len[a];
         atomicMin(&s_first[a], f);
         atomicAdd(&s_forks[a], 1);
     }
-    __syncthreads();
-    if (!s_bad)
+    bad = __syncthreads_or(bad);
+    if (!bad)
         for (int f = tid; f < F; f += kThreads) {
             const int a = p.src[f], n = s_pages[f];
             if (s_used[a >> 5] >> (a & 31) & 1)
-                atomicOr(&s_bad, kBadRequest);
+                bad = 1;
             const bool fits = n >= 0 && n <= (int64_t)p.max_pages << p.c.page_shift;
             if (!fits)
-                atomicOr(&s_bad, kBadLength);
+                bad_len = 1;
             const int pages = fits ? (int)(((int64_t)n + P - 1) >> p.c.page_shift) : 0;
             s_pages[f] = pages;
             s_fresh[f] = shared ? (n & (P - 1)) != 0 : pages;
             s_copies[f] = s_first[a] == f ? s_fresh[f] : 0;
         }
-    __syncthreads();
-    const bool bad = s_bad & kBadRequest, bad_len = s_bad & kBadLength;
+    bad = __syncthreads_or(bad);
+    bad_len = __syncthreads_or(bad_len);
     Counts all{0, 0, 0};
     if (!bad && !bad_len)
         all = exclusive_sums(s_pages, s_fresh, s_copies, F, s_warp);
