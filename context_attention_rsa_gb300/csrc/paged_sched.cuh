@@ -42,6 +42,10 @@ namespace paged {
 
 constexpr int kTileShift = 7, kTileKeys = 1 << kTileShift;
 
+// PrefixAttnParams::side_by_side of a call that wants it: there have to be two workers for two units,
+// and with one the odd groups would lie behind its stretch.
+inline int side_by_side(int workers) { return workers > 1 ? -1 : 0; }
+
 struct Segment {
     int tok0, ntok;        // its query tokens
     int keys;              // its keys

@@ -920,7 +920,7 @@ cudaError_t launch(const PrefixAttnParams &p_in, cudaStream_t s)
     p.heavy_tile = kHeavyTile;
     p.unit = p.mask ? kTreeUnit : kUnit;
     p.unit_shift = p.mask ? kTreeUnitShift : 31;
-    p.side_by_side = p.mask ? -1 : 0;
+    p.side_by_side = p.mask ? side_by_side(p.workers) : 0;
     CUtensorMap mq, mk, mv, mk8, mv8;
     const uint64_t page = 1ull << p.page_shift, heads = (uint64_t)(p.n_pages * p.Hkv), halves = D / 64;
     const uint64_t qd[4] = {(uint64_t)D, (uint64_t)p.G, (uint64_t)p.Hkv, (uint64_t)p.T};
