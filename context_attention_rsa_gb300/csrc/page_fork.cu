@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
     int bad = 0, bad_len = 0;
     for (int f = tid; f < F; f += kThreads) {
         const int a = p.src[f], b = p.dst[f];
+        if (a == -1 && b == -1)
+            continue;  // no fork
         if (a < 0 || a >= p.R || b < 0 || b >= p.R || (atomicOr(&s_used[b >> 5], 1u << (b & 31)) >> (b & 31) & 1)) {
             bad = 1;
             continue;
@@ -121,7 +123,12 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
     bad = __syncthreads_or(bad);
     if (!bad)
         for (int f = tid; f < F; f += kThreads) {
-            const int a = p.src[f], n = s_pages[f];
+            const int a = p.src[f];
+            if (a < 0) {
+                s_pages[f] = s_fresh[f] = s_copies[f] = 0;
+                continue;
+            }
+            const int n = s_pages[f];
             if (s_used[a >> 5] >> (a & 31) & 1)
                 bad = 1;
             const bool fits = n >= 0 && n <= (int64_t)p.max_pages << p.c.page_shift;
@@ -156,7 +163,8 @@ __global__ void __launch_bounds__(kThreads) page_fork_kernel(const __grid_consta
         return;
     // (dst's lengths and rows of the table are written, src's are read: no request is in both)
     for (long long f = g0; f < F; f += gn)
-        p.kv_len[p.dst[f]] = p.kv_len[p.src[f]];
+        if (p.src[f] >= 0)
+            p.kv_len[p.dst[f]] = p.kv_len[p.src[f]];
 
     // ---- table entries -------------------------------------------------------------------
     for (long long i = g0; i < entries; i += gn) {

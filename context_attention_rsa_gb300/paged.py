@@ -280,7 +280,8 @@ def page_fork(k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_
     block_table, kv_len and shares are updated in place, rows are copied in every layer
     of the caches (as in cache_compact; a fork is one call, with all layers); fresh pages come from free_pages as in
     page_plan.  Returns info, int64 [4]: status (PLAN_STATUS), entries shared, pages
-    taken, first free entry after them.  Forks that cannot all be made change nothing."""
+    taken, first free entry after them.  Forks that cannot all be made change nothing; an entry
+    with -1 in both lists is no fork, so that a captured call may make any number up to its own."""
     r = (_native or _load_native()).page_fork(k_cache, v_cache, block_table, kv_len, src, dst, free_pages, free_start, shares, out, stream)
     if r.__class__ is int:
         raise _error("rsa_page_fork", r)

@@ -686,10 +686,11 @@ rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table,
  * free_start is NULL), in the forks' order.  The rows are copied in all layers of
  * the call: a fork is one call, with the caches of every layer.  What
  * dst's row held before is not freed.  dst has no request twice and none that is in
- * src; src may name a request several times.
+ * src; src may name a request several times.  An entry with src[f] = dst[f] = -1 is
+ * no fork: a captured call keeps its F, and how many forks there are may change.
  *   info [4]: status, entries shared, pages taken, first free entry after them.
  * Forks that cannot all be made change nothing: RSA_PLAN_BAD_REQUEST (a request
- * outside [0, R), or twice in dst, or in both), RSA_PLAN_BAD_LENGTH (kv_len of a
+ * outside [0, R), but for -1 in both, or twice in dst, or in both), RSA_PLAN_BAD_LENGTH (kv_len of a
  * source negative or beyond its row), RSA_PLAN_NO_PAGES; the first that
  * applies.  A page id outside [0, n_pages) in a source's row is copied, but neither
  * counted nor its rows copied; it and such an entry of free_pages are reported
