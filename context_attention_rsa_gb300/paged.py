@@ -23,6 +23,14 @@ With a tree of drafted tokens for every request (parent: each token's parent):
     info = page_free(block_table, plan.kv_len, new_len, free_pages, plan.info[3:], page_size, n_pages)
     # the next step: cached_len = new_len, free_start = info[3:]
 
+cache_compact also keeps a window of the cached tokens (cached_len 0, keep the window's tokens).  Keys keep
+their rotation, and the plans go by lengths; from then on a request's new tokens are as many
+positions further as it has dropped tokens (dropped int32 [R], on the device):
+
+    row = torch.arange(max_tokens, device=dropped.device, dtype=torch.int32)
+    request = torch.searchsorted(plan.cu_new[1:], row, right=True).clamp_(max=R - 1)
+    positions = plan.positions + dropped[request]   # tree.positions in the same way
+
 Caches are [n_pages, Hkv, page_size, d]; a step's rows are packed [T, H, d].
 Nothing synchronises, so a step can be captured into a CUDA graph and replayed
 with other lengths: what depends on them is read on the device.
@@ -265,7 +273,8 @@ def cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_
     cached_len[r] + keep[r, i], i < keep_len[r], in every layer of k_cache and v_cache
     [n_pages, Hkv, page_size, d] or [layers, n_pages, Hkv, page_size, d].  keep
     [R, max_keep] int32, strictly ascending in a row's first keep_len[r] entries.
-    Returns the new lengths, int32 [R]: cached_len + keep_len."""
+    Returns the new lengths, int32 [R]: cached_len + keep_len.  Keys keep their rotation:
+    where cached tokens are dropped, later positions go on behind theirs (see the module)."""
     r = (_native or _load_native()).cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_len, out, stream)
     if r.__class__ is int:
         raise _error("rsa_cache_compact", r)

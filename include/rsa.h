@@ -658,10 +658,16 @@ typedef struct {
  * hold or held.  A request whose lengths, list or pages are outside their ranges is
  * left as it is, with new_len[r] = cached_len[r], and is reported by
  * rsa_check_device_error.  The pages that rows move within are the request's
- * own: no other request's moves may touch them in the same call.  Keys are moved
- * as they are, rotated for the position that they had: right for accepted
- * tokens, whose positions were those already.  No buffer written may overlap
- * another operand.  max_keep is at most 2^30.  One launch.
+ * own: no other request's moves may touch them in the same call.
+ *   Keys are moved as they are, rotated for the position that they had.  That is
+ * right for accepted tokens, whose positions were those already.  Where cached tokens
+ * are dropped, a window for instance, the request becomes shorter than its positions:
+ * rsa_page_plan and rsa_tree_plan, which go by lengths, would give its next tokens
+ * positions among those of the kept ones.  Count the tokens that each request has
+ * dropped, and add that to its rows of `positions` before rsa_qk_norm_rope_fwd, in
+ * every later step.
+ *   No buffer written may overlap another operand.  max_keep is at most 2^30.  One
+ * launch.
  */
 rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table, int64_t table_stride, int max_pages,
                              const int32_t *cached_len, const int32_t *kv_len, int R, const int32_t *keep,
