@@ -274,7 +274,8 @@ def cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_
     [n_pages, Hkv, page_size, d] or [layers, n_pages, Hkv, page_size, d].  keep
     [R, max_keep] int32, strictly ascending in a row's first keep_len[r] entries.
     Returns the new lengths, int32 [R]: cached_len + keep_len.  Keys keep their rotation:
-    where cached tokens are dropped, later positions go on behind theirs (see the module)."""
+    where cached tokens are dropped, later positions go on behind theirs (see the module).
+    The pages must be the request's own: one that shares some is forked with shares=None first."""
     r = (_native or _load_native()).cache_compact(k_cache, v_cache, block_table, cached_len, kv_len, keep, keep_len, out, stream)
     if r.__class__ is int:
         raise _error("rsa_cache_compact", r)

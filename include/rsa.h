@@ -657,8 +657,8 @@ typedef struct {
  * or what is to be kept of a long cache.  Rows behind new_len[r] keep what they
  * hold or held.  A request whose lengths, list or pages are outside their ranges is
  * left as it is, with new_len[r] = cached_len[r], and is reported by
- * rsa_check_device_error.  The pages that rows move within are the request's
- * own: no other request's moves may touch them in the same call.
+ * rsa_check_device_error.  Rows move within the request's own pages: a page that
+ * another request uses too is not to be among them (see the next comment).
  *   Keys are moved as they are, rotated for the position that they had.  That is
  * right for accepted tokens, whose positions were those already.  Where cached tokens
  * are dropped, a window for instance, the request becomes shorter than its positions:
@@ -678,9 +678,14 @@ rsa_status rsa_cache_compact(const rsa_cache *cache, const int32_t *block_table,
  * Pages that several requests' tables share are counted in shares [n_pages]: for
  * each page the number of its users beyond the first, 0 for a page that one
  * request has for itself (what rsa_page_plan hands out is, so it needs no
- * counts).  A shared page is not written again: rsa_page_fork shares full ones
- * alone.  (A request that is cut back into a shared page and then grows would
- * write to it: fork it first.)
+ * counts).  A shared page is not to be written again, and nothing checks that:
+ * rsa_page_fork shares full pages alone, so that a request that only grows does not,
+ * but two others would.
+ *   - One that is cut back into a shared page and then grows: after rsa_page_free, fork it
+ *     with shares into a row that no request has, which gets a page of its own for
+ *     the partial one, end the old row and go on in the new one.
+ *   - One whose shared pages are to be compacted: fork it without shares (every page is
+ *     copied) into such a row first, end the old row and compact the new one.
  *
  * Forks: for f in [0, F) request dst[f] becomes a copy of request src[f], whose
  * kv_len[src[f]] tokens lie in ceil(kv_len / page_size) pages.
