@@ -883,7 +883,8 @@ template <class E, int D, int kJoinRows, int kAhead, int kBlocks>
 cudaError_t join_rows(const PrefixAttnParams &p, cudaStream_t s)
 {
     const int64_t items = p.T * p.Hkv * ((p.G + kJoinRows - 1) / kJoinRows), blocks = (items + kJoinWarps - 1) / kJoinWarps;
-    return launch_early(prefix_join_rows_kernel<E, D, kJoinRows, kAhead, kBlocks>, dim3((unsigned)(blocks < 152 * kBlocks ? blocks : 152 * kBlocks)), kJoinThreads, 0, s, 1, p);
+    const dim3 grid((unsigned)(blocks < 152 * kBlocks ? blocks : 152 * kBlocks));
+    return launch_early(prefix_join_rows_kernel<E, D, kJoinRows, kAhead, kBlocks>, grid, kJoinThreads, 0, s, 1, p);
 }
 
 // Up to a row for each SM: four warps a row, since the fewer the rows, the more pieces
@@ -895,8 +896,10 @@ cudaError_t join_any(const PrefixAttnParams &p, cudaStream_t s)
 {
     constexpr int kParts = 4;
     const int64_t rows = p.T * p.Hq;
-    if (rows <= 152)
-        return launch_early(prefix_join_kernel<E, D, kParts>, dim3((unsigned)((rows * kParts + kJoinWarps - 1) / kJoinWarps)), kJoinThreads, 0, s, 1, p);
+    if (rows <= 152) {
+        const dim3 grid((unsigned)((rows * kParts + kJoinWarps - 1) / kJoinWarps));
+        return launch_early(prefix_join_kernel<E, D, kParts>, grid, kJoinThreads, 0, s, 1, p);
+    }
     return rows <= 152 * 32 ? join_rows<E, D, 1, 8, 2>(p, s) : join_rows<E, D, 4, 3, 2>(p, s);
 }
 

@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads) tree_plan_kernel(const __grid_consta
 
 cudaError_t launch_tree_plan(const TreePlanParams &p, cudaStream_t s)
 {
-    const size_t smem = (size_t)(kThreads + 32 * p.words + (p.words > 2 ? kThreads * (p.words + 1) + p.words + kThreads / 32 : 0)) * 4;  // (at most 22 KB)
+    const int gathered = p.words > 2 ? kThreads * (p.words + 1) + p.words + kThreads / 32 : 0;
+    const size_t smem = (size_t)(kThreads + 32 * p.words + gathered) * 4;  // (at most 22 KB)
     auto kernel = p.words <= 2 ? tree_plan_kernel<true> : tree_plan_kernel<false>;
     return launch_early(kernel, dim3((unsigned)((p.T + kThreads - 1) / kThreads)), kThreads, smem, s, 1, p);
 }
