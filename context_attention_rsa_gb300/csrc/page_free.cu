@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) page_free_kernel(const __grid_consta
     }
     int32_t *to = p.free_pages + (start - freed) + before;
     // Each thread lists its words' pages; in shared memory first, where they fit what is no longer
-    // needed, so that they are written side by side (33000 pages 15.0 -> 12.2 us, now 11.3): the other parts
+    // needed, so that they are written side by side (61000 pages 15.0 -> 12.2 us, now 11.3): the other parts
     // of the bitmap, the sums and what lies behind them.
     const bool staged = kWhole && marks == freed && in_cta <= held - words + 2 * R + 1 + spare;
     auto stage = [&](int i) -> int & { return smem[i < rank * words ? i : i + words]; };

@@ -16,10 +16,10 @@
 // and a row's maximum and factors stay in its lanes.  A unit of few rows leaves warps
 // over: they are then cut into 2 or 4 key groups, which take the turn's blocks in
 // parallel and join their rows at the end of the piece.
-// Measured: 5 requests of 2 tokens, 4 key heads of 64, behind 4097 keys 21.3 us (4 key
+// Measured: 5 requests of 2 tokens, 4 key heads of 64, behind 4097 keys 20.5 us (4 key
 // groups and these tiles; with one row or two a warp, every block through all 16, it
 // took 41); one row of 4 heads of 64 over 100000 keys 62 us, 3.3 TB/s; 8 heads of 128 over
-// 60000 keys with 20 rows each 312 us, 15.8 TFLOP/s, and 512 rows over 4608 keys 343 us, 26.6
+// 60000 keys with 20 rows each 274 us, 18.0 TFLOP/s, and 512 rows over 4608 keys 340 us, 26.8
 // TFLOP/s of the visible pairs (a step of 4 columns is six 16-byte shared loads for 32
 // products a lane; which of the two pipes binds has not been counted).
 // Drafted tokens (kTree) in tiles of 32 keys: 5 requests of 3 to 13 tokens, 4 key heads of 64, behind

@@ -44,26 +44,26 @@
 //
 // Measured (64 query heads over 8 key heads of 128; GB/s of the keys and values that
 // have to be read, TFLOP/s of the visible pairs):
-//   4 requests of 131072 to 262144 own keys       426 us, 6.95 TB/s, the rate of a copy
+//   4 requests of 131072 to 262144 own keys       423 us, 7.0 TB/s, the rate of a copy
 //   8 requests of 4 tokens, 32 key heads, behind
-//     100000 keys in pages of 16                   255 us, 6.5 TB/s, 0.96 of a copy
+//     100000 keys in pages of 16                   251 us, 6.6 TB/s, 0.97 of a copy
 //   608 requests behind 262144 keys               3760 us, 1389 TFLOP/s, 0.74 of cuBLAS (ten calls;
-//     after a hundred, power-capped, 4080 us; keys of zeros, which cost less power, 3235 us)
-//   512 new tokens with 32768 before them          421 us, 1316 TFLOP/s; a prompt of 8192 without
-//     a past 1673 us, 657 TFLOP/s: its places count tiles that its rows do not see
-//   64 requests of 4 to 2000 keys behind 32768      91 us: 40 us of two-tile steps and
+//     after fifty to a hundred, power-capped, 4080 to 4210 us; keys of zeros, which cost less power, 3235 us)
+//   512 new tokens with 32768 before them          421 to 445 us, 1245 to 1316 TFLOP/s; a prompt of 8192
+//     without a past 1355 us, 811 TFLOP/s: its places count tiles that its rows do not see
+//   64 requests of 4 to 2000 keys behind 32768      90 us: 40 us of two-tile steps and
 //     18 of short units if perfectly shared; the scan 2, the first loads 5, a piece's end
 //     6 (its 256 rows, 16 bytes a lane and store) and the joining launch 5 us
-//   1 request of 1000 keys                        14.5 us, nearly all latency
+//   1 request of 1000 keys                        12.4 us, nearly all latency
 // Drafted tokens (kTree): keys from the piece's `drafted` on are masked by the rows' bits, in the
 // last tiles only; the words come while the tile's scores are still being computed.  Their
 // units lie on the line in another order (side by side, paged_sched.cuh) and weigh by
 // their rows:
-//   48 requests of 5 to 25 tokens behind 32768     587 us, 1355 TFLOP/s (837 at first: the short units
+//   48 requests of 5 to 25 tokens behind 32768     587 to 607 us, 1311 to 1355 TFLOP/s (837 at first: the short units
 //     weighed too little, 260 us, and the joining launch took 56 instead of 18)
-//   16 requests of 64 tokens, 8192 to 32768 keys   426 us, 1367 TFLOP/s; HBM reads 1.17 GB, each key once
-//     (2.3 GB with the two halves of a request's rows at different times)
-//   38 requests of 16 tokens behind 131072        1650 us, 1585 TFLOP/s, 0.84 of cuBLAS (2003 with the
+//   16 requests of 64 tokens, 8192 to 32768 keys   421 to 465 us, 1252 to 1383 TFLOP/s, by machine and power; HBM reads
+//     1.17 GB, each key once (2.3 GB with the two halves of a request's rows at different times)
+//   38 requests of 16 tokens behind 131072        1642 to 1701 us, 1535 to 1590 TFLOP/s, 0.81 to 0.84 of cuBLAS (2003 with the
 //     prefix read from HBM by every unit)
 // A step takes 2850 cycles, 4400 next to a CTA that runs short units, and what made short
 // units faster by more code made the whole slower: as if two neighbouring SMs shared an

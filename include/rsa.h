@@ -623,8 +623,9 @@ rsa_status rsa_tree_plan(const int32_t *parent, int64_t T, const int32_t *cu_new
  *   own token kv_len[r] - n + j for every j <= i whose bit is set in the row's mask
  * (mask [T, words], rows mask_stride words apart; bits past 32 * words count as not
  * set).  The mask may be any: rsa_tree_plan's, or a caller's own in which a row
- * does not see itself, or nothing.  All else is as for rsa_prefix_attn_fwd; the
- * workspace holds rsa_tree_attn_workspace_size() bytes.
+ * does not see itself, or nothing.  All else is as for rsa_prefix_attn_fwd, also that
+ * rows within the lengths have to be finite (those that a mask hides are multiplied, by
+ * zero: a branch that is rejected later too); the workspace holds rsa_tree_attn_workspace_size() bytes.
  */
 rsa_status rsa_tree_attn_workspace_size(rsa_dtype dt, int64_t T, int Hq, int Hkv, int d, int R, size_t *bytes);
 rsa_status rsa_tree_attn_fwd(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k_cache,
